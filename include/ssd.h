@@ -459,6 +459,114 @@ int ssd_chunk_scan(const void *x, const float *delta, const float *dA_cumsum, co
                    int batch, int seqlen, int nheads, int headdim, int ngroups, int dstate,
                    int chunk, int dtype, void *y, void *stream);
 
+/* ---- The operators around the state-space layer ---------------------------- */
+
+/*
+ * Short causal convolution along the token axis, one filter of `width` (2, 3
+ * or 4) taps per channel, over whole sequences: the convolution that the
+ * blocks put before the state-space layer ("Mamba-2架构深度解析", section 2.1).
+ *   v_t[c] = bias[c] + sum_{k < W} weight[c][k] * x_{t-W+1+k}[c]
+ *   y_t    = v_t * sigmoid(v_t) if silu, else v_t
+ * in float32, rounded once to dtype.
+ *   x            [Bt][L][K] in dtype, channels contiguous; sequences
+ *                x_batch_stride and tokens x_token_stride elements apart, so
+ *                that x may be a slice of a wider projection. Element alignment.
+ *   weight, bias float32 [K][W] and [K] (bias nullable).
+ *   init_state   nullable, [Bt][W-1][K] in dtype: the inputs of the W-1 tokens
+ *                before the first (NULL: zeros).
+ *   cu_seqlens   nullable: packed sequences as for ssd_forward_varlen (batch 1,
+ *                DEVICE int32 [nseq + 1]); each starts from zeros (init_state
+ *                must be NULL, else SSD_ERR_UNSUPPORTED).
+ *   split, y     the channel axis cut into nsplit (1 to 3) parts of split[i]
+ *                channels (a HOST array whose sum is `channels`, else
+ *                SSD_ERR_SHAPE), part i in a tensor of its own y[i],
+ *                [Bt][L][split[i]] in dtype: x, B and C as the state-space layer
+ *                takes them. split NULL: one tensor y[0], [Bt][L][K]. `y` is a
+ *                HOST array of device pointers.
+ *   final_state  nullable, [Bt][W-1][K] ([nseq][W-1][K] for packed sequences) in
+ *                dtype: the last W-1 inputs, what ssd_conv_step goes on from.
+ */
+int ssd_conv_forward(const void *x, long long x_batch_stride, long long x_token_stride,
+                     const float *weight, const float *bias, const void *init_state,
+                     const int *cu_seqlens, int nseq, int batch, int seqlen, int channels,
+                     int width, int silu, int dtype, const int *split, int nsplit, void *const *y,
+                     void *final_state, void *stream);
+
+/*
+ * Gradients of sum(dy * y) + sum(dfinal_state * final_state) for
+ * ssd_conv_forward (without cu_seqlens) on the same inputs; the convolution is
+ * recomputed. split and dy as split and y there. dfinal_state, dbias and
+ * dinit_state are nullable. dx [Bt][L][K] and dinit_state [Bt][W-1][K] in
+ * dtype, dense; dweight [K][W] and dbias [K] float32, overwritten; sums over
+ * tokens are in float32 in a fixed order. workspace: at least
+ * ssd_conv_backward_workspace_size(...) bytes, 256-byte aligned.
+ */
+size_t ssd_conv_backward_workspace_size(int batch, int seqlen, int channels, int width, int dtype);
+int ssd_conv_backward(const void *x, long long x_batch_stride, long long x_token_stride,
+                      const float *weight, const float *bias, const void *init_state,
+                      const int *split, int nsplit, void *const *dy, const void *dfinal_state,
+                      int batch, int seqlen, int channels, int width, int silu, int dtype,
+                      void *dx, float *dweight, float *dbias, void *dinit_state, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the convolution for every sequence: x [Bt][K] (sequences
+ * x_batch_stride elements apart), y as for ssd_conv_forward with L = 1;
+ * `state` [Bt][W-1][K] in dtype is moved up by one token in place. state and y
+ * must not overlap the inputs.
+ */
+int ssd_conv_step(void *state, const void *x, long long x_batch_stride, const float *weight,
+                  const float *bias, int batch, int channels, int width, int silu, int dtype,
+                  const int *split, int nsplit, void *const *y, void *stream);
+
+/*
+ * Normalisation of rows of `width` (at most 16384) values: the one after the
+ * skip connection and the gated one behind the state-space layer ("Mamba 模型",
+ * sections 4.3 and 4.4). For a row u with mean m (0 if rms):
+ *   rstd = 1 / sqrt(mean((u - m)^2) + eps),  y = (u - m) * rstd * weight + bias
+ * in float32, rounded once to dtype.
+ *   x            [rows][width] in dtype, rows x_row_stride elements apart.
+ *   residual     nullable, [rows][width] dense in residual_dtype (dtype or
+ *                SSD_F32): u = x + residual, rounded to residual_dtype and
+ *                written to residual_out (required with it).
+ *   z            nullable, [rows][width] in dtype, rows z_row_stride elements
+ *                apart: u = x * z * sigmoid(z). Not together with residual
+ *                (SSD_ERR_UNSUPPORTED).
+ *   weight, bias float32 [width] (bias nullable).
+ *   y            [rows][width] dense in dtype.
+ *   mean, rstd   nullable, float32 [rows]: what ssd_norm_backward reads (mean is
+ *                not written if rms).
+ * eps must not be negative or NaN (SSD_ERR_OPTION). Outputs must not overlap inputs.
+ */
+int ssd_norm_forward(const void *x, long long x_row_stride, const void *residual,
+                     int residual_dtype, const void *z, long long z_row_stride,
+                     const float *weight, const float *bias, long long rows, int width, int rms,
+                     float eps, int dtype, void *y, void *residual_out, float *mean, float *rstd,
+                     void *stream);
+
+/*
+ * Gradients of ssd_norm_forward. x is the forward's x or, where it had a
+ * residual, its residual_out (x_dtype: that tensor's type); mean NULL: the
+ * rms form. dresidual (nullable, [rows][width] dense in x_dtype) is the
+ * gradient that reaches residual_out by the skip connection and is added to
+ * the stream's. Outputs, overwritten:
+ *   dx [rows][width] dense in dtype: the gradient of the forward's x;
+ *   dresidual_in (nullable, in x_dtype): the gradient of its residual, the same
+ *     values before their rounding to dtype;
+ *   dz (with z, dtype); dweight and dbias (nullable) float32 [width], summed in
+ *   float32 in a fixed order.
+ * With z, x_dtype must be dtype, dresidual and dresidual_in NULL. Outputs must
+ * not overlap inputs. workspace: at least ssd_norm_backward_workspace_size(...)
+ * bytes, 256-byte aligned.
+ */
+size_t ssd_norm_backward_workspace_size(long long rows, int width, int dtype, int want_dbias);
+int ssd_norm_backward(const void *dy, const void *x, long long x_row_stride, int x_dtype,
+                      const void *z, long long z_row_stride, const float *weight,
+                      const float *mean, const float *rstd, const void *dresidual, long long rows,
+                      int width, int dtype, void *dx, void *dresidual_in, void *dz,
+                      float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
 #ifdef __cplusplus
 }
 #endif

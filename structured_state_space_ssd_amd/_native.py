@@ -36,6 +36,7 @@ class SsdPlan(ctypes.Structure):
 
 
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_ll, _f = ctypes.c_longlong, ctypes.c_float
 _op = ctypes.POINTER(SsdOptions)
 _pp = ctypes.POINTER(SsdPlan)
 
@@ -62,6 +63,16 @@ SIGNATURES = {
     "ssd_chunk_state": (_i, [_vp] * 4 + [_i] * 8 + [_vp, _vp]),
     "ssd_state_passing": (_i, [_vp] * 3 + [_i] * 7 + [_vp, _vp, _vp]),
     "ssd_chunk_scan": (_i, [_vp] * 8 + [_i] * 8 + [_vp, _vp]),
+    "ssd_conv_forward": (_i, [_vp, _ll, _ll, _vp, _vp, _vp, _vp] + [_i] * 7 + [_vp, _i, _vp, _vp, _vp]),
+    "ssd_conv_backward_workspace_size": (_sz, [_i] * 5),
+    "ssd_conv_backward": (_i, [_vp, _ll, _ll, _vp, _vp, _vp, _vp, _i, _vp, _vp] + [_i] * 6
+                          + [_vp] * 5 + [_sz, _vp]),
+    "ssd_conv_step": (_i, [_vp, _vp, _ll, _vp, _vp] + [_i] * 5 + [_vp, _i, _vp, _vp]),
+    "ssd_norm_forward": (_i, [_vp, _ll, _vp, _i, _vp, _ll, _vp, _vp, _ll, _i, _i, _f, _i]
+                         + [_vp] * 5),
+    "ssd_norm_backward_workspace_size": (_sz, [_ll, _i, _i, _i]),
+    "ssd_norm_backward": (_i, [_vp, _vp, _ll, _i, _vp, _ll, _vp, _vp, _vp, _vp, _ll, _i, _i]
+                          + [_vp] * 6 + [_sz, _vp]),
 }
 
 

@@ -165,4 +165,67 @@ hipError_t launch_decode_step(float *state, const void *x, const void *dt, const
                               int ngroups, int dstate, bool bf16, const DtOpts &opts, void *y,
                               hipStream_t stream);
 
+// ---- normalisation (norm.hip)
+// Rows of `width` elements; x and z rows `x_stride`, `z_stride` elements
+// apart, every other tensor dense. residual / z / bias / mean / rstd nullable.
+struct NormArgs {
+    const void *x, *residual, *z;
+    size_t x_stride, z_stride;
+    const float *weight, *bias;
+    long long rows;
+    int width, rms;
+    float eps;
+    void *y, *residual_out;
+    float *mean, *rstd;
+};
+hipError_t launch_norm_fwd(const NormArgs &a, bool bf16, bool res_bf16, hipStream_t stream);
+// mean NULL: the root-mean-square form. part: norm_bwd_part_bytes of scratch.
+struct NormBwdArgs {
+    const void *dy, *x, *z, *dresidual;
+    size_t x_stride, z_stride;
+    const float *weight, *mean, *rstd;
+    long long rows;
+    int width;
+    void *dx, *dresidual_in, *dz;
+    float *dweight, *dbias, *part;
+};
+size_t norm_bwd_part_bytes(long long rows, int width, bool bf16, bool want_db);
+hipError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, bool x_bf16, hipStream_t stream);
+// out[c] = sum over k < n of part[k][c], c < cols, in a fixed order; columns
+// below `first` go to out0, the others to out1.
+hipError_t launch_colsum(const float *part, int n, long long cols, long long first, float *out0,
+                         float *out1, hipStream_t stream);
+
+// ---- short causal convolution (conv.hip)
+// The channel axis cut into `n` parts (1 to 3) that live in tensors of their
+// own, each dense [rows][count[i]]; first[i] is the part's first channel.
+struct ConvParts {
+    int n, first[3], count[3];
+    void *ptr[3];
+};
+struct ConvArgs {
+    const void *x, *init;         // init [Bt][W-1][K], nullable
+    size_t x_batch, x_row;        // strides in elements
+    const float *weight, *bias;   // [K][W], [K] (nullable)
+    const int *cu_seqlens;        // packed sequences (batch 1), or NULL
+    int nseq, batch, seqlen, channels, width, silu;
+    ConvParts y;
+    void *final_state;            // [Bt or nseq][W-1][K], nullable
+};
+hipError_t launch_conv_fwd(const ConvArgs &a, bool bf16, hipStream_t stream);
+struct ConvBwdArgs {
+    const void *x, *init, *dfinal;
+    size_t x_batch, x_row;
+    const float *weight, *bias;
+    int batch, seqlen, channels, width, silu;
+    ConvParts dy;
+    void *dx, *dinit;
+    float *dweight, *dbias, *part;  // part: conv_bwd_part_bytes of scratch
+};
+size_t conv_bwd_part_bytes(int batch, int seqlen, int channels, int width);
+hipError_t launch_conv_bwd(const ConvBwdArgs &a, bool bf16, hipStream_t stream);
+hipError_t launch_conv_step(void *state, const void *x, size_t x_row, const float *weight,
+                            const float *bias, int batch, int channels, int width, int silu,
+                            const ConvParts &y, bool bf16, hipStream_t stream);
+
 }  // namespace ssd

@@ -1,0 +1,323 @@
+"""The operators around the state-space layer: the short causal convolution,
+the selective scan and the normalisation.
+
+Like the package's other functions these check tensor metadata, allocate
+outputs and workspaces with torch and call the C ABI (include/ssd.h); nothing
+here computes. Work is enqueued on the current stream of the tensors' device.
+Activations may be slices of a wider projection: their last axis has to be
+contiguous, the others can have any stride. Parameters, states, gradients that
+come in and outputs are dense.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _native
+from ._native import check, dtype_code
+
+__all__ = ["conv_forward", "conv_backward", "conv_step", "norm_forward", "norm_backward"]
+
+_f32 = torch.float32
+
+
+def _param(t, name, shape, like, dtype=_f32):
+    """Address of a dense tensor of this shape and type next to `like` (None: NULL)."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, x on {like.device}")
+    return t.data_ptr()
+
+
+def _slice(t, name, shape, like):
+    """Address of an activation of this shape and like's type whose last axis is contiguous."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, x on {like.device}")
+    return t.data_ptr()
+
+
+def _required(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
+
+
+def _on_gpu(x):
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+
+
+def _call(fn, where, device, *args):
+    """fn(*args, the device's current stream), with that device the current one."""
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    check(rc, where)
+
+
+def _workspace(workspace, need, x):
+    """(address, bytes) of the caller's workspace, or of a new one of `need` bytes."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+    elif not workspace.is_contiguous() or workspace.device != x.device:
+        raise ValueError("workspace must be a contiguous tensor on x's device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+# ---- short causal convolution ---------------------------------------------------
+
+def _conv_sizes(x, weight, ndim):
+    _required(x=x, weight=weight)
+    if x.dim() != ndim or weight.dim() != 2 or weight.shape[0] != x.shape[-1]:
+        raise ValueError("x must be [Bt, K] and weight [K, W]" if ndim == 2 else
+                         "x must be [Bt, L, K] and weight [K, W]")
+    return weight.shape[1]
+
+
+def _conv_parts(split, K):
+    """(ctypes int array or None, its length) of the channel split."""
+    if split is None:
+        return None, 0, (K,)
+    split = tuple(int(k) for k in split)
+    if not 1 <= len(split) <= 3 or min(split) < 1 or sum(split) != K:
+        raise ValueError(f"split must be 1 to 3 positive sizes with sum {K}, got {split}")
+    return (ctypes.c_int * len(split))(*split), len(split), split
+
+
+def _pointers(addresses):
+    return (ctypes.c_void_p * len(addresses))(*addresses)
+
+
+def conv_forward(x, weight, bias=None, silu=True, init_state=None, return_final_state=False,
+                 cu_seqlens=None, split=None):
+    """y_t = act(bias + sum_k weight[:, k] x_{t-W+1+k}) over whole sequences
+    (ssd_conv_forward): the causal convolution in front of the state-space layer.
+
+    x [Bt, L, K] float32 or bfloat16 (a slice of a wider projection is fine),
+    weight [K, W] with W = 2, 3 or 4 and bias [K] float32; act is SiLU or, with
+    silu=False, nothing. init_state [Bt, W-1, K] in x's type: the inputs before
+    the first token (None: zeros). cu_seqlens: packed sequences as for
+    ``forward_varlen`` (Bt 1, no init_state). split: up to 3 sizes that cut the
+    channels, e.g. (H * P, G * N, G * N); y is then a tuple of dense tensors,
+    ready to be viewed as the layer's x, B and C.
+    Returns y, or (y, final_state [Bt or nseq, W-1, K]) if requested.
+    """
+    W = _conv_sizes(x, weight, 3)
+    Bt, L, K = x.shape
+    arr, n, sizes = _conv_parts(split, K)
+    xp = _slice(x, "x", x.shape, x)
+    wp = _param(weight, "weight", (K, W), x)
+    bp = _param(bias, "bias", (K,), x)
+    ip = _param(init_state, "init_state", (Bt, W - 1, K), x, x.dtype)
+    nseq, cp = 0, None
+    if cu_seqlens is not None:
+        if Bt != 1 or init_state is not None:
+            raise ValueError("packed sequences use batch 1 and no init_state")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be [nseq + 1]")
+        nseq = cu_seqlens.numel() - 1
+        cp = _param(cu_seqlens, "cu_seqlens", (nseq + 1,), x, torch.int32)
+    _on_gpu(x)
+    code = dtype_code(x.dtype)
+    ys = [torch.empty((Bt, L, k), dtype=x.dtype, device=x.device) for k in sizes]
+    final = None
+    if return_final_state:
+        final = torch.empty((nseq or Bt, W - 1, K), dtype=x.dtype, device=x.device)
+    _call(_native.lib.ssd_conv_forward, "ssd_conv_forward", x.device, xp, x.stride(0), x.stride(1),
+          wp, bp, ip, cp, nseq, Bt, L, K, W, int(silu), code, arr, n,
+          _pointers([y.data_ptr() for y in ys]), final.data_ptr() if final is not None else None)
+    y = ys[0] if split is None else tuple(ys)
+    return (y, final) if return_final_state else y
+
+
+def conv_backward(x, weight, bias, dy, silu=True, init_state=None, dfinal_state=None,
+                  workspace=None):
+    """Gradients of sum(dy * y) + sum(dfinal_state * final_state) for
+    ``conv_forward`` without cu_seqlens on the same inputs (ssd_conv_backward).
+
+    dy: a tensor [Bt, L, K], or a sequence of up to 3 tensors that split the
+    channels as conv_forward's y was. Returns a dict: dx [Bt, L, K] (x's type),
+    dweight [K, W] float32, dbias ([K] float32, None without a bias) and dinit
+    ([Bt, W-1, K] in x's type, None without an init_state).
+    """
+    W = _conv_sizes(x, weight, 3)
+    _required(dy=dy)
+    Bt, L, K = x.shape
+    dys = [dy] if isinstance(dy, torch.Tensor) else list(dy)
+    arr, n, sizes = _conv_parts([d.shape[-1] for d in dys], K)
+    xp = _slice(x, "x", x.shape, x)
+    wp = _param(weight, "weight", (K, W), x)
+    bp = _param(bias, "bias", (K,), x)
+    ip = _param(init_state, "init_state", (Bt, W - 1, K), x, x.dtype)
+    fp = _param(dfinal_state, "dfinal_state", (Bt, W - 1, K), x, x.dtype)
+    dp = [_param(d, "dy", (Bt, L, k), x, x.dtype) for d, k in zip(dys, sizes)]
+    _on_gpu(x)
+    code = dtype_code(x.dtype)
+    out = {"dx": torch.empty((Bt, L, K), dtype=x.dtype, device=x.device),
+           "dweight": torch.empty_like(weight),
+           "dbias": None if bias is None else torch.empty_like(bias),
+           "dinit": None if init_state is None else torch.empty_like(init_state)}
+    need = _native.lib.ssd_conv_backward_workspace_size(Bt, L, K, W, code)
+    keep, ws, ws_bytes = _workspace(workspace, need, x)
+    _call(_native.lib.ssd_conv_backward, "ssd_conv_backward", x.device, xp, x.stride(0),
+          x.stride(1), wp, bp, ip, arr, n, _pointers(dp), fp, Bt, L, K, W, int(silu), code,
+          out["dx"].data_ptr(), out["dweight"].data_ptr(),
+          None if bias is None else out["dbias"].data_ptr(),
+          None if init_state is None else out["dinit"].data_ptr(), ws, ws_bytes)
+    return out
+
+
+def conv_step(state, x, weight, bias=None, silu=True, split=None):
+    """One token of ``conv_forward`` for every sequence (ssd_conv_step): x [Bt, K];
+    ``state`` [Bt, W-1, K] in x's type, conv_forward's final_state at first, is
+    updated in place. Returns y [Bt, K], or the tuple of its parts with ``split``.
+    """
+    W = _conv_sizes(x, weight, 2)
+    _required(state=state)
+    Bt, K = x.shape
+    arr, n, sizes = _conv_parts(split, K)
+    xp = _slice(x, "x", x.shape, x)
+    wp = _param(weight, "weight", (K, W), x)
+    bp = _param(bias, "bias", (K,), x)
+    sp = _param(state, "state", (Bt, W - 1, K), x, x.dtype)
+    _on_gpu(x)
+    ys = [torch.empty((Bt, k), dtype=x.dtype, device=x.device) for k in sizes]
+    _call(_native.lib.ssd_conv_step, "ssd_conv_step", x.device, sp, xp, x.stride(0), wp, bp, Bt, K,
+          W, int(silu), dtype_code(x.dtype), arr, n, _pointers([y.data_ptr() for y in ys]))
+    return ys[0] if split is None else tuple(ys)
+
+
+# ---- normalisation ---------------------------------------------------------------
+
+def _rows(t, name):
+    """(rows, elements between rows) of a tensor whose leading axes are one run of
+    rows in memory, however far apart."""
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one axis")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    D = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // D if D else 0), D
+    rows, step = 1, None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != step * rows:
+            raise ValueError(f"{name}'s rows must be evenly spaced in memory")
+        rows *= size
+    return rows, D if step is None else step
+
+
+def norm_forward(x, weight, bias=None, residual=None, z=None, eps=1e-5, rms=False,
+                 return_stats=False):
+    """Layer norm (or with rms its root-mean-square form, without the mean) of
+    the rows of x, of x + residual, or of x * silu(z) (ssd_norm_forward).
+
+    x [..., D] float32 or bfloat16, D at most 16384, rows evenly spaced (a
+    slice of a wider projection is fine); weight and bias [D] float32; residual
+    like x, in x's type or float32; z like x (not together with residual).
+    Returns y like x, dense; with residual (y, the sum in residual's type); with
+    return_stats also the rows' mean (None if rms) and reciprocal standard
+    deviation, float32, as norm_backward takes them.
+    """
+    _required(x=x, weight=weight)
+    rows, step = _rows(x, "x")
+    D = x.shape[-1]
+    wp = _param(weight, "weight", (D,), x)
+    bp = _param(bias, "bias", (D,), x)
+    rp = zp = None
+    zstep, rcode = 0, 0
+    if residual is not None:
+        if z is not None:
+            raise ValueError("residual and z exclude each other")
+        if residual.dtype != _f32 and residual.dtype != x.dtype:
+            raise TypeError(f"residual must be float32 or {x.dtype}, got {residual.dtype}")
+        rp = _param(residual, "residual", x.shape, x, residual.dtype)
+        rcode = dtype_code(residual.dtype)
+    if z is not None:
+        zp = _slice(z, "z", x.shape, x)
+        zstep = _rows(z, "z")[1]
+    _on_gpu(x)
+    code = dtype_code(x.dtype)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    total = mean = rstd = None
+    if residual is not None:
+        total = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+    if return_stats:
+        rstd = torch.empty(x.shape[:-1], dtype=_f32, device=x.device)
+        if not rms:
+            mean = torch.empty_like(rstd)
+    _call(_native.lib.ssd_norm_forward, "ssd_norm_forward", x.device, x.data_ptr(), step, rp, rcode,
+          zp, zstep, wp, bp, rows, D, int(rms), eps, code, y.data_ptr(),
+          None if total is None else total.data_ptr(), None if mean is None else mean.data_ptr(),
+          None if rstd is None else rstd.data_ptr())
+    out = (y,) if total is None else (y, total)
+    if return_stats:
+        out += (mean, rstd)
+    return out if len(out) > 1 else y
+
+
+def norm_backward(dy, x, weight, mean, rstd, z=None, dresidual=None, workspace=None):
+    """Gradients of ``norm_forward`` (ssd_norm_backward).
+
+    x: norm_forward's x or, where it had a residual, the sum that it returned.
+    mean (None: the rms form) and rstd: its statistics. dresidual (like x): the
+    gradient that reaches that sum by the skip connection.
+    Returns a dict: dx (dy's type, the gradient of norm_forward's x), dweight,
+    dbias ([D] float32; dbias None in the rms form), dz (with z) and, where
+    dresidual is given, dresidual: the gradient of the residual, in x's type.
+    """
+    _required(dy=dy, x=x, weight=weight, rstd=rstd)
+    rows, step = _rows(x, "x")
+    D = x.shape[-1]
+    if x.dtype != _f32 and x.dtype != dy.dtype:
+        raise TypeError(f"x must be float32 or {dy.dtype}, got {x.dtype}")
+    yp = _param(dy, "dy", x.shape, x, dy.dtype)
+    wp = _param(weight, "weight", (D,), x)
+    mp = _param(mean, "mean", x.shape[:-1], x)
+    sp = _param(rstd, "rstd", x.shape[:-1], x)
+    rp = _param(dresidual, "dresidual", x.shape, x, x.dtype)
+    zp, zstep = None, 0
+    if z is not None:
+        if dresidual is not None:
+            raise ValueError("dresidual and z exclude each other")
+        if x.dtype != dy.dtype:
+            raise TypeError(f"x must be {dy.dtype} with z, got {x.dtype}")
+        zp = _slice(z, "z", x.shape, dy)
+        zstep = _rows(z, "z")[1]
+    _on_gpu(x)
+    code = dtype_code(dy.dtype)
+    out = {"dx": torch.empty_like(dy), "dweight": torch.empty_like(weight),
+           "dbias": None if mean is None else torch.empty_like(weight)}
+    if z is not None:
+        out["dz"] = torch.empty_like(dy)
+    if dresidual is not None:
+        out["dresidual"] = torch.empty_like(dresidual)
+    ptr = lambda k: out[k].data_ptr() if out.get(k) is not None else None  # noqa: E731
+    need = _native.lib.ssd_norm_backward_workspace_size(rows, D, code, int(mean is not None))
+    keep, ws, ws_bytes = _workspace(workspace, need, x)
+    _call(_native.lib.ssd_norm_backward, "ssd_norm_backward", x.device, yp, x.data_ptr(), step,
+          dtype_code(x.dtype), zp, zstep, wp, mp, sp, rp, rows, D, code, ptr("dx"),
+          ptr("dresidual"), ptr("dz"), ptr("dweight"), ptr("dbias"), ws, ws_bytes)
+    return out

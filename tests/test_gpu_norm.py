@@ -1,0 +1,178 @@
+"""The normalisation on the GPU against its plain 64-bit form.
+
+Roundings in 32 bits: a row's sum takes at most V NV + 6 + 16 additions one
+after another (values of a lane, lanes of a wavefront, wavefronts), below 56 at
+16384 values; the mean, then the deviations, their squares' sum, the square
+root and the quotient, the products with weight and bias: 2 * 56 + 10. The
+gate's SiLU adds 8 + 2 |z|. Gradients run through the two sums once more. Sums
+over rows add a rounding per row."""
+import pytest
+import layer_refs as R
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+EPS = 1e-5
+OPS = 2 * 56 + 10
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    import structured_state_space_ssd_amd as m
+    return m
+
+
+def make(rows, D, dtype, seed, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s, dt=dtype, sc=1.0, off=0.0: (torch.randn(*s, generator=g) * sc + off).to(dt).cuda()  # noqa: E731
+    x = r(rows, D + pad, off=0.5)[:, pad:]
+    return x, r(D, dt=F32, off=1.0, sc=0.3), r(D, dt=F32), r
+
+
+# widths below, at and past a vector, a wavefront's vectors (512 / 256 values), a
+# workgroup's (8192 / 4096), odd ones, the largest; rows around those of a workgroup
+SIZES = [(1, 1), (3, 2), (5, 7), (300, 8), (17, 9), (70, 16), (9, 100), (33, 255), (4, 257), (6, 511),
+         (3, 513), (7, 1000), (2, 4097), (5, 5119), (3, 8193), (2, 16383), (2, 16384)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_norm(ssd, size, dtype):
+    rows, D = size
+    for rms, bias, pad in ((False, True, 0), (True, False, 5), (False, False, 8)):
+        x, w, b, r = make(rows, D, dtype, D, pad)
+        b = b if bias else None
+        y, mean, rstd = ssd.norm_forward(x, w, b, eps=EPS, rms=rms, return_stats=True)
+        want, m, s, mag = R.norm(x, w, b, rms, EPS)
+        R.check((size, rms, "y"), y, want, mag, OPS)
+        R.check((size, rms, "rstd"), rstd, s, s + s ** 3 * x.double().cpu().abs().mean(-1) ** 2, OPS)
+        if rms:
+            assert mean is None
+        else:
+            R.check((size, "mean"), mean, m, x.double().cpu().abs().mean(-1), 60)
+        dy = r(rows, D)
+        got = ssd.norm_backward(dy, x, w, mean, rstd)
+        want, mag = R.norm_grads(dy, x, w, rms, EPS)
+        for k in ("dx", "dweight", "dbias"):
+            if k == "dbias" and rms:
+                assert got[k] is None
+                continue
+            R.check((size, rms, k), got[k], want[k], mag[k], 2 * OPS + (rows if k != "dx" else 0))
+
+
+@pytest.mark.parametrize("dtype,stream", [(BF, BF), (BF, F32), (F32, F32)], ids=["bf16", "bf16_f32", "f32"])
+@pytest.mark.parametrize("size", [(3, 5), (40, 64), (7, 513), (5, 2560), (2, 12000)], ids=str)
+def test_norm_residual(ssd, size, dtype, stream):
+    rows, D = size
+    for rms in (False, True):
+        x, w, b, r = make(rows, D, dtype, D, 3)
+        res, dy, dres = r(rows, D, dt=stream), r(rows, D), r(rows, D, dt=stream)
+        y, total, mean, rstd = ssd.norm_forward(x, w, b, residual=res, eps=EPS, rms=rms, return_stats=True)
+        exact = x.double().cpu() + res.double().cpu()
+        R.check((size, "sum"), total, exact, exact.abs(), 1)
+        want, _, _, mag = R.norm(total, w, b, rms, EPS)  # the norm reads the sum as it is kept
+        R.check((size, "y"), y, want, mag, OPS)
+        got = ssd.norm_backward(dy, total, w, mean, rstd, dresidual=dres)
+        want, mag = R.norm_grads(dy, total, w, rms, EPS, dres=dres)
+        assert got["dx"].dtype == dtype and got["dresidual"].dtype == stream
+        R.check((size, "dx"), got["dx"], want["dx"], mag["dx"], 2 * OPS)
+        R.check((size, "dres"), got["dresidual"], want["dx"], mag["dx"], 2 * OPS)
+        R.check((size, "dw"), got["dweight"], want["dweight"], mag["dweight"], 2 * OPS + rows)
+        if not rms:
+            R.check((size, "db"), got["dbias"], want["dbias"], mag["dbias"], rows)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("size", [(3, 5), (40, 64), (7, 513), (5, 5120), (2, 12001)], ids=str)
+def test_norm_gated(ssd, size, dtype):
+    rows, D = size
+    for rms in (True, False):
+        x, w, b, r = make(rows, D, dtype, D + 1)
+        z, dy = r(rows, 2 * D)[:, :D], r(rows, D)
+        y, mean, rstd = ssd.norm_forward(x, w, b, z=z, eps=EPS, rms=rms, return_stats=True)
+        want, _, _, mag = R.norm(x, w, b, rms, EPS, z)
+        gate = 2 * (8 + 2 * float(z.abs().max()))
+        # |silu(z)| can be far below the magnitudes |x| |z| that its rounding is relative to
+        R.check((size, "y"), y, want, mag, OPS + gate)
+        got = ssd.norm_backward(dy, x, w, mean, rstd, z=z)
+        want, mag = R.norm_grads(dy, x, w, rms, EPS, z)
+        for k in ("dx", "dz", "dweight") + (() if rms else ("dbias",)):
+            R.check((size, rms, k), got[k], want[k], mag[k], 2 * (OPS + gate) + (rows if k[1] in "wb" else 0))
+
+
+def test_norm_many_rows(ssd):
+    """More rows than the grid holds at once, short and long ones; the weight's
+    gradient is the same on every call."""
+    for rows, D in ((20011, 24), (5003, 1000)):
+        x, w, b, r = make(rows, D, BF, 1)
+        dy = r(rows, D)
+        y, mean, rstd = ssd.norm_forward(x, w, b, eps=EPS, return_stats=True)
+        want, _, _, mag = R.norm(x, w, b, False, EPS)
+        R.check("y", y, want, mag, OPS)
+        got = ssd.norm_backward(dy, x, w, mean, rstd)
+        want, mag = R.norm_grads(dy, x, w, False, EPS)
+        for k in ("dx", "dweight", "dbias"):
+            R.check((rows, k), got[k], want[k], mag[k], 2 * OPS + (rows if k != "dx" else 0))
+        again = ssd.norm_backward(dy, x, w, mean, rstd)
+        assert all(torch.equal(got[k], again[k]) for k in ("dx", "dweight", "dbias"))
+
+
+def test_norm_special_rows(ssd):
+    """A constant row has no deviation (y = bias exactly where the mean is exact),
+    a row far from zero keeps its small deviations, NaN stays in its row."""
+    D = 512
+    x = torch.zeros(4, D, device="cuda")
+    x[0] = 3.0
+    x[1] = 4096.0 + torch.arange(D, device="cuda") / 512
+    x[2, 5] = float("nan")
+    w, b = torch.ones(D, device="cuda"), torch.full((D,), 0.25, device="cuda")
+    y = ssd.norm_forward(x, w, b, eps=EPS).cpu()
+    assert (y[0] == 0.25).all() and (y[3] == 0.25).all() and y[2].isnan().all()
+    want, _, _, _ = R.norm(x[1:2], w, b, False, EPS)
+    # the row's values need 22 bits: sums round by half of 2^-2 at 2^21; the mean by 2^-13
+    assert float((y[1].double() - want[0]).abs().max()) < 2.0 ** -12 * 4
+
+
+def test_norm_shapes_and_differences(ssd):
+    x = torch.randn(2, 3, 40, device="cuda")
+    w = torch.rand(40, device="cuda") + 0.5
+    b = torch.randn(40, device="cuda")
+    dy = torch.randn_like(x)
+    y, mean, rstd = ssd.norm_forward(x, w, b, return_stats=True)
+    assert y.shape == x.shape and mean.shape == rstd.shape == (2, 3)
+    got = ssd.norm_backward(dy, x, w, mean, rstd)
+    f = lambda xx, ww: (R.norm(xx, ww, b, False, 1e-5)[0] * dy.double().cpu()).sum()  # noqa: E731
+    h = 1e-4
+    for grad, at in (("dx", (1, 2, 7)), ("dx", (0, 0, 39)), ("dweight", (11,))):
+        t = x if grad == "dx" else w
+        d = torch.zeros(t.shape, dtype=torch.float64)
+        d[at] = h
+        t64 = t.double().cpu()
+        if grad == "dx":
+            slope = float(f(t64 + d, w) - f(t64 - d, w)) / (2 * h)
+        else:
+            slope = float(f(x, t64 + d) - f(x, t64 - d)) / (2 * h)
+        assert abs(slope - float(got[grad][at])) < 1e-4 * max(1.0, abs(slope))
+
+
+def test_norm_captured(ssd):
+    x, w, b, r = make(60, 700, BF, 3)
+    dy, res = r(60, 700), r(60, 700, dt=F32)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y, total, mean, rstd = ssd.norm_forward(x, w, b, residual=res, return_stats=True)
+        ssd.norm_backward(dy, total, w, mean, rstd, dresidual=res)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, total, mean, rstd = ssd.norm_forward(x, w, b, residual=res, return_stats=True)
+        grads = ssd.norm_backward(dy, total, w, mean, rstd, dresidual=res)
+    for k in range(4):
+        x.copy_(torch.randn(x.shape).to(BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        ey, et, em, er = ssd.norm_forward(x, w, b, residual=res, return_stats=True)
+        eg = ssd.norm_backward(dy, et, w, em, er, dresidual=res)
+        assert torch.equal(y, ey) and torch.equal(total, et)
+        assert all(torch.equal(grads[n], eg[n]) for n in eg)

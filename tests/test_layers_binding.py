@@ -1,0 +1,172 @@
+"""Refusals of the convolution and the normalisation, on the CPU: the binding's
+own (shapes, types, layout, before any device check) and the C ABI's (every
+call here fails its checks, so nothing is launched)."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+f32, bf = torch.float32, torch.bfloat16
+FAKE = ctypes.c_void_p(0x100000)
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    import structured_state_space_ssd_amd as m
+    return m
+
+
+@pytest.fixture(scope="module")
+def lib(ssd):
+    from structured_state_space_ssd_amd import _native
+    return _native.lib
+
+
+z = torch.zeros
+CONV = dict(x=z(2, 6, 8, dtype=bf), weight=z(8, 4), bias=z(8))
+CONV_BAD = [
+    (ValueError, "x must be", dict(x=z(2, 8, dtype=bf))),
+    (ValueError, "x must be", dict(weight=z(7, 4))),
+    (ValueError, "weight is required", dict(weight=None)),
+    (ValueError, "bias", dict(bias=z(9))),
+    (TypeError, "bias", dict(bias=z(8, dtype=bf))),
+    (TypeError, "weight", dict(weight=z(8, 4, dtype=bf))),
+    (ValueError, "contiguous", dict(x=z(2, 8, 6, dtype=bf).transpose(1, 2))),
+    (ValueError, "init_state", dict(init_state=z(2, 4, 8, dtype=bf))),
+    (TypeError, "init_state", dict(init_state=z(2, 3, 8))),
+    (ValueError, "split", dict(split=(4, 3))),
+    (ValueError, "split", dict(split=(8, 0))),
+    (ValueError, "split", dict(split=(2, 2, 2, 2))),
+    (ValueError, "packed", dict(cu_seqlens=z(3, dtype=torch.int32))),
+    (ValueError, "GPU", dict()),
+]
+
+
+@pytest.mark.parametrize("error,text,over", CONV_BAD, ids=[f"{t}-{i}" for i, (_, t, _) in enumerate(CONV_BAD)])
+def test_conv_forward_refuses(ssd, error, text, over):
+    with pytest.raises(error, match=text):
+        ssd.conv_forward(**{**CONV, **over})
+
+
+def test_conv_packed_refuses(ssd):
+    a = dict(CONV, x=z(1, 6, 8, dtype=bf))
+    with pytest.raises(ValueError, match="packed"):
+        ssd.conv_forward(**a, cu_seqlens=z(2, dtype=torch.int32), init_state=z(1, 3, 8, dtype=bf))
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        ssd.conv_forward(**a, cu_seqlens=z(1, dtype=torch.int32))
+    with pytest.raises(TypeError, match="cu_seqlens"):
+        ssd.conv_forward(**a, cu_seqlens=z(2, dtype=torch.int64))
+
+
+def test_conv_backward_and_step_refuse(ssd):
+    with pytest.raises(ValueError, match="dy is required"):
+        ssd.conv_backward(CONV["x"], CONV["weight"], None, None)
+    with pytest.raises(ValueError, match="dy must have shape"):
+        ssd.conv_backward(CONV["x"], CONV["weight"], None, z(2, 5, 8, dtype=bf))
+    with pytest.raises(ValueError, match="split"):
+        ssd.conv_backward(CONV["x"], CONV["weight"], None, (z(2, 6, 4, dtype=bf),))
+    with pytest.raises(TypeError, match="dy"):
+        ssd.conv_backward(CONV["x"], CONV["weight"], None, z(2, 6, 8))
+    with pytest.raises(ValueError, match="dfinal_state"):
+        ssd.conv_backward(CONV["x"], CONV["weight"], None, z(2, 6, 8, dtype=bf), dfinal_state=z(2, 2, 8, dtype=bf))
+    with pytest.raises(ValueError, match="state"):
+        ssd.conv_step(z(2, 4, 8, dtype=bf), z(2, 8, dtype=bf), z(8, 4))
+    with pytest.raises(ValueError, match="state is required"):
+        ssd.conv_step(None, z(2, 8, dtype=bf), z(8, 4))
+    with pytest.raises(ValueError, match="GPU"):
+        ssd.conv_step(z(2, 3, 8, dtype=bf), z(2, 8, dtype=bf), z(8, 4))
+
+
+NORM_BAD = [
+    (ValueError, "weight must have shape", dict(weight=z(9))),
+    (TypeError, "weight", dict(weight=z(8, dtype=bf))),
+    (ValueError, "exclude", dict(residual=z(4, 8), z=z(4, 8, dtype=bf))),
+    (TypeError, "residual", dict(x=z(4, 8), residual=z(4, 8, dtype=bf))),
+    (ValueError, "residual", dict(residual=z(8, 8)[::2])),
+    (ValueError, "z must have shape", dict(z=z(5, 8, dtype=bf))),
+    (ValueError, "contiguous", dict(x=z(8, 4, dtype=bf).t())),
+    (ValueError, "evenly spaced", dict(x=z(4, 6, 8, dtype=bf)[:, :5])),
+    (ValueError, "GPU", dict()),
+]
+
+
+@pytest.mark.parametrize("error,text,over", NORM_BAD, ids=[f"{t}-{i}" for i, (_, t, _) in enumerate(NORM_BAD)])
+def test_norm_forward_refuses(ssd, error, text, over):
+    with pytest.raises(error, match=text):
+        ssd.norm_forward(**{**dict(x=z(4, 8, dtype=bf), weight=z(8), bias=z(8)), **over})
+
+
+def test_norm_backward_refuses(ssd):
+    a = dict(dy=z(4, 8, dtype=bf), x=z(4, 8), weight=z(8), mean=z(4), rstd=z(4))
+    for error, text, over in ((ValueError, "rstd is required", dict(rstd=None)),
+                              (ValueError, "mean must have shape", dict(mean=z(5))),
+                              (TypeError, "x must be", dict(dy=z(4, 8), x=z(4, 8, dtype=bf))),
+                              (TypeError, "dresidual", dict(dresidual=z(4, 8, dtype=bf))),
+                              (ValueError, "exclude", dict(z=z(4, 8, dtype=bf), dresidual=z(4, 8))),
+                              (TypeError, "with z", dict(z=z(4, 8, dtype=bf))),
+                              (ValueError, "GPU", dict())):
+        with pytest.raises(error, match=text):
+            ssd.norm_backward(**{**a, **over})
+
+
+def _ptrs(*addresses):
+    return (ctypes.c_void_p * len(addresses))(*addresses)
+
+
+def conv_c(lib, **kw):
+    a = dict(x=FAKE, xb=48, xt=8, w=FAKE, b=None, init=None, cu=None, nseq=0, batch=2, seqlen=6,
+             channels=8, width=4, silu=1, dtype=1, split=None, nsplit=0, y=_ptrs(0x100000), fin=None)
+    a.update(kw)
+    return lib.ssd_conv_forward(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), -1), (dict(w=None), -1), (dict(y=None), -1), (dict(y=_ptrs(None)), -1),
+    (dict(batch=0), -2), (dict(seqlen=0), -2), (dict(channels=0), -2), (dict(xt=-1), -2),
+    (dict(seqlen=(1 << 30) + 1), -2),
+    (dict(width=1), -3), (dict(width=5), -3), (dict(dtype=2), -3),
+    (dict(split=(ctypes.c_int * 2)(4, 3), nsplit=2, y=_ptrs(1 << 20, 1 << 20)), -2),
+    (dict(split=(ctypes.c_int * 2)(8, 0), nsplit=2, y=_ptrs(1 << 20, 1 << 20)), -2),
+    (dict(split=(ctypes.c_int * 2)(1 << 30, 1 << 30), nsplit=2, y=_ptrs(1 << 20, 1 << 20)), -2),
+    (dict(split=(ctypes.c_int * 2)(4, 4), nsplit=4, y=_ptrs(1 << 20, 1 << 20)), -2),
+    (dict(split=(ctypes.c_int * 2)(4, 4), nsplit=2, y=_ptrs(1 << 20, None)), -1),
+    (dict(cu=FAKE, nseq=2), -2), (dict(cu=FAKE, nseq=0, batch=1), -2),
+    (dict(cu=FAKE, nseq=2, batch=1, init=FAKE), -3),
+])
+def test_conv_c_abi_refuses(lib, kw, code):
+    assert conv_c(lib, **kw) == code
+
+
+def test_backward_workspaces(lib):
+    n = lib.ssd_conv_backward_workspace_size(2, 6, 8, 4, 1)
+    assert n > 0 and lib.ssd_conv_backward_workspace_size(2, 6, 8, 5, 1) == 0
+    args = [FAKE, 48, 8, FAKE, None, None, None, 0, _ptrs(1 << 20), None, 2, 6, 8, 4, 1, 1, FAKE, FAKE,
+            None, None]
+    assert lib.ssd_conv_backward(*args, FAKE, n - 1, None) == -4
+    assert lib.ssd_conv_backward(*args, None, n, None) == -4
+    assert lib.ssd_conv_backward(*args, ctypes.c_void_p(0x100010), n, None) == -4
+    m = lib.ssd_norm_backward_workspace_size(4, 8, 1, 1)
+    assert m > 0 and lib.ssd_norm_backward_workspace_size(4, 16385, 1, 1) == 0
+    assert lib.ssd_norm_backward_workspace_size(4, 8, 1, 0) * 2 == m
+    args = [FAKE, FAKE, 8, 1, None, 0, FAKE, FAKE, FAKE, None, 4, 8, 1, FAKE, None, None, FAKE, FAKE]
+    assert lib.ssd_norm_backward(*args, FAKE, m - 1, None) == -4
+    args[4] = FAKE  # z without dz
+    assert lib.ssd_norm_backward(*args, FAKE, m, None) == -1
+
+
+def norm_c(lib, **kw):
+    a = dict(x=FAKE, xs=8, res=None, rdt=0, z=None, zs=0, w=FAKE, b=None, rows=4, width=8, rms=0,
+             eps=1e-5, dtype=1, y=FAKE, ro=None, mean=None, rstd=None)
+    a.update(kw)
+    return lib.ssd_norm_forward(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), -1), (dict(w=None), -1), (dict(y=None), -1), (dict(res=FAKE), -1),
+    (dict(rows=0), -2), (dict(width=0), -2), (dict(xs=-8), -2),
+    (dict(width=16385), -3), (dict(dtype=3), -3), (dict(res=FAKE, ro=FAKE, z=FAKE), -3),
+    (dict(res=FAKE, ro=FAKE, rdt=1, dtype=0), -3),
+    (dict(eps=-1e-5), -6), (dict(eps=float("nan")), -6),
+])
+def test_norm_c_abi_refuses(lib, kw, code):
+    assert norm_c(lib, **kw) == code
