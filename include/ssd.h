@@ -520,6 +520,83 @@ int ssd_conv_step(void *state, const void *x, long long x_batch_stride, const fl
                   const int *split, int nsplit, void *const *y, void *stream);
 
 /*
+ * Selective scan with a decay rate for every channel and state ("从Transformer
+ * 到Mamba" tutorial, section 3.2: the diagonal form that the state-space layer
+ * above restricts to one rate per head). For each of `channels` (E) channels e,
+ * with a state of `dstate` (N, 1 to 64) values and B/C group g = e / (E / G):
+ *   h_t[n] = exp(dt_t A[e][n]) h_{t-1}[n] + dt_t x_t B_t[g][n]
+ *   y_t    = sum_n C_t[g][n] h_t[n] + D[e] x_t,   times z_t sigmoid(z_t) with a gate
+ * in float32, rounded once to dtype.
+ *   x, dt, z     [Bt][L][E] in dtype (z nullable); B, C [Bt][L][G][N] in dtype.
+ *                Element alignment; `strides` (NULL: dense) lets each be a slice
+ *                of a wider projection.
+ *   A, D         float32 [E][N] and [E] (D nullable).
+ *   init_state   nullable, float32 [Bt][E][N] (NULL: zero); final_state nullable,
+ *                the same shape: the state after the last token.
+ *   y            [Bt][L][E] dense in dtype.
+ *   opts         nullable, as for ssd_forward_ex with dt_bias float32 [E];
+ *                discretization must be SSD_DISC_EULER (else SSD_ERR_OPTION).
+ *   workspace    at least ssd_selective_forward_workspace_size(...) bytes,
+ *                256-byte aligned (NULL where that is 0): with few channels the
+ *                token axis is cut into segments, whose states it holds.
+ * E % G must be 0 (SSD_ERR_SHAPE). A call whose grid would reach 2^24 workgroups
+ * (1024 / N channels each, N rounded up to a power of two) returns
+ * SSD_ERR_UNSUPPORTED.
+ */
+typedef struct {
+    /* elements between sequences and between tokens; channels, and the [G][N] of
+       one token, are dense */
+    long long x_batch, x_token, dt_batch, dt_token, z_batch, z_token, B_batch, B_token, C_batch,
+        C_token;
+} ssd_selective_strides;
+
+size_t ssd_selective_forward_workspace_size(int batch, int seqlen, int channels, int ngroups,
+                                            int dstate, int dtype);
+int ssd_selective_forward(const void *x, const void *dt, const float *A, const void *B,
+                          const void *C, const float *D, const void *z, int batch, int seqlen,
+                          int channels, int ngroups, int dstate, int dtype,
+                          const float *init_state, void *y, float *final_state, void *workspace,
+                          size_t workspace_bytes, const ssd_selective_strides *strides,
+                          const ssd_options *opts, void *stream);
+
+/*
+ * One token of the selective scan for every sequence: x, dt, z, y [Bt][E], B, C
+ * [Bt][G][N] (of `strides` only the _batch members are read; NULL: dense);
+ * `state` float32 [Bt][E][N] is updated in place. state and y must not overlap
+ * the inputs.
+ */
+int ssd_selective_step(float *state, const void *x, const void *dt, const float *A, const void *B,
+                       const void *C, const float *D, const void *z, int batch, int channels,
+                       int ngroups, int dstate, int dtype, void *y,
+                       const ssd_selective_strides *strides, const ssd_options *opts,
+                       void *stream);
+
+/*
+ * Gradients of sum(dy * y) + sum(dfinal_state * final_state) for
+ * ssd_selective_forward with the same inputs and options; the states are
+ * recomputed, not stored by the forward.
+ *   dy           [Bt][L][E] dense in dtype; dfinal_state nullable, float32 [Bt][E][N].
+ * Outputs (dense, overwritten): dx, ddt (with respect to the raw dt, through
+ * the options; clamp bounds pass the gradient as in ssd_backward), dz (with z)
+ * [Bt][L][E] and dB, dC [Bt][L][G][N] (summed over the channels of each group)
+ * in dtype; dA [E][N], dD and ddt_bias [E] (nullable) and dinit_state
+ * [Bt][E][N] (nullable) float32. Sums are in float32 in a fixed order.
+ *   workspace    at least ssd_selective_backward_workspace_size(...) bytes,
+ *                256-byte aligned: the states before every 16 (dstate <= 8: 8)
+ *                tokens and the partial sums.
+ */
+size_t ssd_selective_backward_workspace_size(int batch, int seqlen, int channels, int ngroups,
+                                             int dstate, int dtype);
+int ssd_selective_backward(const void *x, const void *dt, const float *A, const void *B,
+                           const void *C, const float *D, const void *z, const float *init_state,
+                           const void *dy, const float *dfinal_state, int batch, int seqlen,
+                           int channels, int ngroups, int dstate, int dtype, void *dx, void *ddt,
+                           float *dA, void *dB, void *dC, float *dD, void *dz, float *dinit_state,
+                           float *ddt_bias, void *workspace, size_t workspace_bytes,
+                           const ssd_selective_strides *strides, const ssd_options *opts,
+                           void *stream);
+
+/*
  * Normalisation of rows of `width` (at most 16384) values: the one after the
  * skip connection and the gated one behind the state-space layer ("Mamba 模型",
  * sections 4.3 and 4.4). For a row u with mean m (0 if rms):

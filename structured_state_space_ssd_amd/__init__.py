@@ -13,11 +13,13 @@ import torch
 
 from . import _native
 from ._native import SSDError, check, dtype_code, ptr, stream_handle
-from .layers import conv_backward, conv_forward, conv_step, norm_backward, norm_forward
+from .layers import (conv_backward, conv_forward, conv_step, norm_backward, norm_forward,
+                     selective_backward, selective_forward, selective_step)
 
 __all__ = ["forward", "forward_plan", "plan_info", "backward", "forward_varlen", "step", "options", "workspace_size", "chunk_cumsum", "chunk_state",
            "state_passing", "chunk_cb", "chunk_scan", "SSDError", "stages", "conv_forward", "conv_backward",
-           "conv_step", "norm_forward", "norm_backward"]
+           "conv_step", "selective_forward", "selective_backward", "selective_step", "norm_forward",
+           "norm_backward"]
 
 HEADDIM = 64
 

@@ -35,10 +35,18 @@ class SsdPlan(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class SsdSelectiveStrides(ctypes.Structure):
+    """ssd_selective_strides of include/ssd.h."""
+    _fields_ = [(n, ctypes.c_longlong) for n in
+                ("x_batch", "x_token", "dt_batch", "dt_token", "z_batch", "z_token", "B_batch",
+                 "B_token", "C_batch", "C_token")]
+
+
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _ll, _f = ctypes.c_longlong, ctypes.c_float
 _op = ctypes.POINTER(SsdOptions)
 _pp = ctypes.POINTER(SsdPlan)
+_ssp = ctypes.POINTER(SsdSelectiveStrides)
 
 # name -> (restype, argtypes); mirrors include/ssd.h
 SIGNATURES = {
@@ -68,6 +76,11 @@ SIGNATURES = {
     "ssd_conv_backward": (_i, [_vp, _ll, _ll, _vp, _vp, _vp, _vp, _i, _vp, _vp] + [_i] * 6
                           + [_vp] * 5 + [_sz, _vp]),
     "ssd_conv_step": (_i, [_vp, _vp, _ll, _vp, _vp] + [_i] * 5 + [_vp, _i, _vp, _vp]),
+    "ssd_selective_forward_workspace_size": (_sz, [_i] * 6),
+    "ssd_selective_forward": (_i, [_vp] * 7 + [_i] * 6 + [_vp, _vp, _vp, _vp, _sz, _ssp, _op, _vp]),
+    "ssd_selective_step": (_i, [_vp] * 8 + [_i] * 5 + [_vp, _ssp, _op, _vp]),
+    "ssd_selective_backward_workspace_size": (_sz, [_i] * 6),
+    "ssd_selective_backward": (_i, [_vp] * 10 + [_i] * 6 + [_vp] * 10 + [_sz, _ssp, _op, _vp]),
     "ssd_norm_forward": (_i, [_vp, _ll, _vp, _i, _vp, _ll, _vp, _vp, _ll, _i, _i, _f, _i]
                          + [_vp] * 5),
     "ssd_norm_backward_workspace_size": (_sz, [_ll, _i, _i, _i]),

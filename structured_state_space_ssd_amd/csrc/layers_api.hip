@@ -67,6 +67,81 @@ int check_norm(long long rows, int width, int dtype) {
 // The stream beside x has x's type or is float32.
 bool stream_dtype_ok(int stream, int dtype) { return stream == dtype || stream == SSD_F32; }
 
+// Grids hold fewer than 2^24 workgroups of 256 lanes.
+constexpr long long kMaxBlocks = 1LL << 24;
+
+int check_selective(int batch, int seqlen, int channels, int ngroups, int dstate, int dtype) {
+    if (batch < 1 || seqlen < 1 || channels < 1 || ngroups < 1 || dstate < 1) return SSD_ERR_SHAPE;
+    if (channels % ngroups != 0 || seqlen > kMaxExtent || channels > kMaxExtent)
+        return SSD_ERR_SHAPE;
+    if (!ssd::selective_kernel_dstate(dstate) || !valid_dtype(dtype)) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// Strides (NULL: dense) and options into the kernels' arguments.
+int selective_args(ssd::SelArgs &a, const void *x, const void *dt, const float *A, const void *B,
+                   const void *C, const float *D, const void *z, int batch, int seqlen,
+                   int channels, int ngroups, int dstate, const ssd_selective_strides *st,
+                   const ssd_options *o) {
+    a = ssd::SelArgs{};
+    a.x = x; a.dt = dt; a.z = z; a.B = B; a.C = C; a.A = A; a.D = D;
+    a.batch = batch; a.seqlen = seqlen; a.channels = channels; a.ngroups = ngroups;
+    a.dstate = dstate;
+    const long long e = channels, n = (long long)ngroups * dstate;
+    ssd_selective_strides d = {e * seqlen, e, e * seqlen, e, e * seqlen, e, n * seqlen, n,
+                               n * seqlen, n};
+    if (st) {
+        d = *st;
+        for (long long v : {d.x_batch, d.x_token, d.dt_batch, d.dt_token, d.z_batch, d.z_token,
+                            d.B_batch, d.B_token, d.C_batch, d.C_token})
+            if (v < 0) return SSD_ERR_SHAPE;
+    }
+    a.x_batch = d.x_batch; a.x_token = d.x_token; a.dt_batch = d.dt_batch; a.dt_token = d.dt_token;
+    a.z_batch = d.z_batch; a.z_token = d.z_token; a.B_batch = d.B_batch; a.B_token = d.B_token;
+    a.C_batch = d.C_batch; a.C_token = d.C_token;
+    a.opts = ssd::DtOpts{nullptr, 0.0f, 0.0f, 0, 0, 0};
+    if (!o) return SSD_OK;
+    if (o->discretization != SSD_DISC_EULER) return SSD_ERR_OPTION;
+    if (o->dt_clamp && !(o->dt_min <= o->dt_max)) return SSD_ERR_OPTION;  // NaN bounds fail too
+    if ((reinterpret_cast<uintptr_t>(o->dt_bias) & 3u) != 0) return SSD_ERR_UNSUPPORTED;
+    a.opts = ssd::DtOpts{o->dt_bias, o->dt_min, o->dt_max, o->dt_softplus != 0, o->dt_clamp != 0, 0};
+    return SSD_OK;
+}
+
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+// The selective scan's backward: its plan and where its workspace's parts begin.
+struct SelBwdLayout {
+    ssd::SelPlan plan;
+    int keeps;
+    size_t keep_state, keep_sum, seg_state, seg_sum, seg_adj, dbc, dA, de, total;
+};
+SelBwdLayout selective_bwd_layout(int batch, int seqlen, int channels, int ngroups, int dstate) {
+    SelBwdLayout w{};
+    w.plan = ssd::selective_bwd_plan(batch, seqlen, channels, ngroups, dstate);
+    const size_t nk = ssd::selective_kernel_dstate(dstate), be = (size_t)batch * channels;
+    const int keep = ssd::selective_keep_tokens(dstate);
+    w.keeps = (seqlen + keep - 1) / keep;
+    const size_t segs = w.plan.segs, later = segs - 1;
+    const size_t parts = ssd::selective_blocks(channels, ngroups, dstate) / ngroups;
+    size_t o = 0;
+    auto take = [&](size_t floats) {
+        const size_t at = o;
+        o += align_up(floats * sizeof(float));
+        return at;
+    };
+    w.keep_state = take(be * w.keeps * nk);
+    w.keep_sum = take(be * w.keeps);
+    w.seg_state = take(be * later * nk);
+    w.seg_sum = take(be * later);
+    w.seg_adj = take(be * later * nk);
+    w.dbc = take(parts * 2 * batch * seqlen * ngroups * dstate);
+    w.dA = take(be * segs * dstate);
+    w.de = take(2 * be * segs);
+    w.total = o;
+    return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -228,6 +303,108 @@ int ssd_norm_backward(const void *dy, const void *x, long long x_row_stride, int
     a.part = static_cast<float *>(workspace);
     return status_of(ssd::launch_norm_bwd(a, dtype == SSD_BF16, x_dtype == SSD_BF16,
                                           static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_selective_forward_workspace_size(int batch, int seqlen, int channels, int ngroups,
+                                            int dstate, int dtype) {
+    if (check_selective(batch, seqlen, channels, ngroups, dstate, dtype) != SSD_OK) return 0;
+    return ssd::selective_plan(batch, seqlen, channels, ngroups, dstate).scratch_bytes;
+}
+
+int ssd_selective_forward(const void *x, const void *dt, const float *A, const void *B,
+                          const void *C, const float *D, const void *z, int batch, int seqlen,
+                          int channels, int ngroups, int dstate, int dtype,
+                          const float *init_state, void *y, float *final_state, void *workspace,
+                          size_t workspace_bytes, const ssd_selective_strides *strides,
+                          const ssd_options *opts, void *stream) {
+    if (!x || !dt || !A || !B || !C || !y) return SSD_ERR_NULL;
+    int rc = check_selective(batch, seqlen, channels, ngroups, dstate, dtype);
+    if (rc != SSD_OK) return rc;
+    ssd::SelArgs a;
+    rc = selective_args(a, x, dt, A, B, C, D, z, batch, seqlen, channels, ngroups, dstate, strides,
+                        opts);
+    if (rc != SSD_OK) return rc;
+    const ssd::SelPlan p = ssd::selective_plan(batch, seqlen, channels, ngroups, dstate);
+    if ((long long)ssd::selective_blocks(channels, ngroups, dstate) * p.segs * batch >= kMaxBlocks)
+        return SSD_ERR_UNSUPPORTED;
+    rc = check_workspace(workspace, workspace_bytes, p.scratch_bytes);
+    if (rc != SSD_OK) return rc;
+    a.segs = p.segs;
+    a.seg_len = p.seg_len;
+    a.seg_state = static_cast<float *>(workspace);
+    a.seg_sum = a.seg_state + (size_t)batch * (p.segs - 1) * channels *
+                                  ssd::selective_kernel_dstate(dstate);
+    a.init = init_state;
+    a.y = y;
+    a.final_state = final_state;
+    return status_of(ssd::launch_selective_fwd(a, dtype == SSD_BF16, static_cast<hipStream_t>(stream)));
+}
+
+int ssd_selective_step(float *state, const void *x, const void *dt, const float *A, const void *B,
+                       const void *C, const float *D, const void *z, int batch, int channels,
+                       int ngroups, int dstate, int dtype, void *y,
+                       const ssd_selective_strides *strides, const ssd_options *opts,
+                       void *stream) {
+    if (!state || !x || !dt || !A || !B || !C || !y) return SSD_ERR_NULL;
+    int rc = check_selective(batch, 1, channels, ngroups, dstate, dtype);
+    if (rc != SSD_OK) return rc;
+    if ((long long)batch * channels * (ssd::selective_kernel_dstate(dstate) / 4) / 256 >= kMaxBlocks - 1)
+        return SSD_ERR_UNSUPPORTED;
+    ssd::SelArgs a;
+    rc = selective_args(a, x, dt, A, B, C, D, z, batch, 1, channels, ngroups, dstate, strides, opts);
+    if (rc != SSD_OK) return rc;
+    a.y = y;
+    return status_of(ssd::launch_selective_step(a, state, dtype == SSD_BF16,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_selective_backward_workspace_size(int batch, int seqlen, int channels, int ngroups,
+                                             int dstate, int dtype) {
+    if (check_selective(batch, seqlen, channels, ngroups, dstate, dtype) != SSD_OK) return 0;
+    return selective_bwd_layout(batch, seqlen, channels, ngroups, dstate).total;
+}
+
+int ssd_selective_backward(const void *x, const void *dt, const float *A, const void *B,
+                           const void *C, const float *D, const void *z, const float *init_state,
+                           const void *dy, const float *dfinal_state, int batch, int seqlen,
+                           int channels, int ngroups, int dstate, int dtype, void *dx, void *ddt,
+                           float *dA, void *dB, void *dC, float *dD, void *dz, float *dinit_state,
+                           float *ddt_bias, void *workspace, size_t workspace_bytes,
+                           const ssd_selective_strides *strides, const ssd_options *opts,
+                           void *stream) {
+    if (!x || !dt || !A || !B || !C || !dy || !dx || !ddt || !dA || !dB || !dC || (z && !dz))
+        return SSD_ERR_NULL;
+    int rc = check_selective(batch, seqlen, channels, ngroups, dstate, dtype);
+    if (rc != SSD_OK) return rc;
+    ssd::SelBwdArgs b{};
+    rc = selective_args(b.f, x, dt, A, B, C, D, z, batch, seqlen, channels, ngroups, dstate,
+                        strides, opts);
+    if (rc != SSD_OK) return rc;
+    const SelBwdLayout w = selective_bwd_layout(batch, seqlen, channels, ngroups, dstate);
+    if ((long long)ssd::selective_blocks(channels, ngroups, dstate) * w.plan.segs * batch >= kMaxBlocks ||
+        ((long long)batch * seqlen * ngroups * dstate) / 512 >= kMaxBlocks - 1)
+        return SSD_ERR_UNSUPPORTED;
+    rc = check_workspace(workspace, workspace_bytes, w.total);
+    if (rc != SSD_OK) return rc;
+    char *base = static_cast<char *>(workspace);
+    auto at = [&](size_t off) { return reinterpret_cast<float *>(base + off); };
+    b.f.init = init_state;
+    b.f.segs = w.plan.segs;
+    b.f.seg_len = w.plan.seg_len;
+    b.f.seg_state = at(w.seg_state);
+    b.f.seg_sum = at(w.seg_sum);
+    b.f.keeps = w.keeps;
+    b.f.keep_state = at(w.keep_state);
+    b.f.keep_sum = at(w.keep_sum);
+    b.dy = dy;
+    b.dfinal = dfinal_state;
+    b.seg_adj = at(w.seg_adj);
+    b.dbc_part = at(w.dbc);
+    b.dA_part = at(w.dA);
+    b.de_part = at(w.de);
+    b.dx = dx; b.ddt = ddt; b.dz = dz; b.dB = dB; b.dC = dC;
+    b.dA = dA; b.dD = dD; b.ddt_bias = ddt_bias; b.dinit = dinit_state;
+    return status_of(ssd::launch_selective_bwd(b, dtype == SSD_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

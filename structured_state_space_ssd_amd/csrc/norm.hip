@@ -279,8 +279,9 @@ __global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ 
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < 16; ++k) s += acc[k][l];
-        if (c < first) out0[c] = s;
-        else if (out1) out1[c - first] = s;
+        if (c < first) {
+            if (out0) out0[c] = s;
+        } else if (out1) out1[c - first] = s;
     }
 }
 

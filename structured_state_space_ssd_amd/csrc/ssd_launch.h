@@ -228,4 +228,53 @@ hipError_t launch_conv_step(void *state, const void *x, size_t x_row, const floa
                             const float *bias, int batch, int channels, int width, int silu,
                             const ConvParts &y, bool bf16, hipStream_t stream);
 
+// ---- selective scan (selective.hip, selective_bwd.hip)
+// Strides in elements between sequences and tokens; channels (and a token's
+// [G][N] of B and C) are dense. x, dt, z [Bt][L][E], B, C [Bt][L][G][N].
+struct SelArgs {
+    const void *x, *dt, *z, *B, *C;   // z nullable
+    size_t x_batch, x_token, dt_batch, dt_token, z_batch, z_token, B_batch, B_token, C_batch,
+        C_token;
+    const float *A, *D;               // [E][N], [E] (nullable)
+    const float *init;                // [Bt][E][N], nullable
+    DtOpts opts;                      // bias [E]; no zero-order hold
+    int batch, seqlen, channels, ngroups, dstate;
+    int segs, seg_len;                // segments of the token axis
+    float *seg_state, *seg_sum;       // [Bt][segs - 1][E][NK], [Bt][segs - 1][E]
+    void *y;                          // [Bt][L][E] dense
+    float *final_state;               // [Bt][E][N], nullable
+    // the backward's: states before every so many tokens (selective_keep_tokens)
+    int keeps;                        // of them per sequence
+    float *keep_state, *keep_sum;     // [Bt][keeps][E][NK], [Bt][keeps][E]
+};
+// The state size the kernels hold (4, 8, 16, 32 or 64; 0: not supported) and
+// the workgroups one sequence's channels take.
+int selective_kernel_dstate(int dstate);
+int selective_blocks(int channels, int ngroups, int dstate);
+struct SelPlan {
+    int segs, seg_len;
+    size_t scratch_bytes;  // seg_state, then seg_sum
+};
+SelPlan selective_plan(int batch, int seqlen, int channels, int ngroups, int dstate);
+hipError_t launch_selective_fwd(const SelArgs &a, bool bf16, hipStream_t stream);
+// The backward's first pass: fills seg_state, seg_sum, keep_state, keep_sum.
+hipError_t launch_selective_keep(const SelArgs &a, bool bf16, hipStream_t stream);
+int selective_keep_tokens(int dstate);
+// One token: the token strides and init are not read.
+hipError_t launch_selective_step(const SelArgs &a, float *state, bool bf16, hipStream_t stream);
+
+struct SelBwdArgs {
+    SelArgs f;                  // the forward's inputs; y, final_state unused
+    const void *dy;             // [Bt][L][E] dense
+    const float *dfinal;        // [Bt][E][N], nullable
+    float *seg_adj;             // [Bt][segs - 1][E][NK]: segments 1 .. segs - 1
+    float *dbc_part;            // [workgroups of a group][dB, dC][Bt][L][G][N]
+    float *dA_part;             // [Bt][segs][E][N]
+    float *de_part;             // [Bt][segs][dD, dbias][E]
+    void *dx, *ddt, *dz, *dB, *dC;
+    float *dA, *dD, *ddt_bias, *dinit;  // dD, ddt_bias, dinit nullable
+};
+SelPlan selective_bwd_plan(int batch, int seqlen, int channels, int ngroups, int dstate);
+hipError_t launch_selective_bwd(const SelBwdArgs &a, bool bf16, hipStream_t stream);
+
 }  // namespace ssd

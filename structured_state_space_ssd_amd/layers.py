@@ -17,7 +17,8 @@ import torch
 from . import _native
 from ._native import check, dtype_code
 
-__all__ = ["conv_forward", "conv_backward", "conv_step", "norm_forward", "norm_backward"]
+__all__ = ["conv_forward", "conv_backward", "conv_step", "selective_forward", "selective_backward",
+           "selective_step", "norm_forward", "norm_backward"]
 
 _f32 = torch.float32
 
@@ -203,6 +204,123 @@ def conv_step(state, x, weight, bias=None, silu=True, split=None):
     _call(_native.lib.ssd_conv_step, "ssd_conv_step", x.device, sp, xp, x.stride(0), wp, bp, Bt, K,
           W, int(silu), dtype_code(x.dtype), arr, n, _pointers([y.data_ptr() for y in ys]))
     return ys[0] if split is None else tuple(ys)
+
+
+# ---- selective scan --------------------------------------------------------------
+
+def _selective_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit):
+    """Checked addresses of the scan's inputs, strides and options, and (G, N)."""
+    _required(x=x, dt=dt, A=A, B=B, C=C)
+    lead = x.dim() - 1
+    if lead not in (1, 2) or A.dim() != 2 or B.dim() != lead + 2 or B.shape[:lead] != x.shape[:lead]:
+        raise ValueError("x must be [Bt, L, E], A [E, N] and B [Bt, L, G, N] (without L for one token)")
+    E = x.shape[-1]
+    G, N = B.shape[-2:]
+    if G < 1 or E % G:
+        raise ValueError(f"{E} channels do not divide into {G} groups")
+    pointers = [_slice(x, "x", x.shape, x), _slice(dt, "dt", x.shape, x), _param(A, "A", (E, N), x),
+                _slice(B, "B", B.shape, x), _slice(C, "C", B.shape, x), _param(D, "D", (E,), x),
+                _slice(z, "z", x.shape, x)]
+    for t, name in ((B, "B"), (C, "C")):
+        if G > 1 and t.stride(-2) != N:
+            raise ValueError(f"{name}'s groups must be contiguous")
+    st = _native.SsdSelectiveStrides()
+    for t, name in ((x, "x"), (dt, "dt"), (z, "z"), (B, "B"), (C, "C")):
+        if t is not None:
+            setattr(st, name + "_batch", t.stride(0))
+            if lead == 2:
+                setattr(st, name + "_token", t.stride(1))
+    opts = None
+    if dt_bias is not None or dt_softplus or dt_limit is not None:
+        lo, hi = (0.0, 0.0) if dt_limit is None else (float(dt_limit[0]), float(dt_limit[1]))
+        opts = ctypes.byref(_native.SsdOptions(_param(dt_bias, "dt_bias", (E,), x),
+                                               int(bool(dt_softplus)), int(dt_limit is not None),
+                                               lo, hi, _native.SSD_DISC_EULER))
+    return pointers, ctypes.byref(st), opts, G, N
+
+
+def selective_forward(x, dt, A, B, C, D=None, z=None, init_state=None, return_final_state=False,
+                      workspace=None, dt_bias=None, dt_softplus=False, dt_limit=None):
+    """Selective scan with a decay rate per channel and state over whole
+    sequences (ssd_selective_forward):
+    h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t, y_t = (C_t h_t + D x_t) silu(z_t).
+
+    x, dt, z (None: no gate) [Bt, L, E], B, C [Bt, L, G, N] (float32 or
+    bfloat16, slices of wider projections are fine), A [E, N] and D [E] float32,
+    init_state [Bt, E, N] float32 or None, N at most 64. dt_bias ([E]),
+    dt_softplus, dt_limit: see ``options``.
+    Returns y, or (y, final_state [Bt, E, N] float32) if requested.
+    """
+    p, st, opts, G, N = _selective_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
+    if x.dim() != 3:
+        raise ValueError("x must be [Bt, L, E]")
+    Bt, L, E = x.shape
+    ip = _param(init_state, "init_state", (Bt, E, N), x)
+    _on_gpu(x)
+    code = dtype_code(x.dtype)
+    y = torch.empty((Bt, L, E), dtype=x.dtype, device=x.device)
+    final = torch.empty((Bt, E, N), dtype=_f32, device=x.device) if return_final_state else None
+    need = _native.lib.ssd_selective_forward_workspace_size(Bt, L, E, G, N, code)
+    keep, ws, ws_bytes = _workspace(workspace, need, x)
+    _call(_native.lib.ssd_selective_forward, "ssd_selective_forward", x.device, *p, Bt, L, E, G, N,
+          code, ip, y.data_ptr(), None if final is None else final.data_ptr(), ws, ws_bytes, st, opts)
+    return (y, final) if return_final_state else y
+
+
+def selective_backward(x, dt, A, B, C, D, dy, z=None, init_state=None, dfinal_state=None,
+                       dt_bias=None, dt_softplus=False, dt_limit=None, workspace=None,
+                       want_dinit=True):
+    """Gradients of sum(dy * y) + sum(dfinal_state * final_state) for
+    ``selective_forward`` with the same inputs and options (ssd_selective_backward).
+
+    Returns a dict: dx, ddt, dB, dC and, with z, dz (dense, in x's type), dA
+    [E, N] and dD [E] float32, dinit (float32 [Bt, E, N], None if not
+    want_dinit) and, when dt_bias is given, ddt_bias [E] float32.
+    """
+    p, st, opts, G, N = _selective_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
+    if x.dim() != 3:
+        raise ValueError("x must be [Bt, L, E]")
+    _required(dy=dy)
+    Bt, L, E = x.shape
+    yp = _param(dy, "dy", (Bt, L, E), x, x.dtype)
+    ip = _param(init_state, "init_state", (Bt, E, N), x)
+    fp = _param(dfinal_state, "dfinal_state", (Bt, E, N), x)
+    _on_gpu(x)
+    code = dtype_code(x.dtype)
+    new = lambda shape, dtype=_f32: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
+    out = {"dx": new((Bt, L, E), x.dtype), "ddt": new((Bt, L, E), x.dtype), "dA": new((E, N)),
+           "dB": new((Bt, L, G, N), x.dtype), "dC": new((Bt, L, G, N), x.dtype), "dD": new((E,)),
+           "dinit": new((Bt, E, N)) if want_dinit else None}
+    if z is not None:
+        out["dz"] = new((Bt, L, E), x.dtype)
+    if dt_bias is not None:
+        out["ddt_bias"] = new((E,))
+    ptr = lambda k: out[k].data_ptr() if out.get(k) is not None else None  # noqa: E731
+    need = _native.lib.ssd_selective_backward_workspace_size(Bt, L, E, G, N, code)
+    keep, ws, ws_bytes = _workspace(workspace, need, x)
+    _call(_native.lib.ssd_selective_backward, "ssd_selective_backward", x.device, *p, ip, yp, fp, Bt,
+          L, E, G, N, code, ptr("dx"), ptr("ddt"), ptr("dA"), ptr("dB"), ptr("dC"), ptr("dD"),
+          ptr("dz"), ptr("dinit"), ptr("ddt_bias"), ws, ws_bytes, st, opts)
+    return out
+
+
+def selective_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=False,
+                   dt_limit=None):
+    """One token of ``selective_forward`` for every sequence (ssd_selective_step):
+    x, dt, z [Bt, E], B, C [Bt, G, N]; ``state`` [Bt, E, N] float32,
+    selective_forward's final_state at first, is updated in place. Returns y [Bt, E].
+    """
+    p, st, opts, G, N = _selective_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
+    if x.dim() != 2:
+        raise ValueError("x must be [Bt, E]")
+    _required(state=state)
+    Bt, E = x.shape
+    sp = _param(state, "state", (Bt, E, N), x)
+    _on_gpu(x)
+    y = torch.empty((Bt, E), dtype=x.dtype, device=x.device)
+    _call(_native.lib.ssd_selective_step, "ssd_selective_step", x.device, sp, *p, Bt, E, G, N,
+          dtype_code(x.dtype), y.data_ptr(), st, opts)
+    return y
 
 
 # ---- normalisation ---------------------------------------------------------------

@@ -127,3 +127,92 @@ def norm_grads(dy, x, weight, rms, eps, z=None, dres=None):
         du, da = du + dres.double().cpu(), da + dres.double().cpu().abs()
     out["dx"], mag["dx"] = du, da
     return out, mag
+
+
+def selective(x, dt, A, B, C, D=None, z=None, init=None, bias=None, use_softplus=False, limit=None,
+              grads=None):
+    """The selective scan token by token: dict of y and final with their error
+    bounds (key + "_err"), and with grads = (dy, dfinal or None) every gradient.
+
+    The bounds follow the recurrence. A step size is off by kd = 10 + 2 |v|
+    roundings of itself through softplus (1 for the bias, 2 |v| for the
+    exponent, the rest for e^-|v|, log, reciprocal and sums), else 2; a decay
+    exp(dt A) by (kd + 4) |dt A| + 2 of itself, an input term by kd + 3. So with
+    H the recurrence of absolute values, E_t = a (E_{t-1} + ka H_{t-1}) + ku |u B|,
+    and one rounding of H_t per step. Backward the same for the adjoint, whose
+    products with the states take both errors."""
+    d64 = lambda t: None if t is None else t.detach().double().cpu()  # noqa: E731
+    x, dt, A, B, C, D, z, init, bias = map(d64, (x, dt, A, B, C, D, z, init, bias))
+    Bt, L, E = x.shape
+    N, G = A.shape[1], B.shape[2]
+    each = E // G
+    v = dt if bias is None else dt + bias
+    delta, slope, kd = v, torch.ones_like(v), torch.full_like(v, 2.0)
+    if use_softplus:
+        delta, slope, kd = softplus(v), torch.sigmoid(v), 10 + 2 * v.abs()
+    if limit is not None:
+        slope = slope * ((delta >= limit[0]) & (delta <= limit[1]))
+        delta = delta.clamp(*limit)
+    D = torch.zeros(E, dtype=torch.float64) if D is None else D
+    h = torch.zeros(Bt, E, N, dtype=torch.float64) if init is None else init.clone()
+    H, Er = h.abs(), torch.zeros_like(h)
+    exp = lambda m, t: m[:, t].repeat_interleave(each, 1)  # noqa: E731
+    hs, Hs, Ers, ys, ym = [h], [H], [Er], torch.zeros_like(x), torch.zeros_like(x)
+    for t in range(L):
+        d, k = delta[:, t, :, None], kd[:, t, :, None]
+        a = torch.exp(d * A)
+        u = d * x[:, t, :, None] * exp(B, t)
+        Er = a * (Er + ((k + 4) * (d * A).abs() + 3) * H) + (k + 4) * u.abs()
+        h, H = a * h + u, a * H + u.abs()
+        Er = Er + H
+        ys[:, t] = (h * exp(C, t)).sum(-1) + D * x[:, t]
+        ym[:, t] = ((Er + (N + 2) * H) * exp(C, t).abs()).sum(-1) + 3 * (D * x[:, t]).abs()
+        hs.append(h), Hs.append(H), Ers.append(Er)
+    gate = torch.ones_like(x) if z is None else silu(z)
+    y = ys * gate
+    kz = 0.0 if z is None else 8 + 2 * z.abs()
+    out = {"y": y, "y_err": (ym + ys.abs() * kz) * gate.abs() + y.abs(), "final": h, "final_err": Er}
+    if grads is None:
+        return out
+    dy, dfinal = map(d64, grads)
+    # every product below is off by at most the sum of its factors' errors and a few roundings
+    dys, dye = dy * gate, (dy * gate).abs() * (kz + 1)
+    if z is not None:
+        out["dz"] = dy * ys * silu_grad(z)
+        out["dz_err"] = dy.abs() * (1 + z.abs()) * (ym + ys.abs() * (kz + 8))
+    g = torch.zeros_like(h) if dfinal is None else dfinal.clone()
+    ga, ge = g.abs(), torch.zeros_like(g)
+    zero = {"dx": torch.zeros_like(x), "ddt": torch.zeros_like(x), "dB": torch.zeros_like(B),
+            "dC": torch.zeros_like(C), "dA": torch.zeros_like(A)}
+    out.update({k: t.clone() for k, t in zero.items()}, **{k + "_err": t.clone() for k, t in zero.items()})
+    group = lambda m: m.unflatten(1, (G, each)).sum(2)  # noqa: E731
+    for t in reversed(range(L)):
+        d, k, xt, Bt_ = delta[:, t, :, None], kd[:, t, :, None], x[:, t, :, None], exp(B, t)
+        term = dys[:, t, :, None] * exp(C, t)
+        g, ge = g + term, ge + dye[:, t, :, None] * exp(C, t).abs() + ga + 2 * term.abs()
+        ga = ga + term.abs()
+        a = torch.exp(d * A)
+        ka = (k + 4) * (d * A).abs() + 3
+        out["dC"][:, t] = group(hs[t + 1] * dys[:, t, :, None])
+        out["dC_err"][:, t] = group((Ers[t + 1] + (each + 4) * Hs[t + 1]) * dys[:, t, :, None].abs()
+                                    + Hs[t + 1] * dye[:, t, :, None])
+        out["dB"][:, t] = group(g * d * xt)
+        out["dB_err"][:, t] = group((ge + (k + each + 4) * ga) * (d * xt).abs())
+        gB, gBe = (g * Bt_).sum(-1), ((ge + (N + 4) * ga) * Bt_.abs()).sum(-1)
+        out["dx"][:, t] = gB * d[..., 0] + D * dys[:, t]
+        out["dx_err"][:, t] = (gBe + (k[..., 0] + 2) * gB.abs()) * d[..., 0].abs() + (D * dys[:, t]).abs() * 3 + D.abs() * dye[:, t]
+        q, qa, qe = a * hs[t], a * Hs[t], a * (Ers[t] + (ka + 2) * Hs[t])
+        # a h_{t-1} may be formed from h_t - dt x B_t, whose own error is h_t's
+        qe = qe + Ers[t + 1] + 2 * Hs[t + 1] + (k + 4) * (d * xt * Bt_).abs()
+        back, backe = g * q, ge * qa + ga * qe + 4 * ga * qa
+        out["ddt"][:, t] = (xt[..., 0] * gB + (back * A).sum(-1)) * slope[:, t]
+        out["ddt_err"][:, t] = (xt[..., 0].abs() * (gBe + 3 * gB.abs()) + ((backe + (N + 4) * ga * qa) * A.abs()).sum(-1)
+                                + (k[..., 0] + 8) * (xt[..., 0].abs() * gB.abs() + (back * A).abs().sum(-1)))
+        out["dA"] += (back * d).sum(0)
+        out["dA_err"] += ((backe + (k + Bt * L + 4) * ga * qa) * d).sum(0)
+        g, ga, ge = a * g, a * ga, a * (ge + (ka + 2) * ga)
+    out["dinit"], out["dinit_err"] = g, ge + ga
+    out["dD"], out["dD_err"] = (dys * x).sum((0, 1)), ((dye + (Bt * L + 2) * dys.abs()) * x.abs()).sum((0, 1))
+    out["ddt_bias"] = out["ddt"].sum((0, 1))
+    out["ddt_bias_err"] = (out["ddt_err"] + Bt * L * out["ddt"].abs()).sum((0, 1))
+    return out

@@ -170,3 +170,101 @@ def norm_c(lib, **kw):
 ])
 def test_norm_c_abi_refuses(lib, kw, code):
     assert norm_c(lib, **kw) == code
+
+
+def scan_args(**over):
+    a = dict(x=z(2, 6, 8, dtype=bf), dt=z(2, 6, 8, dtype=bf), A=z(8, 5), B=z(2, 6, 2, 5, dtype=bf),
+             C=z(2, 6, 2, 5, dtype=bf), D=z(8))
+    a.update(over)
+    return a
+
+
+SCAN_BAD = [
+    (ValueError, "x must be", dict(A=z(8))),
+    (ValueError, "x must be", dict(B=z(2, 6, 10, dtype=bf))),
+    (ValueError, "x must be", dict(B=z(2, 5, 2, 5, dtype=bf))),
+    (ValueError, "A must have shape", dict(A=z(9, 5))),
+    (ValueError, "A must have shape", dict(A=z(8, 6))),
+    (ValueError, "C must have shape", dict(C=z(2, 6, 1, 5, dtype=bf))),
+    (ValueError, "dt must have shape", dict(dt=z(2, 6, 1, dtype=bf))),
+    (TypeError, "dt must be", dict(dt=z(2, 6, 8))),
+    (TypeError, "A must be", dict(A=z(8, 5, dtype=bf))),
+    (ValueError, "groups", dict(B=z(2, 6, 3, 5, dtype=bf), C=z(2, 6, 3, 5, dtype=bf))),
+    (ValueError, "groups must be contiguous", dict(B=z(2, 6, 2, 7, dtype=bf)[..., :5])),
+    (ValueError, "last axis", dict(z=z(2, 8, 6, dtype=bf).transpose(1, 2))),
+    (ValueError, "D must have shape", dict(D=z(7))),
+    (ValueError, "dt_bias", dict(dt_bias=z(9))),
+    (ValueError, "GPU", dict()),
+]
+
+
+@pytest.mark.parametrize("error,text,over", SCAN_BAD, ids=[f"{t}-{i}" for i, (_, t, _) in enumerate(SCAN_BAD)])
+def test_selective_refuses(ssd, error, text, over):
+    with pytest.raises(error, match=text):
+        ssd.selective_forward(**scan_args(**over))
+    with pytest.raises(error, match=text):
+        ssd.selective_backward(**scan_args(**over), dy=z(2, 6, 8, dtype=bf))
+
+
+def test_selective_more_refusals(ssd):
+    with pytest.raises(ValueError, match="init_state"):
+        ssd.selective_forward(**scan_args(init_state=z(2, 8, 4)))
+    with pytest.raises(ValueError, match="dfinal_state"):
+        ssd.selective_backward(**scan_args(dfinal_state=z(2, 4, 5)), dy=z(2, 6, 8, dtype=bf))
+    with pytest.raises(ValueError, match="dy must have shape"):
+        ssd.selective_backward(**scan_args(), dy=z(2, 6, 7, dtype=bf))
+    one = {k: (v[:, 0] if k in ("x", "dt", "B", "C") else v) for k, v in scan_args().items()}
+    with pytest.raises(ValueError, match="GPU"):
+        ssd.selective_step(z(2, 8, 5), **one)
+    with pytest.raises(ValueError, match="state must have shape"):
+        ssd.selective_step(z(2, 8, 4), **one)
+    with pytest.raises(ValueError, match="x must be"):
+        ssd.selective_step(z(2, 8, 5), **dict(one, x=z(8, dtype=bf)))
+
+
+def scan_c(lib, **kw):
+    from structured_state_space_ssd_amd import _native
+    strides, opts = kw.pop("strides", None), kw.pop("opts", None)
+    a = dict(x=FAKE, dt=FAKE, A=FAKE, B=FAKE, C=FAKE, D=None, z=None, batch=2, seqlen=6, channels=8,
+             ngroups=2, dstate=5, dtype=1, init=None, y=FAKE, fin=None, ws=None, bytes=0)
+    a.update(kw)
+    st = None if strides is None else ctypes.byref(_native.SsdSelectiveStrides(*strides))
+    return lib.ssd_selective_forward(*a.values(), st, None if opts is None else ctypes.byref(opts), None)
+
+
+def _opt(**kw):
+    from structured_state_space_ssd_amd import _native
+    return _native.SsdOptions(**kw)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), -1), (dict(dt=None), -1), (dict(A=None), -1), (dict(B=None), -1), (dict(C=None), -1),
+    (dict(y=None), -1), (dict(batch=0), -2), (dict(seqlen=0), -2), (dict(channels=0), -2),
+    (dict(ngroups=0), -2), (dict(dstate=0), -2), (dict(ngroups=3), -2), (dict(seqlen=(1 << 30) + 1), -2),
+    (dict(strides=(0, 0, 0, 0, 0, 0, 0, -1, 0, 0)), -2),
+    (dict(dstate=65), -3), (dict(dtype=2), -3), (dict(batch=1 << 24), -3),
+    (dict(seqlen=4096), -4), (dict(seqlen=4096, ws=ctypes.c_void_p(0x100010), bytes=1 << 30), -4),
+], ids=str)
+def test_selective_c_abi_refuses(lib, kw, code):
+    assert scan_c(lib, **kw) == code
+
+
+def test_selective_c_abi_options_and_workspaces(lib):
+    assert scan_c(lib, opts=_opt(discretization=1)) == -6
+    assert scan_c(lib, opts=_opt(dt_clamp=1, dt_min=1.0, dt_max=0.5)) == -6
+    assert scan_c(lib, opts=_opt(dt_clamp=1, dt_min=float("nan"), dt_max=0.5)) == -6
+    size = lib.ssd_selective_forward_workspace_size
+    assert size(2, 6, 8, 2, 5, 1) == 0  # one segment: no workspace
+    assert size(1, 4096, 64, 1, 16, 1) > 0 and size(1, 4096, 64, 1, 65, 1) == 0
+    assert size(64, 4096, 5120, 1, 16, 1) == 0  # channels enough: uncut
+    back = lib.ssd_selective_backward_workspace_size
+    n = back(2, 6, 8, 2, 5, 1)
+    assert n > 0
+    args = [FAKE] * 5 + [None, None, None, FAKE, None, 2, 6, 8, 2, 5, 1] + [FAKE] * 5 + [None] * 4
+    assert lib.ssd_selective_backward(*args, FAKE, n - 1, None, None, None) == -4
+    args[8] = None
+    assert lib.ssd_selective_backward(*args, FAKE, n, None, None, None) == -1
+    args[8], args[6] = FAKE, FAKE  # z without dz
+    assert lib.ssd_selective_backward(*args, FAKE, n, None, None, None) == -1
+    # sizes whose products pass 32 bits
+    assert back(8, 1 << 20, 8192, 1, 64, 0) > (1 << 32)
