@@ -264,6 +264,8 @@ __global__ __launch_bounds__(256, 2) void selective_bwd_kernel(SelBwdArgs ba) {
         float h[TB][4], dec[TB][4];
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
+            // LDS reads of at most two tokens ahead: more would not fit the registers
+            if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);
             const float2 d = du[t * CH + ch];
             const float4 b4 = *reinterpret_cast<const float4 *>(&bs[t * NK + n0]);
             const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
@@ -284,6 +286,7 @@ __global__ __launch_bounds__(256, 2) void selective_bwd_kernel(SelBwdArgs ba) {
         }
 #pragma unroll
         for (int t = TB - 1; t >= 0; --t) {
+            if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);
             const float2 d = du[t * CH + ch];
             const float dyv = dys[t * CH + ch];
             const float4 b4 = *reinterpret_cast<const float4 *>(&bs[t * NK + n0]);
