@@ -110,11 +110,41 @@ int selective_args(ssd::SelArgs &a, const void *x, const void *dt, const float *
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
+struct Taker {
+    size_t o = 0;
+    size_t take(size_t floats) {
+        const size_t at = o;
+        o += align_up(floats * sizeof(float));
+        return at;
+    }
+};
+
+// The selective scan's plan and where its workspace's parts begin.
+struct SelLayout {
+    ssd::SelPlan plan;
+    size_t bc, seg_state, seg_sum, total;
+};
+SelLayout selective_layout(int batch, int seqlen, int channels, int ngroups, int dstate) {
+    SelLayout w{};
+    w.plan = ssd::selective_plan(batch, seqlen, channels, ngroups, dstate);
+    Taker k;
+    w.bc = k.take(ssd::selective_bc_floats(batch, seqlen, ngroups, dstate));
+    w.seg_state = k.take(w.plan.seg_floats);
+    w.seg_sum = k.take((size_t)batch * channels * (w.plan.segs - 1));
+    w.total = k.o;
+    return w;
+}
+
+bool selective_grid_ok(int batch, int seqlen, int channels, int ngroups, int dstate, int segs) {
+    return (long long)ssd::selective_blocks(channels, ngroups, dstate) * segs * batch < kMaxBlocks &&
+           ssd::selective_bc_floats(batch, seqlen, ngroups, dstate) / 256 < (size_t)kMaxBlocks - 1;
+}
+
 // The selective scan's backward: its plan and where its workspace's parts begin.
 struct SelBwdLayout {
     ssd::SelPlan plan;
     int keeps;
-    size_t keep_state, keep_sum, seg_state, seg_sum, seg_adj, dbc, dA, de, total;
+    size_t bc, keep_state, keep_sum, seg_state, seg_sum, seg_adj, dbc, dA, de, total;
 };
 SelBwdLayout selective_bwd_layout(int batch, int seqlen, int channels, int ngroups, int dstate) {
     SelBwdLayout w{};
@@ -123,22 +153,17 @@ SelBwdLayout selective_bwd_layout(int batch, int seqlen, int channels, int ngrou
     const int keep = ssd::selective_keep_tokens(dstate);
     w.keeps = (seqlen + keep - 1) / keep;
     const size_t segs = w.plan.segs, later = segs - 1;
-    const size_t parts = ssd::selective_blocks(channels, ngroups, dstate) / ngroups;
-    size_t o = 0;
-    auto take = [&](size_t floats) {
-        const size_t at = o;
-        o += align_up(floats * sizeof(float));
-        return at;
-    };
-    w.keep_state = take(be * w.keeps * nk);
-    w.keep_sum = take(be * w.keeps);
-    w.seg_state = take(be * later * nk);
-    w.seg_sum = take(be * later);
-    w.seg_adj = take(be * later * nk);
-    w.dbc = take(parts * 2 * batch * seqlen * ngroups * dstate);
-    w.dA = take(be * segs * dstate);
-    w.de = take(2 * be * segs);
-    w.total = o;
+    Taker k;
+    w.bc = k.take(ssd::selective_bc_floats(batch, seqlen, ngroups, dstate));
+    w.keep_state = k.take(be * w.keeps * nk);
+    w.keep_sum = k.take(be * w.keeps);
+    w.seg_state = k.take(w.plan.seg_floats);
+    w.seg_sum = k.take(be * later);
+    w.seg_adj = k.take(w.plan.seg_floats);
+    w.dbc = k.take(ssd::selective_dbc_floats(batch, seqlen, channels, ngroups, dstate));
+    w.dA = k.take(be * segs * dstate);
+    w.de = k.take(2 * be * segs);
+    w.total = k.o;
     return w;
 }
 
@@ -308,7 +333,7 @@ int ssd_norm_backward(const void *dy, const void *x, long long x_row_stride, int
 size_t ssd_selective_forward_workspace_size(int batch, int seqlen, int channels, int ngroups,
                                             int dstate, int dtype) {
     if (check_selective(batch, seqlen, channels, ngroups, dstate, dtype) != SSD_OK) return 0;
-    return ssd::selective_plan(batch, seqlen, channels, ngroups, dstate).scratch_bytes;
+    return selective_layout(batch, seqlen, channels, ngroups, dstate).total;
 }
 
 int ssd_selective_forward(const void *x, const void *dt, const float *A, const void *B,
@@ -324,16 +349,18 @@ int ssd_selective_forward(const void *x, const void *dt, const float *A, const v
     rc = selective_args(a, x, dt, A, B, C, D, z, batch, seqlen, channels, ngroups, dstate, strides,
                         opts);
     if (rc != SSD_OK) return rc;
-    const ssd::SelPlan p = ssd::selective_plan(batch, seqlen, channels, ngroups, dstate);
-    if ((long long)ssd::selective_blocks(channels, ngroups, dstate) * p.segs * batch >= kMaxBlocks)
+    const SelLayout w = selective_layout(batch, seqlen, channels, ngroups, dstate);
+    if (!selective_grid_ok(batch, seqlen, channels, ngroups, dstate, w.plan.segs))
         return SSD_ERR_UNSUPPORTED;
-    rc = check_workspace(workspace, workspace_bytes, p.scratch_bytes);
+    rc = check_workspace(workspace, workspace_bytes, w.total);
     if (rc != SSD_OK) return rc;
-    a.segs = p.segs;
-    a.seg_len = p.seg_len;
-    a.seg_state = static_cast<float *>(workspace);
-    a.seg_sum = a.seg_state + (size_t)batch * (p.segs - 1) * channels *
-                                  ssd::selective_kernel_dstate(dstate);
+    char *base = static_cast<char *>(workspace);
+    auto at = [&](size_t off) { return reinterpret_cast<float *>(base + off); };
+    a.segs = w.plan.segs;
+    a.seg_len = w.plan.seg_len;
+    a.bc = at(w.bc);
+    a.seg_state = at(w.seg_state);
+    a.seg_sum = at(w.seg_sum);
     a.init = init_state;
     a.y = y;
     a.final_state = final_state;
@@ -381,8 +408,7 @@ int ssd_selective_backward(const void *x, const void *dt, const float *A, const 
                         strides, opts);
     if (rc != SSD_OK) return rc;
     const SelBwdLayout w = selective_bwd_layout(batch, seqlen, channels, ngroups, dstate);
-    if ((long long)ssd::selective_blocks(channels, ngroups, dstate) * w.plan.segs * batch >= kMaxBlocks ||
-        ((long long)batch * seqlen * ngroups * dstate) / 512 >= kMaxBlocks - 1)
+    if (!selective_grid_ok(batch, seqlen, channels, ngroups, dstate, w.plan.segs))
         return SSD_ERR_UNSUPPORTED;
     rc = check_workspace(workspace, workspace_bytes, w.total);
     if (rc != SSD_OK) return rc;
@@ -391,6 +417,7 @@ int ssd_selective_backward(const void *x, const void *dt, const float *A, const 
     b.f.init = init_state;
     b.f.segs = w.plan.segs;
     b.f.seg_len = w.plan.seg_len;
+    b.f.bc = at(w.bc);
     b.f.seg_state = at(w.seg_state);
     b.f.seg_sum = at(w.seg_sum);
     b.f.keeps = w.keeps;

@@ -6,27 +6,32 @@
 
 namespace ssd {
 
-// A lane holds 4 states of one channel; the NK/4 lanes that share the channel
-// (NK: the state size rounded up to 4, 8, 16, 32 or 64) are neighbours, so a
-// workgroup of 256 lanes holds 1024 / NK channels.
-template <int NK> struct SelShape {
-    static constexpr int SL = NK / 4;           // lanes per channel
-    static constexpr int CH = 256 / SL;         // channels per workgroup
-    static constexpr int TILE = NK < 16 ? 2 * NK : 32;  // tokens staged at a time
-    static constexpr int BACK = NK < 16 ? 8 : 16;       // and by the backward, which keeps the
-                                                        // states before every so many tokens
+// How a workgroup holds channels and states (NK: the state size rounded up to
+// 4, 8, 16, 32 or 64). A lane holds NS states of one channel; the WS wavefronts
+// that share 64 channels hold different states. So the B and C of a token are
+// the same for a whole wavefront and come from scalar loads, and sums over
+// channels or states never mix the two axes. The backward (BACK) keeps a
+// tile's states and decays in registers, so its lanes hold 4 states (8 at NK
+// 64) and the workgroup has more wavefronts instead.
+template <int NK, bool BACK = false> struct SelShape {
+    static constexpr int NS = BACK ? (NK <= 32 ? 4 : 8) : NK <= 16 ? 4 : NK / 4;  // states per lane
+    static constexpr int WS = NK / NS;                           // wavefronts across the states
+    static constexpr int THREADS = WS > 4 ? 64 * WS : 256;
+    static constexpr int CH = THREADS / WS;                      // channels per workgroup
+    static constexpr int TILE = 2048 / CH;                       // tokens staged at a time
 };
+// Tokens between the states that the backward's first walk keeps: a tile of
+// its second one, whose partial sums (12 bytes per channel, token and
+// wavefront) stay within 48 KB of LDS and whose states within the registers.
+template <int NK> constexpr int sel_keep() { return NK <= 8 ? 8 : NK == 16 ? 16 : NK == 32 ? 8 : 4; }
 
-// Sum over the SL neighbouring lanes, in each of them: DPP moves within a row
-// of 16 lanes (neighbour, neighbour pair, half row, row).
-template <int SL> __device__ __forceinline__ float lanes_sum(float v) {
-    auto add = [](float a, int b) { return a + __int_as_float(b); };
-    if constexpr (SL >= 2) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));
-    if constexpr (SL >= 4) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, true));
-    if constexpr (SL >= 8) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));
-    if constexpr (SL >= 16) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, true));
-    return v;
-}
+// B and C as the scans read them: float32 [Bt][G][tokens][NK / 4][B, C][4], the
+// tokens rounded up to a whole number of tiles and zero behind the last. Four
+// states' B and C are one 32-byte scalar load (SelBC: B in 0 .. 3, C in 4 .. 7).
+constexpr int kSelPad = 32;
+__host__ __device__ constexpr int sel_padded(int seqlen) { return (seqlen + kSelPad - 1) / kSelPad * kSelPad; }
+typedef float SelBC __attribute__((ext_vector_type(8)));
+typedef const __attribute__((address_space(4))) SelBC sel_const;
 
 // The step size of raw value v (bias included): softplus and clamp as chosen.
 __device__ __forceinline__ float sel_step(const DtOpts &o, float v) {
@@ -34,24 +39,71 @@ __device__ __forceinline__ float sel_step(const DtOpts &o, float v) {
     if (o.clamp) v = fminf(fmaxf(v, o.lo), o.hi);
     return v;
 }
+// The same of a vector's values, the choices outside the loops; zero (which
+// moves no state and passes no gradient) past the segment's last row.
+template <int V>
+__device__ __forceinline__ void sel_steps(const DtOpts &o, float (&d)[V], bool in) {
+    if (o.softplus) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[e] = softplus_f32(d[e]);
+    }
+    if (o.clamp) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[e] = fminf(fmaxf(d[e], o.lo), o.hi);
+    }
+    if (!in) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[e] = 0.0f;
+    }
+}
 
 // Where a workgroup of the scan stands: sequence b, segment seg, channels
-// first .. first + n - 1, all of group g.
+// first .. first + n - 1, all of group g, its block-th workgroup.
 struct SelBlock {
-    int b, seg, g, first, n;
+    int b, seg, g, block, first, n;
 };
-template <int NK> __device__ __forceinline__ SelBlock sel_block(int id, int channels, int ngroups, int segs) {
-    constexpr int CH = SelShape<NK>::CH;
+template <int CH> __device__ __forceinline__ SelBlock sel_block(int id, int channels, int ngroups, int segs) {
     const int each = channels / ngroups, per = (each + CH - 1) / CH;
     SelBlock k;
     const int cb = id % (per * ngroups), rest = id / (per * ngroups);
     k.seg = rest % segs;
     k.b = rest / segs;
     k.g = cb / per;
-    const int at = (cb % per) * CH;
+    k.block = cb % per;
+    const int at = k.block * CH;
     k.first = k.g * each + at;
     k.n = each - at < CH ? each - at : CH;
     return k;
+}
+
+// A lane's NS states in scratch, [..][NK / 4][E][4] from its first four on, E
+// channels: 16 bytes a lane and a kilobyte a wavefront at a time.
+template <int NS> __device__ __forceinline__ void lane_load(const float *p, int E, float (&v)[NS]) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(p + (size_t)i * E);
+        v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+    }
+}
+template <int NS> __device__ __forceinline__ void lane_store(float *p, int E, const float (&v)[NS]) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4)
+        *reinterpret_cast<float4 *>(p + (size_t)i * E) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+
+// This lane's decay rates times log2(e), so that a decay is one exp2; states
+// past the state size get 0. -inf becomes the lowest float: the same decay for
+// any step size but zero, which it leaves at 1.
+template <int NS>
+__device__ __forceinline__ void load_rates(const float *A, int nn, float (&A2)[NS]) {
+    RowRaw<float, NS> r;
+    r.zero();
+    if (nn > 0) r.load(A, nn);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const float v = r.get(i) * kLog2e;
+        A2[i] = v < -3.402823466e38f ? -3.402823466e38f : v;
+    }
 }
 
 // FN<type, kernel state size>(...) for a's state size; returns its result.

@@ -5,15 +5,20 @@
 // with B_t, C_t shared by the channels of a group.
 //
 // The decay differs from state to state, so nothing here is a matrix product:
-// an element (token, channel, state) costs one exponential (a quarter-rate
-// instruction) and four multiply-adds, 8 vector-issue slots, and 16 states of
-// one channel-token more time than its 8 bytes do. The kernel is bound by
-// vector issue; what it can do is to issue little else. So
-// * a lane keeps 4 states in registers for the whole walk, and the lanes of a
-//   channel are neighbours: y_t takes two DPP additions at 16 states;
+// an element (token, channel, state) costs one exponential (half rate) and
+// four multiplies or multiply-adds, more issue time at 16 states than the 8
+// bytes of its channel-token take to move. The kernel is bound by vector
+// issue, so it issues little else:
+// * lanes are channels and a lane holds 4 states (16 at 64 states), the other
+//   states of the channel being in the other wavefronts: B_t and C_t are then
+//   uniform, come from scalar loads (a first small kernel writes them as
+//   float, padded) and are scalar operands of the multiply-adds; with the
+//   states across lanes they came through LDS, 20 clocks of it per 256
+//   elements, and LDS was as busy as the vector units;
 // * step sizes (softplus) and gates are computed once per (token, channel) by
 //   the lanes that load them, 16 bytes each, and reach the walk through LDS as
-//   (dt, dt x); B and C reach it as float, one 16-byte read each per 4 states;
+//   (dt, dt x); the wavefronts' parts of y_t meet there too, and the lanes
+//   that loaded x and z finish and store the rows;
 // * the next tile's rows are fetched into registers while a tile is walked.
 // With few channels the token axis is cut into segments: a first kernel makes
 // every segment's state from zero and its sum of step sizes (the decay over
@@ -25,171 +30,168 @@ namespace ssd {
 
 namespace {
 
+// B and C in the walks' layout, zero past the state size and past the last token.
+template <typename T, int NK>
+__global__ __launch_bounds__(256) void selective_bc_kernel(SelArgs a, size_t count) {
+    const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= count) return;
+    const int slot = id % (2 * NK), n = slot / 8 * 4 + slot % 4;
+    const size_t row = id / (2 * NK);
+    const int padded = sel_padded(a.seqlen), t = row % padded, bg = static_cast<int>(row / padded);
+    const int b = bg / a.ngroups, g = bg % a.ngroups;
+    float v = 0.0f;
+    if (t < a.seqlen && n < a.dstate) {
+        const size_t at = (size_t)g * a.dstate + n;
+        v = slot / 4 % 2 ? to_f32(static_cast<const T *>(a.C)[b * a.C_batch + t * a.C_token + at])
+                          : to_f32(static_cast<const T *>(a.B)[b * a.B_batch + t * a.B_token + at]);
+    }
+    a.bc[id] = v;
+}
+
 // What the walk leaves: outputs; a segment's state and step-size sum; or (for
 // the backward) those and, before every BACK tokens, the state from the
 // segment's start (zero, or the first one's initial state) with its step-size sum.
 enum SelMode { SEL_OUT, SEL_STATE, SEL_KEEP };
 
 template <typename T, int NK, SelMode MODE>
-__global__ __launch_bounds__(256) void selective_fwd_kernel(SelArgs a) {
-    constexpr bool STATE = MODE != SEL_OUT;
-    using S = SelShape<NK>;
-    constexpr int SL = S::SL, CH = S::CH, TILE = S::TILE;
+__global__ __launch_bounds__((SelShape<NK, MODE == SEL_KEEP>::THREADS)) void selective_fwd_kernel(SelArgs a) {
+    constexpr bool OUT = MODE == SEL_OUT;
+    using S = SelShape<NK, MODE == SEL_KEEP>;
+    constexpr int NS = S::NS, WS = S::WS, CH = S::CH, TILE = S::TILE, THREADS = S::THREADS;
     constexpr int V = sizeof(T) == 2 ? 8 : 4;
-    constexpr int VPR = CH / V;                              // vectors per row
-    constexpr int IT = (TILE * VPR + 255) / 256;             // row vectors per lane
-    constexpr int IB = (TILE * NK + 255) / 256;              // B and C elements per lane
-    __shared__ float2 du[TILE * CH];                         // (dt, dt x)
-    __shared__ __attribute__((aligned(16))) float bs[TILE * NK];
-    __shared__ __attribute__((aligned(16))) float cs[STATE ? 4 : TILE * NK];
-    __shared__ float ys[STATE ? 1 : TILE * CH];
+    constexpr int VPR = CH / V;                   // vectors per row
+    constexpr int IT = (TILE * VPR + THREADS - 1) / THREADS;  // row vectors per lane
+    constexpr int KEEP = sel_keep<NK>();
+    constexpr int U = MODE == SEL_KEEP && KEEP < 8 ? KEEP : 8;  // tokens per turn of the inner loop
+    __shared__ float2 du[TILE * CH];              // (dt, dt x)
+    __shared__ float ys[OUT ? WS * TILE * CH : 1];
 
     const int segs = MODE == SEL_STATE ? a.segs - 1 : a.segs;
-    const SelBlock k = sel_block<NK>(blockIdx.x, a.channels, a.ngroups, segs);
-    const int tid = threadIdx.x, sl = tid & (SL - 1), ch = tid / SL;
+    const SelBlock k = sel_block<CH>(blockIdx.x, a.channels, a.ngroups, segs);
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ws = w % WS, ch = w / WS * 64 + (tid & 63), n0 = ws * NS;
     const int N = a.dstate, E = a.channels;
     const int t_begin = k.seg * a.seg_len, t_end = min(a.seqlen, t_begin + a.seg_len);
     const T *x = static_cast<const T *>(a.x) + k.b * a.x_batch + k.first;
     const T *dt = static_cast<const T *>(a.dt) + k.b * a.dt_batch + k.first;
     const T *z = a.z ? static_cast<const T *>(a.z) + k.b * a.z_batch + k.first : nullptr;
-    const T *B = static_cast<const T *>(a.B) + k.b * a.B_batch + (size_t)k.g * N;
-    const T *C = static_cast<const T *>(a.C) + k.b * a.C_batch + (size_t)k.g * N;
+    sel_const *const bc = (sel_const *)(a.bc + (size_t)(k.b * a.ngroups + k.g) * sel_padded(a.seqlen) * 2 * NK +
+                                  ws * 2 * NS);
 
-    // this lane's states (those past the state size stay zero: A = B = C = 0)
+    // this lane's states of scratch row `at`
+    auto seg_at = [&](size_t at) { return (at * (NK / 4) + n0 / 4) * E * 4 + (size_t)(k.first + ch) * 4; };
     const bool live = ch < k.n;
-    const int n0 = sl * 4, nn = live ? N - n0 : 0;
-    float A2[4], h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dsum = 0.0f;
+    const int nn = live ? N - n0 : 0;  // states of this lane (those past them stay zero)
+    float A2[NS], h[NS], dsum = 0.0f;
+    load_rates(a.A + (size_t)(k.first + ch) * N + n0, nn, A2);
     {
-        RowRaw<float, 4> r;
+        RowRaw<float, NS> r;
         r.zero();
-        if (nn > 0) r.load(a.A + (size_t)(k.first + ch) * N + n0, nn);
+        if (k.seg == 0 && a.init && nn > 0)
+            r.load(a.init + ((size_t)k.b * E + k.first + ch) * N + n0, nn);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) A2[i] = r.get(i) * kLog2e;
+        for (int i = 0; i < NS; ++i) h[i] = r.get(i);
     }
-    if (k.seg == 0 && a.init && nn > 0) {
-        RowRaw<float, 4> r;
-        r.load(a.init + ((size_t)k.b * E + k.first + ch) * N + n0, nn);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = r.get(i);
-    }
-    if (!STATE && live) {
+    if (OUT && live) {
         // segment s's own state (the first one's goes on from the initial state) and
-        // step-size sum, [b][segs - 1][E], states NK wide
-        const size_t at = (size_t)k.b * (segs - 1) * E + k.first + ch;
+        // step-size sum: [b][segs - 1][NK / 4][E][4] and [b][segs - 1][E]
         for (int s = 0; s < k.seg; ++s) {
-            const float sum = a.seg_sum[at + (size_t)s * E];
-            const float4 st = *reinterpret_cast<const float4 *>(a.seg_state + (at + (size_t)s * E) * NK + n0);
-            const float v[4] = {st.x, st.y, st.z, st.w};
+            const size_t at = (size_t)k.b * (segs - 1) + s;
+            const float sum = a.seg_sum[at * E + k.first + ch];
+            float v[NS];
+            lane_load(a.seg_state + seg_at(at), E, v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < NS; ++i)
                 h[i] = s == 0 ? v[i] : fmaf(__builtin_amdgcn_exp2f(A2[i] * sum), h[i], v[i]);
         }
     }
 
     // this lane's row vectors: row r, channels c .. of the tile
     RowRaw<T, V> xr[2][IT], dr[2][IT], zr[2][IT];
-    float br[2][IB], cr[2][IB];
-    auto fetch = [&](int t0, int w) {
+    auto fetch = [&](int t0, int p) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int id = tid + i * 256, r = id / VPR, c = (id % VPR) * V;
-            xr[w][i].zero();
-            dr[w][i].zero();
-            zr[w][i].zero();
+            const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
+            xr[p][i].zero();
+            dr[p][i].zero();
+            zr[p][i].zero();
             if (r < TILE && t0 + r < t_end && c < k.n) {
                 const size_t t = t0 + r;
-                xr[w][i].load(x + t * a.x_token + c, k.n - c);
-                dr[w][i].load(dt + t * a.dt_token + c, k.n - c);
-                if (!STATE && z) zr[w][i].load(z + t * a.z_token + c, k.n - c);
+                xr[p][i].load(x + t * a.x_token + c, k.n - c);
+                dr[p][i].load(dt + t * a.dt_token + c, k.n - c);
+                if (OUT && z) zr[p][i].load(z + t * a.z_token + c, k.n - c);
             }
         }
-#pragma unroll
-        for (int i = 0; i < IB; ++i) {
-            const int id = tid + i * 256, r = id / NK, n = id % NK;
-            const bool ok = r < TILE && t0 + r < t_end && n < N;
-            br[w][i] = ok ? to_f32(B[(size_t)(t0 + r) * a.B_token + n]) : 0.0f;
-            if (!STATE) cr[w][i] = ok ? to_f32(C[(size_t)(t0 + r) * a.C_token + n]) : 0.0f;
-        }
     };
-
-    float bias[IT][V], Dv[IT][V];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int c = ((tid + i * 256) % VPR) * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            bias[i][e] = a.opts.bias && c + e < k.n ? a.opts.bias[k.first + c + e] : 0.0f;
-            Dv[i][e] = !STATE && a.D && c + e < k.n ? a.D[k.first + c + e] : 0.0f;
-        }
+    RowRaw<float, V> bias, Dv;
+    bias.zero();
+    Dv.zero();
+    if (const int c = (tid % VPR) * V; c < k.n) {
+        if (a.opts.bias) bias.load(a.opts.bias + k.first + c, k.n - c);
+        if (OUT && a.D) Dv.load(a.D + k.first + c, k.n - c);
     }
 
     fetch(t_begin, 0);
-    auto tile = [&](int t0, int w) {
+    auto tile = [&](int t0, int p) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int id = tid + i * 256, r = id / VPR, c = (id % VPR) * V;
+            const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
+            const bool in = t0 + r < t_end;  // rows past the end do not move the state
             if (r < TILE) {
+                float d[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float d = sel_step(a.opts, dr[w][i].get(e) + bias[i][e]);
-                    du[r * CH + c + e] = make_float2(d, d * xr[w][i].get(e));
-                }
-            }
-        }
+                for (int e = 0; e < V; ++e) d[e] = dr[p][i].get(e) + bias.get(e);
+                sel_steps(a.opts, d, in);
 #pragma unroll
-        for (int i = 0; i < IB; ++i) {
-            const int id = tid + i * 256;
-            if (id < TILE * NK) {
-                bs[id] = br[w][i];
-                if (!STATE) cs[id] = cr[w][i];
+                for (int e = 0; e < V; ++e) du[r * CH + c + e] = make_float2(d[e], d[e] * xr[p][i].get(e));
             }
         }
         __syncthreads();
-        if (t0 + TILE < t_end) fetch(t0 + TILE, w ^ 1);
+        if (t0 + TILE < t_end) fetch(t0 + TILE, p ^ 1);
         const int nt = min(TILE, t_end - t0);
-#pragma unroll 4
-        for (int t = 0; t < nt; ++t) {
-            const float2 d = du[t * CH + ch];
-            const float4 b4 = *reinterpret_cast<const float4 *>(&bs[t * NK + n0]);
-            const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
-            float p = 0.0f;
-            if constexpr (STATE) {
-                if constexpr (MODE == SEL_KEEP)
-                    if (t % S::BACK == 0 && live) {
-                        const size_t at = ((size_t)k.b * a.keeps + (t0 + t) / S::BACK) * E + k.first + ch;
-                        *reinterpret_cast<float4 *>(a.keep_state + at * NK + n0) =
-                            make_float4(h[0], h[1], h[2], h[3]);
-                        if (sl == 0) a.keep_sum[at] = dsum;
-                    }
-                dsum += d.x;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    h[i] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[i]), h[i], d.y * bv[i]);
-            } else {
-                const float4 c4 = *reinterpret_cast<const float4 *>(&cs[t * NK + n0]);
-                const float cv[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[i] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[i]), h[i], d.y * bv[i]);
-                    p = fmaf(cv[i], h[i], p);
+        for (int tb = 0; tb < nt; tb += U) {
+            if constexpr (MODE == SEL_KEEP)
+                if (tb % KEEP == 0 && live) {
+                    const size_t at = (size_t)k.b * a.keeps + (t0 + tb) / KEEP;
+                    lane_store(a.keep_state + seg_at(at), E, h);
+                    if (ws == 0) a.keep_sum[at * E + k.first + ch] = dsum;
                 }
-                p = lanes_sum<SL>(p);
-                if (sl == 0) ys[t * CH + ch] = p;
+            sel_const *q = bc + (size_t)(t0 + tb) * (NK / 4);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float2 d = du[(tb + u) * CH + ch];
+                float y = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NS; j += 4) {
+                    const SelBC v = q[u * (NK / 4) + j / 4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        h[j + i] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[j + i]), h[j + i], d.y * v[i]);
+                        if constexpr (OUT) y = fmaf(v[4 + i], h[j + i], y);
+                    }
+                }
+                if constexpr (OUT) ys[(ws * TILE + tb + u) * CH + ch] = y;
+                else dsum += d.x;
             }
         }
         __syncthreads();
-        if constexpr (!STATE) {
+        if constexpr (OUT) {
             T *y = static_cast<T *>(a.y);
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
-                const int id = tid + i * 256, r = id / VPR, c = (id % VPR) * V;
+                const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
                 if (r < nt && c < k.n) {
                     float o[V];
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        o[e] = fmaf(Dv[i][e], xr[w][i].get(e), ys[r * CH + c + e]);
-                        if (z) o[e] *= silu_f32(zr[w][i].get(e));
+                        float s = ys[r * CH + c + e];
+#pragma unroll
+                        for (int j = 1; j < WS; ++j) s += ys[(j * TILE + r) * CH + c + e];
+                        o[e] = fmaf(Dv.get(e), xr[p][i].get(e), s);
                     }
+                    if (z)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) o[e] *= silu_f32(zr[p][i].get(e));
                     row_store(y + ((size_t)k.b * a.seqlen + t0 + r) * E + k.first + c, o, k.n - c);
                 }
             }
@@ -200,14 +202,25 @@ __global__ __launch_bounds__(256) void selective_fwd_kernel(SelArgs a) {
         if (t0 + TILE < t_end) tile(t0 + TILE, 1);
     }
 
-    if constexpr (STATE) {
+    if constexpr (!OUT) {
         if (!live || k.seg >= a.segs - 1) return;
-        const size_t at = ((size_t)k.b * (a.segs - 1) + k.seg) * E + k.first + ch;
-        *reinterpret_cast<float4 *>(a.seg_state + at * NK + n0) = make_float4(h[0], h[1], h[2], h[3]);
-        if (sl == 0) a.seg_sum[at] = dsum;
+        const size_t at = (size_t)k.b * (a.segs - 1) + k.seg;
+        lane_store(a.seg_state + seg_at(at), E, h);
+        if (ws == 0) a.seg_sum[at * E + k.first + ch] = dsum;
     } else if (a.final_state && k.seg == segs - 1 && nn > 0) {
         row_store(a.final_state + ((size_t)k.b * E + k.first + ch) * N + n0, h, nn);
     }
+}
+
+// Sum over the SL neighbouring lanes, in each of them: DPP moves within a row
+// of 16 lanes (neighbour, neighbour pair, half row, row).
+template <int SL> __device__ __forceinline__ float lanes_sum(float v) {
+    auto add = [](float a, int b) { return a + __int_as_float(b); };
+    if constexpr (SL >= 2) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));
+    if constexpr (SL >= 4) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, true));
+    if constexpr (SL >= 8) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));
+    if constexpr (SL >= 16) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, true));
+    return v;
 }
 
 // One token. Bound by the float32 state, read once and written once: a lane
@@ -215,7 +228,7 @@ __global__ __launch_bounds__(256) void selective_fwd_kernel(SelArgs a) {
 template <typename T, int NK>
 __global__ __launch_bounds__(256) void selective_step_kernel(SelArgs a, float *__restrict__ state,
                                                              long long items) {
-    constexpr int SL = SelShape<NK>::SL;
+    constexpr int SL = NK / 4;  // lanes per channel
     const long long item = (long long)blockIdx.x * 256 + threadIdx.x;
     const int sl = threadIdx.x & (SL - 1), n0 = sl * 4;
     const int N = a.dstate, E = a.channels, nn = N - n0;
@@ -251,29 +264,38 @@ __global__ __launch_bounds__(256) void selective_step_kernel(SelArgs a, float *_
     }
 }
 
+template <typename T, int NK> hipError_t sel_bc(const SelArgs &a, hipStream_t stream) {
+    const size_t count = (size_t)a.batch * a.ngroups * sel_padded(a.seqlen) * 2 * NK;
+    selective_bc_kernel<T, NK><<<static_cast<unsigned>((count + 255) / 256), 256, 0, stream>>>(a, count);
+    return hipGetLastError();
+}
+
 template <typename T, int NK> hipError_t sel_fwd(const SelArgs &a, hipStream_t stream) {
+    hipError_t e = sel_bc<T, NK>(a, stream);
     const int blocks = selective_blocks(a.channels, a.ngroups, a.dstate);
-    if (a.segs > 1) {
+    if (e == hipSuccess && a.segs > 1) {
         selective_fwd_kernel<T, NK, SEL_STATE>
             <<<static_cast<unsigned>(blocks * (a.segs - 1) * a.batch), 256, 0, stream>>>(a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        e = hipGetLastError();
     }
+    if (e != hipSuccess) return e;
     selective_fwd_kernel<T, NK, SEL_OUT>
         <<<static_cast<unsigned>(blocks * a.segs * a.batch), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <typename T, int NK> hipError_t sel_keep(const SelArgs &a, hipStream_t stream) {
+    const hipError_t e = sel_bc<T, NK>(a, stream);
+    if (e != hipSuccess) return e;
     selective_fwd_kernel<T, NK, SEL_KEEP>
         <<<static_cast<unsigned>(selective_blocks(a.channels, a.ngroups, a.dstate) * a.segs * a.batch),
-           256, 0, stream>>>(a);
+           SelShape<NK, true>::THREADS, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <typename T, int NK>
 hipError_t sel_step_launch(const SelArgs &a, float *state, hipStream_t stream) {
-    const long long items = (long long)a.batch * a.channels * SelShape<NK>::SL;
+    const long long items = (long long)a.batch * a.channels * (NK / 4);
     selective_step_kernel<T, NK>
         <<<static_cast<unsigned>((items + 255) / 256), 256, 0, stream>>>(a, state, items);
     return hipGetLastError();
@@ -287,16 +309,20 @@ int selective_kernel_dstate(int n) {
     return 0;
 }
 
-int selective_blocks(int channels, int ngroups, int dstate) {
-    const int CH = 1024 / selective_kernel_dstate(dstate), each = channels / ngroups;
-    return ngroups * ((each + CH - 1) / CH);
+static int selective_ch(int dstate) {
+    const int nk = selective_kernel_dstate(dstate);
+    return nk <= 16 ? 1024 / nk : 64;
 }
 
-// Segments of the token axis. One walk costs 8 issue slots per element, a
-// segment's state 7 more, so cutting pays only while the uncut walks leave
-// most of the GPU idle.
+int selective_blocks(int channels, int ngroups, int dstate) {
+    const int ch = selective_ch(dstate), each = channels / ngroups;
+    return ngroups * ((each + ch - 1) / ch);
+}
+
+// Segments of the token axis. A segment's state costs almost what its walk
+// does, so cutting pays only while the uncut walks leave most of the GPU idle.
 SelPlan selective_plan(int batch, int seqlen, int channels, int ngroups, int dstate) {
-    const int nk = selective_kernel_dstate(dstate), tile = nk < 16 ? 2 * nk : 32;
+    const int nk = selective_kernel_dstate(dstate), tile = 2048 / selective_ch(dstate);
     const long long wgs = (long long)batch * selective_blocks(channels, ngroups, dstate);
     SelPlan p{1, seqlen, 0};
     if (wgs < 512) {
@@ -309,9 +335,13 @@ SelPlan selective_plan(int batch, int seqlen, int channels, int ngroups, int dst
             p.segs = (seqlen + p.seg_len - 1) / p.seg_len;
         }
     }
-    if (p.segs <= 1) return SelPlan{1, seqlen, 0};
-    p.scratch_bytes = (size_t)batch * (p.segs - 1) * channels * (nk + 1) * sizeof(float);
+    if (p.segs <= 1) p = SelPlan{1, seqlen, 0};
+    p.seg_floats = (size_t)batch * (p.segs - 1) * channels * nk;
     return p;
+}
+
+size_t selective_bc_floats(int batch, int seqlen, int ngroups, int dstate) {
+    return (size_t)batch * ngroups * sel_padded(seqlen) * 2 * selective_kernel_dstate(dstate);
 }
 
 hipError_t launch_selective_fwd(const SelArgs &a, bool bf16, hipStream_t stream) {

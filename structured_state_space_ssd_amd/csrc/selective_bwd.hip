@@ -6,18 +6,19 @@
 //   dz_t = dy'_t (sum_n C_t h_t + D x_t) silu'(z_t),  ddt then through softplus and clamp.
 //
 // States are recomputed, not stored by the forward: a first walk (the
-// forward's, SEL_KEEP) keeps the state before every 16 tokens (8 at small
-// state sizes), and the walk back rebuilds a tile's 16 states in registers from there,
-// with their decays, then runs the adjoint over them. As in the forward a lane
-// holds 4 states of one channel. Bound by vector issue: about 25 slots per
-// element, of which the rebuilding takes 7.
+// forward's, SEL_KEEP) keeps the state before every 16 tokens (4 or 8 at other
+// state sizes), and the walk back rebuilds a tile's states in registers from
+// there, with their decays, then runs the adjoint over them. Channels and
+// states lie over lanes and wavefronts as in the forward. Bound by vector
+// issue, of which the rebuilding is a quarter.
 //
-// Sums over channels (dB, dC): per token a wavefront adds its channels' eight
-// values by exchanging halves and rows of lanes between two registers (each
-// exchange and addition halves the number of values as it doubles the lanes
-// summed), then within the rows of 16 lanes; wavefronts meet in LDS, and
-// workgroups in partial tensors that are added in a fixed order. Sums over
-// tokens (dA, dD, the bias) stay in registers and end in partial rows the same way.
+// Sums over channels (dB, dC) are sums over lanes, of eight values per token
+// and four states: each wavefront lays them out in LDS, value by value, and
+// reads them back with eight lanes to a value and eight channels to a lane;
+// seven additions and three DPP steps end the sum, where a butterfly over 64
+// lanes in registers takes 26 instructions. Workgroups meet in partial tensors
+// that are added in a fixed order. Sums over tokens (dA, dD, the bias) stay in
+// registers and end in partial rows the same way.
 //
 // With segments (see the forward) every segment's adjoint from zero is made
 // first, and a walk starts by folding the segments after its own.
@@ -27,196 +28,207 @@ namespace ssd {
 
 namespace {
 
-// a's and b's halves (or odd and even rows of 16 lanes) exchanged and added:
-// lower half (even rows): a summed over both, upper half (odd rows): b.
-__device__ __forceinline__ float fold32(float a, float b) {
-    typedef unsigned u2 __attribute__((ext_vector_type(2)));
-    const u2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-__device__ __forceinline__ float fold16(float a, float b) {
-    typedef unsigned u2 __attribute__((ext_vector_type(2)));
-    const u2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-// Sum over the lanes of a row of 16 that share lane % SL, in each of them.
-template <int SL> __device__ __forceinline__ float row_fold(float v) {
-    auto add = [](float a, int b) { return a + __int_as_float(b); };
-    if constexpr (SL <= 8) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xf, 0xf, true));
-    if constexpr (SL <= 4) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xf, 0xf, true));
-    if constexpr (SL <= 2) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x122, 0xf, 0xf, true));
-    if constexpr (SL <= 1) v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x121, 0xf, 0xf, true));
-    return v;
-}
-
-__device__ __forceinline__ float4 f4(const float (&v)[4]) { return make_float4(v[0], v[1], v[2], v[3]); }
-
 // A segment's adjoint from zero (from dfinal for the last one): the gradient
 // of the state entering it, for segments 1 .. segs - 1.
 template <typename T, int NK>
-__global__ __launch_bounds__(256) void selective_adj_kernel(SelBwdArgs ba) {
-    using S = SelShape<NK>;
-    constexpr int SL = S::SL, CH = S::CH, TILE = S::TILE;
+__global__ __launch_bounds__((SelShape<NK, true>::THREADS)) void selective_adj_kernel(SelBwdArgs ba) {
+    using S = SelShape<NK, true>;
+    constexpr int NS = S::NS, WS = S::WS, CH = S::CH, TILE = S::TILE, THREADS = S::THREADS;
     constexpr int V = sizeof(T) == 2 ? 8 : 4;
-    constexpr int VPR = CH / V, IT = (TILE * VPR + 255) / 256, IB = (TILE * NK + 255) / 256;
+    constexpr int VPR = CH / V, IT = (TILE * VPR + THREADS - 1) / THREADS, U = 8;
     __shared__ float2 dd[TILE * CH];  // (dt, dy)
-    __shared__ __attribute__((aligned(16))) float cs[TILE * NK];
     const SelArgs &a = ba.f;
-    SelBlock k = sel_block<NK>(blockIdx.x, a.channels, a.ngroups, a.segs - 1);
+    SelBlock k = sel_block<CH>(blockIdx.x, a.channels, a.ngroups, a.segs - 1);
     k.seg += 1;
-    const int tid = threadIdx.x, sl = tid & (SL - 1), ch = tid / SL, n0 = sl * 4;
-    const int N = a.dstate, E = a.channels, nn = ch < k.n ? N - n0 : 0;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ws = w % WS, ch = w / WS * 64 + (tid & 63), n0 = ws * NS;
+    const int N = a.dstate, E = a.channels;
+    // this lane's states of scratch row `at`
+    auto seg_at = [&](size_t at) { return (at * (NK / 4) + n0 / 4) * E * 4 + (size_t)(k.first + ch) * 4; };
+    const bool live = ch < k.n;
+    const int nn = live ? N - n0 : 0;
     const int t_begin = k.seg * a.seg_len, t_end = min(a.seqlen, t_begin + a.seg_len);
     const T *dt = static_cast<const T *>(a.dt) + k.b * a.dt_batch + k.first;
     const T *z = a.z ? static_cast<const T *>(a.z) + k.b * a.z_batch + k.first : nullptr;
-    const T *C = static_cast<const T *>(a.C) + k.b * a.C_batch + (size_t)k.g * N;
     const T *dy = static_cast<const T *>(ba.dy) + (size_t)k.b * a.seqlen * E + k.first;
-    float A2[4], g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    sel_const *const bc = (sel_const *)(a.bc + (size_t)(k.b * a.ngroups + k.g) * sel_padded(a.seqlen) * 2 * NK +
+                                  ws * 2 * NS);
+    float A2[NS], g[NS];
+    load_rates(a.A + (size_t)(k.first + ch) * N + n0, nn, A2);
     {
-        RowRaw<float, 4> r;
-        r.zero();
-        if (nn > 0) r.load(a.A + (size_t)(k.first + ch) * N + n0, nn);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) A2[i] = r.get(i) * kLog2e;
+        RowRaw<float, NS> r;
         r.zero();
         if (nn > 0 && ba.dfinal && k.seg == a.segs - 1)
             r.load(ba.dfinal + ((size_t)k.b * E + k.first + ch) * N + n0, nn);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) g[i] = r.get(i);
+        for (int i = 0; i < NS; ++i) g[i] = r.get(i);
     }
-    const int tiles = (t_end - t_begin + TILE - 1) / TILE;
-    for (int ti = tiles - 1; ti >= 0; --ti) {
-        const int t0 = t_begin + ti * TILE, nt = min(TILE, t_end - t0);
+    RowRaw<float, V> bias;
+    bias.zero();
+    if (const int c = (tid % VPR) * V; a.opts.bias && c < k.n) bias.load(a.opts.bias + k.first + c, k.n - c);
+    RowRaw<T, V> dr[2][IT], zr[2][IT], yr[2][IT];
+    auto fetch = [&](int t0, int p) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int id = tid + i * 256, r = id / VPR, c = (id % VPR) * V;
-            if (r < nt && c < k.n) {
-                RowRaw<T, V> dr, zr, yr;
+            const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
+            dr[p][i].zero();
+            zr[p][i].zero();
+            yr[p][i].zero();
+            if (r < TILE && t0 + r < t_end && c < k.n) {
                 const size_t t = t0 + r;
-                dr.load(dt + t * a.dt_token + c, k.n - c);
-                yr.load(dy + t * E + c, k.n - c);
-                if (z) zr.load(z + t * a.z_token + c, k.n - c);
+                dr[p][i].load(dt + t * a.dt_token + c, k.n - c);
+                yr[p][i].load(dy + t * E + c, k.n - c);
+                if (z) zr[p][i].load(z + t * a.z_token + c, k.n - c);
+            }
+        }
+    };
+    auto tile = [&](int t0, int p) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
+            const bool in = t0 + r < t_end;  // rows past the end leave the adjoint as it is
+            if (r < TILE) {
+                float d[V], y[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float b = a.opts.bias && c + e < k.n ? a.opts.bias[k.first + c + e] : 0.0f;
-                    const float w = z ? silu_f32(zr.get(e)) : 1.0f;
-                    dd[r * CH + c + e] = make_float2(sel_step(a.opts, dr.get(e) + b), yr.get(e) * w);
+                    d[e] = dr[p][i].get(e) + bias.get(e);
+                    y[e] = yr[p][i].get(e);
+                }
+                sel_steps(a.opts, d, in);
+                if (z)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) y[e] *= silu_f32(zr[p][i].get(e));
+#pragma unroll
+                for (int e = 0; e < V; ++e) dd[r * CH + c + e] = make_float2(d[e], y[e]);
+            }
+        }
+        __syncthreads();
+        if (t0 - TILE >= t_begin) fetch(t0 - TILE, p ^ 1);
+        const int last = (min(TILE, t_end - t0) - 1) / U * U;
+        for (int tb = last; tb >= 0; tb -= U) {
+            sel_const *q = bc + (size_t)(t0 + tb) * (NK / 4);
+#pragma unroll
+            for (int u = U - 1; u >= 0; --u) {
+                const float2 d = dd[(tb + u) * CH + ch];
+#pragma unroll
+                for (int j = 0; j < NS; j += 4) {
+                    const SelBC v = q[u * (NK / 4) + j / 4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        g[j + i] = __builtin_amdgcn_exp2f(d.x * A2[j + i]) * fmaf(d.y, v[4 + i], g[j + i]);
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < IB; ++i) {
-            const int id = tid + i * 256, r = id / NK, n = id % NK;
-            if (r < nt) cs[id] = n < N ? to_f32(C[(size_t)(t0 + r) * a.C_token + n]) : 0.0f;
-        }
         __syncthreads();
-        if (nn > 0)
-#pragma unroll 4
-            for (int t = nt - 1; t >= 0; --t) {
-                const float2 d = dd[t * CH + ch];
-                const float4 c4 = *reinterpret_cast<const float4 *>(&cs[t * NK + n0]);
-                const float cv[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    g[i] = __builtin_amdgcn_exp2f(d.x * A2[i]) * fmaf(d.y, cv[i], g[i]);
-            }
-        __syncthreads();
+    };
+    int t0 = t_begin + (t_end - t_begin - 1) / TILE * TILE;
+    fetch(t0, 0);
+    for (; t0 >= t_begin; t0 -= 2 * TILE) {
+        tile(t0, 0);
+        if (t0 - TILE >= t_begin) tile(t0 - TILE, 1);
     }
-    if (nn > 0)
-        *reinterpret_cast<float4 *>(
-            ba.seg_adj + (((size_t)k.b * (a.segs - 1) + k.seg - 1) * E + k.first + ch) * NK + n0) = f4(g);
+    if (live) {
+        const size_t at = (size_t)k.b * (a.segs - 1) + k.seg - 1;
+        lane_store(ba.seg_adj + seg_at(at), E, g);
+    }
 }
 
+// Tokens of a row of dbc_part, and the rows a sequence and group take: every
+// row holds 64 values per four states, dB of each state for 8 tokens, then dC.
+template <int NK> constexpr int sel_row_tokens() { return sel_keep<NK>() < 8 ? sel_keep<NK>() : 8; }
+
 template <typename T, int NK, bool GATE>
-__global__ __launch_bounds__(256, 2) void selective_bwd_kernel(SelBwdArgs ba) {
-    using S = SelShape<NK>;
-    constexpr int SL = S::SL, CH = S::CH, TB = S::BACK, V = 4;
-    constexpr int VPR = CH / V, IT = (TB * VPR + 255) / 256, IB = (TB * NK + 255) / 256;
-    __shared__ float2 du[TB * CH];  // (dt, dt x); after the walk back sum_n (g B), sum_n (A2 g q)
-    __shared__ float dys[TB * CH];  // dy silu(z)
-    __shared__ float ys[GATE ? TB * CH : 1];
-    __shared__ __attribute__((aligned(16))) float bs[TB * NK];
-    __shared__ __attribute__((aligned(16))) float cs[TB * NK];
-    // dB and dC of every wavefront; after the last tile every lane's dD and bias sums
-    constexpr int RED = 4 * TB * 2 * NK, ACC = 2 * 256 * V;
-    __shared__ __attribute__((aligned(16))) float red[RED > ACC ? RED : ACC];
+__global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bwd_kernel(SelBwdArgs ba) {
+    using S = SelShape<NK, true>;
+    constexpr int NS = S::NS, WS = S::WS, CH = S::CH, THREADS = S::THREADS, TB = sel_keep<NK>(), V = 4;
+    constexpr int VPR = CH / V, IT = (TB * VPR + THREADS - 1) / THREADS, TOK = sel_row_tokens<NK>();
+    __shared__ float2 du[TB * CH];        // (dt, dt x)
+    __shared__ float dys[TB * CH];        // dy silu(z)
+    __shared__ float2 pg[WS * TB * CH];   // each wavefront's sum_n (g B), sum_n (A2 g q)
+    __shared__ float py[GATE ? WS * TB * CH : 1];  // and sum_n (C h)
+    // each wavefront's eight values by 64 channels, twice; after the last tile every
+    // lane's dD and bias sums
+    __shared__ __attribute__((aligned(16))) float tr[THREADS / 64 * 2 * 8 * 64];
 
     const SelArgs &a = ba.f;
-    const SelBlock k = sel_block<NK>(blockIdx.x, a.channels, a.ngroups, a.segs);
-    const int tid = threadIdx.x, sl = tid & (SL - 1), ch = tid / SL, n0 = sl * 4;
-    const int w = tid >> 6, row16 = (tid >> 4) & 3;
+    const SelBlock k = sel_block<CH>(blockIdx.x, a.channels, a.ngroups, a.segs);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ws = w % WS, ch = w / WS * 64 + lane, n0 = ws * NS;
     const int N = a.dstate, E = a.channels, L = a.seqlen;
+    // this lane's states of scratch row `at`
+    auto seg_at = [&](size_t at) { return (at * (NK / 4) + n0 / 4) * E * 4 + (size_t)(k.first + ch) * 4; };
     const bool live = ch < k.n;
     const int nn = live ? N - n0 : 0;
     const int t_begin = k.seg * a.seg_len, t_end = min(L, t_begin + a.seg_len);
     const T *x = static_cast<const T *>(a.x) + k.b * a.x_batch + k.first;
     const T *dt = static_cast<const T *>(a.dt) + k.b * a.dt_batch + k.first;
     const T *z = GATE ? static_cast<const T *>(a.z) + k.b * a.z_batch + k.first : nullptr;
-    const T *B = static_cast<const T *>(a.B) + k.b * a.B_batch + (size_t)k.g * N;
-    const T *C = static_cast<const T *>(a.C) + k.b * a.C_batch + (size_t)k.g * N;
     const T *dy = static_cast<const T *>(ba.dy) + (size_t)k.b * L * E + k.first;
+    sel_const *const bc = (sel_const *)(a.bc + (size_t)(k.b * a.ngroups + k.g) * sel_padded(L) * 2 * NK +
+                                  ws * 2 * NS);
 
-    float A2[4], h_in[4] = {0.0f, 0.0f, 0.0f, 0.0f}, ag[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float dA[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float A2[NS], h_in[NS], ag[NS], dA[NS];
+    load_rates(a.A + (size_t)(k.first + ch) * N + n0, nn, A2);
     {
-        RowRaw<float, 4> r;
+        RowRaw<float, NS> r;
         r.zero();
-        if (nn > 0) r.load(a.A + (size_t)(k.first + ch) * N + n0, nn);
+        if (k.seg == a.segs - 1 && ba.dfinal && nn > 0)
+            r.load(ba.dfinal + ((size_t)k.b * E + k.first + ch) * N + n0, nn);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) A2[i] = r.get(i) * kLog2e;
+        for (int i = 0; i < NS; ++i) {
+            ag[i] = r.get(i);
+            h_in[i] = dA[i] = 0.0f;
+        }
     }
     if (live) {
-        const size_t at = (size_t)k.b * (a.segs - 1) * E + k.first + ch;
+        const size_t at = (size_t)k.b * (a.segs - 1);
+        float v[NS];
         for (int s = 0; s < k.seg; ++s) {
-            const float sum = a.seg_sum[at + (size_t)s * E];
-            const float4 st = *reinterpret_cast<const float4 *>(a.seg_state + (at + (size_t)s * E) * NK + n0);
-            const float v[4] = {st.x, st.y, st.z, st.w};
+            const float sum = a.seg_sum[(at + s) * E + k.first + ch];
+            lane_load(a.seg_state + seg_at(at + s), E, v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < NS; ++i)
                 h_in[i] = s == 0 ? v[i] : fmaf(__builtin_amdgcn_exp2f(A2[i] * sum), h_in[i], v[i]);
-        }
-        if (k.seg == a.segs - 1) {
-            RowRaw<float, 4> r;
-            r.zero();
-            if (ba.dfinal && nn > 0) r.load(ba.dfinal + ((size_t)k.b * E + k.first + ch) * N + n0, nn);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ag[i] = r.get(i);
         }
         for (int s = a.segs - 1; s > k.seg; --s) {
             // the gradient of the state entering segment s
-            const float4 st = *reinterpret_cast<const float4 *>(ba.seg_adj + (at + (size_t)(s - 1) * E) * NK + n0);
-            const float v[4] = {st.x, st.y, st.z, st.w};
-            const float sum = s < a.segs - 1 ? a.seg_sum[at + (size_t)s * E] : 0.0f;
+            const float sum = s < a.segs - 1 ? a.seg_sum[(at + s) * E + k.first + ch] : 0.0f;
+            lane_load(ba.seg_adj + seg_at(at + s - 1), E, v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < NS; ++i)
                 ag[i] = s == a.segs - 1 ? v[i] : fmaf(__builtin_amdgcn_exp2f(A2[i] * sum), ag[i], v[i]);
         }
     }
 
-    float bias[IT][V], Dv[IT][V], dD[IT][V], db[IT][V];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int c = ((tid + i * 256) % VPR) * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            bias[i][e] = a.opts.bias && c + e < k.n ? a.opts.bias[k.first + c + e] : 0.0f;
-            Dv[i][e] = a.D && c + e < k.n ? a.D[k.first + c + e] : 0.0f;
-            dD[i][e] = db[i][e] = 0.0f;
-        }
+    RowRaw<float, V> bias, Dv;
+    float dD[V], db[V];
+    bias.zero();
+    Dv.zero();
+    if (const int c = (tid % VPR) * V; c < k.n) {
+        if (a.opts.bias) bias.load(a.opts.bias + k.first + c, k.n - c);
+        if (a.D) Dv.load(a.D + k.first + c, k.n - c);
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) dD[e] = db[e] = 0.0f;
+    // this wavefront's rows of dbc_part
+    const int part = k.block * (CH / 64) + w / WS;
+    float *rows = ba.dbc_part + (((size_t)part * a.batch + k.b) * a.ngroups + k.g) *
+                                    ((L + TOK - 1) / TOK) * (NK / 4) * 64;
 
-    const int tiles = (t_end - t_begin + TB - 1) / TB;
-    for (int ti = tiles - 1; ti >= 0; --ti) {
-        const int t0 = t_begin + ti * TB, nt = min(TB, t_end - t0);
-        RowRaw<T, V> xr[IT], zr[IT], yr[IT], dr[IT];
+    // A tile's rows and the state before it. The next tile's are fetched when the walk
+    // over a tile is done and its registers are free, and arrive while it is finished.
+    RowRaw<T, V> xr[IT], zr[IT], yr[IT], dr[IT];
+    float hk[NS], hsum = 0.0f;
+    auto fetch = [&](int t0, RowRaw<T, V>(&xr)[IT], RowRaw<T, V>(&dr)[IT], RowRaw<T, V>(&zr)[IT],
+                     RowRaw<T, V>(&yr)[IT]) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int id = tid + i * 256, r = id / VPR, c = (id % VPR) * V;
+            const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
             xr[i].zero();
             dr[i].zero();
             zr[i].zero();
             yr[i].zero();
-            if (r < nt && c < k.n) {
+            if (r < TB && t0 + r < t_end && c < k.n) {
                 const size_t t = t0 + r;
                 xr[i].load(x + t * a.x_token + c, k.n - c);
                 dr[i].load(dt + t * a.dt_token + c, k.n - c);
@@ -225,145 +237,185 @@ __global__ __launch_bounds__(256, 2) void selective_bwd_kernel(SelBwdArgs ba) {
             }
         }
 #pragma unroll
-        for (int i = 0; i < IB; ++i) {
-            const int id = tid + i * 256, r = id / NK, n = id % NK;
-            if (r < TB) {
-                const bool ok = r < nt && n < N;
-                bs[id] = ok ? to_f32(B[(size_t)(t0 + r) * a.B_token + n]) : 0.0f;
-                cs[id] = ok ? to_f32(C[(size_t)(t0 + r) * a.C_token + n]) : 0.0f;
-            }
-        }
-        float hk[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // the state entering the tile
+        for (int i = 0; i < NS; ++i) hk[i] = 0.0f;
         if (live) {
-            const size_t at = ((size_t)k.b * a.keeps + t0 / TB) * E + k.first + ch;
-            const float4 st = *reinterpret_cast<const float4 *>(a.keep_state + at * NK + n0);
-            const float v[4] = {st.x, st.y, st.z, st.w};
-            const float sum = k.seg ? a.keep_sum[at] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                hk[i] = k.seg ? fmaf(__builtin_amdgcn_exp2f(A2[i] * sum), h_in[i], v[i]) : v[i];
+            const size_t at = (size_t)k.b * a.keeps + t0 / TB;
+            lane_load(a.keep_state + seg_at(at), E, hk);
+            if (k.seg) hsum = a.keep_sum[at * E + k.first + ch];
         }
-        float delta[IT][V], dyg[IT][V];
+    };
+    int t0 = t_begin + (t_end - t_begin - 1) / TB * TB;
+    fetch(t0, xr, dr, zr, yr);
+    for (; t0 >= t_begin; t0 -= TB) {
+        const int nt = min(TB, t_end - t0);
+        if (k.seg)
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                hk[i] = fmaf(__builtin_amdgcn_exp2f(A2[i] * hsum), h_in[i], hk[i]);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int id = tid + i * 256, r = id / VPR, c = (id % VPR) * V;
+            const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
+            if (r < TB) {
+                float d[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                // rows past the end neither move the state nor take a gradient
-                delta[i][e] = r < nt ? sel_step(a.opts, dr[i].get(e) + bias[i][e]) : 0.0f;
-                dyg[i][e] = yr[i].get(e);
-                if (GATE) dyg[i][e] *= silu_f32(zr[i].get(e));
-                if (r < TB) {
-                    du[r * CH + c + e] = make_float2(delta[i][e], delta[i][e] * xr[i].get(e));
-                    dys[r * CH + c + e] = dyg[i][e];
-                }
-            }
-        }
-        __syncthreads();
-
-        float h[TB][4], dec[TB][4];
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            // LDS reads of at most two tokens ahead: more would not fit the registers
-            if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);
-            const float2 d = du[t * CH + ch];
-            const float4 b4 = *reinterpret_cast<const float4 *>(&bs[t * NK + n0]);
-            const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dec[t][i] = __builtin_amdgcn_exp2f(d.x * A2[i]);
-                h[t][i] = fmaf(dec[t][i], t ? h[t - 1][i] : hk[i], d.y * bv[i]);
-            }
-            if constexpr (GATE) {
-                const float4 c4 = *reinterpret_cast<const float4 *>(&cs[t * NK + n0]);
-                float p = c4.x * h[t][0];
-                p = fmaf(c4.y, h[t][1], p);
-                p = fmaf(c4.z, h[t][2], p);
-                p = fmaf(c4.w, h[t][3], p);
-                p = lanes_sum<SL>(p);
-                if (sl == 0) ys[t * CH + ch] = p;
-            }
-        }
-#pragma unroll
-        for (int t = TB - 1; t >= 0; --t) {
-            if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);
-            const float2 d = du[t * CH + ch];
-            const float dyv = dys[t * CH + ch];
-            const float4 b4 = *reinterpret_cast<const float4 *>(&bs[t * NK + n0]);
-            const float4 c4 = *reinterpret_cast<const float4 *>(&cs[t * NK + n0]);
-            const float bv[4] = {b4.x, b4.y, b4.z, b4.w}, cv[4] = {c4.x, c4.y, c4.z, c4.w};
-            float gB = 0.0f, gA = 0.0f, v[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float g = fmaf(dyv, cv[i], ag[i]);
-                gB = fmaf(g, bv[i], gB);
-                const float gq = g * (dec[t][i] * (t ? h[t - 1][i] : hk[i]));
-                gA = fmaf(A2[i], gq, gA);
-                dA[i] = fmaf(d.x, gq, dA[i]);
-                ag[i] = dec[t][i] * g;
-                v[i] = d.y * g;
-                v[4 + i] = dyv * h[t][i];
-            }
-            gB = lanes_sum<SL>(gB);
-            gA = lanes_sum<SL>(gA);
-            // every lane of the channel has read du[t] (they are of one wavefront)
-            if (sl == 0) du[t * CH + ch] = make_float2(gB, gA);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = fold32(v[i], v[4 + i]);
-            float q0 = row_fold<SL>(fold16(v[0], v[2])), q1 = row_fold<SL>(fold16(v[1], v[3]));
-            // row 0: dB of states n0, n0 + 1; row 1: n0 + 2, n0 + 3; rows 2, 3: dC
-            if ((tid & 15) < SL) {
-                float *p = &red[((w * TB + t) * 2 + (row16 >> 1)) * NK + n0 + 2 * (row16 & 1)];
-                *reinterpret_cast<float2 *>(p) = make_float2(q0, q1);
-            }
-        }
-        __syncthreads();
-
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int id = tid + i * 256, r = id / VPR, c = (id % VPR) * V;
-            if (r < nt && c < k.n) {
-                float ox[V], ot[V], oz[V];
+                for (int e = 0; e < V; ++e) d[e] = dr[i].get(e) + bias.get(e);
+                sel_steps(a.opts, d, r < nt);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float2 s = du[r * CH + c + e];
-                    const float xv = xr[i].get(e), raw = dr[i].get(e) + bias[i][e];
-                    ox[e] = fmaf(delta[i][e], s.x, Dv[i][e] * dyg[i][e]);
-                    float dd = fmaf(xv, s.x, s.y * 0.6931471805599453f);
-                    if (a.opts.clamp) {
-                        const float free = a.opts.softplus ? softplus_f32(raw) : raw;
-                        if (free < a.opts.lo || free > a.opts.hi) dd = 0.0f;
-                    }
-                    if (a.opts.softplus) dd *= sigmoid_f32(raw);
-                    ot[e] = dd;
-                    if (c + e < k.n) {
-                        dD[i][e] = fmaf(dyg[i][e], xv, dD[i][e]);
-                        db[i][e] += dd;
-                    }
-                    if constexpr (GATE)
-                        oz[e] = yr[i].get(e) * fmaf(Dv[i][e], xv, ys[r * CH + c + e]) *
-                                silu_grad_f32(zr[i].get(e));
+                    du[r * CH + c + e] = make_float2(d[e], d[e] * xr[i].get(e));
+                    dys[r * CH + c + e] = GATE ? yr[i].get(e) * silu_f32(zr[i].get(e)) : yr[i].get(e);
                 }
+            }
+        }
+        __syncthreads();
+
+        // B and C of GR tokens at a time, the next ones on their way while these are used
+        constexpr int GR = NS == 4 ? 2 : 1;
+        sel_const *q = bc + (size_t)t0 * (NK / 4);
+        SelBC bcv[2][GR][NS / 4];
+        auto scalars = [&](int t, int s) {
+#pragma unroll
+            for (int u = 0; u < GR; ++u)
+#pragma unroll
+                for (int i = 0; i < NS / 4; ++i) bcv[s][u][i] = q[(t + u) * (NK / 4) + i];
+        };
+        float h[TB][NS], dec[TB][NS], res[NS / 4];
+        scalars(0, 0);
+#pragma unroll
+        for (int tg = 0; tg < TB; tg += GR) {
+            const int s = tg / GR % 2;
+            // (the last group's serve the walk back as well)
+            if (tg + GR < TB) scalars(tg + GR, s ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < GR; ++u) {
+                const int t = tg + u;
+                const float2 d = du[t * CH + ch];
+                float y = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    dec[t][i] = __builtin_amdgcn_exp2f(d.x * A2[i]);
+                    h[t][i] = fmaf(dec[t][i], t ? h[t - 1][i] : hk[i], d.y * bcv[s][u][i / 4][i % 4]);
+                    if constexpr (GATE) y = fmaf(bcv[s][u][i / 4][4 + i % 4], h[t][i], y);
+                }
+                if constexpr (GATE) py[(ws * TB + t) * CH + ch] = y;
+            }
+        }
+        // a wavefront's eight sums of a token and four states, from its 2 KB of products
+        float *const mine = &tr[w * 1024];
+        const int from = (lane >> 3) * 64 + (lane & 7) * 4;
+        float4 r0, r1;
+        auto sums_load = [&](int buf) {
+            __builtin_amdgcn_wave_barrier();
+            r0 = *reinterpret_cast<const float4 *>(&mine[buf * 512 + from]);
+            r1 = *reinterpret_cast<const float4 *>(&mine[buf * 512 + from + 32]);
+            __builtin_amdgcn_wave_barrier();
+        };
+        auto sums_end = [&](int t, int s4) {
+            float sum = ((r0.x + r0.y) + (r0.z + r0.w)) + ((r1.x + r1.y) + (r1.z + r1.w));
+            auto add = [](float v, int o) { return v + __int_as_float(o); };
+            sum = add(sum, __builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0xB1, 0xf, 0xf, true));
+            sum = add(sum, __builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x4E, 0xf, 0xf, true));
+            sum = add(sum, __builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x141, 0xf, 0xf, true));
+            // lane 8 v + u keeps value v of the row's u-th token
+            if (t % TOK == TOK - 1) res[s4] = sum;
+            else res[s4] = (lane & 7) == t % TOK ? sum : res[s4];
+            if (t % TOK == 0 && t < nt)  // nt: rows past the sequence's are another's
+                rows[((size_t)(t0 + t) / TOK * (NK / 4) + n0 / 4 + s4) * 64 + lane] = res[s4];
+        };
+#pragma unroll
+        for (int tg = TB - GR; tg >= 0; tg -= GR) {
+            const int s = tg / GR % 2;
+            if (tg) scalars(tg - GR, s ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = GR - 1; u >= 0; --u) {
+                const int t = tg + u;
+                const float2 d = du[t * CH + ch];
+                const float dyv = dys[t * CH + ch];
+                float gB = 0.0f, gA = 0.0f;
+#pragma unroll
+                for (int s4 = 0; s4 < NS / 4; ++s4) {
+                    // a set of products is summed while the next one is made
+                    const int step = (TB - 1 - t) * (NS / 4) + s4;
+                    if (step) sums_load((step - 1) % 2);
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int i = s4 * 4 + j;
+                        const float g = fmaf(dyv, bcv[s][u][i / 4][4 + i % 4], ag[i]);
+                        gB = fmaf(g, bcv[s][u][i / 4][i % 4], gB);
+                        const float gq = g * (dec[t][i] * (t ? h[t - 1][i] : hk[i]));
+                        gA = fmaf(A2[i], gq, gA);
+                        dA[i] = fmaf(d.x, gq, dA[i]);
+                        ag[i] = dec[t][i] * g;
+                        v[j] = d.y * g;
+                        v[4 + j] = dyv * h[t][i];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) mine[step % 2 * 512 + j * 64 + lane] = v[j];
+                    if (step) sums_end(s4 ? t : t + 1, s4 ? s4 - 1 : NS / 4 - 1);
+                }
+                pg[(ws * TB + t) * CH + ch] = make_float2(gB, gA);
+            }
+        }
+        sums_load((TB * (NS / 4) - 1) % 2);
+        sums_end(0, NS / 4 - 1);
+        RowRaw<T, V> xn[IT], zn[IT], yn[IT], dn[IT];
+        if (t0 > t_begin) fetch(t0 - TB, xn, dn, zn, yn);
+        __syncthreads();
+
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
+            if (r < nt && c < k.n) {
+                float ox[V], ot[V], oz[V], raws[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const int at = r * CH + c + e;
+                    float sB = pg[at].x, sA = pg[at].y;
+#pragma unroll
+                    for (int j = 1; j < WS; ++j) {
+                        sB += pg[j * TB * CH + at].x;
+                        sA += pg[j * TB * CH + at].y;
+                    }
+                    const float xv = xr[i].get(e), raw = dr[i].get(e) + bias.get(e), dyg = dys[at];
+                    ox[e] = fmaf(du[at].x, sB, Dv.get(e) * dyg);
+                    raws[e] = raw;
+                    ot[e] = fmaf(xv, sB, sA * 0.6931471805599453f);
+                    dD[e] = fmaf(dyg, xv, dD[e]);  // zero past the last channel
+                    if constexpr (GATE) {
+                        float y = py[at];
+#pragma unroll
+                        for (int j = 1; j < WS; ++j) y += py[j * TB * CH + at];
+                        oz[e] = yr[i].get(e) * fmaf(Dv.get(e), xv, y) * silu_grad_f32(zr[i].get(e));
+                    }
+                }
+                if (a.opts.clamp)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float free = a.opts.softplus ? softplus_f32(raws[e]) : raws[e];
+                        if (free < a.opts.lo || free > a.opts.hi) ot[e] = 0.0f;
+                    }
+                if (a.opts.softplus)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) ot[e] *= sigmoid_f32(raws[e]);
+#pragma unroll
+                for (int e = 0; e < V; ++e) db[e] += ot[e];
                 const size_t o = ((size_t)k.b * L + t0 + r) * E + k.first + c;
                 row_store(static_cast<T *>(ba.dx) + o, ox, k.n - c);
                 row_store(static_cast<T *>(ba.ddt) + o, ot, k.n - c);
                 if constexpr (GATE) row_store(static_cast<T *>(ba.dz) + o, oz, k.n - c);
             }
         }
-        // the wavefronts' dB and dC, to this workgroup's partial tensors
-        const int each = E / a.ngroups, part = (k.first - k.g * each) / CH;
-        const size_t count = (size_t)a.batch * L * a.ngroups * N;
-        for (int id = tid; id < nt * 2 * NK; id += 256) {
-            const int t = id / (2 * NK), m = (id / NK) & 1, n = id % NK;
-            if (n < N) {
-                float s = 0.0f;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) s += red[(u * TB + t) * 2 * NK + m * NK + n];
-                ba.dbc_part[((size_t)part * 2 + m) * count +
-                            (((size_t)k.b * L + t0 + t) * a.ngroups + k.g) * N + n] = s;
-            }
-        }
         __syncthreads();
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            xr[i] = xn[i];
+            dr[i] = dn[i];
+            zr[i] = zn[i];
+            yr[i] = yn[i];
+        }
     }
 
     const size_t unit = (size_t)k.b * a.segs + k.seg;
@@ -372,50 +424,47 @@ __global__ __launch_bounds__(256, 2) void selective_bwd_kernel(SelBwdArgs ba) {
         if (ba.dinit && k.seg == 0)
             row_store(ba.dinit + ((size_t)k.b * E + k.first + ch) * N + n0, ag, nn);
     }
-    // dD and the bias: a channel's sums lie in the 256 / VPR lanes (or IT vectors) of its column
-    float sD[V], sb[V];
+    // dD and the bias: a channel's sums lie in the lanes of its column
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        sD[e] = sb[e] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            sD[e] += dD[i][e];
-            sb[e] += db[i][e];
-        }
-        red[tid * V + e] = sD[e];
-        red[256 * V + tid * V + e] = sb[e];
+        tr[tid * V + e] = dD[e];
+        tr[THREADS * V + tid * V + e] = db[e];
     }
     __syncthreads();
-    for (int c = tid; c < k.n; c += 256) {
+    for (int c = tid; c < k.n; c += THREADS) {
         float s0 = 0.0f, s1 = 0.0f;
-        for (int r = c / V; r < 256; r += VPR) {
-            s0 += red[r * V + c % V];
-            s1 += red[256 * V + r * V + c % V];
+        for (int r = c / V; r < THREADS; r += VPR) {
+            s0 += tr[r * V + c % V];
+            s1 += tr[THREADS * V + r * V + c % V];
         }
         ba.de_part[(unit * 2) * E + k.first + c] = s0;
         ba.de_part[(unit * 2 + 1) * E + k.first + c] = s1;
     }
 }
 
-// out (dB, then dC) = sums over `n` partial tensors of `count` values, four to a lane
-template <typename T>
-__global__ __launch_bounds__(256) void selective_dbc_kernel(const float *__restrict__ part, int n,
-                                                            size_t count, T *__restrict__ dB,
-                                                            T *__restrict__ dC) {
-    const size_t vecs = (count + 3) / 4, id = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= 2 * vecs) return;
-    const int m = id >= vecs;
-    const size_t c = (id - m * vecs) * 4;
-    const int left = count - c < 4 ? static_cast<int>(count - c) : 4;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+// dB and dC: sums of the workgroups' rows, in order; `per` rows' values in one part.
+template <typename T, int NK>
+__global__ __launch_bounds__(256) void selective_dbc_kernel(const float *__restrict__ parts, int n,
+                                                            size_t per, int L, int G, int N,
+                                                            T *__restrict__ dB, T *__restrict__ dC) {
+    constexpr int TOK = sel_row_tokens<NK>();
+    const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= per) return;
+    const int v = (id >> 3) & 7, u = id & 7;
+    const size_t row = id / 64;
+    const int state = static_cast<int>(row % (NK / 4)) * 4 + (v & 3);
+    const size_t at = row / (NK / 4), chunks = (L + TOK - 1) / TOK;
+    const size_t t = at % chunks * TOK + u, bg = at / chunks;
+    if (u >= TOK || t >= (size_t)L || state >= N) return;
+    float s = 0.0f;
 #pragma unroll 8
-    for (int p = 0; p < n; ++p) {
-        RowRaw<float, 4> r;
-        r.load(part + ((size_t)p * 2 + m) * count + c, left);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += r.get(e);
-    }
-    row_store((m ? dC : dB) + c, s, left);
+    for (int p = 0; p < n; ++p) s += parts[p * per + id];
+    (v >> 2 ? dC : dB)[((bg / G * L + t) * G + bg % G) * N + state] = from_f32<T>(s);
+}
+
+template <int NK> size_t sel_dbc_part(int batch, int seqlen, int ngroups) {
+    constexpr int TOK = sel_row_tokens<NK>();
+    return (size_t)batch * ngroups * ((seqlen + TOK - 1) / TOK) * (NK / 4) * 64;
 }
 
 template <typename T, int NK> hipError_t sel_bwd(const SelBwdArgs &ba, hipStream_t stream) {
@@ -425,18 +474,20 @@ template <typename T, int NK> hipError_t sel_bwd(const SelBwdArgs &ba, hipStream
     if (e != hipSuccess) return e;
     if (a.segs > 1) {
         selective_adj_kernel<T, NK>
-            <<<static_cast<unsigned>(blocks * (a.segs - 1) * a.batch), 256, 0, stream>>>(ba);
+            <<<static_cast<unsigned>(blocks * (a.segs - 1) * a.batch), SelShape<NK, true>::THREADS, 0,
+               stream>>>(ba);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     const unsigned grid = static_cast<unsigned>(blocks * a.segs * a.batch);
-    if (a.z) selective_bwd_kernel<T, NK, true><<<grid, 256, 0, stream>>>(ba);
-    else selective_bwd_kernel<T, NK, false><<<grid, 256, 0, stream>>>(ba);
+    if (a.z) selective_bwd_kernel<T, NK, true><<<grid, SelShape<NK, true>::THREADS, 0, stream>>>(ba);
+    else selective_bwd_kernel<T, NK, false><<<grid, SelShape<NK, true>::THREADS, 0, stream>>>(ba);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const size_t count = (size_t)a.batch * a.seqlen * a.ngroups * a.dstate;
-    selective_dbc_kernel<T><<<static_cast<unsigned>((2 * ((count + 3) / 4) + 255) / 256), 256, 0, stream>>>(
-        ba.dbc_part, blocks / a.ngroups, count, static_cast<T *>(ba.dB), static_cast<T *>(ba.dC));
+    const size_t per = sel_dbc_part<NK>(a.batch, a.seqlen, a.ngroups);
+    selective_dbc_kernel<T, NK><<<static_cast<unsigned>((per + 255) / 256), 256, 0, stream>>>(
+        ba.dbc_part, blocks / a.ngroups * (SelShape<NK, true>::CH / 64), per, a.seqlen, a.ngroups, a.dstate,
+        static_cast<T *>(ba.dB), static_cast<T *>(ba.dC));
     e = hipGetLastError();
     const int units = a.batch * a.segs;
     const long long en = (long long)a.channels * a.dstate;
@@ -448,10 +499,32 @@ template <typename T, int NK> hipError_t sel_bwd(const SelBwdArgs &ba, hipStream
 
 }  // namespace
 
-int selective_keep_tokens(int dstate) { return selective_kernel_dstate(dstate) < 16 ? 8 : 16; }
+template <int NK> static size_t sel_dbc_floats(int batch, int seqlen, int ngroups, int blocks) {
+    return sel_dbc_part<NK>(batch, seqlen, ngroups) * (blocks / ngroups) * (SelShape<NK, true>::CH / 64);
+}
 
-// As the forward's: the walks back cost about 32 slots per element with the
-// kept states, a segment's adjoint 7 more.
+size_t selective_dbc_floats(int batch, int seqlen, int channels, int ngroups, int dstate) {
+    const int blocks = selective_blocks(channels, ngroups, dstate);
+    switch (selective_kernel_dstate(dstate)) {
+        case 4: return sel_dbc_floats<4>(batch, seqlen, ngroups, blocks);
+        case 8: return sel_dbc_floats<8>(batch, seqlen, ngroups, blocks);
+        case 16: return sel_dbc_floats<16>(batch, seqlen, ngroups, blocks);
+        case 32: return sel_dbc_floats<32>(batch, seqlen, ngroups, blocks);
+        default: return sel_dbc_floats<64>(batch, seqlen, ngroups, blocks);
+    }
+}
+
+int selective_keep_tokens(int dstate) {
+    switch (selective_kernel_dstate(dstate)) {
+        case 4: return sel_keep<4>();
+        case 8: return sel_keep<8>();
+        case 16: return sel_keep<16>();
+        case 32: return sel_keep<32>();
+        default: return sel_keep<64>();
+    }
+}
+
+// As the forward's: a walk back costs four times a segment's adjoint.
 SelPlan selective_bwd_plan(int batch, int seqlen, int channels, int ngroups, int dstate) {
     return selective_plan(batch, seqlen, channels, ngroups, dstate);
 }

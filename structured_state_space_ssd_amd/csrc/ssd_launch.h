@@ -240,12 +240,13 @@ struct SelArgs {
     DtOpts opts;                      // bias [E]; no zero-order hold
     int batch, seqlen, channels, ngroups, dstate;
     int segs, seg_len;                // segments of the token axis
-    float *seg_state, *seg_sum;       // [Bt][segs - 1][E][NK], [Bt][segs - 1][E]
+    float *bc;                        // B and C as the kernels read them: scratch
+    float *seg_state, *seg_sum;       // [Bt][segs - 1][E * NK], [Bt][segs - 1][E]: scratch
     void *y;                          // [Bt][L][E] dense
     float *final_state;               // [Bt][E][N], nullable
     // the backward's: states before every so many tokens (selective_keep_tokens)
     int keeps;                        // of them per sequence
-    float *keep_state, *keep_sum;     // [Bt][keeps][E][NK], [Bt][keeps][E]
+    float *keep_state, *keep_sum;     // [Bt][keeps][E * NK], [Bt][keeps][E]
 };
 // The state size the kernels hold (4, 8, 16, 32 or 64; 0: not supported) and
 // the workgroups one sequence's channels take.
@@ -253,8 +254,9 @@ int selective_kernel_dstate(int dstate);
 int selective_blocks(int channels, int ngroups, int dstate);
 struct SelPlan {
     int segs, seg_len;
-    size_t scratch_bytes;  // seg_state, then seg_sum
+    size_t seg_floats;  // of seg_state
 };
+size_t selective_bc_floats(int batch, int seqlen, int ngroups, int dstate);
 SelPlan selective_plan(int batch, int seqlen, int channels, int ngroups, int dstate);
 hipError_t launch_selective_fwd(const SelArgs &a, bool bf16, hipStream_t stream);
 // The backward's first pass: fills seg_state, seg_sum, keep_state, keep_sum.
@@ -267,14 +269,15 @@ struct SelBwdArgs {
     SelArgs f;                  // the forward's inputs; y, final_state unused
     const void *dy;             // [Bt][L][E] dense
     const float *dfinal;        // [Bt][E][N], nullable
-    float *seg_adj;             // [Bt][segs - 1][E][NK]: segments 1 .. segs - 1
-    float *dbc_part;            // [workgroups of a group][dB, dC][Bt][L][G][N]
+    float *seg_adj;             // [Bt][segs - 1][E * NK]: segments 1 .. segs - 1
+    float *dbc_part;            // selective_dbc_floats: every workgroup's dB and dC
     float *dA_part;             // [Bt][segs][E][N]
     float *de_part;             // [Bt][segs][dD, dbias][E]
     void *dx, *ddt, *dz, *dB, *dC;
     float *dA, *dD, *ddt_bias, *dinit;  // dD, ddt_bias, dinit nullable
 };
 SelPlan selective_bwd_plan(int batch, int seqlen, int channels, int ngroups, int dstate);
+size_t selective_dbc_floats(int batch, int seqlen, int channels, int ngroups, int dstate);
 hipError_t launch_selective_bwd(const SelBwdArgs &a, bool bf16, hipStream_t stream);
 
 }  // namespace ssd

@@ -15,6 +15,14 @@ typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x2_any __attribute__((ext_vector_type(2), aligned(4)));
 
+// A ragged vector's element count, as a value the compiler cannot know ahead:
+// the comparisons with it are then made where a ragged vector is met instead
+// of being kept, one lane mask each, across the whole loop.
+__device__ __forceinline__ int ragged(int n) {
+    asm volatile("" : "+v"(n));
+    return n;
+}
+
 // V consecutive elements as loaded, still packed.
 template <typename T, int V> struct RowRaw;
 
@@ -28,6 +36,7 @@ template <> struct RowRaw<bf16_t, 8> {
     __device__ __forceinline__ void load(const bf16_t *p, int n) {
         if (n >= 8) return load(p);
         zero();
+        n = ragged(n);
 #pragma unroll
         for (int e = 0; e < 7; ++e)
             if (e < n) w[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
@@ -47,6 +56,7 @@ template <> struct RowRaw<bf16_t, 4> {
     __device__ __forceinline__ void load(const bf16_t *p, int n) {
         if (n >= 4) return load(p);
         zero();
+        n = ragged(n);
 #pragma unroll
         for (int e = 0; e < 3; ++e)
             if (e < n) w[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
@@ -73,12 +83,20 @@ template <int V> struct RowRaw<float, V> {
     __device__ __forceinline__ void load(const float *p, int n) {
         if (n >= V) return load(p);
         zero();
+        n = ragged(n);
 #pragma unroll
         for (int e = 0; e < V - 1; ++e)
             if (e < n) w[e] = p[e];
     }
     __device__ __forceinline__ float get(int e) const { return w[e]; }
 };
+
+// Two values rounded to bf16 (nearest even, one instruction), the first one low.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), b2));
+}
 
 // The first n of V values, rounded to nearest even where T is bf16.
 template <int V> __device__ __forceinline__ void row_store(float *p, const float (&v)[V], int n) {
@@ -87,6 +105,7 @@ template <int V> __device__ __forceinline__ void row_store(float *p, const float
         for (int i = 0; i < V; i += 4)
             *reinterpret_cast<f32x4_any *>(p + i) = f32x4_any{v[i], v[i + 1], v[i + 2], v[i + 3]};
     } else {
+        n = ragged(n);
 #pragma unroll
         for (int e = 0; e < V - 1; ++e)
             if (e < n) p[e] = v[e];
@@ -96,15 +115,14 @@ template <int V> __device__ __forceinline__ void row_store(bf16_t *p, const floa
     static_assert(V == 4 || V == 8, "8 or 16 bytes");
     uint32_t w[V / 2];
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i)
-        w[i] = static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i])) |
-               (static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i + 1])) << 16);
+    for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     if (n >= V) {
         if constexpr (V == 8)
             *reinterpret_cast<u32x4_any *>(p) = u32x4_any{w[0], w[1], w[2], w[3]};
         else
             *reinterpret_cast<u32x2_any *>(p) = u32x2_any{w[0], w[1]};
     } else {
+        n = ragged(n);
 #pragma unroll
         for (int e = 0; e < V - 1; ++e)
             if (e < n) p[e] = static_cast<bf16_t>(w[e >> 1] >> (16 * (e & 1)));
@@ -133,7 +151,8 @@ __device__ __forceinline__ float softplus_f32(float v) {
     const float u = 1.0f + t;
     const float c = t - (u - 1.0f);
     const float l = __builtin_amdgcn_logf(u) * 0.6931471805599453f;
-    return fmaxf(v, 0.0f) + fmaf(c, __builtin_amdgcn_rcpf(u), l);
+    // the larger of v and 0: one instruction where fmaxf first quiets its operands
+    return __builtin_amdgcn_fmed3f(v, 0.0f, __builtin_inff()) + fmaf(c, __builtin_amdgcn_rcpf(u), l);
 }
 
 }  // namespace ssd
