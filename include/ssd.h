@@ -539,9 +539,9 @@ int ssd_conv_step(void *state, const void *x, long long x_batch_stride, const fl
  *   workspace    at least ssd_selective_forward_workspace_size(...) bytes,
  *                256-byte aligned (NULL where that is 0): with few channels the
  *                token axis is cut into segments, whose states it holds.
- * E % G must be 0 (SSD_ERR_SHAPE). A call whose grid would reach 2^24 workgroups
- * (1024 / N channels each, N rounded up to a power of two) returns
- * SSD_ERR_UNSUPPORTED.
+ * E % G must be 0 (SSD_ERR_SHAPE). Token strides of 2^24 elements or more, and
+ * a call whose grid would reach 2^24 workgroups (1024 / N channels each, at
+ * least 64, N rounded up to a power of two), return SSD_ERR_UNSUPPORTED.
  */
 typedef struct {
     /* elements between sequences and between tokens; channels, and the [G][N] of

@@ -67,6 +67,7 @@ int check_norm(long long rows, int width, int dtype) {
 // The stream beside x has x's type or is float32.
 bool stream_dtype_ok(int stream, int dtype) { return stream == dtype || stream == SSD_F32; }
 
+constexpr long long kMaxTokenStride = 1LL << 24;
 // Grids hold fewer than 2^24 workgroups of 256 lanes.
 constexpr long long kMaxBlocks = 1LL << 24;
 
@@ -96,6 +97,9 @@ int selective_args(ssd::SelArgs &a, const void *x, const void *dt, const float *
                             d.B_batch, d.B_token, d.C_batch, d.C_token})
             if (v < 0) return SSD_ERR_SHAPE;
     }
+    // offsets within a tile of tokens are 32 bits of bytes
+    for (long long v : {d.x_token, d.dt_token, d.z_token, d.B_token, d.C_token})
+        if (v >= kMaxTokenStride) return SSD_ERR_UNSUPPORTED;
     a.x_batch = d.x_batch; a.x_token = d.x_token; a.dt_batch = d.dt_batch; a.dt_token = d.dt_token;
     a.z_batch = d.z_batch; a.z_token = d.z_token; a.B_batch = d.B_batch; a.B_token = d.B_token;
     a.C_batch = d.C_batch; a.C_token = d.C_token;
@@ -423,9 +427,9 @@ int ssd_selective_backward(const void *x, const void *dt, const float *A, const 
     b.f.keeps = w.keeps;
     b.f.keep_state = at(w.keep_state);
     b.f.keep_sum = at(w.keep_sum);
-    b.dy = dy;
-    b.dfinal = dfinal_state;
-    b.seg_adj = at(w.seg_adj);
+    b.f.dy = dy;
+    b.f.dfinal = dfinal_state;
+    b.f.seg_adj = at(w.seg_adj);
     b.dbc_part = at(w.dbc);
     b.dA_part = at(w.dA);
     b.de_part = at(w.de);

@@ -91,6 +91,46 @@ template <int NS> __device__ __forceinline__ void lane_store(float *p, int E, co
         *reinterpret_cast<float4 *>(p + (size_t)i * E) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 
+// A row vector's place within a tile, in bytes from the tile's first row: with
+// the tile's address uniform it is the 32-bit offset of the load or store, and
+// no lane computes an address (rows of a tile are at most 32, and token strides
+// below 2^24 elements).
+template <typename T>
+__device__ __forceinline__ uint32_t row_offset(int r, size_t stride, int c) {
+    return (static_cast<uint32_t>(r) * static_cast<uint32_t>(stride) + static_cast<uint32_t>(c)) *
+           static_cast<uint32_t>(sizeof(T));
+}
+template <typename T> __device__ __forceinline__ const T *row_at(const T *tile, uint32_t off) {
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(tile) + off);
+}
+template <typename T> __device__ __forceinline__ T *row_at(T *tile, uint32_t off) {
+    return reinterpret_cast<T *>(reinterpret_cast<char *>(tile) + off);
+}
+
+// The state that n spans of tokens leave one after another: h = state of span
+// 0, then h = exp(sum of span s) h + state of span s. Span s lies s * step rows
+// of [NK / 4][E][4] from `state` (this lane's place in row 0) and of [E] from
+// `sum`; four spans are fetched at a time.
+template <int NK, int NS>
+__device__ __forceinline__ void sel_fold(const float *state, const float *sum, long long step, int E,
+                                         int n, const float (&A2)[NS], float (&h)[NS]) {
+    for (int s0 = 0; s0 < n; s0 += 4) {
+        float v[4][NS], m[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const long long s = s0 + u < n ? s0 + u : n - 1;
+            lane_load(state + s * step * E * NK, E, v[u]);
+            m[u] = s ? sum[s * step * E] : 0.0f;  // the first one's decays nothing here
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (s0 + u < n)
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+                    h[i] = s0 + u == 0 ? v[u][i] : fmaf(__builtin_amdgcn_exp2f(A2[i] * m[u]), h[i], v[u][i]);
+    }
+}
+
 // This lane's decay rates times log2(e), so that a decay is one exp2; states
 // past the state size get 0. -inf becomes the lowest float: the same decay for
 // any step size but zero, which it leaves at 1.

@@ -49,22 +49,28 @@ __global__ __launch_bounds__(256) void selective_bc_kernel(SelArgs a, size_t cou
 }
 
 // What the walk leaves: outputs; a segment's state and step-size sum; or (for
-// the backward) those and, before every BACK tokens, the state from the
-// segment's start (zero, or the first one's initial state) with its step-size sum.
-enum SelMode { SEL_OUT, SEL_STATE, SEL_KEEP };
+// the backward) those and, before every few tokens, the state from the
+// segment's start (zero, or the first one's initial state) with its step-size
+// sum; or all that and the segment's adjoint, the gradient of the state
+// entering it when nothing comes from behind it:
+//   sum_t P_t C_t dy_t + P_T dfinal,  P_t = exp(A (dt_1 + .. + dt_t)),
+// which a walk forward can add up as well, P being a product of the decays
+// that it computes anyway: three more instructions per element, where a walk
+// backward of its own takes five and loads the step sizes again.
+enum SelMode { SEL_OUT, SEL_STATE, SEL_KEEP, SEL_BOTH };
 
 template <typename T, int NK, SelMode MODE>
-__global__ __launch_bounds__((SelShape<NK, MODE == SEL_KEEP>::THREADS)) void selective_fwd_kernel(SelArgs a) {
-    constexpr bool OUT = MODE == SEL_OUT;
-    using S = SelShape<NK, MODE == SEL_KEEP>;
+__global__ __launch_bounds__((SelShape<NK, (MODE >= SEL_KEEP)>::THREADS)) void selective_fwd_kernel(SelArgs a) {
+    constexpr bool OUT = MODE == SEL_OUT, BACK = MODE >= SEL_KEEP, ADJ = MODE == SEL_BOTH;
+    using S = SelShape<NK, BACK>;
     constexpr int NS = S::NS, WS = S::WS, CH = S::CH, TILE = S::TILE, THREADS = S::THREADS;
     constexpr int V = sizeof(T) == 2 ? 8 : 4;
-    constexpr int VPR = CH / V;                   // vectors per row
+    constexpr int VPR = CH / V;                               // vectors per row
     constexpr int IT = (TILE * VPR + THREADS - 1) / THREADS;  // row vectors per lane
     constexpr int KEEP = sel_keep<NK>();
-    constexpr int U = MODE == SEL_KEEP && KEEP < 8 ? KEEP : 8;  // tokens per turn of the inner loop
-    __shared__ float2 du[TILE * CH];              // (dt, dt x)
-    __shared__ float ys[OUT ? WS * TILE * CH : 1];
+    constexpr int U = BACK && KEEP < 8 ? KEEP : 8;            // tokens per turn of the inner loop
+    __shared__ float2 du[TILE * CH];                          // (dt, dt x)
+    __shared__ float ys[OUT ? WS * TILE * CH : ADJ ? TILE * CH : 1];  // parts of y; or dy silu(z)
 
     const int segs = MODE == SEL_STATE ? a.segs - 1 : a.segs;
     const SelBlock k = sel_block<CH>(blockIdx.x, a.channels, a.ngroups, segs);
@@ -72,17 +78,22 @@ __global__ __launch_bounds__((SelShape<NK, MODE == SEL_KEEP>::THREADS)) void sel
     const int ws = w % WS, ch = w / WS * 64 + (tid & 63), n0 = ws * NS;
     const int N = a.dstate, E = a.channels;
     const int t_begin = k.seg * a.seg_len, t_end = min(a.seqlen, t_begin + a.seg_len);
-    const T *x = static_cast<const T *>(a.x) + k.b * a.x_batch + k.first;
-    const T *dt = static_cast<const T *>(a.dt) + k.b * a.dt_batch + k.first;
-    const T *z = a.z ? static_cast<const T *>(a.z) + k.b * a.z_batch + k.first : nullptr;
-    sel_const *const bc = (sel_const *)(a.bc + (size_t)(k.b * a.ngroups + k.g) * sel_padded(a.seqlen) * 2 * NK +
+    const bool gate = (OUT || ADJ) && a.z != nullptr;
+    // rows of the tile at hand
+    const T *x = static_cast<const T *>(a.x) + k.b * a.x_batch + k.first + t_begin * a.x_token;
+    const T *dt = static_cast<const T *>(a.dt) + k.b * a.dt_batch + k.first + t_begin * a.dt_token;
+    const T *z = gate ? static_cast<const T *>(a.z) + k.b * a.z_batch + k.first + t_begin * a.z_token : nullptr;
+    const size_t dense = ((size_t)k.b * a.seqlen + t_begin) * E + k.first;
+    const T *dy = ADJ ? static_cast<const T *>(a.dy) + dense : nullptr;
+    T *y = OUT ? static_cast<T *>(a.y) + dense : nullptr;
+    sel_const *bc = (sel_const *)(a.bc + ((size_t)(k.b * a.ngroups + k.g) * sel_padded(a.seqlen) + t_begin) * 2 * NK +
                                   ws * 2 * NS);
 
     // this lane's states of scratch row `at`
     auto seg_at = [&](size_t at) { return (at * (NK / 4) + n0 / 4) * E * 4 + (size_t)(k.first + ch) * 4; };
     const bool live = ch < k.n;
     const int nn = live ? N - n0 : 0;  // states of this lane (those past them stay zero)
-    float A2[NS], h[NS], dsum = 0.0f;
+    float A2[NS], h[NS], P[ADJ ? NS : 1], G[ADJ ? NS : 1], dsum = 0.0f;
     load_rates(a.A + (size_t)(k.first + ch) * N + n0, nn, A2);
     {
         RowRaw<float, NS> r;
@@ -92,34 +103,44 @@ __global__ __launch_bounds__((SelShape<NK, MODE == SEL_KEEP>::THREADS)) void sel
 #pragma unroll
         for (int i = 0; i < NS; ++i) h[i] = r.get(i);
     }
-    if (OUT && live) {
-        // segment s's own state (the first one's goes on from the initial state) and
-        // step-size sum: [b][segs - 1][NK / 4][E][4] and [b][segs - 1][E]
-        for (int s = 0; s < k.seg; ++s) {
-            const size_t at = (size_t)k.b * (segs - 1) + s;
-            const float sum = a.seg_sum[at * E + k.first + ch];
-            float v[NS];
-            lane_load(a.seg_state + seg_at(at), E, v);
+    if constexpr (ADJ)
 #pragma unroll
-            for (int i = 0; i < NS; ++i)
-                h[i] = s == 0 ? v[i] : fmaf(__builtin_amdgcn_exp2f(A2[i] * sum), h[i], v[i]);
+        for (int i = 0; i < NS; ++i) {
+            P[i] = 1.0f;
+            G[i] = 0.0f;
         }
+    if (OUT && live) {
+        const size_t at = (size_t)k.b * (segs - 1);
+        sel_fold<NK>(a.seg_state + seg_at(at), a.seg_sum + at * E + k.first + ch, 1, E, k.seg, A2, h);
     }
 
     // this lane's row vectors: row r, channels c .. of the tile
-    RowRaw<T, V> xr[2][IT], dr[2][IT], zr[2][IT];
-    auto fetch = [&](int t0, int p) {
+    RowRaw<T, V> xr[2][IT], dr[2][IT], zr[2][IT], yr[2][IT];
+    uint32_t xo[IT], dto[IT], zo[IT], yo[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
+        xo[i] = row_offset<T>(r, a.x_token, c);
+        dto[i] = row_offset<T>(r, a.dt_token, c);
+        zo[i] = row_offset<T>(r, a.z_token, c);
+        yo[i] = row_offset<T>(r, E, c);
+    }
+    // the tile `ahead` tokens from the one at hand, which begins at t0
+    auto fetch = [&](int t0, int ahead, int p) {
+        const T *xt = x + ahead * a.x_token, *dtt = dt + ahead * a.dt_token;
+        const T *zt = gate ? z + ahead * a.z_token : nullptr, *yt = ADJ ? dy + (size_t)ahead * E : nullptr;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
             xr[p][i].zero();
             dr[p][i].zero();
-            zr[p][i].zero();
-            if (r < TILE && t0 + r < t_end && c < k.n) {
-                const size_t t = t0 + r;
-                xr[p][i].load(x + t * a.x_token + c, k.n - c);
-                dr[p][i].load(dt + t * a.dt_token + c, k.n - c);
-                if (OUT && z) zr[p][i].load(z + t * a.z_token + c, k.n - c);
+            if (OUT || ADJ) zr[p][i].zero();
+            if (ADJ) yr[p][i].zero();
+            if (r < TILE && t0 + ahead + r < t_end && c < k.n) {
+                xr[p][i].load(row_at(xt, xo[i]), k.n - c);
+                dr[p][i].load(row_at(dtt, dto[i]), k.n - c);
+                if (gate) zr[p][i].load(row_at(zt, zo[i]), k.n - c);
+                if (ADJ) yr[p][i].load(row_at(yt, yo[i]), k.n - c);
             }
         }
     };
@@ -131,7 +152,7 @@ __global__ __launch_bounds__((SelShape<NK, MODE == SEL_KEEP>::THREADS)) void sel
         if (OUT && a.D) Dv.load(a.D + k.first + c, k.n - c);
     }
 
-    fetch(t_begin, 0);
+    fetch(t_begin, 0, 0);
     auto tile = [&](int t0, int p) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -144,39 +165,54 @@ __global__ __launch_bounds__((SelShape<NK, MODE == SEL_KEEP>::THREADS)) void sel
                 sel_steps(a.opts, d, in);
 #pragma unroll
                 for (int e = 0; e < V; ++e) du[r * CH + c + e] = make_float2(d[e], d[e] * xr[p][i].get(e));
+                if constexpr (ADJ) {
+                    float g[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) g[e] = yr[p][i].get(e);
+                    if (gate)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) g[e] *= silu_f32(zr[p][i].get(e));
+#pragma unroll
+                    for (int e = 0; e < V; ++e) ys[r * CH + c + e] = g[e];
+                }
             }
         }
         __syncthreads();
-        if (t0 + TILE < t_end) fetch(t0 + TILE, p ^ 1);
+        if (t0 + TILE < t_end) fetch(t0, TILE, p ^ 1);
         const int nt = min(TILE, t_end - t0);
         for (int tb = 0; tb < nt; tb += U) {
-            if constexpr (MODE == SEL_KEEP)
+            if constexpr (BACK)
                 if (tb % KEEP == 0 && live) {
                     const size_t at = (size_t)k.b * a.keeps + (t0 + tb) / KEEP;
                     lane_store(a.keep_state + seg_at(at), E, h);
                     if (ws == 0) a.keep_sum[at * E + k.first + ch] = dsum;
                 }
-            sel_const *q = bc + (size_t)(t0 + tb) * (NK / 4);
+            sel_const *q = bc + tb * (NK / 4);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const float2 d = du[(tb + u) * CH + ch];
-                float y = 0.0f;
+                const float dyv = ADJ ? ys[(tb + u) * CH + ch] : 0.0f;
+                float yv = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NS; j += 4) {
                     const SelBC v = q[u * (NK / 4) + j / 4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        h[j + i] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[j + i]), h[j + i], d.y * v[i]);
-                        if constexpr (OUT) y = fmaf(v[4 + i], h[j + i], y);
+                        const float decay = __builtin_amdgcn_exp2f(d.x * A2[j + i]);
+                        h[j + i] = fmaf(decay, h[j + i], d.y * v[i]);
+                        if constexpr (OUT) yv = fmaf(v[4 + i], h[j + i], yv);
+                        if constexpr (ADJ) {
+                            P[j + i] *= decay;
+                            G[j + i] = fmaf(P[j + i], dyv * v[4 + i], G[j + i]);
+                        }
                     }
                 }
-                if constexpr (OUT) ys[(ws * TILE + tb + u) * CH + ch] = y;
+                if constexpr (OUT) ys[(ws * TILE + tb + u) * CH + ch] = yv;
                 else dsum += d.x;
             }
         }
         __syncthreads();
         if constexpr (OUT) {
-            T *y = static_cast<T *>(a.y);
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
@@ -189,13 +225,19 @@ __global__ __launch_bounds__((SelShape<NK, MODE == SEL_KEEP>::THREADS)) void sel
                         for (int j = 1; j < WS; ++j) s += ys[(j * TILE + r) * CH + c + e];
                         o[e] = fmaf(Dv.get(e), xr[p][i].get(e), s);
                     }
-                    if (z)
+                    if (gate)
 #pragma unroll
                         for (int e = 0; e < V; ++e) o[e] *= silu_f32(zr[p][i].get(e));
-                    row_store(y + ((size_t)k.b * a.seqlen + t0 + r) * E + k.first + c, o, k.n - c);
+                    row_store(row_at(y, yo[i]), o, k.n - c);
                 }
             }
         }
+        x += TILE * a.x_token;
+        dt += TILE * a.dt_token;
+        if (gate) z += TILE * a.z_token;
+        if (ADJ) dy += TILE * E;
+        if (OUT) y += TILE * E;
+        bc += TILE * (NK / 4);
     };
     for (int t0 = t_begin; t0 < t_end; t0 += 2 * TILE) {
         tile(t0, 0);
@@ -203,10 +245,22 @@ __global__ __launch_bounds__((SelShape<NK, MODE == SEL_KEEP>::THREADS)) void sel
     }
 
     if constexpr (!OUT) {
-        if (!live || k.seg >= a.segs - 1) return;
+        if (!live) return;
         const size_t at = (size_t)k.b * (a.segs - 1) + k.seg;
-        lane_store(a.seg_state + seg_at(at), E, h);
-        if (ws == 0) a.seg_sum[at * E + k.first + ch] = dsum;
+        if (k.seg < a.segs - 1) {
+            lane_store(a.seg_state + seg_at(at), E, h);
+            if (ws == 0) a.seg_sum[at * E + k.first + ch] = dsum;
+        }
+        if constexpr (ADJ)
+            if (k.seg > 0) {
+                if (k.seg == a.segs - 1 && a.dfinal && nn > 0) {
+                    RowRaw<float, NS> r;
+                    r.load(a.dfinal + ((size_t)k.b * E + k.first + ch) * N + n0, nn);
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) G[i] = fmaf(P[i], r.get(i), G[i]);
+                }
+                lane_store(a.seg_adj + seg_at(at - 1), E, G);
+            }
     } else if (a.final_state && k.seg == segs - 1 && nn > 0) {
         row_store(a.final_state + ((size_t)k.b * E + k.first + ch) * N + n0, h, nn);
     }
@@ -284,12 +338,13 @@ template <typename T, int NK> hipError_t sel_fwd(const SelArgs &a, hipStream_t s
     return hipGetLastError();
 }
 
-template <typename T, int NK> hipError_t sel_keep(const SelArgs &a, hipStream_t stream) {
+template <typename T, int NK> hipError_t sel_keep_launch(const SelArgs &a, hipStream_t stream) {
     const hipError_t e = sel_bc<T, NK>(a, stream);
     if (e != hipSuccess) return e;
-    selective_fwd_kernel<T, NK, SEL_KEEP>
-        <<<static_cast<unsigned>(selective_blocks(a.channels, a.ngroups, a.dstate) * a.segs * a.batch),
-           SelShape<NK, true>::THREADS, 0, stream>>>(a);
+    const unsigned grid = selective_blocks(a.channels, a.ngroups, a.dstate) * a.segs * a.batch;
+    constexpr int threads = SelShape<NK, true>::THREADS;
+    if (a.segs > 1) selective_fwd_kernel<T, NK, SEL_BOTH><<<grid, threads, 0, stream>>>(a);
+    else selective_fwd_kernel<T, NK, SEL_KEEP><<<grid, threads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -319,25 +374,42 @@ int selective_blocks(int channels, int ngroups, int dstate) {
     return ngroups * ((each + ch - 1) / ch);
 }
 
-// Segments of the token axis. A segment's state costs almost what its walk
-// does, so cutting pays only while the uncut walks leave most of the GPU idle.
-SelPlan selective_plan(int batch, int seqlen, int channels, int ngroups, int dstate) {
+// The token axis cut so that at most `want` workgroups run, whole tiles to a
+// segment and two at least.
+static SelPlan sel_cut(int batch, int seqlen, int channels, int ngroups, int dstate, long long want) {
     const int nk = selective_kernel_dstate(dstate), tile = 2048 / selective_ch(dstate);
     const long long wgs = (long long)batch * selective_blocks(channels, ngroups, dstate);
+    const int tiles = (seqlen + tile - 1) / tile;
+    long long s = want / wgs;
+    if (s > tiles / 2) s = tiles / 2;
+    if (s > 128) s = 128;  // every segment folds the ones before it
     SelPlan p{1, seqlen, 0};
-    if (wgs < 512) {
-        long long s = (1024 + wgs - 1) / wgs;
-        const int tiles = (seqlen + tile - 1) / tile;
-        if (s > tiles / 2) s = tiles / 2;
-        if (s > 1) {
-            const int per = static_cast<int>((tiles + s - 1) / s);
-            p.seg_len = per * tile;
-            p.segs = (seqlen + p.seg_len - 1) / p.seg_len;
-        }
+    if (s > 1) {
+        const int per = static_cast<int>((tiles + s - 1) / s);
+        p.seg_len = per * tile;
+        p.segs = (seqlen + p.seg_len - 1) / p.seg_len;
     }
     if (p.segs <= 1) p = SelPlan{1, seqlen, 0};
     p.seg_floats = (size_t)batch * (p.segs - 1) * channels * nk;
     return p;
+}
+
+// Cut forward, a walk costs two passes, so it pays only while the uncut walks
+// leave CUs without work. Measured with 5120 channels, 16 states and 2048 tokens
+// in bf16: 320 workgroups (batch 4) 336 us uncut, 322 to 346 in 4 to 16
+// segments; 640 478 uncut, 612 in 4; 160 299 and 186 (in 16); 80 297 and 111 (in 24).
+SelPlan selective_plan(int batch, int seqlen, int channels, int ngroups, int dstate) {
+    const long long wgs = (long long)batch * selective_blocks(channels, ngroups, dstate);
+    return sel_cut(batch, seqlen, channels, ngroups, dstate, wgs < 320 ? 2048 : 1);
+}
+
+// The backward's first walk is made either way, so cutting costs it little and
+// evens out the load; 2048 are four rounds of the two workgroups that a CU
+// holds. Measured as above: 640 workgroups 2543 us uncut, 1979 in 3 segments,
+// 1892 in 8; 320 1624 and 972 (in 6; 1106 in 4, whose last round is half
+// empty); 160 1400 and 523 (in 12); 80 1369 and 296 (in 24).
+SelPlan selective_bwd_plan(int batch, int seqlen, int channels, int ngroups, int dstate) {
+    return sel_cut(batch, seqlen, channels, ngroups, dstate, 2048);
 }
 
 size_t selective_bc_floats(int batch, int seqlen, int ngroups, int dstate) {
@@ -348,7 +420,7 @@ hipError_t launch_selective_fwd(const SelArgs &a, bool bf16, hipStream_t stream)
     SSD_SEL_DISPATCH(sel_fwd, a, stream)
 }
 hipError_t launch_selective_keep(const SelArgs &a, bool bf16, hipStream_t stream) {
-    SSD_SEL_DISPATCH(sel_keep, a, stream)
+    SSD_SEL_DISPATCH(sel_keep_launch, a, stream)
 }
 hipError_t launch_selective_step(const SelArgs &a, float *state, bool bf16, hipStream_t stream) {
     SSD_SEL_DISPATCH(sel_step_launch, a, state, stream)

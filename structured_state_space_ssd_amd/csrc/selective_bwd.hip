@@ -20,118 +20,13 @@
 // that are added in a fixed order. Sums over tokens (dA, dD, the bias) stay in
 // registers and end in partial rows the same way.
 //
-// With segments (see the forward) every segment's adjoint from zero is made
-// first, and a walk starts by folding the segments after its own.
+// With segments (see the forward) the first walk also makes every segment's
+// adjoint from zero, and a walk back starts by folding the segments after its own.
 #include "selective.h"
 
 namespace ssd {
 
 namespace {
-
-// A segment's adjoint from zero (from dfinal for the last one): the gradient
-// of the state entering it, for segments 1 .. segs - 1.
-template <typename T, int NK>
-__global__ __launch_bounds__((SelShape<NK, true>::THREADS)) void selective_adj_kernel(SelBwdArgs ba) {
-    using S = SelShape<NK, true>;
-    constexpr int NS = S::NS, WS = S::WS, CH = S::CH, TILE = S::TILE, THREADS = S::THREADS;
-    constexpr int V = sizeof(T) == 2 ? 8 : 4;
-    constexpr int VPR = CH / V, IT = (TILE * VPR + THREADS - 1) / THREADS, U = 8;
-    __shared__ float2 dd[TILE * CH];  // (dt, dy)
-    const SelArgs &a = ba.f;
-    SelBlock k = sel_block<CH>(blockIdx.x, a.channels, a.ngroups, a.segs - 1);
-    k.seg += 1;
-    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int ws = w % WS, ch = w / WS * 64 + (tid & 63), n0 = ws * NS;
-    const int N = a.dstate, E = a.channels;
-    // this lane's states of scratch row `at`
-    auto seg_at = [&](size_t at) { return (at * (NK / 4) + n0 / 4) * E * 4 + (size_t)(k.first + ch) * 4; };
-    const bool live = ch < k.n;
-    const int nn = live ? N - n0 : 0;
-    const int t_begin = k.seg * a.seg_len, t_end = min(a.seqlen, t_begin + a.seg_len);
-    const T *dt = static_cast<const T *>(a.dt) + k.b * a.dt_batch + k.first;
-    const T *z = a.z ? static_cast<const T *>(a.z) + k.b * a.z_batch + k.first : nullptr;
-    const T *dy = static_cast<const T *>(ba.dy) + (size_t)k.b * a.seqlen * E + k.first;
-    sel_const *const bc = (sel_const *)(a.bc + (size_t)(k.b * a.ngroups + k.g) * sel_padded(a.seqlen) * 2 * NK +
-                                  ws * 2 * NS);
-    float A2[NS], g[NS];
-    load_rates(a.A + (size_t)(k.first + ch) * N + n0, nn, A2);
-    {
-        RowRaw<float, NS> r;
-        r.zero();
-        if (nn > 0 && ba.dfinal && k.seg == a.segs - 1)
-            r.load(ba.dfinal + ((size_t)k.b * E + k.first + ch) * N + n0, nn);
-#pragma unroll
-        for (int i = 0; i < NS; ++i) g[i] = r.get(i);
-    }
-    RowRaw<float, V> bias;
-    bias.zero();
-    if (const int c = (tid % VPR) * V; a.opts.bias && c < k.n) bias.load(a.opts.bias + k.first + c, k.n - c);
-    RowRaw<T, V> dr[2][IT], zr[2][IT], yr[2][IT];
-    auto fetch = [&](int t0, int p) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
-            dr[p][i].zero();
-            zr[p][i].zero();
-            yr[p][i].zero();
-            if (r < TILE && t0 + r < t_end && c < k.n) {
-                const size_t t = t0 + r;
-                dr[p][i].load(dt + t * a.dt_token + c, k.n - c);
-                yr[p][i].load(dy + t * E + c, k.n - c);
-                if (z) zr[p][i].load(z + t * a.z_token + c, k.n - c);
-            }
-        }
-    };
-    auto tile = [&](int t0, int p) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
-            const bool in = t0 + r < t_end;  // rows past the end leave the adjoint as it is
-            if (r < TILE) {
-                float d[V], y[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    d[e] = dr[p][i].get(e) + bias.get(e);
-                    y[e] = yr[p][i].get(e);
-                }
-                sel_steps(a.opts, d, in);
-                if (z)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) y[e] *= silu_f32(zr[p][i].get(e));
-#pragma unroll
-                for (int e = 0; e < V; ++e) dd[r * CH + c + e] = make_float2(d[e], y[e]);
-            }
-        }
-        __syncthreads();
-        if (t0 - TILE >= t_begin) fetch(t0 - TILE, p ^ 1);
-        const int last = (min(TILE, t_end - t0) - 1) / U * U;
-        for (int tb = last; tb >= 0; tb -= U) {
-            sel_const *q = bc + (size_t)(t0 + tb) * (NK / 4);
-#pragma unroll
-            for (int u = U - 1; u >= 0; --u) {
-                const float2 d = dd[(tb + u) * CH + ch];
-#pragma unroll
-                for (int j = 0; j < NS; j += 4) {
-                    const SelBC v = q[u * (NK / 4) + j / 4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        g[j + i] = __builtin_amdgcn_exp2f(d.x * A2[j + i]) * fmaf(d.y, v[4 + i], g[j + i]);
-                }
-            }
-        }
-        __syncthreads();
-    };
-    int t0 = t_begin + (t_end - t_begin - 1) / TILE * TILE;
-    fetch(t0, 0);
-    for (; t0 >= t_begin; t0 -= 2 * TILE) {
-        tile(t0, 0);
-        if (t0 - TILE >= t_begin) tile(t0 - TILE, 1);
-    }
-    if (live) {
-        const size_t at = (size_t)k.b * (a.segs - 1) + k.seg - 1;
-        lane_store(ba.seg_adj + seg_at(at), E, g);
-    }
-}
 
 // Tokens of a row of dbc_part, and the rows a sequence and group take: every
 // row holds 64 values per four states, dB of each state for 8 tokens, then dC.
@@ -160,20 +55,22 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
     const bool live = ch < k.n;
     const int nn = live ? N - n0 : 0;
     const int t_begin = k.seg * a.seg_len, t_end = min(L, t_begin + a.seg_len);
-    const T *x = static_cast<const T *>(a.x) + k.b * a.x_batch + k.first;
-    const T *dt = static_cast<const T *>(a.dt) + k.b * a.dt_batch + k.first;
-    const T *z = GATE ? static_cast<const T *>(a.z) + k.b * a.z_batch + k.first : nullptr;
-    const T *dy = static_cast<const T *>(ba.dy) + (size_t)k.b * L * E + k.first;
-    sel_const *const bc = (sel_const *)(a.bc + (size_t)(k.b * a.ngroups + k.g) * sel_padded(L) * 2 * NK +
-                                  ws * 2 * NS);
+    const int t_last = t_begin + (t_end - t_begin - 1) / TB * TB;  // the first tile walked
+    // rows of the tile at hand
+    const T *x = static_cast<const T *>(a.x) + k.b * a.x_batch + k.first + t_last * a.x_token;
+    const T *dt = static_cast<const T *>(a.dt) + k.b * a.dt_batch + k.first + t_last * a.dt_token;
+    const T *z = GATE ? static_cast<const T *>(a.z) + k.b * a.z_batch + k.first + t_last * a.z_token : nullptr;
+    size_t dense = ((size_t)k.b * L + t_last) * E + k.first;  // in dy and the outputs
+    sel_const *q = (sel_const *)(a.bc + ((size_t)(k.b * a.ngroups + k.g) * sel_padded(L) + t_last) * 2 * NK +
+                                 ws * 2 * NS);
 
     float A2[NS], h_in[NS], ag[NS], dA[NS];
     load_rates(a.A + (size_t)(k.first + ch) * N + n0, nn, A2);
     {
         RowRaw<float, NS> r;
         r.zero();
-        if (k.seg == a.segs - 1 && ba.dfinal && nn > 0)
-            r.load(ba.dfinal + ((size_t)k.b * E + k.first + ch) * N + n0, nn);
+        if (k.seg == a.segs - 1 && a.dfinal && nn > 0)
+            r.load(a.dfinal + ((size_t)k.b * E + k.first + ch) * N + n0, nn);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             ag[i] = r.get(i);
@@ -181,33 +78,18 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
         }
     }
     if (live) {
-        const size_t at = (size_t)k.b * (a.segs - 1);
-        float v[NS];
-        for (int s = 0; s < k.seg; ++s) {
-            const float sum = a.seg_sum[(at + s) * E + k.first + ch];
-            lane_load(a.seg_state + seg_at(at + s), E, v);
-#pragma unroll
-            for (int i = 0; i < NS; ++i)
-                h_in[i] = s == 0 ? v[i] : fmaf(__builtin_amdgcn_exp2f(A2[i] * sum), h_in[i], v[i]);
-        }
-        for (int s = a.segs - 1; s > k.seg; --s) {
-            // the gradient of the state entering segment s
-            const float sum = s < a.segs - 1 ? a.seg_sum[(at + s) * E + k.first + ch] : 0.0f;
-            lane_load(ba.seg_adj + seg_at(at + s - 1), E, v);
-#pragma unroll
-            for (int i = 0; i < NS; ++i)
-                ag[i] = s == a.segs - 1 ? v[i] : fmaf(__builtin_amdgcn_exp2f(A2[i] * sum), ag[i], v[i]);
-        }
+        const size_t at = (size_t)k.b * (a.segs - 1), e = k.first + ch;
+        sel_fold<NK>(a.seg_state + seg_at(at), a.seg_sum + at * E + e, 1, E, k.seg, A2, h_in);
+        // the gradients of the states entering the segments behind, from the last one on
+        if (k.seg < a.segs - 1)
+            sel_fold<NK>(a.seg_adj + seg_at(at + a.segs - 2), a.seg_sum + (at + a.segs - 1) * E + e, -1, E,
+                         a.segs - 1 - k.seg, A2, ag);
     }
 
-    RowRaw<float, V> bias, Dv;
+    RowRaw<float, V> bias;
     float dD[V], db[V];
     bias.zero();
-    Dv.zero();
-    if (const int c = (tid % VPR) * V; c < k.n) {
-        if (a.opts.bias) bias.load(a.opts.bias + k.first + c, k.n - c);
-        if (a.D) Dv.load(a.D + k.first + c, k.n - c);
-    }
+    if (const int c = (tid % VPR) * V; a.opts.bias && c < k.n) bias.load(a.opts.bias + k.first + c, k.n - c);
 #pragma unroll
     for (int e = 0; e < V; ++e) dD[e] = db[e] = 0.0f;
     // this wavefront's rows of dbc_part
@@ -219,8 +101,18 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
     // over a tile is done and its registers are free, and arrive while it is finished.
     RowRaw<T, V> xr[IT], zr[IT], yr[IT], dr[IT];
     float hk[NS], hsum = 0.0f;
+    uint32_t xo[IT], dto[IT], zo[IT], yo[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
+        xo[i] = row_offset<T>(r, a.x_token, c);
+        dto[i] = row_offset<T>(r, a.dt_token, c);
+        zo[i] = row_offset<T>(r, a.z_token, c);
+        yo[i] = row_offset<T>(r, E, c);
+    }
     auto fetch = [&](int t0, RowRaw<T, V>(&xr)[IT], RowRaw<T, V>(&dr)[IT], RowRaw<T, V>(&zr)[IT],
                      RowRaw<T, V>(&yr)[IT]) {
+        const T *dy = static_cast<const T *>(a.dy) + dense;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int id = tid + i * THREADS, r = id / VPR, c = (id % VPR) * V;
@@ -229,11 +121,10 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
             zr[i].zero();
             yr[i].zero();
             if (r < TB && t0 + r < t_end && c < k.n) {
-                const size_t t = t0 + r;
-                xr[i].load(x + t * a.x_token + c, k.n - c);
-                dr[i].load(dt + t * a.dt_token + c, k.n - c);
-                if (GATE) zr[i].load(z + t * a.z_token + c, k.n - c);
-                yr[i].load(dy + t * E + c, k.n - c);
+                xr[i].load(row_at(x, xo[i]), k.n - c);
+                dr[i].load(row_at(dt, dto[i]), k.n - c);
+                if (GATE) zr[i].load(row_at(z, zo[i]), k.n - c);
+                yr[i].load(row_at(dy, yo[i]), k.n - c);
             }
         }
 #pragma unroll
@@ -244,9 +135,8 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
             if (k.seg) hsum = a.keep_sum[at * E + k.first + ch];
         }
     };
-    int t0 = t_begin + (t_end - t_begin - 1) / TB * TB;
-    fetch(t0, xr, dr, zr, yr);
-    for (; t0 >= t_begin; t0 -= TB) {
+    fetch(t_last, xr, dr, zr, yr);
+    for (int t0 = t_last; t0 >= t_begin; t0 -= TB) {
         const int nt = min(TB, t_end - t0);
         if (k.seg)
 #pragma unroll
@@ -271,7 +161,6 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
 
         // B and C of GR tokens at a time, the next ones on their way while these are used
         constexpr int GR = NS == 4 ? 2 : 1;
-        sel_const *q = bc + (size_t)t0 * (NK / 4);
         SelBC bcv[2][GR][NS / 4];
         auto scalars = [&](int t, int s) {
 #pragma unroll
@@ -304,6 +193,8 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
         // a wavefront's eight sums of a token and four states, from its 2 KB of products
         float *const mine = &tr[w * 1024];
         const int from = (lane >> 3) * 64 + (lane & 7) * 4;
+        // not a constant of the loop: eight lane masks would be kept for the comparisons below
+        const int turn = ragged(lane & 7);
         float4 r0, r1;
         auto sums_load = [&](int buf) {
             __builtin_amdgcn_wave_barrier();
@@ -319,7 +210,7 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
             sum = add(sum, __builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x141, 0xf, 0xf, true));
             // lane 8 v + u keeps value v of the row's u-th token
             if (t % TOK == TOK - 1) res[s4] = sum;
-            else res[s4] = (lane & 7) == t % TOK ? sum : res[s4];
+            else res[s4] = turn == t % TOK ? sum : res[s4];
             if (t % TOK == 0 && t < nt)  // nt: rows past the sequence's are another's
                 rows[((size_t)(t0 + t) / TOK * (NK / 4) + n0 / 4 + s4) * 64 + lane] = res[s4];
         };
@@ -362,7 +253,19 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
         sums_load((TB * (NS / 4) - 1) % 2);
         sums_end(0, NS / 4 - 1);
         RowRaw<T, V> xn[IT], zn[IT], yn[IT], dn[IT];
-        if (t0 > t_begin) fetch(t0 - TB, xn, dn, zn, yn);
+        RowRaw<float, V> Dv;  // read again for every tile: the walk leaves no registers for it
+        Dv.zero();
+        if (const int c = (tid % VPR) * V; a.D && c < k.n) Dv.load(a.D + k.first + c, k.n - c);
+        T *const dx = static_cast<T *>(ba.dx) + dense, *const ddt = static_cast<T *>(ba.ddt) + dense;
+        T *const dz = GATE ? static_cast<T *>(ba.dz) + dense : nullptr;
+        if (t0 > t_begin) {
+            x -= TB * a.x_token;
+            dt -= TB * a.dt_token;
+            if (GATE) z -= TB * a.z_token;
+            dense -= (size_t)TB * E;
+            q -= TB * (NK / 4);
+            fetch(t0 - TB, xn, dn, zn, yn);
+        }
         __syncthreads();
 
 #pragma unroll
@@ -402,10 +305,9 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
                     for (int e = 0; e < V; ++e) ot[e] *= sigmoid_f32(raws[e]);
 #pragma unroll
                 for (int e = 0; e < V; ++e) db[e] += ot[e];
-                const size_t o = ((size_t)k.b * L + t0 + r) * E + k.first + c;
-                row_store(static_cast<T *>(ba.dx) + o, ox, k.n - c);
-                row_store(static_cast<T *>(ba.ddt) + o, ot, k.n - c);
-                if constexpr (GATE) row_store(static_cast<T *>(ba.dz) + o, oz, k.n - c);
+                row_store(row_at(dx, yo[i]), ox, k.n - c);
+                row_store(row_at(ddt, yo[i]), ot, k.n - c);
+                if constexpr (GATE) row_store(row_at(dz, yo[i]), oz, k.n - c);
             }
         }
         __syncthreads();
@@ -472,13 +374,6 @@ template <typename T, int NK> hipError_t sel_bwd(const SelBwdArgs &ba, hipStream
     const int blocks = selective_blocks(a.channels, a.ngroups, a.dstate);
     hipError_t e = launch_selective_keep(a, sizeof(T) == 2, stream);
     if (e != hipSuccess) return e;
-    if (a.segs > 1) {
-        selective_adj_kernel<T, NK>
-            <<<static_cast<unsigned>(blocks * (a.segs - 1) * a.batch), SelShape<NK, true>::THREADS, 0,
-               stream>>>(ba);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
     const unsigned grid = static_cast<unsigned>(blocks * a.segs * a.batch);
     if (a.z) selective_bwd_kernel<T, NK, true><<<grid, SelShape<NK, true>::THREADS, 0, stream>>>(ba);
     else selective_bwd_kernel<T, NK, false><<<grid, SelShape<NK, true>::THREADS, 0, stream>>>(ba);
@@ -522,11 +417,6 @@ int selective_keep_tokens(int dstate) {
         case 32: return sel_keep<32>();
         default: return sel_keep<64>();
     }
-}
-
-// As the forward's: a walk back costs four times a segment's adjoint.
-SelPlan selective_bwd_plan(int batch, int seqlen, int channels, int ngroups, int dstate) {
-    return selective_plan(batch, seqlen, channels, ngroups, dstate);
 }
 
 hipError_t launch_selective_bwd(const SelBwdArgs &ba, bool bf16, hipStream_t stream) {

@@ -247,6 +247,9 @@ struct SelArgs {
     // the backward's: states before every so many tokens (selective_keep_tokens)
     int keeps;                        // of them per sequence
     float *keep_state, *keep_sum;     // [Bt][keeps][E * NK], [Bt][keeps][E]
+    const void *dy;                   // [Bt][L][E] dense
+    const float *dfinal;              // [Bt][E][N], nullable
+    float *seg_adj;                   // [Bt][segs - 1][E * NK]: segments 1 .. segs - 1
 };
 // The state size the kernels hold (4, 8, 16, 32 or 64; 0: not supported) and
 // the workgroups one sequence's channels take.
@@ -259,7 +262,7 @@ struct SelPlan {
 size_t selective_bc_floats(int batch, int seqlen, int ngroups, int dstate);
 SelPlan selective_plan(int batch, int seqlen, int channels, int ngroups, int dstate);
 hipError_t launch_selective_fwd(const SelArgs &a, bool bf16, hipStream_t stream);
-// The backward's first pass: fills seg_state, seg_sum, keep_state, keep_sum.
+// The backward's first pass: fills seg_state, seg_sum, seg_adj, keep_state, keep_sum.
 hipError_t launch_selective_keep(const SelArgs &a, bool bf16, hipStream_t stream);
 int selective_keep_tokens(int dstate);
 // One token: the token strides and init are not read.
@@ -267,9 +270,6 @@ hipError_t launch_selective_step(const SelArgs &a, float *state, bool bf16, hipS
 
 struct SelBwdArgs {
     SelArgs f;                  // the forward's inputs; y, final_state unused
-    const void *dy;             // [Bt][L][E] dense
-    const float *dfinal;        // [Bt][E][N], nullable
-    float *seg_adj;             // [Bt][segs - 1][E * NK]: segments 1 .. segs - 1
     float *dbc_part;            // selective_dbc_floats: every workgroup's dB and dC
     float *dA_part;             // [Bt][segs][E][N]
     float *de_part;             // [Bt][segs][dD, dbias][E]

@@ -15,9 +15,9 @@ typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x2_any __attribute__((ext_vector_type(2), aligned(4)));
 
-// A ragged vector's element count, as a value the compiler cannot know ahead:
-// the comparisons with it are then made where a ragged vector is met instead
-// of being kept, one lane mask each, across the whole loop.
+// A ragged vector's element count (or a lane's number) as a value the compiler
+// cannot know ahead: comparisons with it are then made where they are needed
+// instead of being kept, one lane mask each, across the whole loop.
 __device__ __forceinline__ int ragged(int n) {
     asm volatile("" : "+v"(n));
     return n;
