@@ -152,7 +152,19 @@ __global__ __launch_bounds__((SelShape<NK, (MODE >= SEL_KEEP)>::THREADS)) void s
         if (OUT && a.D) Dv.load(a.D + k.first + c, k.n - c);
     }
 
+    // B and C of GR tokens, from the t-th of the tile at hand on (past the tile, the next
+    // one's; the buffer has a tile to spare at its end)
+    constexpr int GR = 16 / NS;
+    SelBC bcv[2][GR][NS / 4];
+    auto scalars = [&](int t, int s) {
+#pragma unroll
+        for (int u = 0; u < GR; ++u)
+#pragma unroll
+            for (int i = 0; i < NS / 4; ++i) bcv[s][u][i] = bc[(t + u) * (NK / 4) + i];
+    };
+
     fetch(t_begin, 0, 0);
+    scalars(0, 0);
     auto tile = [&](int t0, int p) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -187,28 +199,32 @@ __global__ __launch_bounds__((SelShape<NK, (MODE >= SEL_KEEP)>::THREADS)) void s
                     lane_store(a.keep_state + seg_at(at), E, h);
                     if (ws == 0) a.keep_sum[at * E + k.first + ch] = dsum;
                 }
-            sel_const *q = bc + tb * (NK / 4);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float2 d = du[(tb + u) * CH + ch];
-                const float dyv = ADJ ? ys[(tb + u) * CH + ch] : 0.0f;
-                float yv = 0.0f;
+            for (int g = 0; g < U; g += GR) {
+                // the next tokens' B and C set out while these are used
+                const int s = g / GR % 2;
+                scalars(tb + g + GR, s ^ 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < NS; j += 4) {
-                    const SelBC v = q[u * (NK / 4) + j / 4];
+                for (int u = 0; u < GR; ++u) {
+                    const int t = tb + g + u;
+                    const float2 d = du[t * CH + ch];
+                    const float dyv = ADJ ? ys[t * CH + ch] : 0.0f;
+                    float yv = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float decay = __builtin_amdgcn_exp2f(d.x * A2[j + i]);
-                        h[j + i] = fmaf(decay, h[j + i], d.y * v[i]);
-                        if constexpr (OUT) yv = fmaf(v[4 + i], h[j + i], yv);
+                    for (int i = 0; i < NS; ++i) {
+                        const SelBC v = bcv[s][u][i / 4];
+                        const float decay = __builtin_amdgcn_exp2f(d.x * A2[i]);
+                        h[i] = fmaf(decay, h[i], d.y * v[i % 4]);
+                        if constexpr (OUT) yv = fmaf(v[4 + i % 4], h[i], yv);
                         if constexpr (ADJ) {
-                            P[j + i] *= decay;
-                            G[j + i] = fmaf(P[j + i], dyv * v[4 + i], G[j + i]);
+                            P[i] *= decay;
+                            G[i] = fmaf(P[i], dyv * v[4 + i % 4], G[i]);
                         }
                     }
+                    if constexpr (OUT) ys[(ws * TILE + t) * CH + ch] = yv;
+                    else dsum += d.x;
                 }
-                if constexpr (OUT) ys[(ws * TILE + tb + u) * CH + ch] = yv;
-                else dsum += d.x;
             }
         }
         __syncthreads();
@@ -413,7 +429,7 @@ SelPlan selective_bwd_plan(int batch, int seqlen, int channels, int ngroups, int
 }
 
 size_t selective_bc_floats(int batch, int seqlen, int ngroups, int dstate) {
-    return (size_t)batch * ngroups * sel_padded(seqlen) * 2 * selective_kernel_dstate(dstate);
+    return ((size_t)batch * ngroups * sel_padded(seqlen) + kSelPad) * 2 * selective_kernel_dstate(dstate);
 }
 
 hipError_t launch_selective_fwd(const SelArgs &a, bool bf16, hipStream_t stream) {

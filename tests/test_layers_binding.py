@@ -243,7 +243,7 @@ def _opt(**kw):
     (dict(ngroups=0), -2), (dict(dstate=0), -2), (dict(ngroups=3), -2), (dict(seqlen=(1 << 30) + 1), -2),
     (dict(strides=(0, 0, 0, 0, 0, 0, 0, -1, 0, 0)), -2),
     (dict(dstate=65), -3), (dict(dtype=2), -3), (dict(batch=1 << 24), -3),
-    (dict(ws=FAKE, bytes=1023), -4), (dict(ws=ctypes.c_void_p(0x100010), bytes=1 << 30), -4),
+    (dict(ws=FAKE, bytes=(2 * 2 * 32 + 32) * 64 - 1), -4), (dict(ws=ctypes.c_void_p(0x100010), bytes=1 << 30), -4),
     (dict(ws=None, bytes=1 << 30), -4),
 ], ids=str)
 def test_selective_c_abi_refuses(lib, kw, code):
@@ -255,11 +255,11 @@ def test_selective_c_abi_options_and_workspaces(lib):
     assert scan_c(lib, opts=_opt(dt_clamp=1, dt_min=1.0, dt_max=0.5)) == -6
     assert scan_c(lib, opts=_opt(dt_clamp=1, dt_min=float("nan"), dt_max=0.5)) == -6
     size = lib.ssd_selective_forward_workspace_size
-    # B and C as float, the tokens rounded up to 32; 1024-byte segment states where few
-    # channels have the token axis cut
-    assert size(2, 6, 8, 2, 5, 1) == 2 * 2 * 32 * 2 * 8 * 4
-    assert size(64, 4096, 5120, 1, 16, 1) == 64 * 4096 * 32 * 4
-    assert size(1, 4096, 64, 1, 16, 1) > 4096 * 32 * 4 and size(1, 4096, 64, 1, 65, 1) == 0
+    # B and C as float, the tokens rounded up to 32 and 32 to spare; segment states
+    # where few channels have the token axis cut
+    assert size(2, 6, 8, 2, 5, 1) == (2 * 2 * 32 + 32) * 2 * 8 * 4
+    assert size(64, 4096, 5120, 1, 16, 1) == (64 * 4096 + 32) * 32 * 4
+    assert size(1, 4096, 64, 1, 16, 1) > (4096 + 32) * 32 * 4 and size(1, 4096, 64, 1, 65, 1) == 0
     back = lib.ssd_selective_backward_workspace_size
     n = back(2, 6, 8, 2, 5, 1)
     assert n > 0
