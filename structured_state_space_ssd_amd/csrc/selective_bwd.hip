@@ -41,6 +41,8 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
     __shared__ float dys[TB * CH];        // dy silu(z)
     __shared__ float2 pg[WS * TB * CH];   // each wavefront's sum_n (g B), sum_n (A2 g q)
     __shared__ float py[GATE ? WS * TB * CH : 1];  // and sum_n (C h)
+    // the channels' bias and D, which the walk leaves no registers for
+    __shared__ __attribute__((aligned(16))) float biases[CH], Ds[CH];
     // each wavefront's eight values by 64 channels, twice; after the last tile every
     // lane's dD and bias sums
     __shared__ __attribute__((aligned(16))) float tr[THREADS / 64 * 2 * 8 * 64];
@@ -86,10 +88,12 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
                          a.segs - 1 - k.seg, A2, ag);
     }
 
-    RowRaw<float, V> bias;
     float dD[V], db[V];
-    bias.zero();
-    if (const int c = (tid % VPR) * V; a.opts.bias && c < k.n) bias.load(a.opts.bias + k.first + c, k.n - c);
+    for (int c = tid; c < CH; c += THREADS) {
+        biases[c] = a.opts.bias && c < k.n ? a.opts.bias[k.first + c] : 0.0f;
+        Ds[c] = a.D && c < k.n ? a.D[k.first + c] : 0.0f;
+    }
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < V; ++e) dD[e] = db[e] = 0.0f;
     // this wavefront's rows of dbc_part
@@ -97,8 +101,10 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
     float *rows = ba.dbc_part + (((size_t)part * a.batch + k.b) * a.ngroups + k.g) *
                                     ((L + TOK - 1) / TOK) * (NK / 4) * 64;
 
-    // A tile's rows and the state before it. The next tile's are fetched when the walk
-    // over a tile is done and its registers are free, and arrive while it is finished.
+    // A tile's rows and the state before it. The next tile's rows set out halfway back,
+    // when half the tile's states are done with (in float32, and at 64 states, only when
+    // all are: the registers would not do), its state when the walk is done.
+    constexpr bool EARLY = sizeof(T) == 2 && NK <= 32;
     RowRaw<T, V> xr[IT], zr[IT], yr[IT], dr[IT];
     float hk[NS], hsum = 0.0f;
     uint32_t xo[IT], dto[IT], zo[IT], yo[IT];
@@ -110,7 +116,7 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
         zo[i] = row_offset<T>(r, a.z_token, c);
         yo[i] = row_offset<T>(r, E, c);
     }
-    auto fetch = [&](int t0, RowRaw<T, V>(&xr)[IT], RowRaw<T, V>(&dr)[IT], RowRaw<T, V>(&zr)[IT],
+    auto fetch = [&](int t0, size_t dense, RowRaw<T, V>(&xr)[IT], RowRaw<T, V>(&dr)[IT], RowRaw<T, V>(&zr)[IT],
                      RowRaw<T, V>(&yr)[IT]) {
         const T *dy = static_cast<const T *>(a.dy) + dense;
 #pragma unroll
@@ -127,6 +133,8 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
                 yr[i].load(row_at(dy, yo[i]), k.n - c);
             }
         }
+    };
+    auto state = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) hk[i] = 0.0f;
         if (live) {
@@ -135,7 +143,8 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
             if (k.seg) hsum = a.keep_sum[at * E + k.first + ch];
         }
     };
-    fetch(t_last, xr, dr, zr, yr);
+    fetch(t_last, dense, xr, dr, zr, yr);
+    state(t_last);
     for (int t0 = t_last; t0 >= t_begin; t0 -= TB) {
         const int nt = min(TB, t_end - t0);
         if (k.seg)
@@ -148,7 +157,7 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
             if (r < TB) {
                 float d[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) d[e] = dr[i].get(e) + bias.get(e);
+                for (int e = 0; e < V; ++e) d[e] = dr[i].get(e) + biases[c + e];
                 sel_steps(a.opts, d, r < nt);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
@@ -159,27 +168,33 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
         }
         __syncthreads();
 
-        // B and C of GR tokens at a time, the next ones on their way while these are used
-        constexpr int GR = NS == 4 ? 2 : 1;
+        // B and C of GR tokens at a time, the next ones on their way while these
+        // are used (one in float32 at 16 states, where two would spill)
+        constexpr int GR = NS == 4 && (sizeof(T) == 2 || NK != 16) ? 2 : 1;
         SelBC bcv[2][GR][NS / 4];
-        auto scalars = [&](int t, int s) {
+        float2 dv[2][GR];
+        float gv[2][GR];
+        auto operands = [&](int t, int s, bool back) {
 #pragma unroll
-            for (int u = 0; u < GR; ++u)
+            for (int u = 0; u < GR; ++u) {
 #pragma unroll
                 for (int i = 0; i < NS / 4; ++i) bcv[s][u][i] = q[(t + u) * (NK / 4) + i];
+                dv[s][u] = du[(t + u) * CH + ch];
+                if (back) gv[s][u] = dys[(t + u) * CH + ch];
+            }
         };
         float h[TB][NS], dec[TB][NS], res[NS / 4];
-        scalars(0, 0);
+        operands(0, 0, false);
 #pragma unroll
         for (int tg = 0; tg < TB; tg += GR) {
             const int s = tg / GR % 2;
-            // (the last group's serve the walk back as well)
-            if (tg + GR < TB) scalars(tg + GR, s ^ 1);
+            if (tg + GR < TB) operands(tg + GR, s ^ 1, false);
+            else operands(TB - GR, s, true);  // the walk back begins where this one ends
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int u = 0; u < GR; ++u) {
                 const int t = tg + u;
-                const float2 d = du[t * CH + ch];
+                const float2 d = dv[s][u];
                 float y = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
@@ -190,6 +205,13 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
                 if constexpr (GATE) py[(ws * TB + t) * CH + ch] = y;
             }
         }
+        RowRaw<T, V> xn[IT], zn[IT], yn[IT], dn[IT];
+        auto fetch_next = [&]() {
+            x -= TB * a.x_token;
+            dt -= TB * a.dt_token;
+            if (GATE) z -= TB * a.z_token;
+            fetch(t0 - TB, dense - (size_t)TB * E, xn, dn, zn, yn);
+        };
         // a wavefront's eight sums of a token and four states, from its 2 KB of products
         float *const mine = &tr[w * 1024];
         const int from = (lane >> 3) * 64 + (lane & 7) * 4;
@@ -217,13 +239,14 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
 #pragma unroll
         for (int tg = TB - GR; tg >= 0; tg -= GR) {
             const int s = tg / GR % 2;
-            if (tg) scalars(tg - GR, s ^ 1);
+            if (tg) operands(tg - GR, s ^ 1, true);
+            if (EARLY && tg == TB / 2 && t0 > t_begin) fetch_next();
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int u = GR - 1; u >= 0; --u) {
                 const int t = tg + u;
-                const float2 d = du[t * CH + ch];
-                const float dyv = dys[t * CH + ch];
+                const float2 d = dv[s][u];
+                const float dyv = gv[s][u];
                 float gB = 0.0f, gA = 0.0f;
 #pragma unroll
                 for (int s4 = 0; s4 < NS / 4; ++s4) {
@@ -252,19 +275,13 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
         }
         sums_load((TB * (NS / 4) - 1) % 2);
         sums_end(0, NS / 4 - 1);
-        RowRaw<T, V> xn[IT], zn[IT], yn[IT], dn[IT];
-        RowRaw<float, V> Dv;  // read again for every tile: the walk leaves no registers for it
-        Dv.zero();
-        if (const int c = (tid % VPR) * V; a.D && c < k.n) Dv.load(a.D + k.first + c, k.n - c);
         T *const dx = static_cast<T *>(ba.dx) + dense, *const ddt = static_cast<T *>(ba.ddt) + dense;
         T *const dz = GATE ? static_cast<T *>(ba.dz) + dense : nullptr;
         if (t0 > t_begin) {
-            x -= TB * a.x_token;
-            dt -= TB * a.dt_token;
-            if (GATE) z -= TB * a.z_token;
+            if (!EARLY) fetch_next();
             dense -= (size_t)TB * E;
             q -= TB * (NK / 4);
-            fetch(t0 - TB, xn, dn, zn, yn);
+            state(t0 - TB);
         }
         __syncthreads();
 
@@ -282,8 +299,8 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
                         sB += pg[j * TB * CH + at].x;
                         sA += pg[j * TB * CH + at].y;
                     }
-                    const float xv = xr[i].get(e), raw = dr[i].get(e) + bias.get(e), dyg = dys[at];
-                    ox[e] = fmaf(du[at].x, sB, Dv.get(e) * dyg);
+                    const float xv = xr[i].get(e), raw = dr[i].get(e) + biases[c + e], dyg = dys[at];
+                    ox[e] = fmaf(du[at].x, sB, Ds[c + e] * dyg);
                     raws[e] = raw;
                     ot[e] = fmaf(xv, sB, sA * 0.6931471805599453f);
                     dD[e] = fmaf(dyg, xv, dD[e]);  // zero past the last channel
@@ -291,7 +308,7 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
                         float y = py[at];
 #pragma unroll
                         for (int j = 1; j < WS; ++j) y += py[j * TB * CH + at];
-                        oz[e] = yr[i].get(e) * fmaf(Dv.get(e), xv, y) * silu_grad_f32(zr[i].get(e));
+                        oz[e] = yr[i].get(e) * fmaf(Ds[c + e], xv, y) * silu_grad_f32(zr[i].get(e));
                     }
                 }
                 if (a.opts.clamp)
