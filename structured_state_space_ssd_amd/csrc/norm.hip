@@ -12,6 +12,8 @@
 // group of lanes: the smallest power of two of one wavefront that has a lane
 // for every vector of the row, or the whole workgroup for longer rows, whose
 // wavefronts meet once through LDS per sum.
+#include <type_traits>
+
 #include "ssd_launch.h"
 #include "ssd_rows.h"
 
@@ -39,77 +41,115 @@ __device__ __forceinline__ RowGroup row_group(int lpr) {
     return r;
 }
 
+// Sums over groups of `top` lanes (a power of two), in every one of them: moves
+// within the vector unit, which a row's sums, one after the other, wait for far
+// less than for the permutes through LDS that __shfl_xor makes.
+template <int K> __device__ __forceinline__ void lane_sum(float (&v)[K], int top) {
+    auto dpp = [&](auto ctrl) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            v[k] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[k]),
+                                                               decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    if (top > 1) dpp(std::integral_constant<int, 0xB1>());    // the other of two
+    if (top > 2) dpp(std::integral_constant<int, 0x4E>());    // the other two of four
+    if (top > 4) dpp(std::integral_constant<int, 0x141>());   // eight, mirrored
+    if (top > 8) dpp(std::integral_constant<int, 0x140>());   // sixteen, mirrored
+    if (top > 16)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[k]),
+                                                            __float_as_uint(v[k]), false, false);
+            v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+        }
+    if (top > 32)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]),
+                                                            __float_as_uint(v[k]), false, false);
+            v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+        }
+}
+
 // Sums of K values over the lanes of a row, in every one of them. `buf` holds
-// K floats per wavefront; the caller alternates between two of them, so that
-// one barrier per sum is enough (a wavefront can write a buffer again only
-// after it has passed the barrier of the other one).
+// K floats per wavefront (at most 16 wavefronts); the caller alternates between
+// two of them, so that one barrier per sum is enough (a wavefront can write a
+// buffer again only after it has passed the barrier of the other one).
 template <int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], int lpr, float *buf) {
-    const int top = lpr ? lpr : 64;
-    for (int off = 1; off < top; off <<= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], off);
+    lane_sum(v, lpr ? lpr : 64);
     const int waves = blockDim.x >> 6;
     if (lpr || waves == 1) return;
     if (lane_id() == 0)
 #pragma unroll
         for (int k = 0; k < K; ++k) buf[wave_id() * K + k] = v[k];
     __syncthreads();
+    const int w = lane_id() & 15;
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = 0.0f;
-    for (int w = 0; w < waves; ++w)
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += buf[w * K + k];
+    for (int k = 0; k < K; ++k) v[k] = w < waves ? buf[w * K + k] : 0.0f;
+    lane_sum(v, 16);
 }
 
 template <typename T> constexpr int vec_of() { return sizeof(T) == 2 ? 8 : 4; }
 
-// T: type of x, z, y. R: type of the residual stream (RES).
+// Rows are taken with the stride of the grid, which holds as many as run at
+// once; the next row sets out while one is worked on, so that its way from
+// memory hides behind the sums and their barriers.
+//
+// T: type of x, z, y. R: type of the residual stream.
 template <typename T, typename R, int NV>
-__global__ __launch_bounds__(1024) void norm_fwd_kernel(
+__global__ __launch_bounds__(1024, NV == 1 ? 7 : 4) void norm_fwd_kernel(
     const T *__restrict__ x, size_t x_stride, const R *__restrict__ res,
     const float *__restrict__ weight, const float *__restrict__ bias, const T *__restrict__ z,
     size_t z_stride, long long rows, int D, int lpr, int rms, float eps, T *__restrict__ y,
     R *__restrict__ res_out, float *__restrict__ mean_out, float *__restrict__ rstd_out) {
     constexpr int V = vec_of<T>();
     __shared__ float buf[3][16];
+    if (NV > 1) lpr = 0;  // only whole workgroups hold more than a vector per lane
     const RowGroup g = row_group(lpr);
     const int step = (lpr ? lpr : (int)blockDim.x) * V;
     const float inv = 1.0f / static_cast<float>(D);
-    int turn = 0;
-    for (long long row = (long long)blockIdx.x * g.groups + g.group; row < rows;
-         row += (long long)gridDim.x * g.groups, turn ^= 1) {
-        const T *xr = x + row * x_stride;
+    const long long stride = (long long)gridDim.x * g.groups;
+    RowRaw<T, V> xr[NV], zr[NV];
+    RowRaw<R, V> rr[NV];
+    auto fetch = [&](long long row) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = g.lane * V + i * step, n = D - c;
+            xr[i].zero();
+            if (row < rows && n > 0) {
+                xr[i].load(x + row * x_stride + c, n);
+                if (res) rr[i].load(res + row * D + c, n);
+                else if (z) zr[i].load(z + row * z_stride + c, n);
+            }
+        }
+    };
+    constexpr bool AHEAD = NV * V < 16;  // wider rows leave no registers for it
+    long long row = (long long)blockIdx.x * g.groups + g.group;
+    if (AHEAD) fetch(row);
+    for (int turn = 0; row < rows; row += stride, turn ^= 1) {
+        if (!AHEAD) fetch(row);
         float u[NV][V];
         float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = g.lane * V + i * step, n = D - c;
-            if (n > 0) {
-                RowRaw<T, V> a;
-                a.load(xr + c, n);
 #pragma unroll
-                for (int e = 0; e < V; ++e) u[i][e] = a.get(e);
-                if (res) {
-                    RowRaw<R, V> b;
-                    b.load(res + row * D + c, n);
+            for (int e = 0; e < V; ++e) u[i][e] = xr[i].get(e);
+            if (n <= 0) continue;
+            if (res) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e)  // the norm reads the stream as it is kept
-                        u[i][e] = to_f32(from_f32<R>(u[i][e] + b.get(e)));
-                    row_store(res_out + row * D + c, u[i], n);
-                } else if (z) {
-                    RowRaw<T, V> b;
-                    b.load(z + row * z_stride + c, n);
+                for (int e = 0; e < V; ++e)  // the norm reads the stream as it is kept
+                    u[i][e] = to_f32(from_f32<R>(u[i][e] + rr[i].get(e)));
+                row_store(res_out + row * D + c, u[i], n);
+            } else if (z) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) u[i][e] *= silu_f32(b.get(e));
-                }
-#pragma unroll
-                for (int e = 0; e < V; ++e) s[0] += u[i][e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) u[i][e] = 0.0f;
+                for (int e = 0; e < V; ++e) u[i][e] *= silu_f32(zr[i].get(e));
             }
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[0] += u[i][e];
         }
+        if (AHEAD) fetch(row + stride);
         float m = 0.0f;
         if (!rms) {
             row_sum(s, lpr, buf[2]);
@@ -149,13 +189,14 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(
     }
 }
 
-// Each workgroup (or, for short rows, each group of lanes) takes rows with a
-// stride of the grid and keeps its columns' dw and db in registers; it writes
-// them once at its end, and colsum_kernel adds the partial rows in their
-// order, so the result does not depend on timing.
+// Each workgroup (or, for short rows, each group of lanes) keeps its columns'
+// dw and db in registers over its rows and writes them once at its end;
+// colsum_kernel adds the partial rows in their order, so the result does not
+// depend on timing. A row's own values stay as they were loaded: what the sums
+// need of them is computed again for the output, in the shadow of memory.
 // X: type of x (the residual stream's, where there is one).
-template <typename T, typename X, int NV>
-__global__ __launch_bounds__(1024) void norm_bwd_kernel(
+template <typename T, typename X, int NV, bool GATE>
+__global__ __launch_bounds__(NV * vec_of<T>() < 16 ? 1024 : 512, NV == 1 ? 4 : NV == 2 ? 4 : 2) void norm_bwd_kernel(
     const T *__restrict__ dy, const X *__restrict__ x, size_t x_stride,
     const float *__restrict__ weight, const T *__restrict__ z, size_t z_stride,
     const float *__restrict__ mean, const float *__restrict__ rstd, const X *__restrict__ dres,
@@ -163,67 +204,99 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(
     T *__restrict__ dz, float *__restrict__ part, int want_db) {
     constexpr int V = vec_of<T>();
     __shared__ float buf[2][32];
+    if (NV > 1) lpr = 0;  // only whole workgroups hold more than a vector per lane
     const RowGroup g = row_group(lpr);
-    const int step = (lpr ? lpr : (int)blockDim.x) * V;
+    int step = (lpr ? lpr : (int)blockDim.x) * V;
     const float inv = 1.0f / static_cast<float>(D);
-    float w[NV][V], dw[NV][V], db[NV][V];
+    const long long stride = (long long)gridDim.x * g.groups;
+    float dw[NV][V], db[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = g.lane * V + i * step, n = D - c;
-        RowRaw<float, V> a;
-        a.zero();
-        if (n > 0) a.load(weight + c, n);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            w[i][e] = a.get(e);
-            dw[i][e] = db[i][e] = 0.0f;
-        }
-    }
-    int turn = 0;
-    for (long long row = (long long)blockIdx.x * g.groups + g.group; row < rows;
-         row += (long long)gridDim.x * g.groups, turn ^= 1) {
-        const float m = mean ? mean[row] : 0.0f, r = rstd[row];
-        float n_[NV][V], dn[NV][V];
-        RowRaw<X, V> xr[NV];
-        RowRaw<T, V> zr[NV];
-        float s[2] = {0.0f, 0.0f};
+        for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.0f;
+    RowRaw<T, V> yn[NV], zn[NV];
+    RowRaw<X, V> xn[NV];
+    float mn = 0.0f, rn = 0.0f;
+    auto fetch = [&](long long row) {
+        if (row >= rows) return;
+        mn = mean ? mean[row] : 0.0f;
+        rn = rstd[row];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = g.lane * V + i * step, n = D - c;
-            RowRaw<T, V> a;
-            a.zero();
-            xr[i].zero();
-            zr[i].zero();
             if (n > 0) {
-                a.load(dy + row * D + c, n);
-                xr[i].load(x + row * x_stride + c, n);
-                if (z) zr[i].load(z + row * z_stride + c, n);
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float u = xr[i].get(e);
-                if (z) u *= silu_f32(zr[i].get(e));
-                const float d = a.get(e);
-                // past the row's end u = 0, but u - m is not
-                const float nn = e < n ? (u - m) * r : 0.0f;
-                n_[i][e] = nn;
-                dw[i][e] += d * nn;
-                db[i][e] += d;
-                dn[i][e] = d * w[i][e];
-                s[0] += dn[i][e];
-                s[1] += dn[i][e] * nn;
+                yn[i].load(dy + row * D + c, n);
+                xn[i].load(x + row * x_stride + c, n);
+                if (GATE) zn[i].load(z + row * z_stride + c, n);
             }
         }
+    };
+    long long row = (long long)blockIdx.x * g.groups + g.group;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        yn[i].zero();
+        xn[i].zero();
+        if (GATE) zn[i].zero();
+    }
+    constexpr bool AHEAD = NV * V < 16;  // wider rows leave no registers for it
+    if (AHEAD) fetch(row);
+    for (int turn = 0; row < rows; row += stride, turn ^= 1) {
+        if (!AHEAD) {
+            asm volatile("" : "+s"(step));  // the offsets anew each row: kept, they spill
+            fetch(row);
+        }
+        RowRaw<T, V> yr[NV], zr[NV];
+        RowRaw<X, V> xr[NV];
+        const float m = mn, r = rn;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            yr[i] = yn[i];
+            xr[i] = xn[i];
+            if (GATE) zr[i] = zn[i];
+        }
+        if (AHEAD) fetch(row + stride);
+        float s[2] = {0.0f, 0.0f};
+        // normalised value and weighted gradient of element e of vector i
+        auto normal = [&](int i, int e, int n) {
+            float u = xr[i].get(e);
+            if (GATE) u *= silu_f32(zr[i].get(e));
+            return e < n ? (u - m) * r : 0.0f;  // past the row's end u = 0, but u - m is not
+        };
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = g.lane * V + i * step, n = D - c;
+            if (n <= 0) continue;
+            RowRaw<float, V> w;
+            w.load(weight + c, n);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float d = yr[i].get(e), nn = normal(i, e, n), dn = d * w.get(e);
+                dw[i][e] += d * nn;
+                db[i][e] += d;
+                s[0] += dn;
+                s[1] += dn * nn;
+            }
+        }
+        RowRaw<X, V> ar[NV];
+        if (!GATE && AHEAD && dres)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = g.lane * V + i * step, n = D - c;
+                if (n > 0) ar[i].load(dres + row * D + c, n);
+            }
         row_sum(s, lpr, buf[turn]);
         const float c0 = mean ? s[0] * inv : 0.0f, c1 = s[1] * inv;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = g.lane * V + i * step, n = D - c;
             if (n <= 0) continue;
+            RowRaw<float, V> w;
+            w.load(weight + c, n);
             float o[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = r * (dn[i][e] - c0 - n_[i][e] * c1);
-            if (z) {
+            for (int e = 0; e < V; ++e)
+                o[e] = r * (yr[i].get(e) * w.get(e) - c0 - normal(i, e, n) * c1);
+            if (GATE) {
                 float oz[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
@@ -234,10 +307,9 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(
                 row_store(dz + row * D + c, oz, n);
             } else {
                 if (dres) {
-                    RowRaw<X, V> a;
-                    a.load(dres + row * D + c, n);
+                    if (!AHEAD) ar[i].load(dres + row * D + c, n);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) o[e] += a.get(e);
+                    for (int e = 0; e < V; ++e) o[e] += ar[i].get(e);
                 }
                 if (dres_in) row_store(dres_in + row * D + c, o, n);
             }
@@ -309,22 +381,28 @@ NormShape norm_shape(int D, int V, int most) {
     s.threads = ((nvec + s.nv - 1) / s.nv + 63) / 64 * 64;
     return s;
 }
-constexpr int kNormLanes = 1024;
+NormShape norm_fwd_shape(int D, int V) { return norm_shape(D, V, 1024); }
+// The widest rows of the backward (above 8192 values) take half the lanes, which
+// then have twice the registers: 1024 lanes of 128 spilled up to 411 of them.
+NormShape norm_bwd_shape(int D, int V) {
+    const NormShape s = norm_shape(D, V, 1024);
+    return s.nv * V < 16 ? s : norm_shape(D, V, 512);
+}
 
-// Workgroups of the backward: as many as stay resident (2048 lanes per CU at
-// most), but no more than there are rows for, so that few partial rows are
-// written and added up.
-int norm_bwd_blocks(long long rows, const NormShape &s) {
+// Workgroups: as many as run at once (about 1536 lanes to a CU forward, 1024
+// backward, which needs more registers and writes a partial row for each), but
+// no more than there are rows for.
+int norm_blocks(long long rows, const NormShape &s, int lanes) {
     const long long want = (rows + s.groups - 1) / s.groups;
-    const int resident = 256 * (1024 / s.threads > 4 ? 4 : 1024 / s.threads);
+    const int resident = 256 * (lanes / s.threads > 1 ? lanes / s.threads : 1);
     return static_cast<int>(want < resident ? want : resident);
 }
+constexpr int kFwdLanes = 1536, kBwdLanes = 1024;
 
 template <typename T, typename R>
 hipError_t norm_fwd(const NormArgs &a, hipStream_t stream) {
-    const NormShape s = norm_shape(a.width, vec_of<T>(), kNormLanes);
-    const long long want = (a.rows + s.groups - 1) / s.groups;
-    const dim3 grid(static_cast<unsigned>(want < (1 << 20) ? want : (1 << 20)));
+    const NormShape s = norm_fwd_shape(a.width, vec_of<T>());
+    const int grid = norm_blocks(a.rows, s, kFwdLanes);
 #define SSD_NORM_FWD(NV)                                                                          \
     norm_fwd_kernel<T, R, NV><<<grid, s.threads, 0, stream>>>(                                    \
         static_cast<const T *>(a.x), a.x_stride, static_cast<const R *>(a.residual), a.weight,    \
@@ -333,27 +411,37 @@ hipError_t norm_fwd(const NormArgs &a, hipStream_t stream) {
     switch (s.nv) {
         case 1: SSD_NORM_FWD(1); break;
         case 2: SSD_NORM_FWD(2); break;
-        case 4: SSD_NORM_FWD(4); break;
+        case 4:  // float32 only: 16384 values are two vectors of 8 or four of 4 for 1024 lanes
+            if constexpr (sizeof(T) == 4) {
+                SSD_NORM_FWD(4);
+                break;
+            }
         default: return hipErrorInvalidValue;
     }
 #undef SSD_NORM_FWD
     return hipGetLastError();
 }
 
-template <typename T, typename X>
+template <typename T, typename X, bool GATE>
 hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t stream) {
-    const NormShape s = norm_shape(a.width, vec_of<T>(), kNormLanes);
-    const int blocks = norm_bwd_blocks(a.rows, s);
+    const NormShape s = norm_bwd_shape(a.width, vec_of<T>());
+    const int blocks = norm_blocks(a.rows, s, kBwdLanes);
 #define SSD_NORM_BWD(NV)                                                                          \
-    norm_bwd_kernel<T, X, NV><<<blocks, s.threads, 0, stream>>>(                                  \
+    norm_bwd_kernel<T, X, NV, GATE><<<blocks, s.threads, 0, stream>>>(                            \
         static_cast<const T *>(a.dy), static_cast<const X *>(a.x), a.x_stride, a.weight,          \
         static_cast<const T *>(a.z), a.z_stride, a.mean, a.rstd,                                  \
         static_cast<const X *>(a.dresidual), a.rows, a.width, s.lpr, static_cast<T *>(a.dx),      \
         static_cast<X *>(a.dresidual_in), static_cast<T *>(a.dz), a.part, a.dbias != nullptr)
+    constexpr int V = vec_of<T>();  // one vector per lane, float32 two, and the widest rows
     switch (s.nv) {
         case 1: SSD_NORM_BWD(1); break;
-        case 2: SSD_NORM_BWD(2); break;
-        case 4: SSD_NORM_BWD(4); break;
+        case 2:
+            if constexpr (V == 4) {
+                SSD_NORM_BWD(2);
+                break;
+            }
+            return hipErrorInvalidValue;
+        case 32 / V: SSD_NORM_BWD(32 / V); break;
         default: return hipErrorInvalidValue;
     }
 #undef SSD_NORM_BWD
@@ -373,8 +461,8 @@ hipError_t launch_colsum(const float *part, int n, long long cols, long long fir
 }
 
 size_t norm_bwd_part_bytes(long long rows, int width, bool bf16, bool want_db) {
-    const NormShape s = norm_shape(width, bf16 ? 8 : 4, kNormLanes);
-    return (size_t)norm_bwd_blocks(rows, s) * s.groups * (want_db ? 2 : 1) * width * sizeof(float);
+    const NormShape s = norm_bwd_shape(width, bf16 ? 8 : 4);
+    return (size_t)norm_blocks(rows, s, kBwdLanes) * s.groups * (want_db ? 2 : 1) * width * sizeof(float);
 }
 
 hipError_t launch_norm_fwd(const NormArgs &a, bool bf16, bool res_bf16, hipStream_t stream) {
@@ -384,8 +472,13 @@ hipError_t launch_norm_fwd(const NormArgs &a, bool bf16, bool res_bf16, hipStrea
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, bool x_bf16, hipStream_t stream) {
-    if (!bf16) return norm_bwd<float, float>(a, stream);
-    return x_bf16 ? norm_bwd<bf16_t, bf16_t>(a, stream) : norm_bwd<bf16_t, float>(a, stream);
+    // The gate and the residual stream exclude each other, so a gated x has z's type.
+    if (a.z)
+        return bf16 ? norm_bwd<bf16_t, bf16_t, true>(a, stream)
+                    : norm_bwd<float, float, true>(a, stream);
+    if (!bf16) return norm_bwd<float, float, false>(a, stream);
+    return x_bf16 ? norm_bwd<bf16_t, bf16_t, false>(a, stream)
+                  : norm_bwd<bf16_t, float, false>(a, stream);
 }
 
 }  // namespace ssd
