@@ -66,11 +66,14 @@ def _on_gpu(x):
 
 def _call(fn, where, device, *args):
     """fn(*args, the device's current stream), with that device the current one."""
+    # The handle alone: torch.cuda.current_stream builds an object around it, 1.9 us
+    # of a single token's 15 to 17.
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = fn(*args, stream)
     check(rc, where)
 
 
@@ -221,15 +224,15 @@ def _selective_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit):
     pointers = [_slice(x, "x", x.shape, x), _slice(dt, "dt", x.shape, x), _param(A, "A", (E, N), x),
                 _slice(B, "B", B.shape, x), _slice(C, "C", B.shape, x), _param(D, "D", (E,), x),
                 _slice(z, "z", x.shape, x)]
-    for t, name in ((B, "B"), (C, "C")):
-        if G > 1 and t.stride(-2) != N:
-            raise ValueError(f"{name}'s groups must be contiguous")
-    st = _native.SsdSelectiveStrides()
-    for t, name in ((x, "x"), (dt, "dt"), (z, "z"), (B, "B"), (C, "C")):
-        if t is not None:
-            setattr(st, name + "_batch", t.stride(0))
-            if lead == 2:
-                setattr(st, name + "_token", t.stride(1))
+    if G > 1:
+        for t, name in ((B, "B"), (C, "C")):
+            if t.stride(-2) != N:
+                raise ValueError(f"{name}'s groups must be contiguous")
+    strides = []  # (batch, token) of x, dt, z, B, C
+    for t in (x, dt, z, B, C):
+        s = (0, 0) if t is None else t.stride()
+        strides += (s[0], s[1] if lead == 2 else 0)
+    st = _native.SsdSelectiveStrides(*strides)
     opts = None
     if dt_bias is not None or dt_softplus or dt_limit is not None:
         lo, hi = (0.0, 0.0) if dt_limit is None else (float(dt_limit[0]), float(dt_limit[1]))
