@@ -10,6 +10,8 @@
 // registers, so each row is read once per tile and W-1 rows more (its halo);
 // consecutive lanes own consecutive vectors, so a wavefront reads 512 bytes or
 // more of a row at once.
+#include <type_traits>
+
 #include "ssd_launch.h"
 #include "ssd_rows.h"
 
@@ -19,7 +21,7 @@ namespace {
 
 // Vectors of V channels never straddle two parts of the channel axis.
 struct PartVec {
-    int part, col, chan, n;  // part, first column in it, first channel, elements
+    int part, count, col, chan, n;  // part, its width, first column in it, first channel, elements
 };
 template <int V> __device__ __forceinline__ PartVec part_vec(const ConvParts &p, int v) {
     PartVec r;
@@ -30,11 +32,11 @@ template <int V> __device__ __forceinline__ PartVec part_vec(const ConvParts &p,
         v -= nv;
         ++r.part;
     }
-    const int count = r.part == 0 ? p.count[0] : r.part == 1 ? p.count[1] : p.count[2];
+    r.count = r.part == 0 ? p.count[0] : r.part == 1 ? p.count[1] : p.count[2];
     const int first = r.part == 0 ? p.first[0] : r.part == 1 ? p.first[1] : p.first[2];
     r.col = v * V;
     r.chan = first + r.col;
-    r.n = count - r.col;
+    r.n = r.count - r.col;
     return r;
 }
 int part_vecs(const ConvParts &p, int V) {
@@ -79,7 +81,7 @@ __device__ __forceinline__ int find_seq(const int *cu, int nseq, int t) {
 
 // Items: (tile of T tokens, vector), vectors fastest, then (sequence, vector)
 // for the states after each sequence.
-template <typename T, int V, int W>
+template <typename T, int V, int W, int U>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int nvec, int tile, int tiles,
                                                        long long walks, long long items) {
     const long long item = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -137,18 +139,23 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int nvec, int
 #pragma unroll
         for (int e = 0; e < V; ++e) win[j][e] = r.get(e);
     }
-    // rows are fetched U at a time, so U loads are in flight per lane
-    constexpr int U = 8;
-    for (int t = t0; t < t1; t += U) {
+    // U tokens: their rows are fetched together, so U loads are in flight per lane.
+    // `whole`: all of them are in this tile and this sequence and the vector is full,
+    // so nothing is checked row by row.
+    auto rows = [&](int t, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
         RowRaw<T, V> raw[U];
+        const T *from = xp + (size_t)t * a.x_row;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < t1) raw[u].load(xp + (size_t)(t + u) * a.x_row, pv.n);
+        for (int u = 0; u < U; ++u, from += a.x_row)
+            if constexpr (WHOLE) raw[u].load(from);
+            else if (t + u < t1) raw[u].load(from, pv.n);
             else raw[u].zero();
+        T *to = part_row<T>(a.y, pv.part, (size_t)b * L + t) + pv.col;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u >= t1) break;
-            if (t + u >= next) {
+        for (int u = 0; u < U; ++u, to += pv.count) {
+            if (!WHOLE && t + u >= t1) break;
+            if (!WHOLE && t + u >= next) {
                 // a new sequence: nothing before it is seen
                 while (seq + 1 < a.nseq && a.cu_seqlens[seq + 1] <= t + u) ++seq;
                 next = seq + 1 < a.nseq ? a.cu_seqlens[seq + 1] : 0x7fffffff;
@@ -170,9 +177,12 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int nvec, int
                 win[W - 2][e] = xv;
                 o[e] = a.silu ? silu_f32(v) : v;
             }
-            row_store(part_row<T>(a.y, pv.part, (size_t)b * L + t + u) + pv.col, o, pv.n);
+            row_store(to, o, WHOLE ? V : pv.n);
         }
-    }
+    };
+    for (int t = t0; t < t1; t += U)
+        if (pv.n >= V && t + U <= t1 && t + U <= next) rows(t, std::true_type());
+        else rows(t, std::false_type());
 }
 
 // Gradients. With g_t = dy_t silu'(v_t) (v recomputed):
@@ -217,22 +227,33 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdArgs a, int nvec, 
     }
     constexpr int U = 4;
     const int last = t1 + W - 1;  // one past the last token whose g a row of dx here needs
-    for (int t = t0; t < last; t += U) {
+    // `whole`: these tokens are the tile's own (so the rows of dx they write lie
+    // before those that take a gradient of the final state) and the vector is full:
+    // little is checked row by row.
+    auto rows = [&](int t, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
         RowRaw<T, V> xr[U], dr[U];
+        const T *from = xp + (size_t)t * a.x_row;
+        const T *grad = part_row<const T>(a.dy, pv.part, (size_t)b * L + t) + pv.col;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            xr[u].zero();
-            dr[u].zero();
-            if (t + u < last && t + u < L) {
-                xr[u].load(xp + (size_t)(t + u) * a.x_row, pv.n);
-                dr[u].load(part_row<const T>(a.dy, pv.part, (size_t)b * L + t + u) + pv.col, pv.n);
+        for (int u = 0; u < U; ++u, from += a.x_row, grad += pv.count) {
+            if constexpr (WHOLE) {
+                xr[u].load(from);
+                dr[u].load(grad);
+            } else {
+                xr[u].zero();
+                dr[u].zero();
+                if (t + u < last && t + u < L) {
+                    xr[u].load(from, pv.n);
+                    dr[u].load(grad, pv.n);
+                }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int j = t + u;
-            if (j >= last) break;
-            const bool own = j < t1;
+            if (!WHOLE && j >= last) break;
+            const bool own = WHOLE || j < t1;
             float o[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -243,7 +264,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdArgs a, int nvec, 
                 v = fmaf(w[W - 1][e], xv, v);
                 float gv = dr[u].get(e);
                 if (a.silu) gv *= silu_grad_f32(v);
-                if (j >= L) gv = 0.0f;  // past the last token, whatever v is
+                if (!WHOLE && j >= L) gv = 0.0f;  // past the last token, whatever v is
                 if (own) {
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k) dw[k][e] = fmaf(gv, win[k][e], dw[k][e]);
@@ -265,18 +286,21 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdArgs a, int nvec, 
             }
             const int t_out = j - (W - 1);  // token of this row of dx
             if (t_out < t0 && t0 > 0) continue;  // the tile before has it
-            if (dfinal && t_out >= L - (W - 1)) {
+            if (!WHOLE && dfinal && t_out >= L - (W - 1)) {
                 RowRaw<T, V> r;
                 r.load(dfinal + ((size_t)b * (W - 1) + (t_out - (L - (W - 1)))) * K + pv.chan, pv.n);
 #pragma unroll
                 for (int e = 0; e < V; ++e) o[e] += r.get(e);
             }
             if (t_out >= 0)
-                row_store(dx + ((size_t)b * L + t_out) * K + pv.chan, o, pv.n);
+                row_store(dx + ((size_t)b * L + t_out) * K + pv.chan, o, WHOLE ? V : pv.n);
             else if (dinit)
                 row_store(dinit + ((size_t)b * (W - 1) + (t_out + W - 1)) * K + pv.chan, o, pv.n);
         }
-    }
+    };
+    for (int t = t0; t < last; t += U)
+        if (pv.n >= V && t + U <= t1) rows(t, std::true_type());
+        else rows(t, std::false_type());
     // dweight's own layout [K][W], then the bias's [K]
     float *p = a.part + (size_t)ti * (W + 1) * K;
     float flat[V * W];
@@ -324,7 +348,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(T *__restrict__ state,
     row_store(part_row<T>(y, pv.part, b) + pv.col, o, pv.n);
 }
 
-constexpr int kFwdTile = 32, kFwdTileMin = 8;
+constexpr int kFwdTile = 16, kFwdTileMin = 8;
 constexpr int kBwdTile = 128, kBwdTileMin = 8;
 
 // Tokens per tile: long tiles read fewer halo rows (and, backward, write fewer
@@ -335,7 +359,7 @@ int tile_of(int batch, int seqlen, int nvec, int most, int least, long long want
     while (t > least && (long long)batch * ((seqlen + t - 1) / t) * nvec < want) t /= 2;
     return t;
 }
-constexpr long long kFwdLanes = 256LL * 2048 / 2, kBwdLanes = 256LL * 1024;
+constexpr long long kFwdLanes = 256LL * 2048 / 2, kBwdLanes = 256LL * 512;
 
 int bwd_tile(int batch, int seqlen, int channels) {
     return tile_of(batch, seqlen, (channels + 3) / 4, kBwdTile, kBwdTileMin, kBwdLanes);
@@ -343,7 +367,7 @@ int bwd_tile(int batch, int seqlen, int channels) {
 
 template <typename T>
 hipError_t conv_fwd(const ConvArgs &a, hipStream_t stream) {
-    constexpr int V = sizeof(T) == 2 ? 8 : 4;
+    constexpr int V = 4, U = 8;
     const int nvec = part_vecs(a.y, V);
     const int tile = tile_of(a.batch, a.seqlen, nvec, kFwdTile, kFwdTileMin, kFwdLanes);
     const int tiles = (a.seqlen + tile - 1) / tile;
@@ -354,9 +378,9 @@ hipError_t conv_fwd(const ConvArgs &a, hipStream_t stream) {
     if (blocks >= (1LL << 24)) return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(blocks));
     switch (a.width) {
-        case 2: conv_fwd_kernel<T, V, 2><<<grid, 256, 0, stream>>>(a, nvec, tile, tiles, walks, items); break;
-        case 3: conv_fwd_kernel<T, V, 3><<<grid, 256, 0, stream>>>(a, nvec, tile, tiles, walks, items); break;
-        case 4: conv_fwd_kernel<T, V, 4><<<grid, 256, 0, stream>>>(a, nvec, tile, tiles, walks, items); break;
+        case 2: conv_fwd_kernel<T, V, 2, U><<<grid, 256, 0, stream>>>(a, nvec, tile, tiles, walks, items); break;
+        case 3: conv_fwd_kernel<T, V, 3, U><<<grid, 256, 0, stream>>>(a, nvec, tile, tiles, walks, items); break;
+        case 4: conv_fwd_kernel<T, V, 4, U><<<grid, 256, 0, stream>>>(a, nvec, tile, tiles, walks, items); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
@@ -404,7 +428,7 @@ template <typename T>
 static hipError_t conv_step(void *state, const void *x, size_t x_row, const float *weight,
                             const float *bias, int batch, int K, int width, int silu,
                             const ConvParts &y, hipStream_t stream) {
-    constexpr int V = sizeof(T) == 2 ? 8 : 4;
+    constexpr int V = 4, U = 8;
     const int nvec = part_vecs(y, V);
     const long long items = (long long)batch * nvec, blocks = (items + 255) / 256;
     if (blocks >= (1LL << 24)) return hipErrorInvalidValue;
