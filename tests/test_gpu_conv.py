@@ -36,7 +36,7 @@ def check_y(name, y, x, w, b, act, init=None, cu=None):
     return final
 
 
-# lengths around the tile (32 and 8 tokens) and the 8 rows fetched at a time, shorter
+# lengths around the tile (16 and 8 tokens) and the 8 rows fetched at a time, shorter
 # than the filter, one token; channels below, at and past a vector, odd ones
 SIZES = [(1, 1, 1), (2, 1, 16), (1, 2, 7), (3, 3, 8), (2, 9, 33), (1, 31, 64), (2, 32, 5),
          (1, 33, 100), (2, 65, 17), (1, 257, 40), (1, 100, 1025)]
