@@ -360,6 +360,8 @@ int ssd_selective_forward(const void *x, const void *dt, const float *A, const v
     if (rc != SSD_OK) return rc;
     char *base = static_cast<char *>(workspace);
     auto at = [&](size_t off) { return reinterpret_cast<float *>(base + off); };
+    a.units = w.plan.units;
+    a.whole = w.plan.whole;
     a.segs = w.plan.segs;
     a.seg_len = w.plan.seg_len;
     a.bc = at(w.bc);
@@ -419,6 +421,8 @@ int ssd_selective_backward(const void *x, const void *dt, const float *A, const 
     char *base = static_cast<char *>(workspace);
     auto at = [&](size_t off) { return reinterpret_cast<float *>(base + off); };
     b.f.init = init_state;
+    b.f.units = w.plan.units;
+    b.f.whole = w.plan.whole;
     b.f.segs = w.plan.segs;
     b.f.seg_len = w.plan.seg_len;
     b.f.bc = at(w.bc);

@@ -62,12 +62,13 @@ __device__ __forceinline__ void sel_steps(const DtOpts &o, float (&d)[V], bool i
 struct SelBlock {
     int b, seg, g, block, first, n;
 };
-template <int CH> __device__ __forceinline__ SelBlock sel_block(int id, int channels, int ngroups, int segs) {
+// (units: a sequence's workgroups, one sequence after the other)
+template <int CH> __device__ __forceinline__ SelBlock sel_block(int unit, int seg, int channels, int ngroups) {
     const int each = channels / ngroups, per = (each + CH - 1) / CH;
     SelBlock k;
-    const int cb = id % (per * ngroups), rest = id / (per * ngroups);
-    k.seg = rest % segs;
-    k.b = rest / segs;
+    const int cb = unit % (per * ngroups);
+    k.seg = seg;
+    k.b = unit / (per * ngroups);
     k.g = cb / per;
     k.block = cb % per;
     const int at = k.block * CH;
@@ -90,6 +91,10 @@ template <int NS> __device__ __forceinline__ void lane_store(float *p, int E, co
     for (int i = 0; i < NS; i += 4)
         *reinterpret_cast<float4 *>(p + (size_t)i * E) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
+
+// Waits for the scalar loads and LDS reads under way (their counter to 0, the others
+// at their most).
+__device__ __forceinline__ void wait_lgkm() { __builtin_amdgcn_s_waitcnt(0xc07f); }
 
 // A row vector's place within a tile, in bytes from the tile's first row: with
 // the tile's address uniform it is the 32-bit offset of the load or store, and

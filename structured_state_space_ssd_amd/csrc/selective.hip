@@ -72,12 +72,18 @@ __global__ __launch_bounds__((SelShape<NK, (MODE >= SEL_KEEP)>::THREADS)) void s
     __shared__ float2 du[TILE * CH];                          // (dt, dt x)
     __shared__ float ys[OUT ? WS * TILE * CH : ADJ ? TILE * CH : 1];  // parts of y; or dy silu(z)
 
-    const int segs = MODE == SEL_STATE ? a.segs - 1 : a.segs;
-    const SelBlock k = sel_block<CH>(blockIdx.x, a.channels, a.ngroups, segs);
+    // the first `whole` units in one piece, the others segment by segment
+    const int first = MODE == SEL_STATE ? a.whole : 0, id = blockIdx.x + first;
+    const bool uncut = id < a.whole;
+    const int cut = a.units - a.whole;
+    const SelBlock k = uncut ? sel_block<CH>(id, 0, a.channels, a.ngroups)
+                             : sel_block<CH>(a.whole + (id - a.whole) % cut, (id - a.whole) / cut,
+                                             a.channels, a.ngroups);
+    const bool last_seg = uncut || k.seg == a.segs - 1;
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ws = w % WS, ch = w / WS * 64 + (tid & 63), n0 = ws * NS;
     const int N = a.dstate, E = a.channels;
-    const int t_begin = k.seg * a.seg_len, t_end = min(a.seqlen, t_begin + a.seg_len);
+    const int t_begin = k.seg * a.seg_len, t_end = last_seg ? a.seqlen : t_begin + a.seg_len;
     const bool gate = (OUT || ADJ) && a.z != nullptr;
     // rows of the tile at hand
     const T *x = static_cast<const T *>(a.x) + k.b * a.x_batch + k.first + t_begin * a.x_token;
@@ -110,7 +116,7 @@ __global__ __launch_bounds__((SelShape<NK, (MODE >= SEL_KEEP)>::THREADS)) void s
             G[i] = 0.0f;
         }
     if (OUT && live) {
-        const size_t at = (size_t)k.b * (segs - 1);
+        const size_t at = (size_t)k.b * (a.segs - 1);
         sel_fold<NK>(a.seg_state + seg_at(at), a.seg_sum + at * E + k.first + ch, 1, E, k.seg, A2, h);
     }
 
@@ -152,15 +158,26 @@ __global__ __launch_bounds__((SelShape<NK, (MODE >= SEL_KEEP)>::THREADS)) void s
         if (OUT && a.D) Dv.load(a.D + k.first + c, k.n - c);
     }
 
-    // B and C of GR tokens, from the t-th of the tile at hand on (past the tile, the next
-    // one's; the buffer has a tile to spare at its end)
+    // What GR tokens from the t-th of the tile at hand on need: B and C (past the tile,
+    // the next one's; the buffer has a tile to spare at its end), the step sizes and,
+    // for the adjoint, the gradients (past the tile, any).
     constexpr int GR = 16 / NS;
     SelBC bcv[2][GR][NS / 4];
+    float2 dv[2][GR];
+    float gv[2][GR];
     auto scalars = [&](int t, int s) {
 #pragma unroll
         for (int u = 0; u < GR; ++u)
 #pragma unroll
             for (int i = 0; i < NS / 4; ++i) bcv[s][u][i] = bc[(t + u) * (NK / 4) + i];
+    };
+    auto steps = [&](int t, int s) {
+        const int r = t % TILE;
+#pragma unroll
+        for (int u = 0; u < GR; ++u) {
+            dv[s][u] = du[(r + u) * CH + ch];
+            if (ADJ) gv[s][u] = ys[(r + u) * CH + ch];
+        }
     };
 
     fetch(t_begin, 0, 0);
@@ -190,6 +207,7 @@ __global__ __launch_bounds__((SelShape<NK, (MODE >= SEL_KEEP)>::THREADS)) void s
             }
         }
         __syncthreads();
+        steps(0, 0);
         if (t0 + TILE < t_end) fetch(t0, TILE, p ^ 1);
         const int nt = min(TILE, t_end - t0);
         for (int tb = 0; tb < nt; tb += U) {
@@ -201,15 +219,20 @@ __global__ __launch_bounds__((SelShape<NK, (MODE >= SEL_KEEP)>::THREADS)) void s
                 }
 #pragma unroll
             for (int g = 0; g < U; g += GR) {
-                // the next tokens' B and C set out while these are used
+                // The next tokens' operands set out while these are used. Scalar loads
+                // come back in any order, so whoever uses one waits for all under way:
+                // these have to be here before the next are sent for.
                 const int s = g / GR % 2;
+                __builtin_amdgcn_sched_barrier(0);
+                wait_lgkm();
                 scalars(tb + g + GR, s ^ 1);
+                steps(tb + g + GR, s ^ 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int u = 0; u < GR; ++u) {
                     const int t = tb + g + u;
-                    const float2 d = du[t * CH + ch];
-                    const float dyv = ADJ ? ys[t * CH + ch] : 0.0f;
+                    const float2 d = dv[s][u];
+                    const float dyv = ADJ ? gv[s][u] : 0.0f;
                     float yv = 0.0f;
 #pragma unroll
                     for (int i = 0; i < NS; ++i) {
@@ -277,7 +300,7 @@ __global__ __launch_bounds__((SelShape<NK, (MODE >= SEL_KEEP)>::THREADS)) void s
                 }
                 lane_store(a.seg_adj + seg_at(at - 1), E, G);
             }
-    } else if (a.final_state && k.seg == segs - 1 && nn > 0) {
+    } else if (a.final_state && last_seg && nn > 0) {
         row_store(a.final_state + ((size_t)k.b * E + k.first + ch) * N + n0, h, nn);
     }
 }
@@ -342,22 +365,22 @@ template <typename T, int NK> hipError_t sel_bc(const SelArgs &a, hipStream_t st
 
 template <typename T, int NK> hipError_t sel_fwd(const SelArgs &a, hipStream_t stream) {
     hipError_t e = sel_bc<T, NK>(a, stream);
-    const int blocks = selective_blocks(a.channels, a.ngroups, a.dstate);
+    const int cut = a.units - a.whole;
     if (e == hipSuccess && a.segs > 1) {
         selective_fwd_kernel<T, NK, SEL_STATE>
-            <<<static_cast<unsigned>(blocks * (a.segs - 1) * a.batch), 256, 0, stream>>>(a);
+            <<<static_cast<unsigned>(cut * (a.segs - 1)), 256, 0, stream>>>(a);
         e = hipGetLastError();
     }
     if (e != hipSuccess) return e;
     selective_fwd_kernel<T, NK, SEL_OUT>
-        <<<static_cast<unsigned>(blocks * a.segs * a.batch), 256, 0, stream>>>(a);
+        <<<static_cast<unsigned>(a.whole + cut * a.segs), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <typename T, int NK> hipError_t sel_keep_launch(const SelArgs &a, hipStream_t stream) {
     const hipError_t e = sel_bc<T, NK>(a, stream);
     if (e != hipSuccess) return e;
-    const unsigned grid = selective_blocks(a.channels, a.ngroups, a.dstate) * a.segs * a.batch;
+    const unsigned grid = a.units * a.segs;
     constexpr int threads = SelShape<NK, true>::THREADS;
     if (a.segs > 1) selective_fwd_kernel<T, NK, SEL_BOTH><<<grid, threads, 0, stream>>>(a);
     else selective_fwd_kernel<T, NK, SEL_KEEP><<<grid, threads, 0, stream>>>(a);
@@ -390,22 +413,23 @@ int selective_blocks(int channels, int ngroups, int dstate) {
     return ngroups * ((each + ch - 1) / ch);
 }
 
-// The token axis cut so that at most `want` workgroups run, whole tiles to a
-// segment and two at least.
-static SelPlan sel_cut(int batch, int seqlen, int channels, int ngroups, int dstate, long long want) {
+// Units from the `whole`-th on cut along the token axis into at most `most`
+// segments, whole tiles to a segment and two at least.
+static SelPlan sel_cut(int batch, int seqlen, int channels, int ngroups, int dstate, int whole,
+                       long long most) {
     const int nk = selective_kernel_dstate(dstate), tile = 2048 / selective_ch(dstate);
-    const long long wgs = (long long)batch * selective_blocks(channels, ngroups, dstate);
+    const int units = static_cast<int>((long long)batch * selective_blocks(channels, ngroups, dstate));
     const int tiles = (seqlen + tile - 1) / tile;
-    long long s = want / wgs;
+    long long s = most;
     if (s > tiles / 2) s = tiles / 2;
     if (s > 128) s = 128;  // every segment folds the ones before it
-    SelPlan p{1, seqlen, 0};
+    SelPlan p{units, whole, 1, seqlen, 0};
     if (s > 1) {
         const int per = static_cast<int>((tiles + s - 1) / s);
         p.seg_len = per * tile;
         p.segs = (seqlen + p.seg_len - 1) / p.seg_len;
     }
-    if (p.segs <= 1) p = SelPlan{1, seqlen, 0};
+    if (p.segs <= 1) p = SelPlan{units, 0, 1, seqlen, 0};
     p.seg_floats = (size_t)batch * (p.segs - 1) * channels * nk;
     return p;
 }
@@ -415,8 +439,14 @@ static SelPlan sel_cut(int batch, int seqlen, int channels, int ngroups, int dst
 // in bf16: 320 workgroups (batch 4) 336 us uncut, 322 to 346 in 4 to 16
 // segments; 640 478 uncut, 612 in 4; 160 299 and 186 (in 16); 80 297 and 111 (in 24).
 SelPlan selective_plan(int batch, int seqlen, int channels, int ngroups, int dstate) {
-    const long long wgs = (long long)batch * selective_blocks(channels, ngroups, dstate);
-    return sel_cut(batch, seqlen, channels, ngroups, dstate, wgs < 320 ? 2048 : 1);
+    constexpr long long CUS = 256;
+    const long long units = (long long)batch * selective_blocks(channels, ngroups, dstate);
+    if (units < CUS) return sel_cut(batch, seqlen, channels, ngroups, dstate, 0, 2048 / units);
+    const long long rest = units % CUS;
+    if (units < 4 * CUS && rest > 0 && rest <= CUS / 2)
+        return sel_cut(batch, seqlen, channels, ngroups, dstate, static_cast<int>(units - rest),
+                       rest <= 64 ? 8 : 512 / rest);
+    return sel_cut(batch, seqlen, channels, ngroups, dstate, 0, 1);
 }
 
 // The backward's first walk is made either way, so cutting costs it little and
@@ -425,7 +455,8 @@ SelPlan selective_plan(int batch, int seqlen, int channels, int ngroups, int dst
 // 1892 in 8; 320 1624 and 972 (in 6; 1106 in 4, whose last round is half
 // empty); 160 1400 and 523 (in 12); 80 1369 and 296 (in 24).
 SelPlan selective_bwd_plan(int batch, int seqlen, int channels, int ngroups, int dstate) {
-    return sel_cut(batch, seqlen, channels, ngroups, dstate, 2048);
+    const long long units = (long long)batch * selective_blocks(channels, ngroups, dstate);
+    return sel_cut(batch, seqlen, channels, ngroups, dstate, 0, 2048 / units);
 }
 
 size_t selective_bc_floats(int batch, int seqlen, int ngroups, int dstate) {

@@ -48,7 +48,7 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
     __shared__ __attribute__((aligned(16))) float tr[THREADS / 64 * 2 * 8 * 64];
 
     const SelArgs &a = ba.f;
-    const SelBlock k = sel_block<CH>(blockIdx.x, a.channels, a.ngroups, a.segs);
+    const SelBlock k = sel_block<CH>(blockIdx.x % a.units, blockIdx.x / a.units, a.channels, a.ngroups);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ws = w % WS, ch = w / WS * 64 + lane, n0 = ws * NS;
     const int N = a.dstate, E = a.channels, L = a.seqlen;
@@ -391,7 +391,7 @@ template <typename T, int NK> hipError_t sel_bwd(const SelBwdArgs &ba, hipStream
     const int blocks = selective_blocks(a.channels, a.ngroups, a.dstate);
     hipError_t e = launch_selective_keep(a, sizeof(T) == 2, stream);
     if (e != hipSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(blocks * a.segs * a.batch);
+    const unsigned grid = static_cast<unsigned>(a.units * a.segs);
     if (a.z) selective_bwd_kernel<T, NK, true><<<grid, SelShape<NK, true>::THREADS, 0, stream>>>(ba);
     else selective_bwd_kernel<T, NK, false><<<grid, SelShape<NK, true>::THREADS, 0, stream>>>(ba);
     e = hipGetLastError();

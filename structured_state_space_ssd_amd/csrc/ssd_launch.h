@@ -239,7 +239,8 @@ struct SelArgs {
     const float *init;                // [Bt][E][N], nullable
     DtOpts opts;                      // bias [E]; no zero-order hold
     int batch, seqlen, channels, ngroups, dstate;
-    int segs, seg_len;                // segments of the token axis
+    int units, whole;                 // workgroups of all sequences; the first so many uncut
+    int segs, seg_len;                // the others' segments of the token axis
     float *bc;                        // B and C as the kernels read them: scratch
     float *seg_state, *seg_sum;       // [Bt][segs - 1][E * NK], [Bt][segs - 1][E]: scratch
     void *y;                          // [Bt][L][E] dense
@@ -256,7 +257,7 @@ struct SelArgs {
 int selective_kernel_dstate(int dstate);
 int selective_blocks(int channels, int ngroups, int dstate);
 struct SelPlan {
-    int segs, seg_len;
+    int units, whole, segs, seg_len;
     size_t seg_floats;  // of seg_state
 };
 size_t selective_bc_floats(int batch, int seqlen, int ngroups, int dstate);

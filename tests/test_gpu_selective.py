@@ -48,11 +48,12 @@ SIZES = [(1, 1, 1, 1, 1), (2, 1, 64, 16, 1), (1, 2, 5, 3, 1), (2, 7, 256, 4, 1),
          (1, 32, 96, 13, 3), (1, 33, 40, 32, 1), (2, 65, 66, 24, 2), (1, 40, 20, 64, 1),
          (1, 67, 34, 50, 2), (3, 100, 12, 16, 4)]
 # few channels over many tokens: cut into segments (the last one shorter than the others)
+# (260, 270: a few more workgroups than CUs, of which only those few are cut)
 LONG = [(1, 300, 64, 16, 1), (1, 1000, 8, 16, 1), (2, 517, 33, 5, 1), (1, 700, 16, 64, 1), (1, 260, 300, 3, 2)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("size", SIZES + LONG, ids=str)
+@pytest.mark.parametrize("size", SIZES + LONG + [(260, 130, 8, 16, 1), (270, 41, 6, 3, 2)], ids=str)
 def test_selective_forward(ssd, size, dtype):
     for D, z, init, sliced, soft in ((True, True, True, 5, True), (False, False, False, 0, False),
                                      (True, False, True, 8, False)):
