@@ -12,6 +12,13 @@
 // group of lanes: the smallest power of two of one wavefront that has a lane
 // for every vector of the row, or the whole workgroup for longer rows, whose
 // wavefronts meet once through LDS per sum.
+//
+// Measured where a large copy runs at 4.9 to 5.3 TB/s (read and written): 16384
+// rows of 2560 bf16 values with a float32 residual stream, forward 100 us (5.0
+// TB/s), backward 132 us (5.1 TB/s) and 5 us for the sum of the partial rows;
+// gated, 4099 rows of 5120, forward 33 us (3.8 TB/s) and backward 61 us (3.4
+// TB/s): 640 lanes to a row leave a CU two, backward one workgroup, whose
+// wavefronts wait for the sums together. 4 rows of 2560: 3.4 us, a launch.
 #include <type_traits>
 
 #include "ssd_launch.h"
@@ -94,7 +101,8 @@ template <typename T> constexpr int vec_of() { return sizeof(T) == 2 ? 8 : 4; }
 
 // Rows are taken with the stride of the grid, which holds as many as run at
 // once; the next row sets out while one is worked on, so that its way from
-// memory hides behind the sums and their barriers.
+// memory hides behind the sums and their barriers (backward, 16384 rows of 2560:
+// 163 us with a grid of all rows, 132 so).
 //
 // T: type of x, z, y. R: type of the residual stream.
 template <typename T, typename R, int NV>
@@ -327,30 +335,29 @@ __global__ __launch_bounds__(NV * vec_of<T>() < 16 ? 1024 : 512, NV == 1 ? 4 : N
     }
 }
 
-// out[c] = sum over k < n of part[k][c]: 64 columns per workgroup, 16 strands
-// of rows each, added in a fixed order.
+// out[c] = sum over k < n of part[k][c]: 1024 / COLS strands of rows to a column,
+// added in a fixed order. 32 columns to a workgroup while that gives each CU two
+// workgroups at most, else 64, a wavefront's full width: 768 rows of 5120 columns
+// 4.8 us with 32 and 6.0 with 64, 24 rows of 81920 9.2 and 6.1.
+template <int COLS>
 __global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ part, int n,
                                                       long long cols, long long first,
                                                       float *__restrict__ out0,
                                                       float *__restrict__ out1) {
-    __shared__ float acc[16][64];
-    const int l = threadIdx.x & 63, strand = threadIdx.x >> 6;
-    const long long c = (long long)blockIdx.x * 64 + l;
-    float a = 0.0f, b = 0.0f;
-    if (c < cols) {
-        int k = strand;
-        for (; k + 16 < n; k += 32) {
-            a += part[(size_t)k * cols + c];
-            b += part[(size_t)(k + 16) * cols + c];
-        }
-        if (k < n) a += part[(size_t)k * cols + c];
-    }
-    acc[strand][l] = a + b;
+    constexpr int STRANDS = 1024 / COLS;
+    __shared__ float buf[STRANDS][COLS];
+    const int col = threadIdx.x % COLS, strand = threadIdx.x / COLS;
+    const long long c = (long long)blockIdx.x * COLS + col;
+    float s = 0.0f;
+    if (c < cols)
+#pragma unroll 4
+        for (int k = strand; k < n; k += STRANDS) s += part[k * cols + c];
+    buf[strand][col] = s;
     __syncthreads();
     if (strand == 0 && c < cols) {
-        float s = 0.0f;
+        s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) s += acc[k][l];
+        for (int k = 0; k < STRANDS; ++k) s += buf[k][col];
         if (c < first) {
             if (out0) out0[c] = s;
         } else if (out1) out1[c - first] = s;
@@ -391,7 +398,9 @@ NormShape norm_bwd_shape(int D, int V) {
 
 // Workgroups: as many as run at once (about 1536 lanes to a CU forward, 1024
 // backward, which needs more registers and writes a partial row for each), but
-// no more than there are rows for.
+// no more than there are rows for. At 16384 x 2560: forward 106, 99 and 131 us
+// with 1024, 1536 and 2048 lanes to a CU (the last do not all fit, and a second
+// round begins), backward 145, 132 and 156 us with 640, 1024 and 1280.
 int norm_blocks(long long rows, const NormShape &s, int lanes) {
     const long long want = (rows + s.groups - 1) / s.groups;
     const int resident = 256 * (lanes / s.threads > 1 ? lanes / s.threads : 1);
@@ -455,8 +464,10 @@ hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t stream) {
 
 hipError_t launch_colsum(const float *part, int n, long long cols, long long first, float *out0,
                          float *out1, hipStream_t stream) {
-    colsum_kernel<<<static_cast<unsigned>((cols + 63) / 64), 1024, 0, stream>>>(part, n, cols,
-                                                                                 first, out0, out1);
+    const auto grid = [&](int per) { return static_cast<unsigned>((cols + per - 1) / per); };
+    if (cols <= 16384)
+        colsum_kernel<32><<<grid(32), 1024, 0, stream>>>(part, n, cols, first, out0, out1);
+    else colsum_kernel<64><<<grid(64), 1024, 0, stream>>>(part, n, cols, first, out0, out1);
     return hipGetLastError();
 }
 

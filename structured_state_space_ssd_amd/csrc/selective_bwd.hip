@@ -10,7 +10,11 @@
 // state sizes), and the walk back rebuilds a tile's states in registers from
 // there, with their decays, then runs the adjoint over them. Channels and
 // states lie over lanes and wavefronts as in the forward. Bound by vector
-// issue, of which the rebuilding is a quarter.
+// issue, of which the rebuilding is a quarter. Measured in bf16 at 4 x 2048
+// tokens of 5120 channels and 16 states: first walk 226 us, walk back 650 us
+// (vector units busy 73% of the time, two workgroups to a CU by their registers
+// and LDS), partial dB and dC 15 us; float32, 2 x 777 tokens of 1000 channels and
+// 24 states: 24, 70 and 5 us.
 //
 // Sums over channels (dB, dC) are sums over lanes, of eight values per token
 // and four states: each wavefront lays them out in LDS, value by value, and
