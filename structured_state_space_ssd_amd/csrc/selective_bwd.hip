@@ -263,10 +263,10 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
                         const int i = s4 * 4 + j;
                         const float g = fmaf(dyv, bcv[s][u][i / 4][4 + i % 4], ag[i]);
                         gB = fmaf(g, bcv[s][u][i / 4][i % 4], gB);
-                        const float gq = g * (dec[t][i] * (t ? h[t - 1][i] : hk[i]));
+                        ag[i] = dec[t][i] * g;
+                        const float gq = ag[i] * (t ? h[t - 1][i] : hk[i]);
                         gA = fmaf(A2[i], gq, gA);
                         dA[i] = fmaf(d.x, gq, dA[i]);
-                        ag[i] = dec[t][i] * g;
                         v[j] = d.y * g;
                         v[4 + j] = dyv * h[t][i];
                     }
