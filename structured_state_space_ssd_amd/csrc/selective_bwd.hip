@@ -11,17 +11,18 @@
 // there, with their decays, then runs the adjoint over them. Channels and
 // states lie over lanes and wavefronts as in the forward. Bound by vector
 // issue, of which the rebuilding is a quarter. Measured in bf16 at 4 x 2048
-// tokens of 5120 channels and 16 states: first walk 226 us, walk back 650 us
+// tokens of 5120 channels and 16 states: first walk 226 us, walk back 630 us
 // (vector units busy 73% of the time, two workgroups to a CU by their registers
 // and LDS), partial dB and dC 15 us; float32, 2 x 777 tokens of 1000 channels and
-// 24 states: 24, 70 and 5 us.
+// 24 states: 24, 66 and 5 us.
 //
 // Sums over channels (dB, dC) are sums over lanes, of eight values per token
-// and four states: each wavefront lays them out in LDS, value by value, and
-// reads them back with eight lanes to a value and eight channels to a lane;
-// seven additions and three DPP steps end the sum, where a butterfly over 64
-// lanes in registers takes 26 instructions. Workgroups meet in partial tensors
-// that are added in a fixed order. Sums over tokens (dA, dD, the bias) stay in
+// and four states: three steps swap halves between registers, so that each
+// leaves half the values, spread over half the lanes, and three more add up the
+// eight lanes that then hold a value: 24 instructions, where eight butterflies
+// over 64 lanes take 96, and no LDS (through which the same took as long, and
+// 11% of the time in bank conflicts). Workgroups meet in partial tensors that are
+// added in a fixed order. Sums over tokens (dA, dD, the bias) stay in
 // registers and end in partial rows the same way.
 //
 // With segments (see the forward) the first walk also makes every segment's
@@ -47,9 +48,7 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
     __shared__ float py[GATE ? WS * TB * CH : 1];  // and sum_n (C h)
     // the channels' bias and D, which the walk leaves no registers for
     __shared__ __attribute__((aligned(16))) float biases[CH], Ds[CH];
-    // each wavefront's eight values by 64 channels, twice; after the last tile every
-    // lane's dD and bias sums
-    __shared__ __attribute__((aligned(16))) float tr[THREADS / 64 * 2 * 8 * 64];
+    __shared__ float tr[2 * THREADS * V];  // after the last tile every lane's dD and bias sums
 
     const SelArgs &a = ba.f;
     const SelBlock k = sel_block<CH>(blockIdx.x % a.units, blockIdx.x / a.units, a.channels, a.ngroups);
@@ -216,25 +215,32 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
             if (GATE) z -= TB * a.z_token;
             fetch(t0 - TB, dense - (size_t)TB * E, xn, dn, zn, yn);
         };
-        // a wavefront's eight sums of a token and four states, from its 2 KB of products
-        float *const mine = &tr[w * 1024];
-        const int from = (lane >> 3) * 64 + (lane & 7) * 4;
         // not a constant of the loop: eight lane masks would be kept for the comparisons below
         const int turn = ragged(lane & 7);
-        float4 r0, r1;
-        auto sums_load = [&](int buf) {
-            __builtin_amdgcn_wave_barrier();
-            r0 = *reinterpret_cast<const float4 *>(&mine[buf * 512 + from]);
-            r1 = *reinterpret_cast<const float4 *>(&mine[buf * 512 + from + 32]);
-            __builtin_amdgcn_wave_barrier();
-        };
-        auto sums_end = [&](int t, int s4) {
-            float sum = ((r0.x + r0.y) + (r0.z + r0.w)) + ((r1.x + r1.y) + (r1.z + r1.w));
-            auto add = [](float v, int o) { return v + __int_as_float(o); };
+        // The sums over the lanes of a token's eight values with four states. Each of the
+        // first three steps halves the lanes that a value is spread over and with them the
+        // values that a lane holds; lane 8 v + u ends with value v and keeps it for the
+        // row's u-th token.
+        auto sums = [&](int t, int s4, const float (&v)[8]) {
+            auto add = [](float x, int o) { return x + __int_as_float(o); };
+            float p[4], q2[2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[j]), __float_as_uint(v[j + 4]), false, false);
+                p[j] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(p[j]), __float_as_uint(p[j + 2]), false, false);
+                q2[j] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+            }
+            const bool odd = lane & 8;
+            const float send = odd ? q2[0] : q2[1];
+            float sum = add(odd ? q2[1] : q2[0],
+                            __builtin_amdgcn_update_dpp(0, __float_as_int(send), 0x128, 0xf, 0xf, true));
             sum = add(sum, __builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0xB1, 0xf, 0xf, true));
             sum = add(sum, __builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x4E, 0xf, 0xf, true));
             sum = add(sum, __builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x141, 0xf, 0xf, true));
-            // lane 8 v + u keeps value v of the row's u-th token
             if (t % TOK == TOK - 1) res[s4] = sum;
             else res[s4] = turn == t % TOK ? sum : res[s4];
             if (t % TOK == 0 && t < nt)  // nt: rows past the sequence's are another's
@@ -254,9 +260,6 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
                 float gB = 0.0f, gA = 0.0f;
 #pragma unroll
                 for (int s4 = 0; s4 < NS / 4; ++s4) {
-                    // a set of products is summed while the next one is made
-                    const int step = (TB - 1 - t) * (NS / 4) + s4;
-                    if (step) sums_load((step - 1) % 2);
                     float v[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -270,15 +273,11 @@ __global__ __launch_bounds__((SelShape<NK, true>::THREADS), 2) void selective_bw
                         v[j] = d.y * g;
                         v[4 + j] = dyv * h[t][i];
                     }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) mine[step % 2 * 512 + j * 64 + lane] = v[j];
-                    if (step) sums_end(s4 ? t : t + 1, s4 ? s4 - 1 : NS / 4 - 1);
+                    sums(t, s4, v);
                 }
                 pg[(ws * TB + t) * CH + ch] = make_float2(gB, gA);
             }
         }
-        sums_load((TB * (NS / 4) - 1) % 2);
-        sums_end(0, NS / 4 - 1);
         T *const dx = static_cast<T *>(ba.dx) + dense, *const ddt = static_cast<T *>(ba.ddt) + dense;
         T *const dz = GATE ? static_cast<T *>(ba.dz) + dense : nullptr;
         if (t0 > t_begin) {
