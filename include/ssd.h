@@ -485,6 +485,9 @@ int ssd_chunk_scan(const void *x, const float *delta, const float *dA_cumsum, co
  *                HOST array of device pointers.
  *   final_state  nullable, [Bt][W-1][K] ([nseq][W-1][K] for packed sequences) in
  *                dtype: the last W-1 inputs, what ssd_conv_step goes on from.
+ * Outputs must not overlap inputs. A call whose grid would reach 2^24 workgroups
+ * (here one for 256 vectors of 4 channels and 8 tokens at least) returns
+ * SSD_ERR_UNSUPPORTED.
  */
 int ssd_conv_forward(const void *x, long long x_batch_stride, long long x_token_stride,
                      const float *weight, const float *bias, const void *init_state,
@@ -537,10 +540,11 @@ int ssd_conv_step(void *state, const void *x, long long x_batch_stride, const fl
  *   opts         nullable, as for ssd_forward_ex with dt_bias float32 [E];
  *                discretization must be SSD_DISC_EULER (else SSD_ERR_OPTION).
  *   workspace    at least ssd_selective_forward_workspace_size(...) bytes,
- *                256-byte aligned (NULL where that is 0): with few channels the
- *                token axis is cut into segments, whose states it holds.
- * E % G must be 0 (SSD_ERR_SHAPE). Token strides of 2^24 elements or more, and
- * a call whose grid would reach 2^24 workgroups (1024 / N channels each, at
+ *                256-byte aligned: B and C as the kernels read them and, where
+ *                channels are few and the token axis is cut into segments for
+ *                that, the segments' states.
+ * Outputs must not overlap inputs. E % G must be 0 (SSD_ERR_SHAPE). Token strides
+ * or channels of 2^24 or more, and a call whose grid would reach 2^24 workgroups (1024 / N channels each, at
  * least 64, N rounded up to a power of two), return SSD_ERR_UNSUPPORTED.
  */
 typedef struct {
@@ -582,8 +586,8 @@ int ssd_selective_step(float *state, const void *x, const void *dt, const float 
  * in dtype; dA [E][N], dD and ddt_bias [E] (nullable) and dinit_state
  * [Bt][E][N] (nullable) float32. Sums are in float32 in a fixed order.
  *   workspace    at least ssd_selective_backward_workspace_size(...) bytes,
- *                256-byte aligned: the states before every 16 (dstate <= 8: 8)
- *                tokens and the partial sums.
+ *                256-byte aligned: the states before every few (4 to 16) tokens
+ *                and the partial sums. Outputs must not overlap inputs.
  */
 size_t ssd_selective_backward_workspace_size(int batch, int seqlen, int channels, int ngroups,
                                              int dstate, int dtype);

@@ -385,7 +385,7 @@ hipError_t conv_fwd(const ConvArgs &a, hipStream_t stream) {
     const long long items =
         walks + (a.final_state ? (long long)(a.cu_seqlens ? a.nseq : a.batch) * nvec : 0);
     const long long blocks = (items + 255) / 256;
-    if (blocks >= (1LL << 24)) return hipErrorInvalidValue;
+    if (blocks >= (1LL << 24)) return hipErrorNotSupported;
     const dim3 grid(static_cast<unsigned>(blocks));
     switch (a.width) {
         case 2: conv_fwd_kernel<T, V, 2, U><<<grid, 256, 0, stream>>>(a, nvec, tile, tiles, walks, items); break;
@@ -404,7 +404,7 @@ hipError_t conv_bwd(const ConvBwdArgs &a, hipStream_t stream) {
     const int tiles = (a.seqlen + tile - 1) / tile;
     const long long items = (long long)a.batch * tiles * nvec;
     const long long blocks = (items + 255) / 256;
-    if (blocks >= (1LL << 24)) return hipErrorInvalidValue;
+    if (blocks >= (1LL << 24) || (long long)a.batch * tiles > 0x7fffffff) return hipErrorNotSupported;
     const dim3 grid(static_cast<unsigned>(blocks));
     switch (a.width) {
         case 2: conv_bwd_kernel<T, V, 2><<<grid, 256, 0, stream>>>(a, nvec, tile, tiles, items); break;
@@ -441,7 +441,7 @@ static hipError_t conv_step(void *state, const void *x, size_t x_row, const floa
     constexpr int V = 4, U = 8;
     const int nvec = part_vecs(y, V);
     const long long items = (long long)batch * nvec, blocks = (items + 255) / 256;
-    if (blocks >= (1LL << 24)) return hipErrorInvalidValue;
+    if (blocks >= (1LL << 24)) return hipErrorNotSupported;
     const dim3 grid(static_cast<unsigned>(blocks));
     T *st = static_cast<T *>(state);
     const T *xx = static_cast<const T *>(x);

@@ -16,7 +16,10 @@ constexpr int kMaxNormWidth = 16384;
 constexpr int kMaxExtent = 1 << 30;
 
 bool valid_dtype(int d) { return d == SSD_F32 || d == SSD_BF16; }
-int status_of(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
+// (hipErrorNotSupported: a launch's own refusal of a grid, before anything is enqueued)
+int status_of(hipError_t e) {
+    return e == hipSuccess ? SSD_OK : e == hipErrorNotSupported ? SSD_ERR_UNSUPPORTED : SSD_ERR_HIP;
+}
 
 int check_workspace(const void *ws, size_t bytes, size_t need) {
     if (need == 0) return SSD_OK;
@@ -97,7 +100,8 @@ int selective_args(ssd::SelArgs &a, const void *x, const void *dt, const float *
                             d.B_batch, d.B_token, d.C_batch, d.C_token})
             if (v < 0) return SSD_ERR_SHAPE;
     }
-    // offsets within a tile of tokens are 32 bits of bytes
+    // offsets within a tile of tokens are 32 bits of bytes, in dense tensors as well
+    if (e >= kMaxTokenStride) return SSD_ERR_UNSUPPORTED;
     for (long long v : {d.x_token, d.dt_token, d.z_token, d.B_token, d.C_token})
         if (v >= kMaxTokenStride) return SSD_ERR_UNSUPPORTED;
     a.x_batch = d.x_batch; a.x_token = d.x_token; a.dt_batch = d.dt_batch; a.dt_token = d.dt_token;

@@ -136,19 +136,20 @@ __device__ __forceinline__ void sel_fold(const float *state, const float *sum, l
     }
 }
 
-// This lane's decay rates times log2(e), so that a decay is one exp2; states
-// past the state size get 0. -inf becomes the lowest float: the same decay for
-// any step size but zero, which it leaves at 1.
+// A decay rate times log2(e), so that a decay is one exp2. -inf becomes the lowest
+// float: the same decay for any step size but zero, which it leaves at 1.
+__device__ __forceinline__ float sel_rate(float a) {
+    const float v = a * kLog2e;
+    return v < -3.402823466e38f ? -3.402823466e38f : v;
+}
+// This lane's rates; states past the state size get 0.
 template <int NS>
 __device__ __forceinline__ void load_rates(const float *A, int nn, float (&A2)[NS]) {
     RowRaw<float, NS> r;
     r.zero();
     if (nn > 0) r.load(A, nn);
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const float v = r.get(i) * kLog2e;
-        A2[i] = v < -3.402823466e38f ? -3.402823466e38f : v;
-    }
+    for (int i = 0; i < NS; ++i) A2[i] = sel_rate(r.get(i));
 }
 
 // FN<type, kernel state size>(...) for a's state size; returns its result.

@@ -354,7 +354,7 @@ __global__ __launch_bounds__(256) void selective_step_kernel(SelArgs a, float *_
     float h[4], p = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(__builtin_amdgcn_exp2f(d * (Ar.get(i) * kLog2e)), hr.get(i), u * Br.get(i));
+        h[i] = fmaf(__builtin_amdgcn_exp2f(d * (sel_rate(Ar.get(i)))), hr.get(i), u * Br.get(i));
         p = fmaf(Cr.get(i), h[i], p);
     }
     if (nn > 0) row_store(st, h, nn);

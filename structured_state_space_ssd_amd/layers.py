@@ -166,6 +166,8 @@ def conv_backward(x, weight, bias, dy, silu=True, init_state=None, dfinal_state=
     _required(dy=dy)
     Bt, L, K = x.shape
     dys = [dy] if isinstance(dy, torch.Tensor) else list(dy)
+    for d in dys:
+        _required(dy=d)
     arr, n, sizes = _conv_parts([d.shape[-1] for d in dys], K)
     xp = _slice(x, "x", x.shape, x)
     wp = _param(weight, "weight", (K, W), x)

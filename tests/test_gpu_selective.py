@@ -117,6 +117,30 @@ def test_selective_strong_and_no_decay(ssd):
     check("none", ssd.selective_forward(**a), want, "y")
 
 
+@pytest.mark.parametrize("size", [(2, 33, 70, 16, 1), (1, 700, 16, 13, 1)], ids=str)
+def test_selective_no_memory(ssd, size):
+    """A = -inf forgets everything at a step and nothing where the step size is zero
+    (the rows past a tile's end among them); -1e30 is the same to any step size here."""
+    a, r = make(*size, F32, 5, soft=False)
+    a["dt"] = a["dt"].clamp(min=1e-3)
+    dy = r(*size[:3])
+    a["A"][:, ::2] = -1e30
+    y, final = ssd.selective_forward(**a, return_final_state=True)
+    check("finite", y, ref(a), "y")
+    grads = ssd.selective_backward(**a, dy=dy)
+    b = dict(a, A=a["A"].clone())
+    b["A"][:, ::2] = -float("inf")
+    y2, final2 = ssd.selective_forward(**b, return_final_state=True)
+    assert torch.equal(y, y2) and torch.equal(final, final2)
+    got = ssd.selective_backward(**b, dy=dy)
+    assert all(torch.equal(got[k], grads[k]) for k in grads if grads[k] is not None)
+    state = a["init_state"].clone()
+    one = {k: (v[:, 0] if k in ("x", "dt", "B", "C", "z") and v is not None else v) for k, v in b.items()
+           if k != "init_state"}
+    ssd.selective_step(state, **dict(one, dt=torch.zeros_like(one["dt"])))
+    assert torch.equal(state, a["init_state"])
+
+
 def test_selective_nan_stays_in_its_channel(ssd):
     a, _ = make(1, 300, 64, 16, 1, F32, 4)
     a["x"] = a["x"].clone()

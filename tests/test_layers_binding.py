@@ -48,6 +48,17 @@ def test_conv_forward_refuses(ssd, error, text, over):
         ssd.conv_forward(**{**CONV, **over})
 
 
+def test_conv_other_refusals(ssd, lib):
+    x, w, b = CONV.values()
+    with pytest.raises(ValueError, match="dy is required"):
+        ssd.conv_backward(x, w, b, (z(2, 6, 4, dtype=bf), None))
+    with pytest.raises(ValueError, match="split"):
+        ssd.conv_backward(x, w, b, (z(2, 6, 4, dtype=bf), z(2, 6, 5, dtype=bf)))
+    # too many workgroups
+    one = _ptrs(0x100000)
+    assert lib.ssd_conv_step(FAKE, FAKE, 1 << 20, FAKE, None, 1 << 20, 1 << 20, 4, 1, 1, None, 0, one, None) == -3
+
+
 def test_conv_packed_refuses(ssd):
     a = dict(CONV, x=z(1, 6, 8, dtype=bf))
     with pytest.raises(ValueError, match="packed"):
@@ -132,6 +143,7 @@ def conv_c(lib, **kw):
     (dict(split=(ctypes.c_int * 2)(4, 4), nsplit=2, y=_ptrs(1 << 20, None)), -1),
     (dict(cu=FAKE, nseq=2), -2), (dict(cu=FAKE, nseq=0, batch=1), -2),
     (dict(cu=FAKE, nseq=2, batch=1, init=FAKE), -3),
+    (dict(batch=1 << 20, seqlen=1 << 30), -3),
 ])
 def test_conv_c_abi_refuses(lib, kw, code):
     assert conv_c(lib, **kw) == code
@@ -243,6 +255,8 @@ def _opt(**kw):
     (dict(ngroups=0), -2), (dict(dstate=0), -2), (dict(ngroups=3), -2), (dict(seqlen=(1 << 30) + 1), -2),
     (dict(strides=(0, 0, 0, 0, 0, 0, 0, -1, 0, 0)), -2),
     (dict(dstate=65), -3), (dict(dtype=2), -3), (dict(batch=1 << 24), -3),
+    # rows too long for offsets in 32 bits, whatever the inputs' strides
+    (dict(channels=1 << 24, batch=1, strides=(0,) * 10), -3), (dict(strides=(0, 0, 0, 0, 0, 1 << 24, 0, 0, 0, 0)), -3),
     (dict(ws=FAKE, bytes=(2 * 2 * 32 + 32) * 64 - 1), -4), (dict(ws=ctypes.c_void_p(0x100010), bytes=1 << 30), -4),
     (dict(ws=None, bytes=1 << 30), -4),
 ], ids=str)
