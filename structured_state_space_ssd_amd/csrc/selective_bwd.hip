@@ -12,7 +12,7 @@
 // states lie over lanes and wavefronts as in the forward. Bound by vector
 // issue, of which the rebuilding is a quarter. Measured in bf16 at 4 x 2048
 // tokens of 5120 channels and 16 states: first walk 226 us, walk back 630 us
-// (vector units busy 73% of the time, two workgroups to a CU by their registers
+// (vector units busy 81% of the time, two workgroups to a CU by their registers
 // and LDS), partial dB and dC 15 us; float32, 2 x 777 tokens of 1000 channels and
 // 24 states: 24, 66 and 5 us.
 //
