@@ -27,11 +27,11 @@
 // segments before it, in their order.
 //
 // Measured in bf16 with 5120 channels and 16 states: 1 x 8192 tokens 151 us for
-// the segments' states and 206 us for the walk, whose vector units are busy 94%
-// of the time; 4 x 2048 tokens 38 + 238 us (63%: mostly one workgroup to a CU). One token for 256
-// sequences 38 us (4.7 TB/s, bound by the states' way from memory and back), for
-// one 3.7 us, a launch. Float32, 2 x 777 tokens of 1000 channels and 24 states:
-// 21 + 22 us.
+// the segments' states and 205 us for the walk, whose vector units are busy 94%
+// of the time; 4 x 2048 tokens 38 + 238 us (63%: mostly one workgroup to a CU).
+// One token for 256 sequences 38 us (4.7 TB/s, bound by the states' way from
+// memory and back), for one 3.7 us, a launch. Float32, 2 x 777 tokens of 1000
+// channels and 24 states: 21 + 22 us.
 #include "selective.h"
 
 namespace ssd {
