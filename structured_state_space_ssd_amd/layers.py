@@ -33,7 +33,7 @@ def _param(t, name, shape, like, dtype=_f32):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, x on {like.device}")
     return t.data_ptr()
 
@@ -48,7 +48,7 @@ def _slice(t, name, shape, like):
         raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
     if t.stride(-1) != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, x on {like.device}")
     return t.data_ptr()
 
@@ -80,7 +80,7 @@ def _call(fn, where, device, *args):
 def _workspace(workspace, need, x):
     """(address, bytes) of the caller's workspace, or of a new one of `need` bytes."""
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+        workspace = x.new_empty(max(need, 1), dtype=torch.uint8)
     elif not workspace.is_contiguous() or workspace.device != x.device:
         raise ValueError("workspace must be a contiguous tensor on x's device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -106,8 +106,11 @@ def _conv_parts(split, K):
     return (ctypes.c_int * len(split))(*split), len(split), split
 
 
+_POINTERS = [ctypes.c_void_p * n for n in range(4)]
+
+
 def _pointers(addresses):
-    return (ctypes.c_void_p * len(addresses))(*addresses)
+    return _POINTERS[len(addresses)](*addresses)
 
 
 def conv_forward(x, weight, bias=None, silu=True, init_state=None, return_final_state=False,
@@ -141,10 +144,10 @@ def conv_forward(x, weight, bias=None, silu=True, init_state=None, return_final_
         cp = _param(cu_seqlens, "cu_seqlens", (nseq + 1,), x, torch.int32)
     _on_gpu(x)
     code = dtype_code(x.dtype)
-    ys = [torch.empty((Bt, L, k), dtype=x.dtype, device=x.device) for k in sizes]
+    ys = [x.new_empty((Bt, L, k)) for k in sizes]
     final = None
     if return_final_state:
-        final = torch.empty((nseq or Bt, W - 1, K), dtype=x.dtype, device=x.device)
+        final = x.new_empty((nseq or Bt, W - 1, K))
     _call(_native.lib.ssd_conv_forward, "ssd_conv_forward", x.device, xp, x.stride(0), x.stride(1),
           wp, bp, ip, cp, nseq, Bt, L, K, W, int(silu), code, arr, n,
           _pointers([y.data_ptr() for y in ys]), final.data_ptr() if final is not None else None)
@@ -177,7 +180,7 @@ def conv_backward(x, weight, bias, dy, silu=True, init_state=None, dfinal_state=
     dp = [_param(d, "dy", (Bt, L, k), x, x.dtype) for d, k in zip(dys, sizes)]
     _on_gpu(x)
     code = dtype_code(x.dtype)
-    out = {"dx": torch.empty((Bt, L, K), dtype=x.dtype, device=x.device),
+    out = {"dx": x.new_empty((Bt, L, K)),
            "dweight": torch.empty_like(weight),
            "dbias": None if bias is None else torch.empty_like(bias),
            "dinit": None if init_state is None else torch.empty_like(init_state)}
@@ -205,7 +208,7 @@ def conv_step(state, x, weight, bias=None, silu=True, split=None):
     bp = _param(bias, "bias", (K,), x)
     sp = _param(state, "state", (Bt, W - 1, K), x, x.dtype)
     _on_gpu(x)
-    ys = [torch.empty((Bt, k), dtype=x.dtype, device=x.device) for k in sizes]
+    ys = [x.new_empty((Bt, k)) for k in sizes]
     _call(_native.lib.ssd_conv_step, "ssd_conv_step", x.device, sp, xp, x.stride(0), wp, bp, Bt, K,
           W, int(silu), dtype_code(x.dtype), arr, n, _pointers([y.data_ptr() for y in ys]))
     return ys[0] if split is None else tuple(ys)
@@ -263,8 +266,8 @@ def selective_forward(x, dt, A, B, C, D=None, z=None, init_state=None, return_fi
     ip = _param(init_state, "init_state", (Bt, E, N), x)
     _on_gpu(x)
     code = dtype_code(x.dtype)
-    y = torch.empty((Bt, L, E), dtype=x.dtype, device=x.device)
-    final = torch.empty((Bt, E, N), dtype=_f32, device=x.device) if return_final_state else None
+    y = x.new_empty((Bt, L, E))
+    final = x.new_empty((Bt, E, N), dtype=_f32) if return_final_state else None
     need = _native.lib.ssd_selective_forward_workspace_size(Bt, L, E, G, N, code)
     keep, ws, ws_bytes = _workspace(workspace, need, x)
     _call(_native.lib.ssd_selective_forward, "ssd_selective_forward", x.device, *p, Bt, L, E, G, N,
@@ -292,7 +295,7 @@ def selective_backward(x, dt, A, B, C, D, dy, z=None, init_state=None, dfinal_st
     fp = _param(dfinal_state, "dfinal_state", (Bt, E, N), x)
     _on_gpu(x)
     code = dtype_code(x.dtype)
-    new = lambda shape, dtype=_f32: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
+    new = lambda shape, dtype=_f32: x.new_empty(shape, dtype=dtype)  # noqa: E731
     out = {"dx": new((Bt, L, E), x.dtype), "ddt": new((Bt, L, E), x.dtype), "dA": new((E, N)),
            "dB": new((Bt, L, G, N), x.dtype), "dC": new((Bt, L, G, N), x.dtype), "dD": new((E,)),
            "dinit": new((Bt, E, N)) if want_dinit else None}
@@ -322,7 +325,7 @@ def selective_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softp
     Bt, E = x.shape
     sp = _param(state, "state", (Bt, E, N), x)
     _on_gpu(x)
-    y = torch.empty((Bt, E), dtype=x.dtype, device=x.device)
+    y = x.new_empty((Bt, E))
     _call(_native.lib.ssd_selective_step, "ssd_selective_step", x.device, sp, *p, Bt, E, G, N,
           dtype_code(x.dtype), y.data_ptr(), st, opts)
     return y
@@ -383,12 +386,12 @@ def norm_forward(x, weight, bias=None, residual=None, z=None, eps=1e-5, rms=Fals
         zstep = _rows(z, "z")[1]
     _on_gpu(x)
     code = dtype_code(x.dtype)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = x.new_empty(x.shape)
     total = mean = rstd = None
     if residual is not None:
-        total = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+        total = torch.empty_like(residual)
     if return_stats:
-        rstd = torch.empty(x.shape[:-1], dtype=_f32, device=x.device)
+        rstd = x.new_empty(x.shape[:-1], dtype=_f32)
         if not rms:
             mean = torch.empty_like(rstd)
     _call(_native.lib.ssd_norm_forward, "ssd_norm_forward", x.device, x.data_ptr(), step, rp, rcode,
