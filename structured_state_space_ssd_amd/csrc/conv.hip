@@ -232,6 +232,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdArgs a, int nvec, 
 #pragma unroll
         for (int e = 0; e < V; ++e) win[j][e] = r.get(e);
     }
+    // tokens fetched together: 2, 4 and 8 took 150, 137 and 153 us at the size above
     constexpr int U = 4;
     const int last = t1 + W - 1;  // one past the last token whose g a row of dx here needs
     // `whole`: these tokens are the tile's own (so the rows of dx they write lie
