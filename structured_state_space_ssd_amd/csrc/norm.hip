@@ -97,6 +97,8 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int lpr, float *buf) {
     lane_sum(v, 16);
 }
 
+constexpr int kShortWaves = 4;  // wavefronts of a workgroup that takes several rows at once
+
 template <typename T> constexpr int vec_of() { return sizeof(T) == 2 ? 8 : 4; }
 
 // Rows are taken with the stride of the grid, which holds as many as run at
@@ -198,7 +200,7 @@ __global__ __launch_bounds__(1024, NV == 1 ? 7 : 4) void norm_fwd_kernel(
 }
 
 // Each workgroup (or, for short rows, each group of lanes) keeps its columns'
-// dw and db in registers over its rows and writes them once at its end;
+// dw and db in registers over its rows; a workgroup writes them once at its end;
 // colsum_kernel adds the partial rows in their order, so the result does not
 // depend on timing. A row's own values stay as they were loaded: what the sums
 // need of them is computed again for the output, in the shadow of memory.
@@ -212,6 +214,7 @@ __global__ __launch_bounds__(NV * vec_of<T>() < 16 ? 1024 : 512, NV == 1 ? 4 : N
     T *__restrict__ dz, float *__restrict__ part, int want_db) {
     constexpr int V = vec_of<T>();
     __shared__ float buf[2][32];
+    __shared__ float acc[2][NV == 1 ? kShortWaves * V * 64 : 1];
     if (NV > 1) lpr = 0;  // only whole workgroups hold more than a vector per lane
     const RowGroup g = row_group(lpr);
     int step = (lpr ? lpr : (int)blockDim.x) * V;
@@ -324,8 +327,31 @@ __global__ __launch_bounds__(NV * vec_of<T>() < 16 ? 1024 : 512, NV == 1 ? 4 : N
             row_store(dx + row * D + c, o, n);
         }
     }
-    // [partial row][dw, db][D]
-    float *p = part + ((size_t)blockIdx.x * g.groups + g.group) * (want_db ? 2 : 1) * D;
+    if (NV == 1 && lpr) {  // short rows: the groups of a wavefront meet, then the wavefronts
+        const int w = wave_id(), l = lane_id();
+        for (int off = lpr; off < 64; off <<= 1)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                dw[0][e] += __shfl_xor(dw[0][e], off);
+                db[0][e] += __shfl_xor(db[0][e], off);
+            }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            acc[0][(w * V + e) * 64 + l] = dw[0][e];
+            acc[1][(w * V + e) * 64 + l] = db[0][e];
+        }
+        __syncthreads();
+        if (w || l >= lpr) return;
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+#pragma unroll
+            for (int k = 1; k < kShortWaves; ++k) {
+                dw[0][e] += acc[0][(k * V + e) * 64 + l];
+                db[0][e] += acc[1][(k * V + e) * 64 + l];
+            }
+    }
+    // [workgroup][dw, db][D]
+    float *p = part + (size_t)blockIdx.x * (want_db ? 2 : 1) * D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = g.lane * V + i * step, n = D - c;
@@ -376,9 +402,9 @@ NormShape norm_shape(int D, int V, int most) {
     if (nvec <= 64) {
         s.lpr = 1;
         while (s.lpr < nvec) s.lpr <<= 1;
-        s.threads = 256;
+        s.threads = 64 * kShortWaves;
         s.nv = 1;
-        s.groups = 256 / s.lpr;
+        s.groups = s.threads / s.lpr;
         return s;
     }
     s.lpr = 0;
@@ -457,7 +483,7 @@ hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t stream) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const long long cols = (long long)a.width * (a.dbias ? 2 : 1);
-    return launch_colsum(a.part, blocks * s.groups, cols, a.width, a.dweight, a.dbias, stream);
+    return launch_colsum(a.part, blocks, cols, a.width, a.dweight, a.dbias, stream);
 }
 
 }  // namespace
@@ -473,7 +499,7 @@ hipError_t launch_colsum(const float *part, int n, long long cols, long long fir
 
 size_t norm_bwd_part_bytes(long long rows, int width, bool bf16, bool want_db) {
     const NormShape s = norm_bwd_shape(width, bf16 ? 8 : 4);
-    return (size_t)norm_blocks(rows, s, kBwdLanes) * s.groups * (want_db ? 2 : 1) * width * sizeof(float);
+    return (size_t)norm_blocks(rows, s, kBwdLanes) * (want_db ? 2 : 1) * width * sizeof(float);
 }
 
 hipError_t launch_norm_fwd(const NormArgs &a, bool bf16, bool res_bf16, hipStream_t stream) {
