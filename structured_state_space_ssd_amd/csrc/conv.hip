@@ -416,8 +416,9 @@ hipError_t conv_bwd(const ConvBwdArgs &a, hipStream_t stream) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const long long K = a.channels;
+    const size_t rows = (size_t)a.batch * tiles;
     return launch_colsum(a.part, a.batch * tiles, K * (a.width + 1), K * a.width, a.dweight,
-                         a.dbias, stream);
+                         a.dbias, stream, a.part + rows * K * (a.width + 1));
 }
 
 }  // namespace
@@ -428,7 +429,8 @@ hipError_t launch_conv_fwd(const ConvArgs &a, bool bf16, hipStream_t stream) {
 
 size_t conv_bwd_part_bytes(int batch, int seqlen, int channels, int width) {
     const int tile = bwd_tile(batch, seqlen, channels);
-    return (size_t)batch * ((seqlen + tile - 1) / tile) * channels * (width + 1) * sizeof(float);
+    const size_t rows = (size_t)batch * ((seqlen + tile - 1) / tile);
+    return (rows + (rows > kColsumRows ? kColsumChunks : 0)) * channels * (width + 1) * sizeof(float);
 }
 
 hipError_t launch_conv_bwd(const ConvBwdArgs &a, bool bf16, hipStream_t stream) {

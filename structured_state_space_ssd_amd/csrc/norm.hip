@@ -362,12 +362,13 @@ __global__ __launch_bounds__(NV * vec_of<T>() < 16 ? 1024 : 512, NV == 1 ? 4 : N
 }
 
 // out[c] = sum over k < n of part[k][c]: 1024 / COLS strands of rows to a column,
-// added in a fixed order. 32 columns to a workgroup while that gives each CU two
+// added in a fixed order; with several workgroups to a column (blockIdx.y) each
+// takes `chunk` rows and leaves a row of its own. 32 columns to a workgroup while that gives each CU two
 // workgroups at most, else 64, a wavefront's full width: 768 rows of 5120 columns
 // 4.8 us with 32 and 6.0 with 64, 24 rows of 81920 9.2 and 6.1.
 template <int COLS>
 __global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ part, int n,
-                                                      long long cols, long long first,
+                                                      int chunk, long long cols, long long first,
                                                       float *__restrict__ out0,
                                                       float *__restrict__ out1) {
     constexpr int STRANDS = 1024 / COLS;
@@ -375,9 +376,10 @@ __global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ 
     const int col = threadIdx.x % COLS, strand = threadIdx.x / COLS;
     const long long c = (long long)blockIdx.x * COLS + col;
     float s = 0.0f;
+    const long long end = min((long long)n, (blockIdx.y + 1LL) * chunk);
     if (c < cols)
 #pragma unroll 4
-        for (int k = strand; k < n; k += STRANDS) s += part[k * cols + c];
+        for (long long k = (long long)blockIdx.y * chunk + strand; k < end; k += STRANDS) s += part[k * cols + c];
     buf[strand][col] = s;
     __syncthreads();
     if (strand == 0 && c < cols) {
@@ -385,7 +387,7 @@ __global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ 
 #pragma unroll
         for (int k = 0; k < STRANDS; ++k) s += buf[k][col];
         if (c < first) {
-            if (out0) out0[c] = s;
+            if (out0) out0[blockIdx.y * cols + c] = s;
         } else if (out1) out1[c - first] = s;
     }
 }
@@ -489,11 +491,20 @@ hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_colsum(const float *part, int n, long long cols, long long first, float *out0,
-                         float *out1, hipStream_t stream) {
+                         float *out1, hipStream_t stream, float *spare) {
     const auto grid = [&](int per) { return static_cast<unsigned>((cols + per - 1) / per); };
+    if (spare && n > kColsumRows) {
+        const int chunk = (n + kColsumChunks - 1) / kColsumChunks;
+        colsum_kernel<32><<<dim3(grid(32), kColsumChunks), 1024, 0, stream>>>(part, n, chunk, cols,
+                                                                              cols, spare, nullptr);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        part = spare;
+        n = kColsumChunks;
+    }
     if (cols <= 16384)
-        colsum_kernel<32><<<grid(32), 1024, 0, stream>>>(part, n, cols, first, out0, out1);
-    else colsum_kernel<64><<<grid(64), 1024, 0, stream>>>(part, n, cols, first, out0, out1);
+        colsum_kernel<32><<<grid(32), 1024, 0, stream>>>(part, n, n, cols, first, out0, out1);
+    else colsum_kernel<64><<<grid(64), 1024, 0, stream>>>(part, n, n, cols, first, out0, out1);
     return hipGetLastError();
 }
 

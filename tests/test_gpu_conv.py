@@ -103,6 +103,18 @@ def test_conv_backward(ssd, size, dtype, W):
             R.check((size, k, act), got[k], want[k], mag[k], ops + n)
 
 
+def test_conv_backward_many_tiles(ssd):
+    """Few channels over many tokens: more partial rows than one pass sums up."""
+    Bt, L, K, W = 3, 8000, 5, 3
+    x, w, b, _, g = make(Bt, L, K, W, F32, 77)
+    dy = torch.randn(Bt, L, K, generator=g).cuda()
+    got = ssd.conv_backward(x, w, b, dy)
+    want, mag = R.conv_grads(x, w, b, True, dy)
+    ops = W + 14 + (W + 1) * float(R.conv(x, w, b, True)[3].max())
+    for k in ("dx", "dweight", "dbias"):
+        R.check(k, got[k], want[k], mag[k], ops + (Bt * L if k != "dx" else 0))
+
+
 def test_conv_backward_split_and_differences(ssd):
     """dy in parts gives the same as whole; the gradient is the loss's slope:
     a central difference of the 64-bit form with step h is off by h^2 / 6 times
