@@ -407,15 +407,19 @@ def norm_forward(x, weight, bias=None, residual=None, z=None, eps=1e-5, rms=Fals
     return out if len(out) > 1 else y
 
 
-def norm_backward(dy, x, weight, mean, rstd, z=None, dresidual=None, workspace=None):
+def norm_backward(dy, x, weight, mean, rstd, z=None, dresidual=None, workspace=None,
+                  want_dbias=None, want_dresidual=None):
     """Gradients of ``norm_forward`` (ssd_norm_backward).
 
     x: norm_forward's x or, where it had a residual, the sum that it returned.
     mean (None: the rms form) and rstd: its statistics. dresidual (like x): the
     gradient that reaches that sum by the skip connection.
-    Returns a dict: dx (dy's type, the gradient of norm_forward's x), dweight,
-    dbias ([D] float32; dbias None in the rms form), dz (with z) and, where
-    dresidual is given, dresidual: the gradient of the residual, in x's type.
+    Returns a dict: dx (dy's type, the gradient of norm_forward's x), dweight and
+    dbias ([D] float32), dz (with z) and dresidual, the gradient of
+    norm_forward's residual, in x's type. want_dbias: whether dbias is formed or
+    None (default: formed where there is a mean; the rms form's bias needs True).
+    want_dresidual: whether dresidual is among them (default: where one is
+    given; True without one where nothing comes back by the skip connection).
     """
     _required(dy=dy, x=x, weight=weight, rstd=rstd)
     rows, step = _rows(x, "x")
@@ -428,8 +432,10 @@ def norm_backward(dy, x, weight, mean, rstd, z=None, dresidual=None, workspace=N
     sp = _param(rstd, "rstd", x.shape[:-1], x)
     rp = _param(dresidual, "dresidual", x.shape, x, x.dtype)
     zp, zstep = None, 0
+    want_dbias = mean is not None if want_dbias is None else bool(want_dbias)
+    want_dresidual = dresidual is not None if want_dresidual is None else bool(want_dresidual)
     if z is not None:
-        if dresidual is not None:
+        if dresidual is not None or want_dresidual:
             raise ValueError("dresidual and z exclude each other")
         if x.dtype != dy.dtype:
             raise TypeError(f"x must be {dy.dtype} with z, got {x.dtype}")
@@ -438,13 +444,13 @@ def norm_backward(dy, x, weight, mean, rstd, z=None, dresidual=None, workspace=N
     _on_gpu(x)
     code = dtype_code(dy.dtype)
     out = {"dx": torch.empty_like(dy), "dweight": torch.empty_like(weight),
-           "dbias": None if mean is None else torch.empty_like(weight)}
+           "dbias": torch.empty_like(weight) if want_dbias else None}
     if z is not None:
         out["dz"] = torch.empty_like(dy)
-    if dresidual is not None:
-        out["dresidual"] = torch.empty_like(dresidual)
+    if want_dresidual:
+        out["dresidual"] = x.new_empty(x.shape)
     ptr = lambda k: out[k].data_ptr() if out.get(k) is not None else None  # noqa: E731
-    need = _native.lib.ssd_norm_backward_workspace_size(rows, D, code, int(mean is not None))
+    need = _native.lib.ssd_norm_backward_workspace_size(rows, D, code, int(want_dbias))
     keep, ws, ws_bytes = _workspace(workspace, need, x)
     _call(_native.lib.ssd_norm_backward, "ssd_norm_backward", x.device, yp, x.data_ptr(), step,
           dtype_code(x.dtype), zp, zstep, wp, mp, sp, rp, rows, D, code, ptr("dx"),

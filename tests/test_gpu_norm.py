@@ -176,3 +176,70 @@ def test_norm_captured(ssd):
         eg = ssd.norm_backward(dy, et, w, em, er, dresidual=res)
         assert torch.equal(y, ey) and torch.equal(total, et)
         assert all(torch.equal(grads[n], eg[n]) for n in eg)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("size", [(40, 24), (7, 513), (5, 2560), (2, 12000)], ids=str)
+def test_norm_rms_bias_gradient(ssd, size, dtype):
+    """The root-mean-square form takes a bias too; its gradient on request. A
+    sum over rows adds at most a rounding per row of its terms."""
+    rows, D = size
+    x, w, b, r = make(rows, D, dtype, D, 3)
+    y, mean, rstd = ssd.norm_forward(x, w, b, eps=EPS, rms=True, return_stats=True)
+    want, _, _, mag = R.norm(x, w, b, True, EPS)
+    R.check((size, "y"), y, want, mag, OPS)
+    dy = r(rows, D)
+    plain = ssd.norm_backward(dy, x, w, mean, rstd)
+    got = ssd.norm_backward(dy, x, w, mean, rstd, want_dbias=True)
+    assert plain["dbias"] is None and all(torch.equal(plain[k], got[k]) for k in ("dx", "dweight"))
+    want, mag = R.norm_grads(dy, x, w, True, EPS)
+    R.check((size, "dbias"), got["dbias"], want["dbias"], mag["dbias"], rows)
+    h = 1e-3  # y is linear in the bias: a difference is exact up to 64-bit rounding
+    step = torch.zeros(D, dtype=torch.float64)
+    step[D - 1] = h
+    f = lambda bb: (R.norm(x, w, bb, True, EPS)[0] * dy.double().cpu()).sum()  # noqa: E731
+    slope = float(f(b.double().cpu() + step) - f(b.double().cpu() - step)) / (2 * h)
+    assert abs(slope - float(got["dbias"][D - 1])) < 1e-4 * max(1.0, abs(slope))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("size", [(40, 24), (7, 513), (2, 12000)], ids=str)
+def test_norm_without_bias_gradient(ssd, size, dtype):
+    """A layer norm without a bias asks for no gradient of it, and the other
+    gradients are the same."""
+    rows, D = size
+    x, w, _, r = make(rows, D, dtype, D)
+    _, mean, rstd = ssd.norm_forward(x, w, eps=EPS, return_stats=True)
+    dy = r(rows, D)
+    whole = ssd.norm_backward(dy, x, w, mean, rstd)
+    got = ssd.norm_backward(dy, x, w, mean, rstd, want_dbias=False)
+    assert got["dbias"] is None and whole["dbias"] is not None
+    assert all(torch.equal(got[k], whole[k]) for k in ("dx", "dweight"))
+    from structured_state_space_ssd_amd._native import lib
+    need = lib.ssd_norm_backward_workspace_size(rows, D, int(dtype == BF), 0)
+    again = ssd.norm_backward(dy, x, w, mean, rstd, want_dbias=False,
+                              workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(again["dweight"], got["dweight"])
+
+
+@pytest.mark.parametrize("dtype,stream", [(BF, BF), (BF, F32), (F32, F32)], ids=["bf16", "bf16_f32", "f32"])
+@pytest.mark.parametrize("size", [(40, 24), (5, 2560), (2, 12000)], ids=str)
+def test_norm_residual_without_skip(ssd, size, dtype, stream):
+    """After the last norm nothing comes back by the skip connection: the
+    stream's gradient is the norm's alone, in the stream's own type."""
+    rows, D = size
+    x, w, b, r = make(rows, D, dtype, D)
+    res, dy = r(rows, D, dt=stream), r(rows, D)
+    _, total, mean, rstd = ssd.norm_forward(x, w, b, residual=res, eps=EPS, return_stats=True)
+    got = ssd.norm_backward(dy, total, w, mean, rstd, want_dresidual=True)
+    plain = ssd.norm_backward(dy, total, w, mean, rstd)
+    assert "dresidual" not in plain and torch.equal(plain["dx"], got["dx"])
+    want, mag = R.norm_grads(dy, total, w, False, EPS)
+    assert got["dresidual"].dtype == stream and got["dx"].dtype == dtype
+    R.check((size, "dresidual"), got["dresidual"], want["dx"], mag["dx"], 2 * OPS)
+    assert torch.equal(got["dx"], got["dresidual"].to(dtype))
+    # a skip gradient may also reach the sum while only x needs a gradient
+    dres = r(rows, D, dt=stream)
+    both = ssd.norm_backward(dy, total, w, mean, rstd, dresidual=dres)
+    one = ssd.norm_backward(dy, total, w, mean, rstd, dresidual=dres, want_dresidual=False)
+    assert "dresidual" not in one and torch.equal(one["dx"], both["dx"])

@@ -285,3 +285,12 @@ def test_selective_c_abi_options_and_workspaces(lib):
     assert lib.ssd_selective_backward(*args, FAKE, n, None, None, None) == -1
     # sizes whose products pass 32 bits
     assert back(8, 1 << 20, 8192, 1, 64, 0) > (1 << 32)
+
+
+def test_norm_backward_wanted_refuses(ssd):
+    a = dict(dy=z(4, 8, dtype=bf), x=z(4, 8, dtype=bf), weight=z(8), mean=None, rstd=z(4))
+    with pytest.raises(ValueError, match="exclude"):
+        ssd.norm_backward(**a, z=z(4, 8, dtype=bf), want_dresidual=True)
+    for over in (dict(want_dbias=True), dict(want_dresidual=True), dict(z=z(4, 8, dtype=bf), want_dresidual=False)):
+        with pytest.raises(ValueError, match="GPU"):
+            ssd.norm_backward(**a, **over)
