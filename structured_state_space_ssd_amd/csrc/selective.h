@@ -36,7 +36,7 @@ typedef const __attribute__((address_space(4))) SelBC sel_const;
 // The step size of raw value v (bias included): softplus and clamp as chosen.
 __device__ __forceinline__ float sel_step(const DtOpts &o, float v) {
     if (o.softplus) v = softplus_f32(v);
-    if (o.clamp) v = fminf(fmaxf(v, o.lo), o.hi);
+    if (o.clamp) v = clamp_step(o, v);
     return v;
 }
 // The same of a vector's values, the choices outside the loops; zero (which
@@ -49,7 +49,7 @@ __device__ __forceinline__ void sel_steps(const DtOpts &o, float (&d)[V], bool i
     }
     if (o.clamp) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) d[e] = fminf(fmaxf(d[e], o.lo), o.hi);
+        for (int e = 0; e < V; ++e) d[e] = clamp_step(o, d[e]);
     }
     if (!in) {
 #pragma unroll

@@ -25,6 +25,12 @@ typedef uint16_t bf16_t;  // bf16 storage in global memory
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// v within the options' bounds. By comparisons, which leave a value that is not a
+// number as it is, where the larger and the smaller of two make it a bound.
+__device__ __forceinline__ float clamp_step(const DtOpts &o, float v) {
+    return v < o.lo ? o.lo : v > o.hi ? o.hi : v;
+}
+
 // The step size for raw value v of a head whose bias is `bias` (0 if none).
 __device__ __forceinline__ float step_size(const DtOpts &o, float v, float bias) {
     v += bias;

@@ -235,3 +235,35 @@ def test_selective_captured(ssd):
         es = ssd.selective_step(st, **one)
         assert torch.equal(y, ey) and torch.equal(fin, efin) and torch.equal(ys, es) and torch.equal(state, st)
         assert all(torch.equal(g[n], eg[n]) for n in eg)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("soft", [True, False], ids=["softplus", "raw"])
+@pytest.mark.parametrize("size", [(2, 40, 70, 16, 1), (1, 700, 16, 13, 1)], ids=str)
+def test_selective_clamp_keeps_nan(ssd, size, soft, dtype):
+    """A step size that is not a number stays one through the clamp, as without
+    it: in its channel from its token on, in the gradients, and in single tokens."""
+    a, r = make(*size, dtype, 6, soft=soft)
+    t, e = 20, 5
+    a["dt"] = a["dt"].clone()
+    a["dt"][0, t, e] = float("nan")
+    dy = r(*size[:3])
+    free = ssd.selective_backward(**a, dy=dy)
+    a["dt_limit"] = (0.02, 0.08)
+    y, final = ssd.selective_forward(**a, return_final_state=True)
+    bad = torch.zeros(y.shape, dtype=torch.bool)
+    bad[0, t:, e] = True
+    assert torch.equal(y.isnan().cpu(), bad) and final[0, e].isnan().all()
+    final[0, e] = 0
+    assert final.isfinite().all()
+    got = ssd.selective_backward(**a, dy=dy)
+    assert got["ddt"][0, t, e].isnan() and (not soft or got["ddt_bias"][e].isnan())
+    for k in got:
+        if k != "ddt" and got[k] is not None:  # (outside the bounds ddt is 0, whatever comes back)
+            assert torch.equal(got[k].isnan(), free[k].isnan()), k
+    state = a["init_state"].clone()
+    one = {k: (v[:, t] if k in ("x", "dt", "B", "C", "z") else v) for k, v in a.items() if k != "init_state"}
+    ys = ssd.selective_step(state, **one)
+    bad = torch.zeros(ys.shape, dtype=torch.bool)
+    bad[0, e] = True
+    assert torch.equal(ys.isnan().cpu(), bad) and state[0, e].isnan().all()
