@@ -94,7 +94,8 @@ typedef enum {
  *                                            per-head constant term)
  *   dt <- log(1 + exp(dt))                   if dt_softplus
  *   dt <- min(max(dt, dt_min), dt_max)       if dt_clamp (the step-size range the
- *                                            tutorial's section 8.2 adjusts)
+ *                                            tutorial's section 8.2 adjusts; a
+ *                                            NaN stays a NaN)
  * in float32. The decay uses the result; the input term uses it (Euler) or its
  * zero-order-hold weight (SSD_DISC_ZOH).
  *   dt_bias         DEVICE pointer, float32 [H], 4-byte aligned, or NULL.

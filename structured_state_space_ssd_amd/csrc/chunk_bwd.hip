@@ -694,7 +694,7 @@ __global__ __launch_bounds__(1024) void bwd_dt_kernel(
         }
         if (o.clamp) {
             if (v < o.lo || v > o.hi) slope = 0.0f;
-            v = fminf(fmaxf(v, o.lo), o.hi);
+            v = clamp_step(o, v);
         }
         float wd = 1.0f, wa = 0.0f;  // dw/dstep, dw/dA
         if (o.zoh) {

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(1024) void chunk_cumsum_kernel(const T *__restrict_
     }
     if (o.clamp) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) d[r] = fminf(fmaxf(d[r], o.lo), o.hi);
+        for (int r = 0; r < R; ++r) d[r] = clamp_step(o, d[r]);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {

@@ -35,7 +35,7 @@ __device__ __forceinline__ float clamp_step(const DtOpts &o, float v) {
 __device__ __forceinline__ float step_size(const DtOpts &o, float v, float bias) {
     v += bias;
     if (o.softplus) v = fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v)));  // log(1 + e^v)
-    if (o.clamp) v = fminf(fmaxf(v, o.lo), o.hi);
+    if (o.clamp) v = clamp_step(o, v);
     return v;
 }
 

@@ -61,3 +61,19 @@ def test_oracle_rejects_bad_shapes():
     B = np.zeros((1, 4, 2, 2), np.float32)  # 3 heads not divisible by 2 groups
     with pytest.raises(RuntimeError):
         oracle.forward(x, dt, np.zeros(3, np.float32), B, B, None)
+
+
+def test_clamp_keeps_nan():
+    """A step size that is not a number stays one through the clamp: its head's
+    outputs from its token on and its state, forward and token by token."""
+    rng = np.random.default_rng(5)
+    Bt, L, H, P, N = 1, 9, 2, 4, 3
+    x, B, C = (rng.standard_normal(s) for s in ((Bt, L, H, P), (Bt, L, 1, N), (Bt, L, 1, N)))
+    dt = rng.uniform(0.01, 0.1, (Bt, L, H))
+    A = -np.ones(H, np.float32)
+    dt[0, 4, 1] = np.nan
+    y, state, _ = oracle.forward(x, dt, A, B, C, dt_limit=(0.02, 0.05))
+    bad = np.zeros((H, L), bool)
+    bad[1, 4:] = True
+    assert (np.isnan(y).reshape(H, L, P).all(-1) == bad).all() and (np.isnan(y).reshape(H, L, P).any(-1) == bad).all()
+    assert (np.isnan(state).reshape(H, -1).all(-1) == [False, True]).all()
