@@ -387,8 +387,14 @@ int ssd_selective_step(float *state, const void *x, const void *dt, const float 
     if (rc != SSD_OK) return rc;
     if ((long long)batch * channels * (ssd::selective_kernel_dstate(dstate) / 4) / 256 >= kMaxBlocks - 1)
         return SSD_ERR_UNSUPPORTED;
+    ssd_selective_strides st{};  // a single token has no stride between tokens
+    if (strides) {
+        st = *strides;
+        st.x_token = st.dt_token = st.z_token = st.B_token = st.C_token = 0;
+    }
     ssd::SelArgs a;
-    rc = selective_args(a, x, dt, A, B, C, D, z, batch, 1, channels, ngroups, dstate, strides, opts);
+    rc = selective_args(a, x, dt, A, B, C, D, z, batch, 1, channels, ngroups, dstate,
+                        strides ? &st : nullptr, opts);
     if (rc != SSD_OK) return rc;
     a.y = y;
     return status_of(ssd::launch_selective_step(a, state, dtype == SSD_BF16,

@@ -267,3 +267,23 @@ def test_selective_clamp_keeps_nan(ssd, size, soft, dtype):
     bad = torch.zeros(ys.shape, dtype=torch.bool)
     bad[0, e] = True
     assert torch.equal(ys.isnan().cpu(), bad) and state[0, e].isnan().all()
+
+
+def test_selective_step_reads_batch_strides_only(ssd):
+    """Whatever the strides' token members hold: a single token has none."""
+    import ctypes
+    from structured_state_space_ssd_amd import _native
+    Bt, E, N = 3, 20, 6
+    a, _ = make(Bt, 1, E, N, 1, F32, 8, soft=False)
+    one = {k: v[:, 0].contiguous() for k, v in a.items() if k in ("x", "dt", "B", "C")}
+    state, again = a["init_state"].clone(), a["init_state"].clone()
+    want = ssd.selective_step(state, one["x"], one["dt"], a["A"], one["B"], one["C"])
+    y = torch.empty_like(want)
+    for token in (-1, 1 << 40):
+        st = _native.SsdSelectiveStrides(E, token, E, token, 0, token, N, token, N, token)
+        again.copy_(a["init_state"])
+        rc = _native.lib.ssd_selective_step(
+            again.data_ptr(), one["x"].data_ptr(), one["dt"].data_ptr(), a["A"].data_ptr(), one["B"].data_ptr(),
+            one["C"].data_ptr(), None, None, Bt, E, 1, N, 0, y.data_ptr(), ctypes.byref(st), None,
+            _native.stream_handle())
+        assert rc == 0 and torch.equal(y, want) and torch.equal(again, state)

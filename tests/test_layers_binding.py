@@ -294,3 +294,16 @@ def test_norm_backward_wanted_refuses(ssd):
     for over in (dict(want_dbias=True), dict(want_dresidual=True), dict(z=z(4, 8, dtype=bf), want_dresidual=False)):
         with pytest.raises(ValueError, match="GPU"):
             ssd.norm_backward(**a, **over)
+
+
+def test_selective_step_c_abi_token_strides(lib):
+    """Only the strides between sequences are a single token's: the others may hold
+    anything. (An invalid option is the last check, so nothing is launched.)"""
+    from structured_state_space_ssd_amd import _native
+    bad = _opt(discretization=1)
+    args = [FAKE] * 6 + [None, None, 2, 8, 2, 5, 1, FAKE]
+    for token in (8, -1, 1 << 40):
+        st = _native.SsdSelectiveStrides(8, token, 8, token, 8, token, 10, token, 10, token)
+        assert lib.ssd_selective_step(*args, ctypes.byref(st), ctypes.byref(bad), None) == -6
+    st = _native.SsdSelectiveStrides(-8, 0, 8, 0, 8, 0, 10, 0, 10, 0)
+    assert lib.ssd_selective_step(*args, ctypes.byref(st), ctypes.byref(bad), None) == -2
