@@ -503,7 +503,9 @@ int ssd_conv_forward(const void *x, long long x_batch_stride, long long x_token_
  * dinit_state are nullable. dx [Bt][L][K] and dinit_state [Bt][W-1][K] in
  * dtype, dense; dweight [K][W] and dbias [K] float32, overwritten; sums over
  * tokens are in float32 in a fixed order. workspace: at least
- * ssd_conv_backward_workspace_size(...) bytes, 256-byte aligned.
+ * ssd_conv_backward_workspace_size(...) bytes, 256-byte aligned. A grid of 2^32
+ * lanes or more (channels * (width + 1) of 2^28, which their sums reach it with,
+ * or as for ssd_conv_forward) returns SSD_ERR_UNSUPPORTED.
  */
 size_t ssd_conv_backward_workspace_size(int batch, int seqlen, int channels, int width, int dtype);
 int ssd_conv_backward(const void *x, long long x_batch_stride, long long x_token_stride,
@@ -589,6 +591,10 @@ int ssd_selective_step(float *state, const void *x, const void *dt, const float 
  *   workspace    at least ssd_selective_backward_workspace_size(...) bytes,
  *                256-byte aligned: the states before every few (4 to 16) tokens
  *                and the partial sums. Outputs must not overlap inputs.
+ * Refused as ssd_selective_forward does, and with SSD_ERR_UNSUPPORTED where one of its
+ * own grids would reach 2^32 lanes: 2^23 workgroups with more than 16 states,
+ * channels * dstate of 2^28, or 2^24 tokens (of all sequences and groups) with
+ * more than 32 states.
  */
 size_t ssd_selective_backward_workspace_size(int batch, int seqlen, int channels, int ngroups,
                                              int dstate, int dtype);

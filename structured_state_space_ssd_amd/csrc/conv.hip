@@ -405,7 +405,6 @@ hipError_t conv_bwd(const ConvBwdArgs &a, hipStream_t stream) {
     const int tiles = (a.seqlen + tile - 1) / tile;
     const long long items = (long long)a.batch * tiles * nvec;
     const long long blocks = (items + 255) / 256;
-    if (blocks >= (1LL << 24) || (long long)a.batch * tiles > 0x7fffffff) return hipErrorNotSupported;
     const dim3 grid(static_cast<unsigned>(blocks));
     switch (a.width) {
         case 2: conv_bwd_kernel<T, V, 2><<<grid, 256, 0, stream>>>(a, nvec, tile, tiles, items); break;
@@ -431,6 +430,13 @@ size_t conv_bwd_part_bytes(int batch, int seqlen, int channels, int width) {
     const int tile = bwd_tile(batch, seqlen, channels);
     const size_t rows = (size_t)batch * ((seqlen + tile - 1) / tile);
     return (rows + (rows > kColsumRows ? kColsumChunks : 0)) * channels * (width + 1) * sizeof(float);
+}
+
+bool conv_bwd_grid_ok(int batch, int seqlen, int channels, int width, const ConvParts &dy) {
+    const int tile = bwd_tile(batch, seqlen, channels);
+    const long long rows = (long long)batch * ((seqlen + tile - 1) / tile);
+    return rows <= 0x7fffffff && (rows * part_vecs(dy, 4) + 255) / 256 < (1LL << 24) &&
+           colsum_grid_ok(static_cast<int>(rows), (long long)channels * (width + 1), true);
 }
 
 hipError_t launch_conv_bwd(const ConvBwdArgs &a, bool bf16, hipStream_t stream) {

@@ -143,6 +143,7 @@ SelLayout selective_layout(int batch, int seqlen, int channels, int ngroups, int
     return w;
 }
 
+// The layout of B and C, and the walks' workgroups of 256 lanes.
 bool selective_grid_ok(int batch, int seqlen, int channels, int ngroups, int dstate, int segs) {
     return (long long)ssd::selective_blocks(channels, ngroups, dstate) * segs * batch < kMaxBlocks &&
            ssd::selective_bc_floats(batch, seqlen, ngroups, dstate) / 256 < (size_t)kMaxBlocks - 1;
@@ -228,6 +229,7 @@ int ssd_conv_backward(const void *x, long long x_batch_stride, long long x_token
     ssd::ConvBwdArgs a{};
     rc = conv_parts(split, nsplit, channels, dy, a.dy);
     if (rc != SSD_OK) return rc;
+    if (!ssd::conv_bwd_grid_ok(batch, seqlen, channels, width, a.dy)) return SSD_ERR_UNSUPPORTED;
     rc = check_workspace(workspace, workspace_bytes,
                          ssd::conv_bwd_part_bytes(batch, seqlen, channels, width));
     if (rc != SSD_OK) return rc;
@@ -424,7 +426,8 @@ int ssd_selective_backward(const void *x, const void *dt, const float *A, const 
                         strides, opts);
     if (rc != SSD_OK) return rc;
     const SelBwdLayout w = selective_bwd_layout(batch, seqlen, channels, ngroups, dstate);
-    if (!selective_grid_ok(batch, seqlen, channels, ngroups, dstate, w.plan.segs))
+    if (!selective_grid_ok(batch, seqlen, channels, ngroups, dstate, w.plan.segs) ||
+        !ssd::selective_bwd_grid_ok(batch, seqlen, channels, ngroups, dstate, w.plan.segs))
         return SSD_ERR_UNSUPPORTED;
     rc = check_workspace(workspace, workspace_bytes, w.total);
     if (rc != SSD_OK) return rc;

@@ -490,6 +490,14 @@ hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t stream) {
 
 }  // namespace
 
+// Columns of a workgroup in a sum's only or last pass.
+static int colsum_cols(long long cols) { return cols <= 16384 ? 32 : 64; }
+
+bool colsum_grid_ok(int n, long long cols, bool spare) {
+    const auto fits = [&](int per) { return (cols + per - 1) / per < (1LL << 32) / 1024; };
+    return fits(colsum_cols(cols)) && (!spare || n <= kColsumRows || fits(32));
+}
+
 hipError_t launch_colsum(const float *part, int n, long long cols, long long first, float *out0,
                          float *out1, hipStream_t stream, float *spare) {
     const auto grid = [&](int per) { return static_cast<unsigned>((cols + per - 1) / per); };
@@ -502,7 +510,7 @@ hipError_t launch_colsum(const float *part, int n, long long cols, long long fir
         part = spare;
         n = kColsumChunks;
     }
-    if (cols <= 16384)
+    if (colsum_cols(cols) == 32)
         colsum_kernel<32><<<grid(32), 1024, 0, stream>>>(part, n, n, cols, first, out0, out1);
     else colsum_kernel<64><<<grid(64), 1024, 0, stream>>>(part, n, n, cols, first, out0, out1);
     return hipGetLastError();

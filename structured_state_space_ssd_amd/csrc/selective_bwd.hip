@@ -429,6 +429,25 @@ size_t selective_dbc_floats(int batch, int seqlen, int channels, int ngroups, in
     }
 }
 
+template <int NK>
+static bool sel_bwd_grid_ok(int batch, int seqlen, int channels, int ngroups, int dstate, int segs) {
+    const long long units = (long long)batch * selective_blocks(channels, ngroups, dstate) * segs;
+    return units < (1LL << 32) / SelShape<NK, true>::THREADS &&
+           (sel_dbc_part<NK>(batch, seqlen, ngroups) + 255) / 256 < (1u << 24) &&
+           colsum_grid_ok(batch * segs, (long long)channels * dstate, false) &&
+           colsum_grid_ok(batch * segs, 2LL * channels, false);
+}
+
+bool selective_bwd_grid_ok(int batch, int seqlen, int channels, int ngroups, int dstate, int segs) {
+    switch (selective_kernel_dstate(dstate)) {
+        case 4: return sel_bwd_grid_ok<4>(batch, seqlen, channels, ngroups, dstate, segs);
+        case 8: return sel_bwd_grid_ok<8>(batch, seqlen, channels, ngroups, dstate, segs);
+        case 16: return sel_bwd_grid_ok<16>(batch, seqlen, channels, ngroups, dstate, segs);
+        case 32: return sel_bwd_grid_ok<32>(batch, seqlen, channels, ngroups, dstate, segs);
+        default: return sel_bwd_grid_ok<64>(batch, seqlen, channels, ngroups, dstate, segs);
+    }
+}
+
 int selective_keep_tokens(int dstate) {
     switch (selective_kernel_dstate(dstate)) {
         case 4: return sel_keep<4>();

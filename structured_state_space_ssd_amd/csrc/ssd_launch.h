@@ -197,6 +197,9 @@ hipError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, bool x_bf16, hipStre
 // would leave all rows to few workgroups (convolution backward, 1048576 tokens of 16
 // channels: 115 us in one pass, 36 in two).
 constexpr int kColsumRows = 2048, kColsumChunks = 64;
+// Whether the launches fit a grid (fewer than 2^32 lanes): to be asked before anything
+// that they sum up is enqueued.
+bool colsum_grid_ok(int n, long long cols, bool spare);
 hipError_t launch_colsum(const float *part, int n, long long cols, long long first, float *out0,
                          float *out1, hipStream_t stream, float *spare = nullptr);
 
@@ -227,6 +230,8 @@ struct ConvBwdArgs {
     float *dweight, *dbias, *part;  // part: conv_bwd_part_bytes of scratch
 };
 size_t conv_bwd_part_bytes(int batch, int seqlen, int channels, int width);
+// Whether every launch of launch_conv_bwd fits a grid.
+bool conv_bwd_grid_ok(int batch, int seqlen, int channels, int width, const ConvParts &dy);
 hipError_t launch_conv_bwd(const ConvBwdArgs &a, bool bf16, hipStream_t stream);
 hipError_t launch_conv_step(void *state, const void *x, size_t x_row, const float *weight,
                             const float *bias, int batch, int channels, int width, int silu,
@@ -283,6 +288,8 @@ struct SelBwdArgs {
 };
 SelPlan selective_bwd_plan(int batch, int seqlen, int channels, int ngroups, int dstate);
 size_t selective_dbc_floats(int batch, int seqlen, int channels, int ngroups, int dstate);
+// Whether every launch of launch_selective_bwd fits a grid (beside the layout of B and C).
+bool selective_bwd_grid_ok(int batch, int seqlen, int channels, int ngroups, int dstate, int segs);
 hipError_t launch_selective_bwd(const SelBwdArgs &a, bool bf16, hipStream_t stream);
 
 }  // namespace ssd

@@ -307,3 +307,28 @@ def test_selective_step_c_abi_token_strides(lib):
         assert lib.ssd_selective_step(*args, ctypes.byref(st), ctypes.byref(bad), None) == -6
     st = _native.SsdSelectiveStrides(-8, 0, 8, 0, 8, 0, 10, 0, 10, 0)
     assert lib.ssd_selective_step(*args, ctypes.byref(st), ctypes.byref(bad), None) == -2
+
+
+def test_grids_past_the_limit_refused_before_any_work(lib):
+    """A grid takes fewer than 2^32 lanes. Every launch of a call is looked at
+    before its first one: calls whose later kernels pass the limit are refused as
+    unsupported, those just below it get to the workspace (missing here)."""
+    def back(batch, seqlen, channels, ngroups, dstate):
+        args = [FAKE] * 5 + [None, None, None, FAKE, None, batch, seqlen, channels, ngroups, dstate, 1]
+        return lib.ssd_selective_backward(*args, *[FAKE] * 5, *[None] * 4, None, 0, None, None, None)
+
+    # the sums of dB and dC: 4 tokens to a row of 1024 values at 64 states, 256 to a workgroup
+    assert back(1, 1 << 24, 64, 1, 64) == -3 and back(1, (1 << 24) - 4, 64, 1, 64) == -4
+    # 512 lanes to a workgroup at 32 states and more: 2^23 of them are too many
+    assert back(1 << 20, 1, 512, 1, 32) == -3 and back((1 << 20) - 1, 1, 512, 1, 32) == -4
+    # the sum of the rates' partial rows: 1024 lanes to 64 columns of channels x states
+    assert back(1, 1, 1 << 23, 1, 32) == -3 and back(1, 1, (1 << 23) - 64, 1, 32) == -4
+    assert back(1, 1, 1 << 22, 1, 64) == -3 and back(1, 1, 1 << 22, 1, 63) == -4
+
+    def conv(batch, seqlen, channels, width):
+        args = [FAKE, 0, 0, FAKE, None, None, None, 0, _ptrs(1 << 20), None, batch, seqlen, channels, width, 1, 1]
+        return lib.ssd_conv_backward(*args, FAKE, FAKE, None, None, None, 0, None)
+
+    # the sum of the filters' partial rows: channels x (width + 1) columns
+    assert conv(1, 1, 1 << 26, 3) == -3 and conv(1, 1, (1 << 26) - 16, 3) == -4
+    assert conv(1 << 20, 1 << 20, 64, 4) == -3  # the walk itself
