@@ -62,6 +62,13 @@ def _required(**tensors):
             raise ValueError(f"{name} is required")
 
 
+def _int_sizes(*tensors):
+    # the C ABI's sizes are ints, of which ctypes would pass the low 32 bits
+    for t in tensors:
+        if t.numel() > 0x7fffffff and max(t.shape) > 0x7fffffff:
+            raise ValueError(f"sizes must be below 2^31, got {tuple(t.shape)}")
+
+
 def _on_gpu(x):
     if not x.is_cuda:
         raise ValueError("x must be a GPU tensor")
@@ -96,6 +103,7 @@ def _conv_sizes(x, weight, ndim):
     if x.dim() != ndim or weight.dim() != 2 or weight.shape[0] != x.shape[-1]:
         raise ValueError("x must be [Bt, K] and weight [K, W]" if ndim == 2 else
                          "x must be [Bt, L, K] and weight [K, W]")
+    _int_sizes(x, weight)
     return weight.shape[1]
 
 
@@ -143,6 +151,7 @@ def conv_forward(x, weight, bias=None, silu=True, init_state=None, return_final_
             raise ValueError("packed sequences use batch 1 and no init_state")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be [nseq + 1]")
+        _int_sizes(cu_seqlens)
         nseq = cu_seqlens.numel() - 1
         cp = _param(cu_seqlens, "cu_seqlens", (nseq + 1,), x, torch.int32)
     _on_gpu(x)
@@ -225,6 +234,7 @@ def _selective_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit):
     lead = x.dim() - 1
     if lead not in (1, 2) or A.dim() != 2 or B.dim() != lead + 2 or B.shape[:lead] != x.shape[:lead]:
         raise ValueError("x must be [Bt, L, E], A [E, N] and B [Bt, L, G, N] (without L for one token)")
+    _int_sizes(x, B)
     E = x.shape[-1]
     G, N = B.shape[-2:]
     if G < 1 or E % G:
@@ -344,6 +354,8 @@ def _rows(t, name):
     if t.stride(-1) != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
     D = t.shape[-1]
+    if D > 0x7fffffff:  # (rows are a long long)
+        raise ValueError(f"{name}'s width must be below 2^31, got {D}")
     if t.is_contiguous():
         return (t.numel() // D if D else 0), D
     rows, step = 1, None

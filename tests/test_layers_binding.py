@@ -332,3 +332,34 @@ def test_grids_past_the_limit_refused_before_any_work(lib):
     # the sum of the filters' partial rows: channels x (width + 1) columns
     assert conv(1, 1, 1 << 26, 3) == -3 and conv(1, 1, (1 << 26) - 16, 3) == -4
     assert conv(1 << 20, 1 << 20, 64, 4) == -3  # the walk itself
+
+
+def _far(*shape, dtype=f32):
+    """A tensor of this shape that holds one element (its last axis one long or dense)."""
+    return torch.zeros(1, dtype=dtype).expand(shape)
+
+
+def test_sizes_past_an_int_refused(ssd):
+    """The C ABI's sizes are ints; a size that one does not hold is refused, not cut to
+    its low 32 bits (2^32 + 8 tokens would be 8)."""
+    many = (1 << 32) + 8
+    with pytest.raises(ValueError, match="2\\^31"):
+        ssd.conv_forward(_far(1, many, 1), z(1, 4))
+    with pytest.raises(ValueError, match="2\\^31"):
+        ssd.conv_backward(_far(1, many, 1), z(1, 4), None, _far(1, many, 1))
+    with pytest.raises(ValueError, match="2\\^31"):
+        ssd.conv_step(_far(many, 3, 1), _far(many, 1), z(1, 4))
+    with pytest.raises(ValueError, match="2\\^31"):
+        ssd.conv_forward(z(1, 6, 8), z(8, 4), cu_seqlens=_far(many, dtype=torch.int32))
+    scan = dict(x=_far(1, many, 1), dt=_far(1, many, 1), A=z(1, 1), B=_far(1, many, 1, 1), C=_far(1, many, 1, 1))
+    for call in (ssd.selective_forward, lambda **a: ssd.selective_backward(**a, D=None, dy=scan["x"])):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call(**scan)
+    one = dict(x=_far(many, 1), dt=_far(many, 1), A=z(1, 1), B=_far(many, 1, 1), C=_far(many, 1, 1))
+    with pytest.raises(ValueError, match="2\\^31"):
+        ssd.selective_step(_far(many, 1, 1), **one)
+    wide = _far(2, many)
+    for call in (lambda: ssd.norm_forward(wide, _far(many)),
+                 lambda: ssd.norm_backward(wide, wide, _far(many), None, z(2))):
+        with pytest.raises(ValueError, match="2\\^31|contiguous"):
+            call()
