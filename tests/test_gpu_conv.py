@@ -206,3 +206,165 @@ def test_conv_captured(ssd):
         es = ssd.conv_step(st, x[:, 0], w, b)
         assert torch.equal(y, ey) and torch.equal(fin, efin) and torch.equal(ys, es)
         assert torch.equal(state, st) and all(torch.equal(grads[n], eg[n]) for n in eg)
+
+
+# ---- exact sums -------------------------------------------------------------
+# Small integers in float32, without the activation: every product and every
+# partial sum is a whole number below 2^24 and so exact in any order, and each
+# result is compared for equality. All gradients are positive, so that every
+# token moves dbias: a partial row left out or added twice changes it.
+
+def integers(Bt, L, K, W, seed, dtype=F32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda lo, hi, *s: torch.randint(lo, hi + 1, s, generator=g, device="cuda")  # noqa: E731
+    return (r(-3, 3, Bt, L, K).to(dtype), r(-2, 2, K, W).float(), r(-3, 3, K).float(),
+            r(-3, 3, Bt, W - 1, K).to(dtype), r(1, 3, Bt, L, K).to(dtype), r(-3, 3, Bt, W - 1, K).to(dtype))
+
+
+def exact_forward(x, w, b, init=None, cu=None):
+    """y and the final states in float64, which holds every value exactly."""
+    Bt, L, K = x.shape
+    W = w.shape[1]
+    x, w = x.double(), w.double()
+    head = x.new_zeros(Bt, W - 1, K) if init is None else init.double()
+    xs = torch.cat([head, x], 1)
+    y = b.double().expand(Bt, L, K).clone()
+    since = None
+    if cu is not None:  # tokens of the same sequence before each one
+        at = torch.arange(L, device=x.device)
+        c = torch.tensor(cu, device=x.device)
+        since = at - c[torch.searchsorted(c, at, right=True) - 1]
+    for k in range(W):
+        term = w[:, k] * xs[:, k:k + L]
+        y += term if since is None else term * (since >= W - 1 - k)[:, None]
+    if cu is None:
+        return y, xs[:, L:]
+    c = torch.tensor(cu, device=x.device)
+    rows = c[1:, None] - (W - 1) + torch.arange(W - 1, device=x.device)
+    return y, torch.where((rows >= c[:-1, None])[..., None], x[0][rows.clamp(min=0)], 0.0)
+
+
+def exact_backward(x, w, dy, init, dfinal):
+    Bt, L, K = x.shape
+    W = w.shape[1]
+    head = x.new_zeros(Bt, W - 1, K) if init is None else init
+    xs, dy, w = torch.cat([head, x], 1).double(), dy.double(), w.double()
+    dxs = torch.zeros_like(xs)
+    if dfinal is not None:
+        dxs[:, L:] += dfinal.double()
+    for k in range(W):
+        dxs[:, k:k + L] += dy * w[:, k]
+    dw = torch.stack([(dy * xs[:, k:k + L]).sum((0, 1)) for k in range(W)], 1)
+    return {"dx": dxs[:, W - 1:], "dinit": dxs[:, :W - 1], "dweight": dw, "dbias": dy.sum((0, 1))}
+
+
+def backward_rows(Bt, L, K, W, dtype):
+    """Partial rows of a backward call, by its workspace (64 more where they are
+    summed in two passes)."""
+    from structured_state_space_ssd_amd._native import lib
+    return lib.ssd_conv_backward_workspace_size(Bt, L, K, W, int(dtype == BF)) // (4 * K * (W + 1))
+
+
+def check_exact_backward(ssd, Bt, L, K, W, dtype=F32, ends=True):
+    x, w, b, init, dy, dfinal = integers(Bt, L, K, W, L + K, dtype)
+    if not ends:
+        init = dfinal = None
+    got = ssd.conv_backward(x, w, b, dy, silu=False, init_state=init, dfinal_state=dfinal)
+    want = exact_backward(x, w, dy, init, dfinal)
+    for k in ("dweight", "dbias", "dx") + (("dinit",) if ends else ()):
+        # (dx of at most 4 * 6 + 3 is exact in bf16 as well)
+        assert torch.equal(got[k].double(), want[k]), (k, Bt, L, K, W)
+
+
+# Rows around 2048, above which they are summed to 64 rows first: ceil(rows / 64) to
+# each, so that 2049 rows of 33 leave the 63rd three and the 64th none, and 2112 none short.
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("rows", [1, 33, 2047, 2048, 2049, 2079, 2080, 2112, 2113, 3000])
+def test_conv_backward_row_sums_exact(ssd, rows, W):
+    K, tile = 5, 8
+    two = 64 if rows > 2048 else 0
+    for Bt, L in ((1, rows * tile), (1, rows * tile - 5), (rows, 3)):
+        assert backward_rows(Bt, L, K, W, F32) == rows + two
+        check_exact_backward(ssd, Bt, L, K, W)
+
+
+def test_conv_backward_row_sums_see_every_row(ssd):
+    """What the test above relies on: leaving any one tile's tokens out of the
+    reference's sum changes every column of dbias."""
+    x, w, b, init, dy, _ = integers(1, 2049 * 8 - 5, 5, 3, 1)
+    whole = dy.double().sum((0, 1))
+    tiles = torch.nn.functional.pad(dy[0].double(), (0, 0, 0, 5)).view(2049, 8, 5).sum(1)
+    assert bool((whole - tiles != whole).all()) and torch.equal(tiles.sum(0), whole)
+    assert torch.equal(ssd.conv_backward(x, w, b, dy, silu=False)["dbias"].double(), whole)
+
+
+# A tile takes more than 8 tokens only where that leaves 131072 lanes: tiles of 16, 32,
+# 64 and 128 tokens, the last one part full, with a ragged last vector of channels.
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("L,K,W,tile", [(1030, 8191, 4, 16), (1027, 8191, 2, 16), (2077, 8190, 3, 32),
+                                        (4133, 8189, 4, 64), (4001, 16383, 4, 128)], ids=str)
+def test_conv_backward_long_tiles_exact(ssd, L, K, W, tile, dtype):
+    assert backward_rows(1, L, K, W, dtype) == -(-L // tile)
+    check_exact_backward(ssd, 1, L, K, W, dtype, ends=tile != 64)
+
+
+# Forward, a tile takes 16 tokens where that leaves 262144 lanes: two groups of 8 rows,
+# over which the window, and in packed sequences the place, is carried.
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("Bt,L,K,W", [(1, 2061, 8193, 4), (3, 687, 8190, 3), (2, 1039, 8191, 2)], ids=str)
+def test_conv_forward_long_tiles_exact(ssd, Bt, L, K, W, dtype):
+    assert Bt * -(-L // 16) * -(-K // 4) >= 262144
+    x, w, b, init, _, _ = integers(Bt, L, K, W, L)
+    x, init = x.to(dtype), init.to(dtype)
+    for start in (init, None):
+        y, final = ssd.conv_forward(x, w, b, silu=False, init_state=start, return_final_state=True)
+        want, last = exact_forward(x, w, b, start)  # at most 4 * 6 + 3: exact in bf16 as well
+        assert torch.equal(y.double(), want) and torch.equal(final.double(), last)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lengths", ["short", "mixed", "second_group"])
+def test_conv_packed_long_tiles_exact(ssd, lengths, dtype):
+    L, K, W = 2061, 8193, 4
+    g = torch.Generator().manual_seed(3)
+    if lengths == "second_group":  # every boundary in a tile's second group of 8 tokens
+        cu = [0] + [16 * i + 9 + i % 7 for i in range(L // 16)] + [L]
+    else:
+        most = 6 if lengths == "short" else 60
+        cu = [0]
+        while cu[-1] < L:  # empty sequences among them
+            cu.append(min(L, cu[-1] + int(torch.randint(0, most, (1,), generator=g))))
+    x, w, b, _, _, _ = integers(1, L, K, W, 4)
+    x = x.to(dtype)
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    y, final = ssd.conv_forward(x, w, b, silu=False, cu_seqlens=c, return_final_state=True)
+    want, last = exact_forward(x, w, b, None, cu)
+    assert torch.equal(y.double(), want) and torch.equal(final.double(), last)
+
+
+def test_conv_long_tiles_silu(ssd):
+    """The activation on the longer tiles, forward and backward, under the bounds of
+    the short ones (64-bit forms with all tokens at once)."""
+    L, K, W = 2061, 8193, 4
+    x, w, b, _, g = make(1, L, K, W, BF, 8)
+    dy = torch.randn(1, L, K, generator=g).to(BF).cuda()
+    y, got = ssd.conv_forward(x, w, b), ssd.conv_backward(x, w, b, dy)
+    assert backward_rows(1, L, K, W, BF) == -(-L // 32)
+    xs = torch.cat([x.new_zeros(1, W - 1, K), x], 1).double()
+    terms = [w[:, k].double() * xs[:, k:k + L] for k in range(W)]
+    v, mag = b.double() + sum(terms), b.double().abs() + sum(t.abs() for t in terms)
+    want = R.silu(v)
+    R.check("y", y, want.cpu(), (1.1 * (W + 1) * mag + want.abs() * (8 + 2 * v.abs())).cpu(), 1.0)
+    gr, ga = dy.double() * R.silu_grad(v), dy.double().abs() * (1 + v.abs())
+    dxs, ma = torch.zeros_like(xs), torch.zeros_like(xs)
+    for k in range(W):
+        dxs[:, k:k + L] += gr * w[:, k].double()
+        ma[:, k:k + L] += ga * w[:, k].double().abs()
+    ops = W + 14 + (W + 1) * float(mag.max())
+    R.check("dx", got["dx"], dxs[:, W - 1:].cpu(), ma[:, W - 1:].cpu(), ops)
+    # A column's sum: a tile's 32 tokens one after another, then at most 3 of its 65 rows
+    # in each of 32 strands, then those
+    R.check("dbias", got["dbias"], gr.sum((0, 1)).cpu(), ga.sum((0, 1)).cpu(), ops + 32 + 3 + 32)
+    for k in range(W):
+        R.check(("dweight", k), got["dweight"][:, k], (gr * xs[:, k:k + L]).sum((0, 1)).cpu(),
+                (ga * xs[:, k:k + L].abs()).sum((0, 1)).cpu(), ops + 32 + 3 + 32)

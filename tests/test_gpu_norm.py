@@ -243,3 +243,82 @@ def test_norm_residual_without_skip(ssd, size, dtype, stream):
     both = ssd.norm_backward(dy, total, w, mean, rstd, dresidual=dres)
     one = ssd.norm_backward(dy, total, w, mean, rstd, dresidual=dres, want_dresidual=False)
     assert "dresidual" not in one and torch.equal(one["dx"], both["dx"])
+
+
+# ---- exact sums -------------------------------------------------------------
+# The statistics are inputs of the backward: with whole-number means and a power of
+# two for rstd, n = (u - m) r and its products with whole-number gradients are small
+# integers, so that the sums over rows are exact in any order and compared for equality.
+# The gradients are positive, so that every row moves dbias.
+
+def blocks_of(rows, D, dtype, want_db=True):
+    """Workgroups of a backward call, by its workspace."""
+    from structured_state_space_ssd_amd._native import lib
+    return lib.ssd_norm_backward_workspace_size(rows, D, int(dtype == BF), int(want_db)) // (4 * D * (1 + want_db))
+
+
+def check_exact_sums(ssd, rows, D, dtype, rms, gate, stream=None):
+    g = torch.Generator(device="cuda").manual_seed(rows + D)
+    r = lambda lo, hi, *s: torch.randint(lo, hi + 1, s, generator=g, device="cuda")  # noqa: E731
+    x, dy, mean = r(-3, 3, rows, D), r(1, 3, rows, D), r(-2, 2, rows)
+    w = torch.ones(D, device="cuda")
+    m = None if rms else mean.float()
+    scale, z = 1.0, None
+    if gate:  # silu(128) = 128 in float32: u = 128 x
+        z, scale = torch.full((rows, D), 128.0, dtype=dtype, device="cuda"), 128.0
+        m = None if rms else m * scale
+    # (rows differ in rstd, so that a row taken with another's statistics shows)
+    power = r(0, 2, rows)
+    rstd = 2.0 ** power.float() / scale
+    got = ssd.norm_backward(dy.to(dtype), x.to(stream or dtype), w, m, rstd, z=z, want_dbias=True)
+    # n = (x - m) 2^power, at most 20 of them and dy 3 to a row: exact to 2^24 / 60 rows
+    assert rows * 60 < 1 << 24
+    n = (x.double() - (0 if rms else mean.double()[:, None])) * 2.0 ** power.double()[:, None]
+    assert torch.equal(got["dweight"].double(), (dy * n).sum(0)), "dweight"
+    assert torch.equal(got["dbias"].double(), dy.double().sum(0)), "dbias"
+
+
+# (rows, width): more short rows than the grid's lanes hold at once, so that groups of
+# 1 to 64 lanes of a wavefront take several each and some one less; and long rows, one
+# or several vectors to a lane
+MANY = [(270001, 8), (140003, 16), (70005, 24), (140001, 33), (9001, 256), (9003, 512), (5003, 1000),
+        (2050, 2560), (1031, 8200), (777, 16384)]
+
+
+@pytest.mark.parametrize("gate", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("dtype,stream", [(BF, BF), (BF, F32), (F32, F32)], ids=["bf16", "bf16_f32", "f32"])
+@pytest.mark.parametrize("size", MANY, ids=str)
+def test_norm_row_sums_exact(ssd, size, dtype, stream, gate):
+    rows, D = size
+    if gate and stream != dtype:
+        pytest.skip("a gated x has the gate's type")
+    V = 8 if dtype == BF else 4
+    vectors, lanes = -(-D // V), 1
+    while lanes < min(vectors, 64):
+        lanes *= 2
+    groups = 256 // lanes if vectors <= 64 else 1
+    assert blocks_of(rows, D, dtype) * groups < rows  # a group takes more than one row
+    for rms in (False, True):
+        check_exact_sums(ssd, rows, D, dtype, rms, gate, stream)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("gate", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("size", [(200003, 16), (100005, 24), (13001, 256), (9003, 512)], ids=str)
+def test_norm_many_short_rows(ssd, size, dtype, gate):
+    """y, statistics, dx and dz of more short rows than the grid holds, forward too
+    (1536 lanes to a CU: 6 workgroups of 256)."""
+    rows, D = size
+    V = 8 if dtype == BF else 4
+    assert rows * 2 ** (-(-D // V) - 1).bit_length() > 256 * 6 * 256
+    for rms in (False, True):
+        x, w, b, r = make(rows, D, dtype, D)
+        z, dy = (r(rows, D), r(rows, D)) if gate else (None, r(rows, D))
+        y, mean, rstd = ssd.norm_forward(x, w, b, z=z, eps=EPS, rms=rms, return_stats=True)
+        want, m, s, mag = R.norm(x, w, b, rms, EPS, z)
+        extra = 2 * (8 + 2 * float(z.abs().max())) if gate else 0
+        R.check((size, rms, "y"), y, want, mag, OPS + extra)
+        got = ssd.norm_backward(dy, x, w, mean, rstd, z=z)
+        want, mag = R.norm_grads(dy, x, w, rms, EPS, z)
+        for k in ("dx", "dz") if gate else ("dx",):
+            R.check((size, rms, k), got[k], want[k], mag[k], 2 * (OPS + extra))

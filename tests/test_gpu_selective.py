@@ -287,3 +287,25 @@ def test_selective_step_reads_batch_strides_only(ssd):
             one["C"].data_ptr(), None, None, Bt, E, 1, N, 0, y.data_ptr(), ctypes.byref(st), None,
             _native.stream_handle())
         assert rc == 0 and torch.equal(y, want) and torch.equal(again, state)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("size", [(1, 5000, 6, 3, 1), (2, 2100, 3, 64, 1)], ids=str)
+def test_selective_many_segments(ssd, size, dtype):
+    """Few channels over very many tokens: up to 125 segments, which the last one folds
+    one after another (and the first one's adjoint from behind)."""
+    a, r = make(*size, dtype, 12)
+    dy, dfinal = r(*size[:3]), r(size[0], size[2], size[3], dt=F32)
+    want = ref(a, grads=(dy, dfinal))
+    y, final = ssd.selective_forward(**a, return_final_state=True)
+    check(size, y, want, "y")
+    check(size, final, want, "final")
+    check_grads(size, ssd.selective_backward(**a, dy=dy, dfinal_state=dfinal), want)
+
+
+@pytest.mark.parametrize("size", [(1100, 70, 8, 3, 1), (1030, 40, 6, 13, 2)], ids=str)
+def test_selective_uncut_backward(ssd, size):
+    """So many sequences that the backward walks each in one piece, over several tiles."""
+    a, r = make(*size, F32, 13)
+    dy, dfinal = r(*size[:3]), r(size[0], size[2], size[3])
+    check_grads(size, ssd.selective_backward(**a, dy=dy, dfinal_state=dfinal), ref(a, grads=(dy, dfinal)))
