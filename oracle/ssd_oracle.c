@@ -64,11 +64,10 @@ typedef struct {
 /* The step size the recurrence uses for raw dt value v of head h. */
 static double step_size(const oracle_opts *o, double v, int h)
 {
-    if (!o) return v;
+    if (!o || v != v) return v; /* a NaN stays one, where fmax and fmin would take a bound */
     if (o->dt_bias) v += (double)o->dt_bias[h];
     if (o->dt_softplus) v = fmax(v, 0.0) + log1p(exp(-fabs(v))); /* log(1 + e^v), no overflow */
-    /* by comparisons, which leave a NaN as it is */
-    if (o->dt_clamp) v = v < o->dt_min ? o->dt_min : v > o->dt_max ? o->dt_max : v;
+    if (o->dt_clamp) v = fmin(fmax(v, o->dt_min), o->dt_max);
     return v;
 }
 
