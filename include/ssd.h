@@ -547,7 +547,7 @@ int ssd_conv_step(void *state, const void *x, long long x_batch_stride, const fl
  *                channels are few and the token axis is cut into segments for
  *                that, the segments' states.
  * Outputs must not overlap inputs. E % G must be 0 (SSD_ERR_SHAPE). Token strides
- * or channels of 2^24 or more, and a call whose grid would reach 2^24 workgroups (1024 / N channels each, at
+ * (not looked at where L is 1) or channels of 2^24 or more, and a call whose grid would reach 2^24 workgroups (1024 / N channels each, at
  * least 64, N rounded up to a power of two), return SSD_ERR_UNSUPPORTED.
  */
 typedef struct {

@@ -96,6 +96,8 @@ int selective_args(ssd::SelArgs &a, const void *x, const void *dt, const float *
                                n * seqlen, n};
     if (st) {
         d = *st;
+        if (seqlen == 1)  // a single token has no stride between tokens
+            d.x_token = d.dt_token = d.z_token = d.B_token = d.C_token = 0;
         for (long long v : {d.x_batch, d.x_token, d.dt_batch, d.dt_token, d.z_batch, d.z_token,
                             d.B_batch, d.B_token, d.C_batch, d.C_token})
             if (v < 0) return SSD_ERR_SHAPE;
@@ -389,14 +391,8 @@ int ssd_selective_step(float *state, const void *x, const void *dt, const float 
     if (rc != SSD_OK) return rc;
     if ((long long)batch * channels * (ssd::selective_kernel_dstate(dstate) / 4) / 256 >= kMaxBlocks - 1)
         return SSD_ERR_UNSUPPORTED;
-    ssd_selective_strides st{};  // a single token has no stride between tokens
-    if (strides) {
-        st = *strides;
-        st.x_token = st.dt_token = st.z_token = st.B_token = st.C_token = 0;
-    }
     ssd::SelArgs a;
-    rc = selective_args(a, x, dt, A, B, C, D, z, batch, 1, channels, ngroups, dstate,
-                        strides ? &st : nullptr, opts);
+    rc = selective_args(a, x, dt, A, B, C, D, z, batch, 1, channels, ngroups, dstate, strides, opts);
     if (rc != SSD_OK) return rc;
     a.y = y;
     return status_of(ssd::launch_selective_step(a, state, dtype == SSD_BF16,

@@ -309,3 +309,19 @@ def test_selective_uncut_backward(ssd, size):
     a, r = make(*size, F32, 13)
     dy, dfinal = r(*size[:3]), r(size[0], size[2], size[3])
     check_grads(size, ssd.selective_backward(**a, dy=dy, dfinal_state=dfinal), ref(a, grads=(dy, dfinal)))
+
+
+def test_selective_one_token_far_apart(ssd):
+    """One token of many sequences out of a tensor with the tokens in front."""
+    Bt, E, N = 3, 40, 6
+    a, r = make(Bt, 1, E, N, 1, F32, 9)
+    dy = r(Bt, 1, E)
+    y, final = ssd.selective_forward(**a, return_final_state=True)
+    grads = ssd.selective_backward(**a, dy=dy)
+    for k in ("x", "dt", "z", "B", "C"):
+        t = a[k]
+        a[k] = t.as_strided(t.shape, (t.stride(0), 1 << 30) + t.stride()[2:])
+    y2, final2 = ssd.selective_forward(**a, return_final_state=True)
+    again = ssd.selective_backward(**a, dy=dy)
+    assert torch.equal(y, y2) and torch.equal(final, final2)
+    assert all(torch.equal(grads[k], again[k]) for k in grads)

@@ -363,3 +363,11 @@ def test_sizes_past_an_int_refused(ssd):
                  lambda: ssd.norm_backward(wide, wide, _far(many), None, z(2))):
         with pytest.raises(ValueError, match="2\\^31|contiguous"):
             call()
+
+
+def test_selective_one_token_has_no_token_stride(lib):
+    """A sequence of one token may come with any stride between tokens (torch leaves
+    that of an axis of length one open): it is not looked at."""
+    for token in (1 << 24, 1 << 40, -1):
+        st = (8, token, 8, token, 8, token, 10, token, 10, token)
+        assert scan_c(lib, seqlen=1, strides=st) == -4 and scan_c(lib, seqlen=2, strides=st) in (-2, -3)
