@@ -447,7 +447,7 @@ template <typename T>
 static hipError_t conv_step(void *state, const void *x, size_t x_row, const float *weight,
                             const float *bias, int batch, int K, int width, int silu,
                             const ConvParts &y, hipStream_t stream) {
-    constexpr int V = 4, U = 8;
+    constexpr int V = 4;
     const int nvec = part_vecs(y, V);
     const long long items = (long long)batch * nvec, blocks = (items + 255) / 256;
     if (blocks >= (1LL << 24)) return hipErrorNotSupported;
