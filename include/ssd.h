@@ -557,6 +557,13 @@ typedef struct {
         C_token;
 } ssd_selective_strides;
 
+/*
+ * Ends of the range: a rate of -inf forgets the state at any step size but zero, which
+ * keeps it. Infinite inputs give values that are not finite, but not always the
+ * formula's: the kernels hold 4, 8, 16, 32 or 64 states, and in those past dstate an
+ * infinity meets a zero, so that outputs can be NaN where the formula has an infinity. So
+ * can states whose decays over many tokens (exp(A sum dt) with A dt > 0) pass float32.
+ */
 size_t ssd_selective_forward_workspace_size(int batch, int seqlen, int channels, int ngroups,
                                             int dstate, int dtype);
 int ssd_selective_forward(const void *x, const void *dt, const float *A, const void *B,
@@ -590,7 +597,8 @@ int ssd_selective_step(float *state, const void *x, const void *dt, const float 
  * [Bt][E][N] (nullable) float32. Sums are in float32 in a fixed order.
  *   workspace    at least ssd_selective_backward_workspace_size(...) bytes,
  *                256-byte aligned: the states before every few (4 to 16) tokens
- *                and the partial sums. Outputs must not overlap inputs.
+ *                (per token and channel 2 bytes up to 4 states, 4 up to 16, 16 up
+ *                to 32, 64 up to 64) and the partial sums. Outputs must not overlap inputs.
  * Refused as ssd_selective_forward does, and with SSD_ERR_UNSUPPORTED where one of its
  * own grids would reach 2^32 lanes: 2^23 workgroups with more than 16 states,
  * channels * dstate of 2^28, or 2^24 tokens (of all sequences and groups) with
@@ -633,9 +641,9 @@ int ssd_norm_forward(const void *x, long long x_row_stride, const void *residual
                      void *stream);
 
 /*
- * Gradients of ssd_norm_forward. x is the forward's x or, where it had a
- * residual, its residual_out (x_dtype: that tensor's type); mean NULL: the
- * rms form. dresidual (nullable, [rows][width] dense in x_dtype) is the
+ * Gradients of ssd_norm_forward (dbias in either form). x is the forward's x
+ * or, where it had a residual, its residual_out (x_dtype: that tensor's type);
+ * mean NULL: the rms form. dresidual (nullable, [rows][width] dense in x_dtype) is the
  * gradient that reaches residual_out by the skip connection and is added to
  * the stream's. Outputs, overwritten:
  *   dx [rows][width] dense in dtype: the gradient of the forward's x;

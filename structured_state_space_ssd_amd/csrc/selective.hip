@@ -26,12 +26,15 @@
 // any span is exp(A sum dt)), and the walk of a segment starts by folding the
 // segments before it, in their order.
 //
-// Measured in bf16 with 5120 channels and 16 states: 1 x 8192 tokens 151 us for
-// the segments' states and 205 us for the walk, whose vector units are busy 94%
-// of the time; 4 x 2048 tokens 38 + 238 us (63%: mostly one workgroup to a CU).
+// Measured in bf16 with 5120 channels and 16 states: 1 x 8192 tokens 154 us for
+// the segments' states and 209 us for the walk, whose vector units are busy 94%
+// of the time; 4 x 2048 tokens 39 + 241 us (63%: mostly one workgroup to a CU), with
+// 32 states 56 + 367 us, with 64 104 + 626 us.
 // One token for 256 sequences 38 us (4.7 TB/s, bound by the states' way from
 // memory and back), for one 3.7 us, a launch. Float32, 2 x 777 tokens of 1000
-// channels and 24 states: 21 + 22 us.
+// channels and 24 states: 21 + 22 us, the time that one segment of 96 tokens takes (an
+// uncut walk takes 0.145 us a token), with vector units busy 45 to 50%: segments are two
+// tiles at least and rounded up to whole ones, too long to fill the GPU here.
 #include "selective.h"
 
 namespace ssd {

@@ -11,10 +11,14 @@
 // there, with their decays, then runs the adjoint over them. Channels and
 // states lie over lanes and wavefronts as in the forward. Bound by vector
 // issue, of which the rebuilding is a quarter. Measured in bf16 at 4 x 2048
-// tokens of 5120 channels and 16 states: first walk 226 us, walk back 630 us
+// tokens of 5120 channels and 16 states: first walk 227 us, walk back 640 us
 // (vector units busy 81% of the time, two workgroups to a CU by their registers
-// and LDS), partial dB and dC 15 us; float32, 2 x 777 tokens of 1000 channels and
-// 24 states: 24, 66 and 5 us.
+// and LDS), partial dB and dC 15 us; with 32 states 404, 1463 and 33 us, with 64, where
+// a state is kept every 4 tokens, 878, 3047 and 130 us; float32, 2 x 777 tokens of 1000
+// channels and 24 states: 24, 68 and 5 us (segments of 96 tokens, see the forward).
+//
+// What the first walk keeps is 4 bytes per (token, channel) at 16 states, 16 at 32 and
+// 64 at 64: 4 x 2048 tokens of 5120 channels take a workspace of 0.29, 0.91 and 3.5 GB.
 //
 // Sums over channels (dB, dC) are sums over lanes, of eight values per token
 // and four states: three steps swap halves between registers, so that each
