@@ -62,11 +62,10 @@ def _required(**tensors):
             raise ValueError(f"{name} is required")
 
 
-def _int_sizes(*tensors):
+def _int_sizes(*sizes):
     # the C ABI's sizes are ints, of which ctypes would pass the low 32 bits
-    for t in tensors:
-        if t.numel() > 0x7fffffff and max(t.shape) > 0x7fffffff:
-            raise ValueError(f"sizes must be below 2^31, got {tuple(t.shape)}")
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes must be below 2^31, got {sizes}")
 
 
 def _on_gpu(x):
@@ -100,11 +99,12 @@ def _workspace(workspace, need, x):
 
 def _conv_sizes(x, weight, ndim):
     _required(x=x, weight=weight)
-    if x.dim() != ndim or weight.dim() != 2 or weight.shape[0] != x.shape[-1]:
+    xs, ws = x.shape, weight.shape
+    if len(xs) != ndim or len(ws) != 2 or ws[0] != xs[-1]:
         raise ValueError("x must be [Bt, K] and weight [K, W]" if ndim == 2 else
                          "x must be [Bt, L, K] and weight [K, W]")
-    _int_sizes(x, weight)
-    return weight.shape[1]
+    _int_sizes(*xs, ws[1])
+    return ws[1]
 
 
 def _conv_parts(split, K):
@@ -151,7 +151,7 @@ def conv_forward(x, weight, bias=None, silu=True, init_state=None, return_final_
             raise ValueError("packed sequences use batch 1 and no init_state")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be [nseq + 1]")
-        _int_sizes(cu_seqlens)
+        _int_sizes(cu_seqlens.numel())
         nseq = cu_seqlens.numel() - 1
         cp = _param(cu_seqlens, "cu_seqlens", (nseq + 1,), x, torch.int32)
     _on_gpu(x)
@@ -231,17 +231,18 @@ def conv_step(state, x, weight, bias=None, silu=True, split=None):
 def _selective_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit):
     """Checked addresses of the scan's inputs, strides and options, and (G, N)."""
     _required(x=x, dt=dt, A=A, B=B, C=C)
-    lead = x.dim() - 1
-    if lead not in (1, 2) or A.dim() != 2 or B.dim() != lead + 2 or B.shape[:lead] != x.shape[:lead]:
+    xs, bs = x.shape, B.shape
+    lead = len(xs) - 1
+    if lead not in (1, 2) or A.dim() != 2 or len(bs) != lead + 2 or bs[:lead] != xs[:lead]:
         raise ValueError("x must be [Bt, L, E], A [E, N] and B [Bt, L, G, N] (without L for one token)")
-    _int_sizes(x, B)
-    E = x.shape[-1]
-    G, N = B.shape[-2:]
+    E = xs[-1]
+    G, N = bs[-2:]
+    _int_sizes(*xs, G, N)
     if G < 1 or E % G:
         raise ValueError(f"{E} channels do not divide into {G} groups")
-    pointers = [_slice(x, "x", x.shape, x), _slice(dt, "dt", x.shape, x), _param(A, "A", (E, N), x),
-                _slice(B, "B", B.shape, x), _slice(C, "C", B.shape, x), _param(D, "D", (E,), x),
-                _slice(z, "z", x.shape, x)]
+    pointers = [_slice(x, "x", xs, x), _slice(dt, "dt", xs, x), _param(A, "A", (E, N), x),
+                _slice(B, "B", bs, x), _slice(C, "C", bs, x), _param(D, "D", (E,), x),
+                _slice(z, "z", xs, x)]
     if G > 1:
         for t, name in ((B, "B"), (C, "C")):
             if t.stride(-2) != N:
