@@ -560,9 +560,10 @@ typedef struct {
 /*
  * Ends of the range: a rate of -inf forgets the state at any step size but zero, which
  * keeps it. Infinite inputs give values that are not finite, but not always the
- * formula's: the kernels hold 4, 8, 16, 32 or 64 states, and in those past dstate an
- * infinity meets a zero, so that outputs can be NaN where the formula has an infinity. So
- * can states whose decays over many tokens (exp(A sum dt) with A dt > 0) pass float32.
+ * formula's: the kernels hold 4, 8, 16, 32 or 64 states, and in those past dstate, as in
+ * a D that is not there, an infinity meets a zero, so that outputs can be NaN where the
+ * formula has an infinity. So can states whose decays over many tokens (exp(A sum dt)
+ * with A dt > 0) pass float32.
  */
 size_t ssd_selective_forward_workspace_size(int batch, int seqlen, int channels, int ngroups,
                                             int dstate, int dtype);
