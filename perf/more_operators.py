@@ -1,0 +1,573 @@
+"""The operators of a recurrent block, as cases to be measured: the gated linear
+recurrence, the join of a block's output with the residual stream and its norms,
+and dropout, for prompts, single tokens and training.
+
+``run`` computes a case with elementary torch operations, or (``own``) with the
+library's entry points. ``exact`` computes the same from the definition in 64
+bits, the recurrence token by token.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda"
+EPS = 1e-5
+C = 8.0  # the decay gates' sharpness
+
+
+def listed():
+    return [
+        # one long prompt: few channels to fill the GPU with, so the token axis has to be split;
+        # both gates are halves of one projection
+        dict(name="recurrence prompt", op="rec", mode="forward", form="gated", batch=1, seqlen=8192,
+             channels=2560, dtype="bf16", init=0, gate=0, pad=2560),
+        # a training step of a layer of the same width with its output gate
+        dict(name="recurrence train", op="rec", mode="train", form="gated", batch=8, seqlen=2048,
+             channels=2560, dtype="bf16", init=0, gate=1, pad=0),
+        # a training step over short documents packed into one token axis
+        dict(name="recurrence packed", op="rec", mode="packed", form="gated", batch=1, seqlen=16384,
+             channels=2560, dtype="bf16", init=0, gate=0, pad=0),
+        # a continued sequence of odd length in float32, log-decays made by the caller
+        dict(name="recurrence train f32", op="rec", mode="train", form="direct", batch=3, seqlen=1021,
+             channels=1312, dtype="f32", init=1, gate=0, pad=0),
+        # one token for each of 256 sequences in decoding
+        dict(name="recurrence step", op="rec", mode="step", form="gated", batch=256, seqlen=1,
+             channels=5120, dtype="bf16", init=1, gate=1, pad=5120),
+        # between two blocks in training: norm after the one, layer scale, dropout, a float32
+        # stream, norm before the next
+        dict(name="block train", op="block", mode="train", rows=16384, width=2560, dtype="bf16",
+             stream="f32", rms=1, post=1, pre=1, scale=1, gate=0, p=0.1),
+        # layer norms with a gate for every token, no dropout, an odd number of long rows
+        dict(name="block train gated", op="block", mode="train", rows=4099, width=5120, dtype="bf16",
+             stream="f32", rms=0, post=1, pre=1, scale=0, gate=1, p=0.0),
+        # a prompt through the same join in a model without dropout
+        dict(name="block prompt", op="block", mode="forward", rows=8192, width=2560, dtype="bf16",
+             stream="bf16", rms=1, post=1, pre=1, scale=1, gate=0, p=0.0),
+        # one token of a few sequences
+        dict(name="block step", op="block", mode="forward", rows=4, width=2560, dtype="bf16",
+             stream="bf16", rms=1, post=1, pre=1, scale=1, gate=0, p=0.0),
+        # dropout of a layer's activations and of their gradient
+        dict(name="dropout train", op="dropout", mode="train", rows=16384, width=5120, dtype="bf16", p=0.1, pad=0),
+        # a small odd tensor, a slice of a wider one, in float32
+        dict(name="dropout f32", op="dropout", mode="train", rows=1021, width=333, dtype="f32", p=0.35, pad=7),
+    ]
+
+
+def _loguniform(rng, lo, hi):
+    return max(lo, min(hi, int(math.exp(rng.uniform(math.log(lo), math.log(hi + 1))))))
+
+
+def draw(rng):
+    op = rng.choice(["rec", "rec", "block", "block", "dropout"])
+    dtype = rng.choice(["bf16", "f32"])
+    if op == "rec":
+        mode = rng.choice(["forward", "train", "packed", "step"])
+        channels = _loguniform(rng, 16, 8192)
+        batch = _loguniform(rng, 1, {"step": 256, "packed": 1}.get(mode, 8))
+        most = (40 << 20) // (batch * channels * (1 if dtype == "bf16" else 2))
+        seqlen = 1 if mode == "step" else _loguniform(rng, 1, max(1, min(16384, most)))
+        return dict(op=op, mode=mode, form=rng.choice(["gated", "gated", "direct"]), batch=batch,
+                    seqlen=seqlen, channels=channels, dtype=dtype,
+                    init={"step": 1, "packed": 0}.get(mode, rng.randint(0, 1)), gate=rng.randint(0, 1),
+                    pad=rng.choice([0, 0, 64, 5]))
+    width = _loguniform(rng, 16, 16384)
+    mode = rng.choice(["forward", "train"])
+    if op == "dropout":
+        rows = _loguniform(rng, 1, min(65536, (1 << 26) // width))
+        return dict(op=op, mode=mode, rows=rows, width=width, dtype=dtype, p=rng.choice([0.05, 0.1, 0.5, 0.9]),
+                    pad=rng.choice([0, 0, 8, 3]))
+    post, pre = rng.choice([(1, 1), (1, 1), (0, 1), (1, 0)])
+    # (the gradient of a norm whose input has been rounded to 8 bits depends on which way: training
+    # keeps the stream in float32)
+    return dict(op=op, mode=mode, rows=_loguniform(rng, 1, min(16384, (1 << 25) // width)), width=width,
+                dtype=dtype, stream="f32" if mode == "train" else rng.choice(["f32", dtype]), rms=rng.randint(0, 1), post=post, pre=pre,
+                scale=rng.randint(0, 1), gate=rng.randint(0, 1), p=rng.choice([0.0, 0.1, 0.3]))
+
+
+def _type(name):
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def prepare(case, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed))
+
+    def normal(*shape, dtype=torch.float32, scale=1.0):
+        return torch.randn(*shape, generator=g, device=DEV).mul_(scale).to(dtype)
+
+    def uniform(*shape, lo, hi):
+        return torch.rand(*shape, generator=g, device=DEV).mul_(hi - lo).add_(lo)
+
+    t = _type(case["dtype"])
+    train = case["mode"] in ("train", "packed")
+    s = dict(case=dict(case))
+    if case["op"] == "rec":
+        Bt, L, E, pad = (case[k] for k in ("batch", "seqlen", "channels", "pad"))
+        lead = (Bt,) if case["mode"] == "step" else (Bt, L)
+        s["x"] = normal(*lead, E, dtype=t)
+        s["z"] = normal(*lead, E, dtype=t) if case["gate"] else None
+        if case["form"] == "gated":
+            both = normal(*lead, E + max(pad, E), dtype=t)
+            s["r"], s["i"] = both[..., :E], both[..., max(pad, E):]
+            # channels that keep 0.9 to 0.999 of their state per token where the gate is open
+            rate = -torch.log(uniform(E, lo=0.9, hi=0.999)) / C
+            s["decay"] = torch.log(torch.expm1(rate))
+        else:
+            wide = -torch.exp(uniform(*lead, E + pad, lo=math.log(1e-3), hi=math.log(2.0)))
+            s["r"], s["i"], s["decay"] = wide.to(t)[..., pad:], None, None
+        s["init"] = normal(Bt, E) if case["init"] else None
+        s["cu"] = None
+        if case["mode"] == "packed":
+            q = torch.Generator().manual_seed(int(seed))
+            lengths = torch.exp(torch.rand(1 + L // 300, generator=q, dtype=torch.float64) * math.log(2049))
+            cu = torch.cat([torch.zeros(1), (lengths.cumsum(0) / lengths.sum() * L).round()])
+            s["cu"] = cu.to(torch.int32).to(DEV)
+        if train:
+            s["dy"] = normal(Bt, L, E, dtype=t)
+        return s
+    R, D = case["rows"], case["width"]
+    # the state of a counter-based generator: seed and offset
+    s["rng"] = (int(seed) * 7919 + 12345, 1 << 33 | int(seed))
+    if case["op"] == "dropout":
+        s["x"] = normal(R, D + case["pad"], dtype=t)[:, case["pad"]:]
+        s["dy"] = normal(R, D, dtype=t) if train else None
+        return s
+    st = _type(case["stream"])
+    s["x"], s["residual"] = normal(R, D, dtype=t), normal(R, D, dtype=st)
+    for k in ("post", "pre"):
+        s[k + "_w"] = 1.0 + normal(D, scale=0.1) if case[k] else None
+        s[k + "_b"] = normal(D, scale=0.1) if case[k] and not case["rms"] else None
+    s["scale"] = uniform(D, lo=0.1, hi=1.0) if case["scale"] else None
+    s["z"] = normal(R, 2 * D, dtype=t)[:, D:] if case["gate"] else None
+    # a captured step reads seed and offset from the GPU
+    s["rng_gpu"] = torch.tensor(s["rng"], dtype=torch.int64, device=DEV)
+    s["alpha"], s["beta"] = 1.25, 0.75
+    if train:
+        s["dy"] = normal(R, D, dtype=t) if case["pre"] else None
+        s["dsum"] = normal(R, D, dtype=st)
+    return s
+
+
+def run(state):
+    op = state["case"]["op"]
+    if own:
+        return {"rec": _own_rec, "block": _own_block, "dropout": _own_dropout}[op](state)
+    return {"rec": _plain_rec, "block": _plain_block, "dropout": _plain_dropout}[op](state)
+
+
+# ---- the library's entry points ------------------------------------------------
+
+def _own_rec(s):
+    import structured_state_space_ssd_amd as ssd
+    c = s["case"]
+    if c["mode"] == "step":
+        y = ssd.recurrence_step(s["init"], s["x"], s["r"], s["i"], s["decay"], z=s["z"], c=C)
+        return {"y": y, "state": s["init"]}
+    train = c["mode"] != "forward"
+    f = ssd.recurrence_forward(s["x"], s["r"], s["i"], s["decay"], z=s["z"], init_state=s["init"], c=C,
+                               cu_seqlens=s["cu"], return_final_state=True, return_states=train)
+    out = {"y": f[0], "final": f[1]}
+    if train:
+        g = ssd.recurrence_backward(s["x"], s["r"], s["i"], s["decay"], s["dy"], z=s["z"], init_state=s["init"],
+                                    c=C, cu_seqlens=s["cu"], states=f[2])
+        out.update({k: g[k] for k in ("dx", "dr", "di", "ddecay", "dz", "dinit") if g[k] is not None})
+    return out
+
+
+def _own_block(s):
+    import structured_state_space_ssd_amd as ssd
+    c = s["case"]
+    train = c["mode"] == "train"
+    kw = dict(post_weight=s["post_w"], post_bias=s["post_b"], scale=s["scale"], z=s["z"],
+              residual_scale=s["alpha"], branch_scale=s["beta"], p=c["p"], rng=s["rng_gpu"] if c["p"] else None)
+    f = ssd.block_norm_forward(s["x"], s["residual"], s["pre_w"], s["pre_b"], eps=EPS, rms=bool(c["rms"]),
+                               return_stats=train, **kw)
+    out = {"sum": f[1]}
+    if c["pre"]:
+        out["y"] = f[0]
+    if train:
+        g = ssd.block_norm_backward(s["dy"], s["dsum"], s["x"], f[1], f[2], s["pre_w"], s["pre_b"], **kw)
+        out.update({k: v for k, v in g.items() if v is not None})
+    return out
+
+
+def _own_dropout(s):
+    import structured_state_space_ssd_amd as ssd
+    out = {"y": ssd.dropout(s["x"], s["case"]["p"], s["rng"])}
+    if s["dy"] is not None:
+        out["dx"] = ssd.dropout(s["dy"], s["case"]["p"], s["rng"])
+    return out
+
+
+# ---- plain forms: 32 bits, rounded once at the end --------------------------------
+
+def _silu_grad(v):
+    p = torch.sigmoid(v)
+    return p * (1 + v * (1 - p))
+
+
+def _scan(a, u, h0):
+    """h_t = a_t h_{t-1} + u_t along dim 1, by doubling: after k rounds a and u span 2^k tokens."""
+    if h0 is not None:
+        u = torch.cat([(u[:, 0] + a[:, 0] * h0)[:, None], u[:, 1:]], 1)
+    n = 1
+    while n < a.shape[1]:
+        u = torch.cat([u[:, :n], u[:, n:] + a[:, n:] * u[:, :-n]], 1)
+        a = torch.cat([a[:, :n], a[:, n:] * a[:, :-n]], 1)
+        n *= 2
+    return u
+
+
+def _plain_rec(s):
+    c = s["case"]
+    t = s["x"].dtype
+    step = c["mode"] == "step"
+    x, r = s["x"].float(), s["r"].float()
+    if step:
+        x, r = x[:, None], r[:, None]
+    if c["form"] == "gated":
+        i = s["i"].float()
+        i = i[:, None] if step else i
+        v = s["decay"]
+        sp = torch.clamp(v, min=0) + torch.log1p(torch.exp(-v.abs()))
+        sr, si = torch.sigmoid(r), torch.sigmoid(i)
+        la = -C * sp * sr
+        b = torch.sqrt(-torch.expm1(2 * la))
+        u = b * si * x
+    else:
+        la, u = r, x
+    a = torch.exp(la)
+    if s["cu"] is not None:
+        # a sequence's first token takes nothing from the one before
+        cu = s["cu"].long()
+        first = torch.zeros(c["seqlen"] + 1, dtype=torch.bool, device=x.device)
+        first[cu[:-1]] = True
+        keep = torch.where(first[:-1], 0.0, 1.0)[:, None]
+        h = _scan(a * keep, u, None)
+        final = torch.where((cu[1:] > cu[:-1])[:, None], h[0][(cu[1:] - 1).clamp(min=0)], 0)
+    else:
+        keep = 1.0
+        h = _scan(a, u, s["init"])
+        final = h[:, -1].contiguous()
+    y = h
+    if s["z"] is not None:
+        z = s["z"].float()
+        z = z[:, None] if step else z
+        gate = z * torch.sigmoid(z)
+        y = h * gate
+    y = y.to(t)
+    if step:
+        s["init"].copy_(final)
+        return {"y": y[:, 0].contiguous(), "state": s["init"]}
+    out = {"y": y, "final": final}
+    if c["mode"] == "forward":
+        return out
+    dy = s["dy"].float()
+    if s["z"] is not None:
+        out["dz"] = (dy * h * _silu_grad(z)).to(t)
+        dy = dy * gate
+    # the adjoint runs backward: g_t = dy_t + a_{t+1} g_{t+1}
+    later = torch.cat([(a * keep)[:, 1:], torch.zeros_like(a[:, :1])], 1)
+    g = _scan(later.flip(1), dy.flip(1), None).flip(1)
+    first_h = s["init"][:, None] if s["init"] is not None else torch.zeros_like(h[:, :1])
+    back = g * a * keep * torch.cat([first_h, h[:, :-1]], 1)
+    if s["init"] is not None:
+        out["dinit"] = a[:, 0] * g[:, 0]
+    if c["form"] == "direct":
+        out["dx"], out["dr"] = g.to(t), back.to(t)
+        return out
+    out["dx"] = (g * b * si).to(t)
+    out["di"] = (g * b * x * si * (1 - si)).to(t)
+    ratio = torch.where(b > 0, la / b, 0)
+    w = back * la - g * si * x * a * a * ratio  # the log-decay's gradient times the log-decay
+    out["dr"] = (w * (1 - sr)).to(t)
+    out["ddecay"] = w.sum((0, 1)) * torch.sigmoid(v) / sp
+    return out
+
+
+def _philox(rows, groups, seed, offset):
+    """Four 32-bit words of Philox 4x32-10 (Salmon, Moraes, Dror and Shaw, 2011) for each
+    (row, group of 8 columns); seed and offset are numbers or 64-bit tensors."""
+    low = 0xFFFFFFFF
+    dev = torch.device(DEV)
+    c0 = torch.arange(groups, device=dev).expand(rows, groups)
+    c1 = torch.arange(rows, device=dev)[:, None].expand(rows, groups)
+    c2, c3 = offset & low, (offset >> 32) & low
+    k0, k1 = seed & low, (seed >> 32) & low
+    for _ in range(10):
+        # (64-bit products wrap; the masks keep their two halves)
+        p0, p1 = c0 * 0xD2511F53, c2 * 0xCD9E8D57
+        c0, c1, c2, c3 = ((p1 >> 32) & low) ^ c1 ^ k0, p1 & low, ((p0 >> 32) & low) ^ c3 ^ k1, p0 & low
+        k0, k1 = (k0 + 0x9E3779B9) & low, (k1 + 0xBB67AE85) & low
+    return [w if torch.is_tensor(w) and w.dim() == 2 else torch.as_tensor(w, device=dev).expand(rows, groups)
+            for w in (c0, c1, c2, c3)]
+
+
+def _keep(rows, width, p, seed, offset):
+    """Which elements stay: 16 bits of the generator are not below p of their range."""
+    words = torch.stack(_philox(rows, -(-width // 8), seed, offset), -1)
+    bits = torch.stack([words & 0xFFFF, words >> 16], -1).reshape(rows, -1)[:, :width]
+    return bits >= _threshold(p)
+
+
+def _threshold(p):
+    return int(math.floor(p * 65536 + 0.5))
+
+
+def _plain_dropout(s):
+    c, x = s["case"], s["x"]
+    scale = 65536 / (65536 - _threshold(c["p"]))
+
+    def drop(v):
+        keep = _keep(c["rows"], c["width"], c["p"], *s["rng"])
+        return torch.where(keep, v.float() * scale, 0).to(v.dtype)
+
+    out = {"y": drop(x)}
+    if s["dy"] is not None:
+        out["dx"] = drop(s["dy"])
+    return out
+
+
+def _plain_norm(v, w, b, rms):
+    d = v if rms else v - v.mean(-1, keepdim=True)
+    r = torch.rsqrt((d * d).mean(-1, keepdim=True) + EPS)
+    n = d * r
+    return n, r, n * w if b is None else n * w + b
+
+
+def _plain_norm_grad(dn, n, r, rms):
+    d = dn - n * (dn * n).mean(-1, keepdim=True)
+    return (d if rms else d - dn.mean(-1, keepdim=True)) * r
+
+
+def _plain_block(s):
+    c, x, res = s["case"], s["x"].float(), s["residual"]
+    rms, p, out = c["rms"], c["p"], {}
+    v = x
+    if c["post"]:
+        n1, r1, v = _plain_norm(x, s["post_w"], s["post_b"], rms)
+    m = 1.0  # what v is multiplied with on its way to the stream
+    if s["scale"] is not None:
+        m = s["scale"]
+    gate = 1.0
+    if s["z"] is not None:
+        z = s["z"].float()
+        gate = z * torch.sigmoid(z)
+    drop = 1.0
+    b = v * m * gate
+    if p:
+        keep = _keep(c["rows"], c["width"], p, s["rng_gpu"][0], s["rng_gpu"][1])
+        drop = torch.where(keep, 65536 / (65536 - _threshold(p)), 0.0)
+        b = b * drop
+    total = (s["alpha"] * res.float() + s["beta"] * b).to(res.dtype)
+    out["sum"] = total
+    if c["pre"]:
+        # the stream is what is kept, so the norm reads it as it is kept
+        n2, r2, y = _plain_norm(total.float(), s["pre_w"], s["pre_b"], rms)
+        out["y"] = y.to(s["x"].dtype)
+    if c["mode"] != "train":
+        return out
+    ds = s["dsum"].float()
+    if c["pre"]:
+        dy = s["dy"].float()
+        ds = ds + _plain_norm_grad(dy * s["pre_w"], n2, r2, rms)
+        out["dweight"] = (dy * n2).sum(0)
+        if not rms:
+            out["dbias"] = dy.sum(0)
+    out["dresidual"] = (s["alpha"] * ds).to(res.dtype)
+    db = s["beta"] * ds * drop
+    if s["z"] is not None:
+        out["dz"] = (db * v * m * _silu_grad(z)).to(s["x"].dtype)
+    db = db * gate
+    if s["scale"] is not None:
+        out["dscale"] = (db * v).sum(0)
+    dv = db * m
+    if c["post"]:
+        out["dpost_weight"] = (dv * n1).sum(0)
+        if not rms:
+            out["dpost_bias"] = dv.sum(0)
+        dv = _plain_norm_grad(dv * s["post_w"], n1, r1, rms)
+    out["dx"] = dv.to(s["x"].dtype)
+    return out
+
+
+# ---- what a pass cannot do without --------------------------------------------------
+
+def work(case):
+    e = 2 if case["dtype"] == "bf16" else 4
+    train = case["mode"] in ("train", "packed")
+    if case["op"] == "rec":
+        n, E = case["batch"] * case["seqlen"] * case["channels"], case["channels"]
+        gated = case["form"] == "gated"
+        inputs = 2 + gated + case["gate"]  # x, r, i, z
+        states = case["batch"] * E * 4
+        b, flops = n * e * (inputs + 1) + states * (1 + case["init"]) + 4 * E * gated, n * (25 if gated else 4)
+        if train:  # the inputs are there once; dy in, their gradients out
+            b += n * e * (1 + inputs) + states * case["init"] + 4 * E * gated
+            flops += n * (45 if gated else 8)
+        return {"bytes": b, "flops": flops}
+    n, D = case["rows"] * case["width"], case["width"]
+    if case["op"] == "dropout":
+        return {"bytes": n * e * (4 if train else 2), "flops": n * 15 * (2 if train else 1)}
+    r = 4 if case["stream"] == "f32" else 2
+    each = e * (1 + case["pre"] + case["gate"]) + 2 * r  # x, y, z; the stream in and out
+    params = 4 * D * ((2 - case["rms"]) * (case["post"] + case["pre"]) + case["scale"])
+    flops = n * (8 * (case["post"] + case["pre"]) + 6 + 15 * (case["p"] > 0))
+    if train:
+        each += e * (1 + case["pre"] + case["gate"]) + 2 * r  # dx, dy, dz; the stream's gradient in and out
+        params, flops = 2 * params, 3 * flops
+    return {"bytes": n * each + params, "flops": flops}
+
+
+# ---- the definition in 64 bits, the recurrence token by token -------------------------
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    s = {k: v.double() if torch.is_tensor(v) and v.is_floating_point() else v for k, v in s.items()}
+    return {"rec": _exact_rec, "block": _exact_block, "dropout": _exact_dropout}[case["op"]](s)
+
+
+def _exact_rec(s):
+    c = s["case"]
+    mode, gated = c["mode"], c["form"] == "gated"
+    x, r, i, z = (s[k][:, None] if mode == "step" and s[k] is not None else s[k] for k in ("x", "r", "i", "z"))
+    Bt, L, E = x.shape
+    cu = [0, L] if s["cu"] is None else s["cu"].tolist()
+    starts = {a for a, b in zip(cu[:-1], cu[1:]) if b > a}
+    if gated:
+        rate = C * torch.nn.functional.softplus(s["decay"], threshold=700.0)
+    h = s["init"].clone() if s["init"] is not None else x.new_zeros(Bt, E)
+    hs = x.new_empty(L + 1, Bt, E)
+    # one token's decay and input term
+    def token(t):
+        if not gated:
+            return torch.exp(r[:, t]), x[:, t], r[:, t], None, None, None
+        sr, si = torch.sigmoid(r[:, t]), torch.sigmoid(i[:, t])
+        la = -rate * sr
+        b = torch.sqrt(-torch.expm1(2 * la))
+        return torch.exp(la), b * si * x[:, t], la, b, sr, si
+
+    hs[0] = h
+    for t in range(L):
+        a, u = token(t)[:2]
+        if t in starts and s["cu"] is not None:
+            h = torch.zeros_like(h)
+        h = a * h + u
+        hs[t + 1] = h
+    H = hs[1:].transpose(0, 1)
+    y = H if z is None else H * torch.nn.functional.silu(z)
+    if mode == "step":
+        return {"y": y[:, 0], "state": h}
+    if s["cu"] is None:
+        final = h
+    else:
+        final = torch.stack([hs[b][0] if b > a else torch.zeros_like(h[0]) for a, b in zip(cu[:-1], cu[1:])])
+    out = {"y": y, "final": final}
+    if mode == "forward":
+        return out
+    dy = s["dy"]
+    if z is not None:
+        p = torch.sigmoid(z)
+        out["dz"] = dy * H * (p + z * p * (1 - p))
+        dy = dy * z * p
+    g = torch.zeros_like(h)
+    out["dx"], out["dr"] = torch.empty_like(x), torch.empty_like(x)
+    if gated:
+        out["di"], dd = torch.empty_like(x), torch.zeros_like(h)
+    for t in reversed(range(L)):
+        a, _, la, b, sr, si = token(t)
+        g = g + dy[:, t]
+        first = t in starts and s["cu"] is not None
+        dla = torch.zeros_like(g) if first else g * a * hs[t]
+        if gated:
+            # d sqrt(1 - e^(2 la)) / d la = -a^2 / b
+            dla = dla - g * si * x[:, t] * a * a / b
+            out["dx"][:, t] = g * b * si
+            out["di"][:, t] = g * b * x[:, t] * si * (1 - si)
+            out["dr"][:, t] = dla * -rate * sr * (1 - sr)
+            dd += dla * sr
+        else:
+            out["dx"][:, t], out["dr"][:, t] = g, dla
+        g = torch.zeros_like(g) if first else a * g
+    if gated:
+        out["ddecay"] = dd.sum(0) * -C * torch.sigmoid(s["decay"])
+    if s["init"] is not None:
+        out["dinit"] = g
+    return out
+
+
+def _exact_kept(rows, width, p, seed, offset):
+    groups = -(-width // 8)
+    u32 = np.uint64(0xFFFFFFFF)
+    x = [np.tile(np.arange(groups, dtype=np.uint64), rows), np.repeat(np.arange(rows, dtype=np.uint64), groups),
+         np.full(rows * groups, offset % 2 ** 32, np.uint64), np.full(rows * groups, offset // 2 ** 32, np.uint64)]
+    key = [seed % 2 ** 32, seed // 2 ** 32]
+    for n in range(10):
+        left, right = x[0] * np.uint64(0xD2511F53), x[2] * np.uint64(0xCD9E8D57)
+        k = [np.uint64((key[0] + n * 0x9E3779B9) % 2 ** 32), np.uint64((key[1] + n * 0xBB67AE85) % 2 ** 32)]
+        x = [(right >> np.uint64(32)) ^ x[1] ^ k[0], right & u32, (left >> np.uint64(32)) ^ x[3] ^ k[1], left & u32]
+    words = np.stack(x, -1).astype("<u4")
+    halves = words.view("<u2").reshape(rows, groups * 8)[:, :width]
+    return torch.from_numpy(halves.astype(np.int32) >= int(np.floor(p * 65536 + 0.5))).to(DEV)
+
+
+def _exact_dropout(s):
+    c = s["case"]
+    kept = _exact_kept(c["rows"], c["width"], c["p"], *s["rng"])
+    share = 1 - np.floor(c["p"] * 65536 + 0.5) / 65536
+    out = {"y": s["x"] * kept / share}
+    if s["dy"] is not None:
+        out["dx"] = s["dy"] * kept / share
+    return out
+
+
+def _exact_block(s):
+    c = s["case"]
+    train = c["mode"] == "train"
+    names = ["x", "residual", "post_w", "post_b", "scale", "z"]
+    leaves = {k: s[k].clone().requires_grad_(train) if s[k] is not None else None for k in names}
+
+    def norm(v, w, b):
+        m = 0.0 if c["rms"] else v.sum(-1, keepdim=True) / c["width"]
+        var = ((v - m) ** 2).sum(-1, keepdim=True) / c["width"]
+        y = (v - m) / torch.sqrt(var + EPS) * w
+        return y if b is None else y + b
+
+    v = leaves["x"]
+    if c["post"]:
+        v = norm(v, leaves["post_w"], leaves["post_b"])
+    if s["scale"] is not None:
+        v = v * leaves["scale"]
+    if s["z"] is not None:
+        v = v * torch.nn.functional.silu(leaves["z"])
+    if c["p"]:
+        share = 1 - np.floor(c["p"] * 65536 + 0.5) / 65536
+        v = v * _exact_kept(c["rows"], c["width"], c["p"], *s["rng"]) / share
+    total = s["alpha"] * leaves["residual"] + s["beta"] * v
+    out = {"sum": total.detach()}
+    dtotal = s["dsum"] if train else None
+    if c["pre"]:
+        # the norm's input is the stream as it is kept, in its own type
+        kept = total.detach().to(_type(c["stream"])).double().requires_grad_(train)
+        w = s["pre_w"].clone().requires_grad_(train)
+        b = s["pre_b"].clone().requires_grad_(train) if s["pre_b"] is not None else None
+        y = norm(kept, w, b)
+        out["y"] = y.detach()
+        if train:
+            got = torch.autograd.grad(y, [kept, w] + ([b] if b is not None else []), s["dy"])
+            dtotal = dtotal + got[0]
+            out["dweight"] = got[1]
+            if b is not None:
+                out["dbias"] = got[2]
+    if not train:
+        return out
+    keys = [k for k in names if leaves[k] is not None]
+    got = dict(zip(keys, torch.autograd.grad(total, [leaves[k] for k in keys], dtotal)))
+    for k, name in (("x", "dx"), ("residual", "dresidual"), ("post_w", "dpost_weight"), ("post_b", "dpost_bias"),
+                    ("scale", "dscale"), ("z", "dz")):
+        if k in got:
+            out[name] = got[k]
+    return out
