@@ -73,7 +73,7 @@ def draw(rng):
                     seqlen=seqlen, channels=channels, dtype=dtype,
                     init={"step": 1, "packed": 0}.get(mode, rng.randint(0, 1)), gate=rng.randint(0, 1),
                     pad=rng.choice([0, 0, 64, 5]))
-    width = _loguniform(rng, 16, 16384)
+    width = _loguniform(rng, 16, 16384 if op == "dropout" else 8192)
     mode = rng.choice(["forward", "train"])
     if op == "dropout":
         rows = _loguniform(rng, 1, min(65536, (1 << 26) // width))
