@@ -664,6 +664,145 @@ int ssd_norm_backward(const void *dy, const void *x, long long x_row_stride, int
                       float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
                       void *stream);
 
+/* ---- Operators of a recurrent block ----------------------------------------- */
+
+/*
+ * Gated linear recurrence with one state per channel:
+ *   h_t = a_t h_{t-1} + u_t,   y_t = h_t, or h_t silu(z_t) with z,
+ * gated (decay and i given): log a_t = -c softplus(decay_e) sigmoid(r_t),
+ *   u_t = sqrt(1 - a_t^2) sigmoid(i_t) x_t;
+ * direct (both NULL): log a_t = r_t, u_t = x_t.
+ *   x, r, i, z [Bt][L][E] in dtype (i with decay only, z nullable): rows with
+ *              dense channels, `strides` elements apart (NULL: dense). Strides are
+ *              non-negative, those between tokens below 2^24 (of a single token they
+ *              are not read); E below 2^24.
+ *   decay      float32 [E]; c positive and finite, not looked at without decay.
+ *   init_state float32 [Bt][E], the state before the first token (NULL: zeros).
+ *   cu_seqlens packed sequences as for ssd_forward_varlen: device int32 [nseq + 1],
+ *              batch 1, no init_state; every sequence starts from a zero state,
+ *              whatever the one before ended in. NULL: nseq is not looked at.
+ *   y          [Bt][L][E] dense, dtype.
+ *   final_state nullable, float32 [Bt][E] ([nseq][E] packed; zero for an empty one).
+ *   states     nullable, float32 [Bt][ceil(L / 32)][E]: the state before every 32nd
+ *              token, for ssd_recurrence_backward.
+ *   workspace  ssd_recurrence_forward_workspace_size bytes, 256-byte aligned.
+ * All in float32 with one rounding at the end. 1 - a^2 is formed without
+ * cancellation, so channels that hardly decay keep their input. The result does not
+ * depend on timing.
+ */
+typedef struct {
+    long long x_batch, x_token, r_batch, r_token, i_batch, i_token, z_batch, z_token;
+} ssd_recurrence_strides;
+
+size_t ssd_recurrence_forward_workspace_size(int batch, int seqlen, int channels, int packed, int dtype);
+int ssd_recurrence_forward(const void *x, const void *r, const void *i, const float *decay, float c,
+                           const void *z, int batch, int seqlen, int channels, int dtype,
+                           const float *init_state, const int *cu_seqlens, int nseq, void *y,
+                           float *final_state, float *states, void *workspace, size_t workspace_bytes,
+                           const ssd_recurrence_strides *strides, void *stream);
+
+/* One token: x, r, i, z, y [Bt][E]; `state` float32 [Bt][E] is updated in place. */
+int ssd_recurrence_step(float *state, const void *x, const void *r, const void *i, const float *decay,
+                        float c, const void *z, int batch, int channels, int dtype, void *y,
+                        const ssd_recurrence_strides *strides, void *stream);
+
+/*
+ * Gradients of sum(dy * y) + sum(dfinal_state * final_state) for
+ * ssd_recurrence_forward on the same inputs.
+ *   states       what the forward wrote for these inputs, or NULL: they are made
+ *                again in the workspace.
+ *   dy           dense, dtype. dfinal_state nullable, float32 like final_state.
+ * Outputs (overwritten): dx, dr, di (with decay), dz (with z), dense, dtype;
+ *   ddecay float32 [E] (with decay); dinit_state nullable, float32 [Bt][E], not packed.
+ * workspace: ssd_recurrence_backward_workspace_size bytes, 256-byte aligned;
+ * have_states: whether `states` is given.
+ */
+size_t ssd_recurrence_backward_workspace_size(int batch, int seqlen, int channels, int packed,
+                                              int have_states, int dtype);
+int ssd_recurrence_backward(const void *x, const void *r, const void *i, const float *decay, float c,
+                            const void *z, const float *init_state, const int *cu_seqlens, int nseq,
+                            const float *states, const void *dy, const float *dfinal_state, int batch,
+                            int seqlen, int channels, int dtype, void *dx, void *dr, void *di,
+                            float *ddecay, void *dz, float *dinit_state, void *workspace,
+                            size_t workspace_bytes, const ssd_recurrence_strides *strides, void *stream);
+
+/*
+ * What dropout draws from: the mask is a function of these and an element's row and
+ * column, computed wherever it is needed and never stored.
+ *   p      the share that is dropped, 0 to 1; taken to the nearest 1/65536 (a half up),
+ *          what stays is multiplied by 65536 / (65536 - that). 1: everything is dropped.
+ *   state  nullable DEVICE pointer to two 64-bit words, seed and offset, read by the
+ *          kernels in place of the next two fields: a captured graph draws anew
+ *          on a replay when they have changed. 8-byte aligned.
+ *   seed, offset  of Philox 4x32-10: its key is the seed, its counter
+ *          (column / 8, row, offset low, offset high). Column c takes the lower (c even)
+ *          or upper 16 bits of word (c % 8) / 2 and is dropped where they are
+ *          below round(65536 p).
+ */
+typedef struct {
+    double p;
+    unsigned long long seed, offset;
+    const unsigned long long *state;
+} ssd_random;
+
+/*
+ * y = x / (1 - p) where an element stays, 0 where it is dropped (also where it was
+ * infinite or not a number). x [rows][width], rows x_row_stride elements apart, y
+ * dense, dtype; at most 2^31 - 1 rows. On the gradient, with the same `random`, it is the
+ * backward pass. y must not overlap x.
+ */
+int ssd_dropout(const void *x, long long x_row_stride, long long rows, int width, const ssd_random *random,
+                int dtype, void *y, void *stream);
+
+/*
+ * A block's output joined with the residual stream, and the next block's input, for
+ * every row:
+ *   v = norm(x) post_weight + post_bias     (no post_weight: v = x)
+ *   sum = residual_scale residual + branch_scale dropout(v scale silu(z))
+ *   y = norm(sum) weight + bias             (no weight: no y)
+ * with layer norms or (rms) their root-mean-square form, over sum as it is kept.
+ *   x, z       [rows][width] in dtype, rows x_row_stride and z_row_stride elements
+ *              apart; z nullable. width at most 8192, at most 2^31 - 1 rows.
+ *   residual, sum  [rows][width] dense, stream_dtype: dtype or SSD_F32.
+ *   block      the parameters, float32 [width] each; any may be NULL, but not both
+ *              weights, nor a weight whose bias is given. Scales finite, eps >= 0.
+ *   random     NULL: no dropout.
+ *   y          dense, dtype. mean, rstd, post_mean, post_rstd: nullable, float32
+ *              [rows], the norms' statistics (means not written with rms).
+ * Outputs must not overlap inputs, except that sum may be residual.
+ */
+typedef struct {
+    const float *weight, *bias, *post_weight, *post_bias, *scale;
+    float residual_scale, branch_scale;
+    int rms;
+    float eps;
+} ssd_block;
+
+int ssd_block_norm_forward(const void *x, long long x_row_stride, const void *residual, int stream_dtype,
+                           const void *z, long long z_row_stride, const ssd_block *block,
+                           const ssd_random *random, long long rows, int width, int dtype, void *y,
+                           void *sum, float *mean, float *rstd, float *post_mean, float *post_rstd,
+                           void *stream);
+
+/*
+ * Gradients of sum(dy * y) + sum(dsum * sum), given the forward's arguments, sum and
+ * statistics.
+ *   dy         with block->weight only, dense, dtype. dsum nullable, like sum.
+ * Outputs (overwritten): dx, dz (with z) dense, dtype; dresidual dense, stream_dtype;
+ *   the parameters' gradients float32 [width], NULL where not wanted and where there is no
+ *   such parameter (block->bias alone is not looked at: dbias is a sum of dy).
+ * workspace: ssd_block_norm_backward_workspace_size bytes, 256-byte aligned.
+ * eps is not read, but checked.
+ */
+size_t ssd_block_norm_backward_workspace_size(long long rows, int width, int dtype);
+int ssd_block_norm_backward(const void *dy, const void *dsum, const void *x, long long x_row_stride,
+                            const void *sum, int stream_dtype, const void *z, long long z_row_stride,
+                            const ssd_block *block, const ssd_random *random, const float *mean,
+                            const float *rstd, const float *post_mean, const float *post_rstd,
+                            long long rows, int width, int dtype, void *dx, void *dresidual, void *dz,
+                            float *dweight, float *dbias, float *dpost_weight, float *dpost_bias,
+                            float *dscale, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,13 +13,16 @@ import torch
 
 from . import _native
 from ._native import SSDError, check, dtype_code, ptr, stream_handle
+from .blocks import (block_norm_backward, block_norm_forward, dropout, recurrence_backward,
+                     recurrence_forward, recurrence_step)
 from .layers import (conv_backward, conv_forward, conv_step, norm_backward, norm_forward,
                      selective_backward, selective_forward, selective_step)
 
 __all__ = ["forward", "forward_plan", "plan_info", "backward", "forward_varlen", "step", "options", "workspace_size", "chunk_cumsum", "chunk_state",
            "state_passing", "chunk_cb", "chunk_scan", "SSDError", "stages", "conv_forward", "conv_backward",
            "conv_step", "selective_forward", "selective_backward", "selective_step", "norm_forward",
-           "norm_backward"]
+           "norm_backward", "recurrence_forward", "recurrence_backward", "recurrence_step",
+           "block_norm_forward", "block_norm_backward", "dropout"]
 
 HEADDIM = 64
 

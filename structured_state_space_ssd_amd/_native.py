@@ -42,11 +42,33 @@ class SsdSelectiveStrides(ctypes.Structure):
                  "B_token", "C_batch", "C_token")]
 
 
+class SsdRecurrenceStrides(ctypes.Structure):
+    """ssd_recurrence_strides of include/ssd.h."""
+    _fields_ = [(n, ctypes.c_longlong) for n in
+                ("x_batch", "x_token", "r_batch", "r_token", "i_batch", "i_token", "z_batch", "z_token")]
+
+
+class SsdRandom(ctypes.Structure):
+    """ssd_random of include/ssd.h."""
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_ulonglong), ("offset", ctypes.c_ulonglong),
+                ("state", ctypes.c_void_p)]
+
+
+class SsdBlock(ctypes.Structure):
+    """ssd_block of include/ssd.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("weight", "bias", "post_weight", "post_bias", "scale")] + \
+               [("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float), ("rms", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _ll, _f = ctypes.c_longlong, ctypes.c_float
 _op = ctypes.POINTER(SsdOptions)
 _pp = ctypes.POINTER(SsdPlan)
 _ssp = ctypes.POINTER(SsdSelectiveStrides)
+_rsp = ctypes.POINTER(SsdRecurrenceStrides)
+_rp = ctypes.POINTER(SsdRandom)
+_bp = ctypes.POINTER(SsdBlock)
 
 # name -> (restype, argtypes); mirrors include/ssd.h
 SIGNATURES = {
@@ -86,6 +108,17 @@ SIGNATURES = {
     "ssd_norm_backward_workspace_size": (_sz, [_ll, _i, _i, _i]),
     "ssd_norm_backward": (_i, [_vp, _vp, _ll, _i, _vp, _ll, _vp, _vp, _vp, _vp, _ll, _i, _i]
                           + [_vp] * 6 + [_sz, _vp]),
+    "ssd_recurrence_forward_workspace_size": (_sz, [_i] * 5),
+    "ssd_recurrence_forward": (_i, [_vp] * 4 + [_f, _vp] + [_i] * 4 + [_vp, _vp, _i] + [_vp] * 4 + [_sz, _rsp, _vp]),
+    "ssd_recurrence_step": (_i, [_vp] * 5 + [_f, _vp] + [_i] * 3 + [_vp, _rsp, _vp]),
+    "ssd_recurrence_backward_workspace_size": (_sz, [_i] * 6),
+    "ssd_recurrence_backward": (_i, [_vp] * 4 + [_f, _vp, _vp, _vp, _i] + [_vp] * 3 + [_i] * 4 + [_vp] * 7
+                                + [_sz, _rsp, _vp]),
+    "ssd_dropout": (_i, [_vp, _ll, _ll, _i, _rp, _i, _vp, _vp]),
+    "ssd_block_norm_forward": (_i, [_vp, _ll, _vp, _i, _vp, _ll, _bp, _rp, _ll, _i, _i] + [_vp] * 7),
+    "ssd_block_norm_backward_workspace_size": (_sz, [_ll, _i, _i]),
+    "ssd_block_norm_backward": (_i, [_vp] * 3 + [_ll, _vp, _i, _vp, _ll, _bp, _rp] + [_vp] * 4 + [_ll, _i, _i]
+                                + [_vp] * 9 + [_sz, _vp]),
 }
 
 

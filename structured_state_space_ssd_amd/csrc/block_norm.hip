@@ -1,0 +1,511 @@
+// What joins a block's output x to the residual stream r and makes the next
+// block's input, in one pass over both, and its gradients. For a row:
+//   v = norm(x) w1 + b1   (the norm after the block; without it v = x)
+//   b = v g silu(z)       (layer scale g per column, gate z per element)
+//   d = b / (1 - p) where the element stays, else 0                (dropout.h)
+//   s = alpha r + beta d  (kept in the stream's type)
+//   y = norm(s) w2 + b2   (the norm before the next block, of s as it is kept)
+// norm(u) = (u - m) / sqrt(mean((u - m)^2) + eps) = n, m the mean or, in the
+// root-mean-square form, 0; its gradient of dn is rstd (dn - mean(dn) - n mean(dn n)).
+// Backward, with ds the gradient of s (dsum and, through the norm before, dy's):
+//   dr = alpha ds,  db = beta ds / (1 - p) or 0,  dz = db v g silu'(z),
+//   e = db silu(z),  dx = gradient of norm(x) for e g w1,
+//   dw2 = sum dy n2, db2 = sum dy, and from P = sum e n1 and Q = sum e over the rows
+//   dw1 = g P, db1 = g Q, dg = w1 P + b1 Q (without the norm after: dg = sum e x).
+// So four sums per column give all five parameters' gradients.
+//
+// Bound by memory: every tensor is read once and written once. A row stays in
+// registers from the load to the stores, held by a group of lanes as in norm.hip;
+// the two norms are two rounds of sums over it. Nothing between x and y goes
+// through memory but the stream and, for training, four numbers a row.
+#include "dropout.h"
+#include "ssd_launch.h"
+#include "ssd_rows.h"
+
+namespace ssd {
+
+namespace {
+
+// Lanes of a workgroup at most, forward and backward: the backward's four sums per
+// column want registers.
+constexpr int kBlockFwdMost = 1024, kBlockBwdMost = 512;
+
+// A column parameter's values at c .. c + V - 1; none given: `none`.
+template <int V>
+__device__ __forceinline__ void col_load(float (&v)[V], const float *p, int c, int n, float none) {
+    RowRaw<float, V> r;
+    if (p) r.load(p + c, n);
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = p ? r.get(e) : none;
+}
+
+// The bits of columns c .. c + V - 1 (c a multiple of V, 4 or 8), the first one's first.
+template <int V>
+__device__ __forceinline__ DropBits drop_bits(const DropState &rng, int c, long long row) {
+    DropBits b;
+    b.set(rng, c, static_cast<uint32_t>(row));
+    if (V == 4 && (c & 4)) {
+        b.w[0] = b.w[2];
+        b.w[1] = b.w[3];
+    }
+    return b;
+}
+
+// T: type of x, z, y. R: type of the stream.
+template <typename T, typename R, int NV>
+__global__ __launch_bounds__(kBlockFwdMost, 4) void block_fwd_kernel(BlockArgs a, int lpr) {
+    constexpr int V = vec_of<T>();
+    __shared__ float buf[2][16];
+    int turn = 0;  // sums take the two buffers in turn (row_sum)
+    if (NV > 1) lpr = 0;  // only whole workgroups hold more than a vector per lane
+    const RowGroup g = row_group(lpr);
+    const int D = a.width, step = (lpr ? lpr : (int)blockDim.x) * V;
+    const float inv = 1.0f / static_cast<float>(D);
+    const long long stride = (long long)gridDim.x * g.groups;
+    const T *x = static_cast<const T *>(a.x), *z = static_cast<const T *>(a.z);
+    const R *res = static_cast<const R *>(a.residual);
+    T *y = static_cast<T *>(a.y);
+    R *sum = static_cast<R *>(a.sum);
+    DropState rng{};
+    if (a.drop.threshold) rng = drop_state(a.drop);
+    RowRaw<T, V> xr[NV], zr[NV];
+    RowRaw<R, V> rr[NV];
+    auto fetch = [&](long long row) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = g.lane * V + i * step, n = D - c;
+            xr[i].zero();
+            if (row < a.rows && n > 0) {
+                xr[i].load(x + row * a.x_stride + c, n);
+                rr[i].load(res + row * D + c, n);
+                if (z) zr[i].load(z + row * a.z_stride + c, n);
+            }
+        }
+    };
+    // u - m for the norm's mean m (0 past the row's end), and 1 / deviation
+    auto norm = [&](float (&u)[NV][V], float &m) {
+        m = 0.0f;
+        if (!a.rms) {
+            float s[1] = {0.0f};
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[0] += u[i][e];
+            row_sum(s, lpr, buf[turn]);
+            turn ^= 1;
+            m = s[0] * inv;
+        }
+        float q[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int n = D - (g.lane * V + i * step);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (e < n) {
+                    u[i][e] -= m;
+                    q[0] += u[i][e] * u[i][e];
+                }
+        }
+        row_sum(q, lpr, buf[turn]);
+        turn ^= 1;
+        return 1.0f / sqrtf(q[0] * inv + a.eps);
+    };
+    long long row = (long long)blockIdx.x * g.groups + g.group;
+    constexpr bool AHEAD = NV == 1;
+    if (AHEAD) fetch(row);
+    for (; row < a.rows; row += stride) {
+        if (!AHEAD) fetch(row);
+        float u[NV][V], s[NV][V];
+        RowRaw<T, V> zk[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                u[i][e] = xr[i].get(e);
+                s[i][e] = rr[i].get(e);
+            }
+            zk[i] = zr[i];
+        }
+        if (AHEAD) fetch(row + stride);
+        if (a.post_weight) {
+            float m;
+            const float r = norm(u, m);
+            if (g.lane == 0) {
+                if (a.post_mean && !a.rms) a.post_mean[row] = m;
+                if (a.post_rstd) a.post_rstd[row] = r;
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = g.lane * V + i * step, n = D - c;
+                if (n <= 0) continue;
+                float w[V], b[V];
+                col_load(w, a.post_weight, c, n, 0.0f);
+                col_load(b, a.post_bias, c, n, 0.0f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) u[i][e] = u[i][e] * r * w[e] + b[e];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = g.lane * V + i * step, n = D - c;
+            if (n <= 0) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[i][e] = 0.0f;
+                continue;
+            }
+            if (a.scale) {
+                float k[V];
+                col_load(k, a.scale, c, n, 1.0f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) u[i][e] *= k[e];
+            }
+            if (z)
+#pragma unroll
+                for (int e = 0; e < V; ++e) u[i][e] *= silu_f32(zk[i].get(e));
+            if (a.drop.threshold) {
+                const DropBits bits = drop_bits<V>(rng, c, row);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    u[i][e] = bits.keep(e, a.drop.threshold) ? u[i][e] * a.drop.scale : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e)  // the next norm reads the stream as it is kept
+                s[i][e] = to_f32(from_f32<R>(fmaf(a.beta, u[i][e], a.alpha * s[i][e])));
+            row_store(sum + row * D + c, s[i], n);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (e >= n) s[i][e] = 0.0f;
+        }
+        if (!a.weight) continue;
+        float m;
+        const float r = norm(s, m);
+        if (g.lane == 0) {
+            if (a.mean && !a.rms) a.mean[row] = m;
+            if (a.rstd) a.rstd[row] = r;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = g.lane * V + i * step, n = D - c;
+            if (n <= 0) continue;
+            float w[V], b[V];
+            col_load(w, a.weight, c, n, 0.0f);
+            col_load(b, a.bias, c, n, 0.0f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) w[e] = s[i][e] * r * w[e] + b[e];
+            row_store(y + row * D + c, w, n);
+        }
+    }
+}
+
+// Each workgroup (or, for short rows, each group of lanes) keeps its columns' four
+// sums in registers over its rows and writes them once at its end, those that are
+// wanted: part[workgroup][dw2, db2, P, Q][D]. block_sum_kernel adds them up in a fixed
+// order.
+template <typename T, typename R, int NV>
+__global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kernel(BlockBwdArgs a, int lpr) {
+    constexpr int V = vec_of<T>();
+    constexpr bool AHEAD = NV == 1;  // wider rows leave no registers for the next one
+    __shared__ float buf[2][32];
+    __shared__ float acc[NV == 1 ? kShortWaves * V * 64 : 1];
+    if (NV > 1) lpr = 0;  // only whole workgroups hold more than a vector per lane
+    const RowGroup g = row_group(lpr);
+    const int D = a.width;
+    int step = (lpr ? lpr : (int)blockDim.x) * V;
+    const float inv = 1.0f / static_cast<float>(D);
+    const long long stride = (long long)gridDim.x * g.groups;
+    const T *dy = static_cast<const T *>(a.dy), *x = static_cast<const T *>(a.x);
+    const T *z = static_cast<const T *>(a.z);
+    const R *dsum = static_cast<const R *>(a.dsum), *sum = static_cast<const R *>(a.sum);
+    DropState rng{};
+    if (a.drop.threshold) rng = drop_state(a.drop);
+    float dw[NV][V], db[NV][V], sp[NV][V], sq[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = sp[i][e] = sq[i][e] = 0.0f;
+    RowRaw<T, V> yn[NV], xn[NV], zn[NV];
+    RowRaw<R, V> sn[NV];
+    float m2n = 0.0f, r2n = 0.0f, m1n = 0.0f, r1n = 1.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        yn[i].zero();
+        xn[i].zero();
+        zn[i].zero();
+        sn[i].zero();
+    }
+    auto fetch = [&](long long row) {
+        if (row >= a.rows) return;
+        if (a.weight) {
+            m2n = a.mean ? a.mean[row] : 0.0f;
+            r2n = a.rstd[row];
+        }
+        if (a.post_weight) {
+            m1n = a.post_mean ? a.post_mean[row] : 0.0f;
+            r1n = a.post_rstd[row];
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = g.lane * V + i * step, n = D - c;
+            if (n <= 0) continue;
+            if (a.weight) {
+                yn[i].load(dy + row * D + c, n);
+                sn[i].load(sum + row * D + c, n);
+            }
+            xn[i].load(x + row * a.x_stride + c, n);
+            if (z) zn[i].load(z + row * a.z_stride + c, n);
+        }
+    };
+    long long row = (long long)blockIdx.x * g.groups + g.group;
+    int turn = 0;  // sums take the two buffers in turn (row_sum)
+    if (AHEAD) fetch(row);
+    for (; row < a.rows; row += stride) {
+        if (!AHEAD) {
+            asm volatile("" : "+s"(step));  // the offsets anew each row: kept, they spill
+            fetch(row);
+        }
+        RowRaw<T, V> yr[NV], xr[NV], zr[NV];
+        RowRaw<R, V> sr[NV], dr[NV];
+        const float m1 = m1n, r1 = r1n, m2 = m2n, r2 = r2n;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            yr[i] = yn[i];
+            xr[i] = xn[i];
+            zr[i] = zn[i];
+            sr[i] = sn[i];
+            const int c = g.lane * V + i * step, n = D - c;
+            dr[i].zero();
+            if (dsum && n > 0) dr[i].load(dsum + row * D + c, n);
+        }
+        if (AHEAD) fetch(row + stride);
+        float ds[NV][V];
+        if (!a.weight) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < V; ++e) ds[i][e] = dr[i].get(e);
+        } else {
+            float s[2] = {0.0f, 0.0f};
+            // (past the row's end s = 0, but s - m is not)
+            auto normal = [&](int i, int e, int n) { return e < n ? (sr[i].get(e) - m2) * r2 : 0.0f; };
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = g.lane * V + i * step, n = D - c;
+                if (n <= 0) continue;
+                float w[V];
+                col_load(w, a.weight, c, n, 0.0f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float d = yr[i].get(e), nn = normal(i, e, n), t = d * w[e];
+                    dw[i][e] += d * nn;
+                    db[i][e] += d;
+                    s[0] += t;
+                    s[1] += t * nn;
+                }
+            }
+            row_sum(s, lpr, buf[turn]);
+            turn ^= 1;
+            const float c0 = a.mean ? s[0] * inv : 0.0f, c1 = s[1] * inv;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = g.lane * V + i * step, n = D - c;
+                if (n <= 0) continue;
+                float w[V];
+                col_load(w, a.weight, c, n, 0.0f);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    ds[i][e] = dr[i].get(e) + r2 * (yr[i].get(e) * w[e] - c0 - normal(i, e, n) * c1);
+            }
+        }
+        float s[2] = {0.0f, 0.0f};
+        // x as it goes into the gate's product: normalised, or itself
+        auto inner = [&](int i, int e, int n) { return e < n ? (xr[i].get(e) - m1) * r1 : 0.0f; };
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = g.lane * V + i * step, n = D - c;
+            if (n <= 0) continue;
+            float o[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                o[e] = a.alpha * ds[i][e];
+                ds[i][e] *= a.beta;
+            }
+            row_store(static_cast<R *>(a.dresidual) + row * D + c, o, n);
+            if (a.drop.threshold) {
+                const DropBits bits = drop_bits<V>(rng, c, row);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    ds[i][e] = bits.keep(e, a.drop.threshold) ? ds[i][e] * a.drop.scale : 0.0f;
+            }
+            float k[V], w[V];
+            col_load(k, a.scale, c, n, 1.0f);
+            col_load(w, a.post_weight, c, n, 1.0f);
+            if (z) {
+                float b[V];
+                col_load(b, a.post_bias, c, n, 0.0f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float zv = zr[i].get(e);
+                    o[e] = ds[i][e] * (inner(i, e, n) * w[e] + b[e]) * k[e] * silu_grad_f32(zv);
+                    ds[i][e] *= silu_f32(zv);
+                }
+                row_store(static_cast<T *>(a.dz) + row * D + c, o, n);
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float nn = inner(i, e, n);
+                sp[i][e] += ds[i][e] * nn;
+                sq[i][e] += ds[i][e];
+                ds[i][e] *= k[e] * w[e];
+                if (e < n) s[0] += ds[i][e];
+                s[1] += ds[i][e] * nn;
+            }
+        }
+        float c0 = 0.0f, c1 = 0.0f;
+        if (a.post_weight) {
+            row_sum(s, lpr, buf[turn]);
+            turn ^= 1;
+            c0 = a.post_mean ? s[0] * inv : 0.0f;
+            c1 = s[1] * inv;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = g.lane * V + i * step, n = D - c;
+            if (n <= 0) continue;
+            float o[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                o[e] = a.post_weight ? r1 * (ds[i][e] - c0 - inner(i, e, n) * c1) : ds[i][e];
+            row_store(static_cast<T *>(a.dx) + row * D + c, o, n);
+        }
+    }
+    // [workgroup][the wanted of dw2, db2, P, Q][D]
+    float *p = a.part + (size_t)blockIdx.x * a.sums * D;
+    auto put = [&](float (&v)[NV][V]) {
+        if (NV == 1 && lpr) {  // short rows: the groups of a wavefront meet, then the wavefronts
+            const int w = wave_id(), l = lane_id();
+            for (int off = lpr; off < 64; off <<= 1)
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[0][e] += __shfl_xor(v[0][e], off);
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[(w * V + e) * 64 + l] = v[0][e];
+            __syncthreads();
+            if (!w && l < lpr)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+#pragma unroll
+                    for (int k = 1; k < kShortWaves; ++k) v[0][e] += acc[(k * V + e) * 64 + l];
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = g.lane * V + i * step, n = D - c;
+            if (n > 0 && (!lpr || threadIdx.x < (unsigned)lpr)) row_store(p + c, v[i], n);
+        }
+        p += D;
+    };
+    if (a.dweight) put(dw);
+    if (a.dbias) put(db);
+    if (a.want_p) put(sp);
+    if (a.want_q) put(sq);
+}
+
+// Adds up the partial rows, 32 strands of them to a column, and makes the parameters'
+// gradients of the sums: blockIdx.y 0 the norm before's, 1 what lies after the block.
+__global__ __launch_bounds__(1024) void block_sum_kernel(BlockBwdArgs a, int rows) {
+    __shared__ float buf[32][32];
+    const int col = threadIdx.x & 31, strand = threadIdx.x >> 5, D = a.width;
+    const int c = blockIdx.x * 32 + col;
+    const bool first = blockIdx.y == 0;
+    auto total = [&](int which) {  // of partial row `which` of every workgroup
+        float s = 0.0f;
+        if (c < D)
+#pragma unroll 4
+            for (int k = strand; k < rows; k += 32) s += a.part[((size_t)k * a.sums + which) * D + c];
+        __syncthreads();
+        buf[strand][col] = s;
+        __syncthreads();
+        s = 0.0f;
+        if (strand == 0)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s += buf[k][col];
+        return s;
+    };
+    const bool out = strand == 0 && c < D;
+    const int before = (a.dweight != nullptr) + (a.dbias != nullptr);
+    if (first) {
+        int k = 0;
+        if (a.dweight) {
+            const float s = total(k++);
+            if (out) a.dweight[c] = s;
+        }
+        if (a.dbias) {
+            const float s = total(k++);
+            if (out) a.dbias[c] = s;
+        }
+        return;
+    }
+    const float p = a.want_p ? total(before) : 0.0f, q = a.want_q ? total(before + a.want_p) : 0.0f;
+    if (!out) return;
+    const float g = a.scale ? a.scale[c] : 1.0f;
+    if (a.dpost_weight) a.dpost_weight[c] = g * p;
+    if (a.dpost_bias) a.dpost_bias[c] = g * q;
+    if (a.dscale)
+        a.dscale[c] = a.post_weight ? a.post_weight[c] * p + (a.post_bias ? a.post_bias[c] * q : 0.0f) : p;
+}
+
+constexpr int kBlockFwdLanes = 1024, kBlockBwdLanes = 768;
+
+// Workgroups: as many as run at once, but no more than there are rows for.
+int block_blocks(long long rows, const NormShape &s, int lanes) {
+    const long long want = (rows + s.groups - 1) / s.groups;
+    const int resident = 256 * (lanes / s.threads > 1 ? lanes / s.threads : 1);
+    return static_cast<int>(want < resident ? want : resident);
+}
+
+template <typename T, typename R> hipError_t block_fwd(const BlockArgs &a, hipStream_t stream) {
+    const NormShape s = norm_shape(a.width, vec_of<T>(), kBlockFwdMost);
+    const int grid = block_blocks(a.rows, s, kBlockFwdLanes);
+    if (s.nv == 1) {
+        block_fwd_kernel<T, R, 1><<<grid, s.threads, 0, stream>>>(a, s.lpr);
+        return hipGetLastError();
+    }
+    if constexpr (sizeof(T) == 4)  // 8192 float32 values are two vectors of 4 for 1024 lanes
+        if (s.nv == 2) {
+            block_fwd_kernel<T, R, 2><<<grid, s.threads, 0, stream>>>(a, s.lpr);
+            return hipGetLastError();
+        }
+    return hipErrorInvalidValue;
+}
+
+template <typename T, typename R> hipError_t block_bwd(const BlockBwdArgs &a, hipStream_t stream) {
+    const NormShape s = norm_shape(a.width, vec_of<T>(), kBlockBwdMost);
+    const int grid = block_blocks(a.rows, s, kBlockBwdLanes);
+    constexpr int WIDEST = kMaxBlockWidth / kBlockBwdMost / vec_of<T>();  // 2, float32 4
+    if (s.nv == 1) block_bwd_kernel<T, R, 1><<<grid, s.threads, 0, stream>>>(a, s.lpr);
+    else if (s.nv == 2) block_bwd_kernel<T, R, 2><<<grid, s.threads, 0, stream>>>(a, s.lpr);
+    else if (s.nv == WIDEST) block_bwd_kernel<T, R, WIDEST><<<grid, s.threads, 0, stream>>>(a, s.lpr);
+    else return hipErrorInvalidValue;
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.sums == 0) return e;
+    block_sum_kernel<<<dim3((a.width + 31) / 32, a.want_p || a.want_q ? 2 : 1), 1024, 0, stream>>>(a, grid);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t block_bwd_part_bytes(long long rows, int width, bool bf16, int sums) {
+    const NormShape s = norm_shape(width, bf16 ? 8 : 4, kBlockBwdMost);
+    return (size_t)block_blocks(rows, s, kBlockBwdLanes) * sums * width * sizeof(float);
+}
+
+hipError_t launch_block_fwd(const BlockArgs &a, bool bf16, bool stream_bf16, hipStream_t stream) {
+    if (!bf16) return block_fwd<float, float>(a, stream);
+    return stream_bf16 ? block_fwd<bf16_t, bf16_t>(a, stream) : block_fwd<bf16_t, float>(a, stream);
+}
+
+hipError_t launch_block_bwd(const BlockBwdArgs &a, bool bf16, bool stream_bf16, hipStream_t stream) {
+    if (!bf16) return block_bwd<float, float>(a, stream);
+    return stream_bf16 ? block_bwd<bf16_t, bf16_t>(a, stream) : block_bwd<bf16_t, float>(a, stream);
+}
+
+}  // namespace ssd

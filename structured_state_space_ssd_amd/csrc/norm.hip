@@ -21,87 +21,12 @@
 // wavefronts wait for the sums together; 4096 gated rows of 8192 53 and 82 us. Short
 // rows: 1048576 of 16 values 15 us forward, 24 + 4 us backward, 65536 of 256 values 16
 // and 23 + 4 us. 4 rows of 2560: 3.4 us, a launch.
-#include <type_traits>
-
 #include "ssd_launch.h"
 #include "ssd_rows.h"
 
 namespace ssd {
 
 namespace {
-
-// Lanes that share a row, as the kernels see it: `lpr` <= 64 lanes of one
-// wavefront (a power of two), or the workgroup (lpr = 0).
-struct RowGroup {
-    int lpr, lane, group, groups;
-};
-__device__ __forceinline__ RowGroup row_group(int lpr) {
-    RowGroup r;
-    r.lpr = lpr;
-    if (lpr) {
-        r.lane = threadIdx.x & (lpr - 1);
-        r.group = threadIdx.x / lpr;
-        r.groups = blockDim.x / lpr;
-    } else {
-        r.lane = threadIdx.x;
-        r.group = 0;
-        r.groups = 1;
-    }
-    return r;
-}
-
-// Sums over groups of `top` lanes (a power of two), in every one of them: moves
-// within the vector unit, which a row's sums, one after the other, wait for far
-// less than for the permutes through LDS that __shfl_xor makes.
-template <int K> __device__ __forceinline__ void lane_sum(float (&v)[K], int top) {
-    auto dpp = [&](auto ctrl) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            v[k] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[k]),
-                                                               decltype(ctrl)::value, 0xf, 0xf, true));
-    };
-    if (top > 1) dpp(std::integral_constant<int, 0xB1>());    // the other of two
-    if (top > 2) dpp(std::integral_constant<int, 0x4E>());    // the other two of four
-    if (top > 4) dpp(std::integral_constant<int, 0x141>());   // eight, mirrored
-    if (top > 8) dpp(std::integral_constant<int, 0x140>());   // sixteen, mirrored
-    if (top > 16)
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[k]),
-                                                            __float_as_uint(v[k]), false, false);
-            v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-        }
-    if (top > 32)
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]),
-                                                            __float_as_uint(v[k]), false, false);
-            v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-        }
-}
-
-// Sums of K values over the lanes of a row, in every one of them. `buf` holds
-// K floats per wavefront (at most 16 wavefronts); the caller alternates between
-// two of them, so that one barrier per sum is enough (a wavefront can write a
-// buffer again only after it has passed the barrier of the other one).
-template <int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], int lpr, float *buf) {
-    lane_sum(v, lpr ? lpr : 64);
-    const int waves = blockDim.x >> 6;
-    if (lpr || waves == 1) return;
-    if (lane_id() == 0)
-#pragma unroll
-        for (int k = 0; k < K; ++k) buf[wave_id() * K + k] = v[k];
-    __syncthreads();
-    const int w = lane_id() & 15;
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = w < waves ? buf[w * K + k] : 0.0f;
-    lane_sum(v, 16);
-}
-
-constexpr int kShortWaves = 4;  // wavefronts of a workgroup that takes several rows at once
-
-template <typename T> constexpr int vec_of() { return sizeof(T) == 2 ? 8 : 4; }
 
 // Rows are taken with the stride of the grid, which holds as many as run at
 // once; the next row sets out while one is worked on, so that its way from
@@ -394,30 +319,6 @@ __global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ 
     }
 }
 
-struct NormShape {
-    int lpr, threads, nv, groups;
-};
-// One vector per lane where the row allows it: more lanes per row keep more
-// loads in flight than more vectors per lane do. `most`: lanes of a workgroup
-// that a row may take.
-NormShape norm_shape(int D, int V, int most) {
-    const int nvec = (D + V - 1) / V;
-    NormShape s;
-    if (nvec <= 64) {
-        s.lpr = 1;
-        while (s.lpr < nvec) s.lpr <<= 1;
-        s.threads = 64 * kShortWaves;
-        s.nv = 1;
-        s.groups = s.threads / s.lpr;
-        return s;
-    }
-    s.lpr = 0;
-    s.groups = 1;
-    s.nv = 1;
-    while ((nvec + s.nv - 1) / s.nv > most) s.nv *= 2;
-    s.threads = ((nvec + s.nv - 1) / s.nv + 63) / 64 * 64;
-    return s;
-}
 NormShape norm_fwd_shape(int D, int V) { return norm_shape(D, V, 1024); }
 // The widest rows of the backward (above 8192 values) take half the lanes, which
 // then have twice the registers: 1024 lanes of 128 spilled up to 411 of them.

@@ -1,0 +1,283 @@
+// Gradients of the gated recurrence (recurrence.hip). With g_t the gradient of h_t,
+//   g_t = dy_t silu(z_t) + a_{t+1} g_{t+1},  dinit = a_0 g_0,  dz = dy h silu'(z);
+// gated, with b = sqrt(1 - a^2), p = sigmoid(i) and w the gradient of log a times log a,
+//   dx = g b p,  di = g b p x (1 - p),  w = g log a (a h_{t-1} - p x a^2 / b),
+//   dr = w (1 - sigmoid(r)),  ddecay = sum of w, times sigmoid(decay) / softplus(decay);
+// direct, dx = g and dr = g a h_{t-1}.
+// (log a / b goes to 0 with log a, so w does too, where the gradient of log a itself grows
+// without bound.)
+//
+// The walk goes back over the tiles. A wavefront's 32 tokens find the state entering
+// them in memory, where the forward kept one every kRecKeep tokens (1/8 of a byte a
+// channel and token), and make their states from it again in registers; the adjoint is
+// put together like the forward's state, against the tokens' order.
+#include "recurrence.h"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kRecBwdWaves = 8;  // of a workgroup at most: its lanes hold a token's every operand
+
+// OUT: the gradients, from the adjoint that the later segments give. Else what
+// segments 1 .. segs - 1 do to the adjoint that comes to their end: seg_a, seg_h.
+template <typename T, bool GATED, bool PACKED, bool OUT>
+__global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b) {
+    __shared__ float buf[2][kRecBwdWaves][16][4];
+    const RecArgs &a = b.f;
+    RecPlace p = rec_place(a, OUT ? a.segs : a.segs - 1);
+    if (!p.live) return;
+    if (!OUT) {
+        ++p.seg;
+        p.begin = p.seg * a.seg_len;
+        p.end = min(p.begin + a.seg_len, a.seqlen);
+    }
+    const int tile = a.waves * kRecWaveTokens, E = a.channels;
+    const size_t row0 = (size_t)p.batch * E + p.ch;
+    // q: what comes to the last token walked so far from the tokens after it
+    float rate[2] = {0.0f, 0.0f}, q[2] = {0.0f, 0.0f}, A[2] = {1.0f, 1.0f}, sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (e < p.nch) {
+            if (GATED) rate[e] = rec_rate(a.decay[p.ch + e], a.c);
+            if (OUT && !PACKED && b.dfinal) q[e] = b.dfinal[row0 + e];
+            if (OUT)
+                for (int s = a.segs - 1; s > p.seg; --s) {
+                    const size_t k = ((size_t)p.batch * (a.segs - 1) + s - 1) * E + p.ch + e;
+                    q[e] = rec_apply<PACKED>({a.seg_a[k], a.seg_h[k]}, q[e]);
+                }
+        }
+    const size_t xb = p.batch * a.x_batch, rb = p.batch * a.r_batch, ib = p.batch * a.i_batch, zb = p.batch * a.z_batch;
+    const size_t yb = (size_t)p.batch * a.seqlen * E;
+    int turn = 0;
+    auto walk = [&](auto whole, int t0) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        const int tw = t0 + p.wave * kRecWaveTokens, ts = tw + p.sub * kStrand;
+        const int nt = min(max(p.end - ts, 0), kStrand);
+        RecPair<T> x[kStrand], r[kStrand], in[kStrand], z[kStrand], dy[kStrand];
+        rec_load<T, WHOLE>(r, a.r, rb + tw * a.r_token, a.r_token, p, nt);
+        rec_load<T, WHOLE>(dy, b.dy, yb + (size_t)tw * E, E, p, nt);
+        if (a.z) rec_load<T, WHOLE>(z, a.z, zb + tw * a.z_token, a.z_token, p, nt);
+        if (OUT) {
+            rec_load<T, WHOLE>(x, a.x, xb + tw * a.x_token, a.x_token, p, nt);
+            if (GATED) rec_load<T, WHOLE>(in, a.i, ib + tw * a.i_token, a.i_token, p, nt);
+        }
+        float hw[2] = {0.0f, 0.0f};  // the state entering the wavefront's tokens
+        if (OUT && (WHOLE || tw < p.end)) {
+            const float *s = a.states + ((size_t)p.batch * a.keeps + tw / kRecKeep) * E + p.ch;
+            if (p.nch > 0) hw[0] = s[0];
+            if (p.nch > 1) hw[1] = s[1];
+        }
+        int code[kStrand];
+        if (PACKED)
+#pragma unroll
+            for (int j = 0; j < kStrand; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
+        float av[kStrand][2], hv[kStrand][2], gv[kStrand][2];
+        RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mg[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
+#pragma unroll
+        for (int j = 0; j < kStrand; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float d, u = 0.0f;
+                if (GATED) {
+                    const float la = rate[e] * sigmoid_f32(r[j].get(e));
+                    d = __builtin_amdgcn_exp2f(la);
+                    if (OUT)
+                        u = __builtin_amdgcn_sqrtf(one_minus_square(2.0f * kLn2 * la, d)) *
+                            sigmoid_f32(in[j].get(e)) * x[j].get(e);
+                } else {
+                    d = __builtin_amdgcn_exp2f(kLog2e * r[j].get(e));
+                    if (OUT) u = x[j].get(e);
+                }
+                float g = dy[j].get(e);
+                if (a.z) g *= silu_f32(z[j].get(e));
+                if (!WHOLE && j >= nt) {
+                    d = 1.0f;
+                    u = g = 0.0f;
+                }
+                if (PACKED) {
+                    if (code[j] & 1) d = -1.0f;
+                    if (b.dfinal && code[j] >> 1 && e < p.nch)
+                        g += b.dfinal[(size_t)((code[j] >> 1) - 1) * E + p.ch + e];
+                }
+                av[j][e] = d;
+                hv[j][e] = u;
+                gv[j][e] = g;
+                if (OUT) m[e] = rec_then<PACKED>(m[e], {d, u});
+            }
+        if (OUT)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                RecMap before, all;
+                rec_wave<PACKED, false>(m[e], p.sub, before, all);
+                float h = rec_apply<PACKED>(before, hw[e]);
+#pragma unroll
+                for (int j = 0; j < kStrand; ++j) {  // the state before each token, in its input's place
+                    const float next = rec_apply<PACKED>({av[j][e], hv[j][e]}, h);
+                    hv[j][e] = h;
+                    h = next;
+                }
+            }
+        // a token passes a (g + what comes to it) on to the one before, nothing from a first one
+#pragma unroll
+        for (int j = kStrand - 1; j >= 0; --j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const bool first = PACKED && av[j][e] < 0.0f;
+                mg[e] = {first || (PACKED && mg[e].a < 0.0f) ? -1.0f : av[j][e] * mg[e].a,
+                         first ? 0.0f : av[j][e] * (gv[j][e] + mg[e].h)};
+            }
+        RecMap after[2], all[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) rec_wave<PACKED, true>(mg[e], p.sub, after[e], all[e]);
+        if (p.sub == 0) {
+            float *w = buf[turn][p.wave][p.col];
+            w[0] = all[0].a; w[1] = all[0].h; w[2] = all[1].a; w[3] = all[1].h;
+        }
+        __syncthreads();
+        float qs[2] = {q[0], q[1]};
+        for (int w = a.waves - 1; w >= 0; --w) {
+            const float *v = buf[turn][w][p.col];
+            const RecMap mw[2] = {{v[0], v[1]}, {v[2], v[3]}};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (w == p.wave) qs[e] = q[e];
+                q[e] = rec_apply<PACKED>(mw[e], q[e]);
+                if (!OUT) A[e] = PACKED && (A[e] < 0.0f || mw[e].a < 0.0f) ? -1.0f : A[e] * mw[e].a;
+            }
+        }
+        turn ^= 1;
+        if (!OUT) return;
+        // the gates are made again: to keep those of all tokens takes more registers than there are
+#pragma unroll
+        for (int j = 0; j < kStrand; ++j) {
+            r[j].fresh();
+            if (GATED) in[j].fresh();
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) qs[e] = rec_apply<PACKED>(after[e], qs[e]);
+        const size_t at = (yb + (size_t)tw * E) * sizeof(T);
+        const uint32_t step = rec_bytes<T>(E);
+        uint32_t off = rec_offset<T>(step, p) + (kStrand - 1) * step;
+#pragma unroll
+        for (int j = kStrand - 1; j >= 0; --j, off -= step) {
+            float ox[2], orr[2], oi[2], oz[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const bool first = PACKED && av[j][e] < 0.0f;
+                const float xv = x[j].get(e);
+                const float g = gv[j][e] + qs[e];
+                float d = av[j][e], u = xv;
+                if (GATED) {
+                    const float sr = sigmoid_f32(r[j].get(e)), la = rate[e] * sr * kLn2;
+                    if (PACKED) d = __builtin_amdgcn_exp2f(rate[e] * sr);
+                    const float s2 = one_minus_square(2.0f * la, d);
+                    const float inv = s2 > 0.0f ? __builtin_amdgcn_rsqf(s2) : 0.0f;
+                    const float si = sigmoid_f32(in[j].get(e)), beta = s2 * inv, gs = g * si;
+                    u = beta * si * xv;
+                    ox[e] = gs * beta;
+                    oi[e] = ox[e] * xv * (1.0f - si);
+                    // a^2 log a / b, the product that stays finite
+                    float w = -gs * xv * (d * d) * (la * inv);
+                    if (!first) w = fmaf(g * d * hv[j][e], la, w);
+                    orr[e] = w * (1.0f - sr);
+                    if (WHOLE || j < nt) sum[e] += w;
+                } else {
+                    ox[e] = g;
+                    orr[e] = first ? 0.0f : g * d * hv[j][e];
+                }
+                if (a.z) {
+                    const float h = first ? u : fmaf(d, hv[j][e], u);
+                    oz[e] = dy[j].get(e) * h * silu_grad_f32(z[j].get(e));
+                }
+                qs[e] = first ? 0.0f : d * g;
+            }
+            if (!WHOLE && j >= nt) continue;
+            const auto out = [&](void *t, float (&v)[2]) {
+                rec_store<T, WHOLE>(static_cast<char *>(t) + at, off, p.nch, v[0], v[1]);
+            };
+            out(b.dx, ox);
+            out(b.dr, orr);
+            if (GATED) out(b.di, oi);
+            if (a.z) out(b.dz, oz);
+        }
+    };
+    const bool inner = p.ch - 2 * p.col + kRecCols <= E;
+    int t0 = p.begin + (p.end - p.begin - 1) / tile * tile;
+    for (; t0 >= p.begin; t0 -= tile) {
+        if (inner && t0 + tile <= p.end) walk(std::true_type(), t0);
+        else walk(std::false_type(), t0);
+    }
+    if (OUT && GATED) {  // the strands' sums of w, then the wavefronts'
+        float v[2] = {sum[0], sum[1]};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[e]), __float_as_uint(v[e]), false, false);
+            v[e] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+            const auto k = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[e]), __float_as_uint(v[e]), false, false);
+            v[e] = __uint_as_float(k[0]) + __uint_as_float(k[1]);
+        }
+        // (the buffer that the last tile did not read)
+        if (p.sub == 0) {
+            buf[turn][p.wave][p.col][0] = v[0];
+            buf[turn][p.wave][p.col][1] = v[1];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            sum[e] = 0.0f;
+            for (int w = 0; w < a.waves; ++w) sum[e] += buf[turn][w][p.col][e];
+        }
+    }
+    if (p.wave || p.sub) return;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (e < p.nch) {
+            if (!OUT) {
+                const size_t k = ((size_t)p.batch * (a.segs - 1) + p.seg - 1) * E + p.ch + e;
+                a.seg_a[k] = A[e];
+                a.seg_h[k] = q[e];
+                continue;
+            }
+            if (GATED) {
+                // sigmoid / softplus goes to 1 as both go to e^decay, and beyond what 32 bits hold of that
+                const float v = a.decay[p.ch + e];
+                const float k = v < -20.0f ? 1.0f : sigmoid_f32(v) / softplus_f32(v);
+                b.part[((size_t)p.batch * a.segs + p.seg) * E + p.ch + e] = k * sum[e];
+            }
+            if (!PACKED && b.dinit && p.seg == 0) b.dinit[row0 + e] = q[e];
+        }
+}
+
+template <typename T, bool GATED, bool PACKED> hipError_t bwd(const RecBwdArgs &b, hipStream_t stream) {
+    const RecArgs &a = b.f;
+    const int threads = a.waves * 64;
+    hipError_t e;
+    if (a.segs > 1) {
+        rec_bwd_kernel<T, GATED, PACKED, false><<<rec_grid(a, a.segs - 1), threads, 0, stream>>>(b);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    rec_bwd_kernel<T, GATED, PACKED, true><<<rec_grid(a, a.segs), threads, 0, stream>>>(b);
+    e = hipGetLastError();
+    if (e != hipSuccess || !GATED) return e;
+    return launch_colsum(b.part, a.batch * a.segs, a.channels, a.channels, b.ddecay, nullptr, stream);
+}
+
+}  // namespace
+
+RecPlan rec_bwd_plan(int batch, int seqlen, int channels) {
+    return rec_plan(batch, seqlen, channels, kRecBwdWaves);
+}
+
+hipError_t launch_rec_bwd(const RecBwdArgs &b, bool bf16, hipStream_t stream) {
+    const bool gated = b.f.decay != nullptr, packed = b.f.token != nullptr;
+    if (bf16) {
+        if (gated) return packed ? bwd<bf16_t, true, true>(b, stream) : bwd<bf16_t, true, false>(b, stream);
+        return packed ? bwd<bf16_t, false, true>(b, stream) : bwd<bf16_t, false, false>(b, stream);
+    }
+    if (gated) return packed ? bwd<float, true, true>(b, stream) : bwd<float, true, false>(b, stream);
+    return packed ? bwd<float, false, true>(b, stream) : bwd<float, false, false>(b, stream);
+}
+
+}  // namespace ssd

@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 #include <stddef.h>
+#include <stdint.h>
 
 namespace ssd {
 
@@ -291,5 +292,98 @@ size_t selective_dbc_floats(int batch, int seqlen, int channels, int ngroups, in
 // Whether every launch of launch_selective_bwd fits a grid (beside the layout of B and C).
 bool selective_bwd_grid_ok(int batch, int seqlen, int channels, int ngroups, int dstate, int segs);
 hipError_t launch_selective_bwd(const SelBwdArgs &a, bool bf16, hipStream_t stream);
+
+// ---- dropout (dropout.h, dropout.hip)
+// threshold: round(65536 p), nothing dropped at 0, everything at 65536; scale:
+// 65536 / (65536 - threshold) (0 at 65536). rng: seed and offset on the GPU, or NULL.
+struct DropArgs {
+    unsigned long long seed, offset;
+    const unsigned long long *rng;
+    uint32_t threshold;
+    float scale;
+};
+struct DropoutArgs {
+    const void *x;
+    size_t x_stride;  // elements between rows; y is dense
+    long long rows;   // below 2^31
+    int width;
+    DropArgs drop;
+    void *y;
+};
+constexpr int kDropGrid = 256 * 8;  // workgroups: as many as run at once
+hipError_t launch_dropout(const DropoutArgs &a, bool bf16, hipStream_t stream);
+
+// ---- a block's end: norm after it, gate, dropout, stream, norm before the next (block_norm.hip)
+// Rows of `width` elements (at most kMaxBlockWidth); x and z rows x_stride, z_stride
+// elements apart, every other tensor dense. weight: of the norm before the next block,
+// post_weight: of the norm after this one; either NULL, with its bias: no such norm.
+// scale, z and the statistics are nullable too; without rms a norm has a mean.
+constexpr int kMaxBlockWidth = 8192;
+struct BlockArgs {
+    const void *x, *residual, *z;
+    size_t x_stride, z_stride;
+    const float *weight, *bias, *post_weight, *post_bias, *scale;
+    float alpha, beta, eps;
+    DropArgs drop;
+    long long rows;  // below 2^31
+    int width, rms;
+    void *y, *sum;
+    float *mean, *rstd, *post_mean, *post_rstd;
+};
+hipError_t launch_block_fwd(const BlockArgs &a, bool bf16, bool stream_bf16, hipStream_t stream);
+struct BlockBwdArgs {
+    const void *dy, *dsum, *x, *sum, *z;  // dy and sum unused without weight; dsum nullable
+    size_t x_stride, z_stride;
+    const float *weight, *post_weight, *post_bias, *scale;
+    const float *mean, *rstd, *post_mean, *post_rstd;  // means NULL: the root-mean-square form
+    float alpha, beta;
+    DropArgs drop;
+    long long rows;
+    int width;
+    void *dx, *dresidual, *dz;
+    float *dweight, *dbias, *dpost_weight, *dpost_bias, *dscale;  // NULL: not wanted
+    int want_p, want_q, sums;  // the sums behind the last three; how many sums there are in all
+    float *part;               // block_bwd_part_bytes of scratch
+};
+size_t block_bwd_part_bytes(long long rows, int width, bool bf16, int sums);
+hipError_t launch_block_bwd(const BlockBwdArgs &a, bool bf16, bool stream_bf16, hipStream_t stream);
+
+// ---- gated recurrence (recurrence.hip, recurrence_bwd.hip)
+// x, r, i, z [Bt][L][E] with strides in elements between sequences and tokens; channels dense.
+constexpr int kRecKeep = 32;      // tokens between the states that the backward starts from
+struct RecArgs {
+    const void *x, *r, *i, *z;    // z nullable; i NULL without decay
+    size_t x_batch, x_token, r_batch, r_token, i_batch, i_token, z_batch, z_token;
+    const float *decay;           // [E]; NULL: r is the log-decay, x the input term
+    float c;
+    const float *init;            // [Bt][E], nullable
+    const int *token;             // packed sequences: launch_rec_tokens' codes, else NULL
+    int batch, seqlen, channels;
+    int blocks, waves, segs, seg_len, keeps;  // rec_plan
+    float *seg_a, *seg_h;         // [Bt][segs - 1][E]: scratch
+    void *y;                      // [Bt][L][E] dense (NULL: states only)
+    float *final_state;           // [Bt or nseq][E], nullable
+    float *states;                // [Bt][keeps][E]: the state before every so many tokens, nullable
+};
+struct RecPlan {
+    int blocks, waves, segs, seg_len, keeps;
+};
+RecPlan rec_plan(int batch, int seqlen, int channels, int most_waves);
+RecPlan rec_bwd_plan(int batch, int seqlen, int channels);
+unsigned rec_grid(const RecArgs &a, int segs);
+// The codes of a packed axis' tokens; zeroes `final` ([nseq][E], nullable).
+hipError_t launch_rec_tokens(const RecArgs &a, const int *cu, int nseq, int *token, float *final, hipStream_t stream);
+hipError_t launch_rec_fwd(const RecArgs &a, bool bf16, hipStream_t stream);
+// One token: the token strides and init are not read.
+hipError_t launch_rec_step(const RecArgs &a, float *state, bool bf16, hipStream_t stream);
+struct RecBwdArgs {
+    RecArgs f;                    // the forward's inputs and states, the backward's plan
+    const void *dy;               // [Bt][L][E] dense
+    const float *dfinal;          // [Bt or nseq][E], nullable
+    void *dx, *dr, *di, *dz;      // dense
+    float *ddecay, *dinit;        // dinit nullable
+    float *part;                  // [Bt][segs][E]: scratch
+};
+hipError_t launch_rec_bwd(const RecBwdArgs &b, bool bf16, hipStream_t stream);
 
 }  // namespace ssd
