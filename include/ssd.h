@@ -680,7 +680,9 @@ int ssd_norm_backward(const void *dy, const void *x, long long x_row_stride, int
  *   init_state float32 [Bt][E], the state before the first token (NULL: zeros).
  *   cu_seqlens packed sequences as for ssd_forward_varlen: device int32 [nseq + 1],
  *              batch 1, no init_state; every sequence starts from a zero state,
- *              whatever the one before ended in. NULL: nseq is not looked at.
+ *              whatever the one before ended in. Tokens that no sequence holds (in
+ *              front of cu_seqlens[0], from cu_seqlens[nseq] on) are padding: zero in y
+ *              and in every gradient, whatever they hold. NULL: nseq is not looked at.
  *   y          [Bt][L][E] dense, dtype.
  *   final_state nullable, float32 [Bt][E] ([nseq][E] packed; zero for an empty one).
  *   states     nullable, float32 [Bt][ceil(L / 32)][E]: the state before every 32nd
@@ -769,7 +771,7 @@ int ssd_dropout(const void *x, long long x_row_stride, long long rows, int width
  *   random     NULL: no dropout.
  *   y          dense, dtype. mean, rstd, post_mean, post_rstd: nullable, float32
  *              [rows], the norms' statistics (means not written with rms).
- * Outputs must not overlap inputs, except that sum may be residual.
+ * Outputs must not overlap inputs.
  */
 typedef struct {
     const float *weight, *bias, *post_weight, *post_bias, *scale;

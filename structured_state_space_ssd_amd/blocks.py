@@ -70,7 +70,8 @@ def recurrence_forward(x, r, i=None, decay=None, z=None, init_state=None, c=8.0,
     log-decay itself, a_t = exp(r_t), and u_t = x_t.
     x, r, i, z [Bt, L, E] float32 or bfloat16 (slices of wider projections are
     fine), decay [E] float32, init_state [Bt, E] float32 or None (zeros).
-    cu_seqlens: packed sequences as for ``forward_varlen`` (Bt 1, no init_state).
+    cu_seqlens: packed sequences as for ``forward_varlen`` (Bt 1, no init_state);
+    tokens in front of the first and behind the last one give zeros.
     Returns y, or a tuple of y, final_state ([Bt or nseq, E] float32, if
     requested) and states (if requested; float32, for recurrence_backward).
     """

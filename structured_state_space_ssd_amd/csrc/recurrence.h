@@ -19,6 +19,9 @@
 
 namespace ssd {
 
+// The code of a token that no sequence of a packed axis holds: padding, which starts from a
+// zero state like a first token and gives zeros, whatever it holds.
+constexpr int kRecNone = -0x7fffffff;
 constexpr int kStrand = 8, kRecWaveTokens = 4 * kStrand, kRecCols = 32;
 
 // Two channels' values of one token.

@@ -16,8 +16,8 @@ namespace ssd {
 namespace {
 
 // What tokens of a packed axis are: bit 0, the first of its sequence; above, 1 + the
-// number of the sequence whose last token it is. `final`: set to the state of an empty
-// sequence. Any contents of `cu` are read within its nseq + 1 entries.
+// number of the sequence whose last token it is; kRecNone: in no sequence. `final`: set to
+// the state of an empty sequence. Any contents of `cu` are read within its nseq + 1 entries.
 __global__ __launch_bounds__(256) void rec_token_kernel(const int *__restrict__ cu, int nseq, int L,
                                                         int *__restrict__ token, float *__restrict__ final,
                                                         long long finals) {
@@ -31,7 +31,8 @@ __global__ __launch_bounds__(256) void rec_token_kernel(const int *__restrict__ 
             if (cu[mid] <= t) lo = mid;
             else hi = mid;
         }
-        token[t] = (cu[lo] == t ? 1 : 0) | (cu[lo + 1] - 1LL == t ? 2 * (lo + 1) : 0);
+        const int from = cu[lo], to = cu[lo + 1];
+        token[t] = t < from || t >= to ? kRecNone : (from == t ? 1 : 0) | (to - 1 == t ? 2 * (lo + 1) : 0);
     }
 }
 
@@ -93,6 +94,7 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(RecArgs a) {
                     u = 0.0f;
                 }
                 if (PACKED && (code[j] & 1)) d = -1.0f;
+                if (PACKED && code[j] < 0) u = 0.0f;
                 av[j][e] = d;
                 uv[j][e] = u;
                 m[e] = rec_then<PACKED>(m[e], {d, u});
@@ -136,9 +138,10 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(RecArgs a) {
                 hs[e] = rec_apply<PACKED>({av[j][e], uv[j][e]}, hs[e]);
                 o[e] = hs[e];
                 if (a.z) o[e] *= silu_f32(z[j].get(e));
+                if (PACKED && code[j] < 0) o[e] = 0.0f;
             }
             if (a.y && (WHOLE || j < nt)) rec_store<T, WHOLE>(y, off, p.nch, o[0], o[1]);
-            if (PACKED && a.final_state && (WHOLE || j < nt) && code[j] >> 1) {
+            if (PACKED && a.final_state && (WHOLE || j < nt) && code[j] > 1) {
                 float *f = a.final_state + (size_t)((code[j] >> 1) - 1) * E + p.ch;
                 if (p.nch > 0) f[0] = hs[0];
                 if (p.nch > 1) f[1] = hs[1];

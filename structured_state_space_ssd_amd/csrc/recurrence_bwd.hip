@@ -97,7 +97,8 @@ __global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b
                 }
                 if (PACKED) {
                     if (code[j] & 1) d = -1.0f;
-                    if (b.dfinal && code[j] >> 1 && e < p.nch)
+                    if (code[j] < 0) u = g = 0.0f;
+                    if (b.dfinal && code[j] > 1 && e < p.nch)
                         g += b.dfinal[(size_t)((code[j] >> 1) - 1) * E + p.ch + e];
                 }
                 av[j][e] = d;
@@ -181,7 +182,7 @@ __global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b
                     float w = -gs * xv * (d * d) * (la * inv);
                     if (!first) w = fmaf(g * d * hv[j][e], la, w);
                     orr[e] = w * (1.0f - sr);
-                    if (WHOLE || j < nt) sum[e] += w;
+                    if ((WHOLE || j < nt) && !(PACKED && code[j] < 0)) sum[e] += w;
                 } else {
                     ox[e] = g;
                     orr[e] = first ? 0.0f : g * d * hv[j][e];
@@ -193,6 +194,7 @@ __global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b
                 qs[e] = first ? 0.0f : d * g;
             }
             if (!WHOLE && j >= nt) continue;
+            if (PACKED && code[j] < 0) ox[0] = ox[1] = orr[0] = orr[1] = oi[0] = oi[1] = oz[0] = oz[1] = 0.0f;
             const auto out = [&](void *t, float (&v)[2]) {
                 rec_store<T, WHOLE>(static_cast<char *>(t) + at, off, p.nch, v[0], v[1]);
             };

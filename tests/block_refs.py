@@ -32,6 +32,12 @@ def recurrence(x, r, i=None, decay=None, z=None, init=None, c=8.0, cu=None, grad
     gated = decay is not None
     spans = [(0, L)] if cu is None else list(zip(cu[:-1], cu[1:]))
     first = {a for a, b in spans if b > a} if cu is not None else set()
+    dy, dfinal = map(_d, grads or (None, None))
+    if cu is not None:  # padding: no sequence's, as if it held zeros and began anew with every token
+        pad = [t for t in range(L) if t < cu[0] or t >= cu[-1]]
+        first |= set(pad)
+        x, r, i, z, dy = (t if t is None else t.index_fill(1, torch.tensor(pad, dtype=torch.int64), 0.0)
+                          for t in (x, r, i, z, dy))
     last = {b - 1: k for k, (a, b) in enumerate(spans) if b > a}
     if gated:
         sr, si = torch.sigmoid(r), torch.sigmoid(i)
@@ -78,7 +84,6 @@ def recurrence(x, r, i=None, decay=None, z=None, init=None, c=8.0, cu=None, grad
            "states": states, "states_err": states_err}
     if grads is None:
         return out
-    dy, dfinal = map(_d, grads)
     if z is not None:
         out["dz"] = dy * hy * R.silu_grad(z)
         out["dz_err"] = dy.abs() * (1 + z.abs()) * (Ey + (kz + 8) * Hy)
@@ -142,12 +147,12 @@ def philox(counter, key):
     return np.stack(x, -1)
 
 
-def kept(rows, width, p, seed, offset):
-    """Which elements of [rows, width] stay."""
+def kept(rows, width, p, seed, offset, first=0):
+    """Which elements of [rows, width] stay, from row `first` on."""
     groups = -(-width // 8)
     counter = np.zeros((rows, groups, 4), np.uint64)
     counter[..., 0] = np.arange(groups)
-    counter[..., 1] = np.arange(rows)[:, None]
+    counter[..., 1] = first + np.arange(rows)[:, None]
     counter[..., 2], counter[..., 3] = offset % 2 ** 32, offset >> 32
     w = philox(counter, (seed % 2 ** 32, seed >> 32))
     bits = np.stack([w & np.uint64(0xFFFF), w >> np.uint64(16)], -1).reshape(rows, -1)[:, :width]
@@ -204,7 +209,7 @@ class Block:
         self.gate = one if self.z is None else R.silu(self.z)
         self.drop = one
         if p:
-            self.drop = kept(one.numel() // one.shape[-1], one.shape[-1], p, *rng).view(one.shape) * share(p)
+            self.drop = kept(one.numel() // one.shape[-1], one.shape[-1], p, *rng).view(one.shape).double() * share(p)
         m = self.k * self.gate * self.drop
         self.total = alpha * res + beta * v * m
         self.total_mag = abs(alpha) * res.abs() + abs(beta) * va * m.abs()

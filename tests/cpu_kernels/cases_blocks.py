@@ -135,6 +135,7 @@ def run_recurrence():
             recurrence(size, *args, keep=args[0] is BF)
     # sequences inside strands, across wavefronts, tiles and segments, empty ones, one of one token
     for L, cu in ((40, [0, 40]), (40, [0, 0, 1, 2, 2, 15, 31, 40, 40]), (700, [0, 3, 300, 300, 301, 511, 700]),
+                  (300, [7, 9, 64, 200]),
                   (1100, [0, 64, 1000, 1100]), (1030, list(range(0, 1031, 103)))):
         for args in ((BF, True, True, 3, True), (F32, False, False, 0, True), (F32, True, False, 0, False)):
             print("recurrence packed", cu, *args, flush=True)
