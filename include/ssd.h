@@ -685,7 +685,7 @@ int ssd_norm_backward(const void *dy, const void *x, long long x_row_stride, int
  *              and in every gradient, whatever they hold. NULL: nseq is not looked at.
  *   y          [Bt][L][E] dense, dtype.
  *   final_state nullable, float32 [Bt][E] ([nseq][E] packed; zero for an empty one).
- *   states     nullable, float32 [Bt][ceil(L / 32)][E]: the state before every 32nd
+ *   states     nullable, float32 [Bt][ceil(L / 16)][E]: the state before every 16th
  *              token, for ssd_recurrence_backward.
  *   workspace  ssd_recurrence_forward_workspace_size bytes, 256-byte aligned.
  * All in float32 with one rounding at the end. 1 - a^2 is formed without

@@ -22,7 +22,7 @@ from .layers import _call, _f32, _int_sizes, _on_gpu, _param, _required, _rows, 
 __all__ = ["recurrence_forward", "recurrence_backward", "recurrence_step", "block_norm_forward",
            "block_norm_backward", "dropout"]
 
-KEEP = 32  # tokens between the states that recurrence_forward keeps for recurrence_backward
+KEEP = 16  # tokens between the states that recurrence_forward keeps for recurrence_backward
 
 
 def _ptr(t):

@@ -91,9 +91,9 @@ struct RecLayout {
     ssd::RecPlan plan;
     size_t token, seg_a, seg_h, total;
 };
-RecLayout recurrence_layout(int batch, int seqlen, int channels, bool packed) {
+RecLayout recurrence_layout(int batch, int seqlen, int channels, bool packed, int dtype) {
     RecLayout w{};
-    w.plan = ssd::rec_plan(batch, seqlen, channels, 16);
+    w.plan = ssd::rec_fwd_plan(batch, seqlen, channels, dtype == SSD_BF16);
     Taker k;
     const size_t segs = (size_t)batch * (w.plan.segs - 1) * channels;
     w.token = k.take(packed ? seqlen : 0);
@@ -109,10 +109,11 @@ struct RecBwdLayout {
     ssd::RecPlan plan, keep;
     size_t token, seg_a, seg_h, part, states, total;
 };
-RecBwdLayout recurrence_bwd_layout(int batch, int seqlen, int channels, bool packed, bool have_states) {
+RecBwdLayout recurrence_bwd_layout(int batch, int seqlen, int channels, bool packed, bool have_states,
+                                   int dtype) {
     RecBwdLayout w{};
     w.plan = ssd::rec_bwd_plan(batch, seqlen, channels);
-    w.keep = ssd::rec_plan(batch, seqlen, channels, 16);
+    w.keep = ssd::rec_fwd_plan(batch, seqlen, channels, dtype == SSD_BF16);
     const size_t be = (size_t)batch * channels;
     size_t segs = be * (w.plan.segs - 1);
     if (!have_states && be * (w.keep.segs - 1) > segs) segs = be * (w.keep.segs - 1);
@@ -171,7 +172,7 @@ extern "C" {
 
 size_t ssd_recurrence_forward_workspace_size(int batch, int seqlen, int channels, int packed, int dtype) {
     if (check_recurrence(batch, seqlen, channels, dtype) != SSD_OK) return 0;
-    return recurrence_layout(batch, seqlen, channels, packed != 0).total;
+    return recurrence_layout(batch, seqlen, channels, packed != 0, dtype).total;
 }
 
 int ssd_recurrence_forward(const void *x, const void *r, const void *i, const float *decay, float c,
@@ -187,7 +188,7 @@ int ssd_recurrence_forward(const void *x, const void *r, const void *i, const fl
     if (rc != SSD_OK) return rc;
     rc = check_packed(cu_seqlens, nseq, batch, init_state);
     if (rc != SSD_OK) return rc;
-    const RecLayout w = recurrence_layout(batch, seqlen, channels, cu_seqlens != nullptr);
+    const RecLayout w = recurrence_layout(batch, seqlen, channels, cu_seqlens != nullptr, dtype);
     if (!plan_fits(batch, w.plan)) return SSD_ERR_UNSUPPORTED;
     rc = check_workspace(workspace, workspace_bytes, w.total);
     if (rc != SSD_OK) return rc;
@@ -226,7 +227,7 @@ int ssd_recurrence_step(float *state, const void *x, const void *r, const void *
 size_t ssd_recurrence_backward_workspace_size(int batch, int seqlen, int channels, int packed,
                                               int have_states, int dtype) {
     if (check_recurrence(batch, seqlen, channels, dtype) != SSD_OK) return 0;
-    return recurrence_bwd_layout(batch, seqlen, channels, packed != 0, have_states != 0).total;
+    return recurrence_bwd_layout(batch, seqlen, channels, packed != 0, have_states != 0, dtype).total;
 }
 
 int ssd_recurrence_backward(const void *x, const void *r, const void *i, const float *decay, float c,
@@ -245,7 +246,8 @@ int ssd_recurrence_backward(const void *x, const void *r, const void *i, const f
     rc = check_packed(cu_seqlens, nseq, batch, init_state);
     if (rc != SSD_OK) return rc;
     if (cu_seqlens && dinit_state) return SSD_ERR_UNSUPPORTED;
-    const RecBwdLayout w = recurrence_bwd_layout(batch, seqlen, channels, cu_seqlens != nullptr, states != nullptr);
+    const RecBwdLayout w = recurrence_bwd_layout(batch, seqlen, channels, cu_seqlens != nullptr,
+                                                 states != nullptr, dtype);
     if (!plan_fits(batch, w.plan) || !plan_fits(batch, w.keep) ||
         !ssd::colsum_grid_ok(batch * w.plan.segs, channels, false))
         return SSD_ERR_UNSUPPORTED;

@@ -1,9 +1,9 @@
 // Device code shared by the gated recurrence's walks, forward (recurrence.hip) and
 // back (recurrence_bwd.hip). The layout of a workgroup:
 //   it holds 32 channels of one sequence; a strand of 16 lanes with two channels
-//   each holds kStrand consecutive tokens, a wavefront four strands one after the
+//   each holds S (4 or 8) consecutive tokens, a wavefront four strands one after the
 //   other, the workgroup `waves` wavefronts one after the other: a tile of
-//   32 waves tokens, which it walks along the token axis.
+//   4 S waves tokens, which it walks along the token axis.
 // A strand's tokens are a map h -> A h + H of the state entering it; maps are put
 // together across the strands of a wavefront by swaps of registers and across the
 // wavefronts through LDS, so one barrier a tile is all that the walk waits for.
@@ -22,7 +22,7 @@ namespace ssd {
 // The code of a token that no sequence of a packed axis holds: padding, which starts from a
 // zero state like a first token and gives zeros, whatever it holds.
 constexpr int kRecNone = -0x7fffffff;
-constexpr int kStrand = 8, kRecWaveTokens = 4 * kStrand, kRecCols = 32;
+constexpr int kRecCols = 32;
 
 // Two channels' values of one token.
 template <typename T> struct RecPair;
@@ -35,8 +35,6 @@ template <> struct RecPair<bf16_t> {
     __device__ __forceinline__ float get(int e) const {
         return __uint_as_float(e ? (w & 0xffff0000u) : (w << 16));
     }
-    // as a value the compiler has not seen: what was made of it is made again, not kept
-    __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(w)); }
     static __device__ __forceinline__ void store(char *p, float a, float b) {
         *reinterpret_cast<u32_any *>(p) = pack_bf16(a, b);
     }
@@ -56,12 +54,6 @@ template <> struct RecPair<float> {
         w[1] = 0.0f;
     }
     __device__ __forceinline__ float get(int e) const { return w[e]; }
-    __device__ __forceinline__ void fresh() {
-        float u = w[0], v = w[1];
-        asm volatile("" : "+v"(u));
-        asm volatile("" : "+v"(v));
-        w[0] = u; w[1] = v;
-    }
     static __device__ __forceinline__ void store(char *p, float a, float b) {
         *reinterpret_cast<f32x2_any *>(p) = f32x2_any{a, b};
     }
@@ -103,19 +95,19 @@ template <typename T> __device__ __forceinline__ uint32_t rec_bytes(size_t token
     return step;
 }
 // Byte offset of a lane's first token and channel (strides are below 2^24 elements).
-template <typename T> __device__ __forceinline__ uint32_t rec_offset(uint32_t step, const RecPlace &p) {
-    return static_cast<uint32_t>(p.sub * kStrand) * step + p.ch * static_cast<uint32_t>(sizeof(T));
+template <typename T, int S> __device__ __forceinline__ uint32_t rec_offset(uint32_t step, const RecPlace &p) {
+    return static_cast<uint32_t>(p.sub * S) * step + p.ch * static_cast<uint32_t>(sizeof(T));
 }
-// A lane's kStrand tokens of one tensor, whose wavefront's first is element `at` (uniform).
+// A lane's tokens of one tensor, whose wavefront's first is element `at` (uniform).
 // WHOLE: every token and channel is there.
-template <typename T, bool WHOLE>
-__device__ __forceinline__ void rec_load(RecPair<T> (&r)[kStrand], const void *t, size_t at, size_t token,
+template <typename T, bool WHOLE, int S>
+__device__ __forceinline__ void rec_load(RecPair<T> (&r)[S], const void *t, size_t at, size_t token,
                                          const RecPlace &p, int nt) {
     const char *base = static_cast<const char *>(t) + at * sizeof(T);
     const uint32_t step = rec_bytes<T>(token);
-    uint32_t off = rec_offset<T>(step, p);
+    uint32_t off = rec_offset<T, S>(step, p);
 #pragma unroll
-    for (int j = 0; j < kStrand; ++j, off += step) {
+    for (int j = 0; j < S; ++j, off += step) {
         if (WHOLE) r[j].load(base + off);
         else {
             r[j].zero();

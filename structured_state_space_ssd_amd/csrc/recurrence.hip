@@ -36,14 +36,18 @@ __global__ __launch_bounds__(256) void rec_token_kernel(const int *__restrict__ 
     }
 }
 
+// Tokens of a strand: float32 operands of 8 do not fit the registers.
+template <typename T> constexpr int rec_fwd_strand() { return sizeof(T) == 2 ? 8 : 4; }
+
 // OUT: the outputs, from the state that the segments before give. Else what a segment
 // does to the state entering it: seg_a, seg_h.
 template <typename T, bool GATED, bool PACKED, bool OUT>
 __global__ __launch_bounds__(1024) void rec_fwd_kernel(RecArgs a) {
+    constexpr int S = rec_fwd_strand<T>();
     __shared__ float buf[2][16][16][4];
     const RecPlace p = rec_place(a, OUT ? a.segs : a.segs - 1);
     if (!p.live) return;
-    const int tile = a.waves * kRecWaveTokens, E = a.channels;
+    const int tile = a.waves * 4 * S, E = a.channels;
     const size_t row0 = (size_t)p.batch * E + p.ch;
     float rate[2] = {0.0f, 0.0f}, h[2] = {0.0f, 0.0f}, A[2] = {1.0f, 1.0f};
 #pragma unroll
@@ -60,23 +64,35 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(RecArgs a) {
     const size_t xb = p.batch * a.x_batch, rb = p.batch * a.r_batch, ib = p.batch * a.i_batch, zb = p.batch * a.z_batch;
     const size_t yb = (size_t)p.batch * a.seqlen * E;
     int turn = 0;
+    const bool inner = p.ch - 2 * p.col + kRecCols <= E;
+    // The next tile's operands are on their way while this one's states are put together.
+    RecPair<T> x[S], r[S], in[S];
+    auto fetch = [&](int t0) {
+        if (t0 >= p.end) return;
+        const int tw = t0 + p.wave * 4 * S, nt = min(max(p.end - tw - p.sub * S, 0), S);
+        auto load = [&](auto whole) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            rec_load<T, WHOLE>(r, a.r, rb + tw * a.r_token, a.r_token, p, nt);
+            if (GATED) rec_load<T, WHOLE>(in, a.i, ib + tw * a.i_token, a.i_token, p, nt);
+            rec_load<T, WHOLE>(x, a.x, xb + tw * a.x_token, a.x_token, p, nt);
+        };
+        if (inner && t0 + tile <= p.end) load(std::true_type());
+        else load(std::false_type());
+    };
     auto walk = [&](auto whole, int t0) {
         constexpr bool WHOLE = decltype(whole)::value;
-        const int tw = t0 + p.wave * kRecWaveTokens, ts = tw + p.sub * kStrand;
-        const int nt = min(max(p.end - ts, 0), kStrand);
-        RecPair<T> x[kStrand], r[kStrand], in[kStrand], z[kStrand];
-        rec_load<T, WHOLE>(x, a.x, xb + tw * a.x_token, a.x_token, p, nt);
-        rec_load<T, WHOLE>(r, a.r, rb + tw * a.r_token, a.r_token, p, nt);
-        if (GATED) rec_load<T, WHOLE>(in, a.i, ib + tw * a.i_token, a.i_token, p, nt);
+        const int tw = t0 + p.wave * 4 * S, ts = tw + p.sub * S;
+        const int nt = min(max(p.end - ts, 0), S);
+        RecPair<T> z[S];
         if (OUT && a.z) rec_load<T, WHOLE>(z, a.z, zb + tw * a.z_token, a.z_token, p, nt);
-        int code[kStrand];
+        int code[S];
         if (PACKED)
 #pragma unroll
-            for (int j = 0; j < kStrand; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
-        float av[kStrand][2], uv[kStrand][2];
+            for (int j = 0; j < S; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
+        float av[S][2], uv[S][2];
         RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
 #pragma unroll
-        for (int j = 0; j < kStrand; ++j)
+        for (int j = 0; j < S; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float d, u;
@@ -99,6 +115,7 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(RecArgs a) {
                 uv[j][e] = u;
                 m[e] = rec_then<PACKED>(m[e], {d, u});
             }
+        fetch(t0 + tile);
         RecMap before[2], all[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) rec_wave<PACKED, false>(m[e], p.sub, before[e], all[e]);
@@ -129,9 +146,9 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(RecArgs a) {
         }
         char *y = static_cast<char *>(a.y) + (yb + (size_t)tw * E) * sizeof(T);
         const uint32_t step = rec_bytes<T>(E);
-        uint32_t off = rec_offset<T>(step, p);
+        uint32_t off = rec_offset<T, S>(step, p);
 #pragma unroll
-        for (int j = 0; j < kStrand; ++j, off += step) {
+        for (int j = 0; j < S; ++j, off += step) {
             float o[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -148,8 +165,8 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(RecArgs a) {
             }
         }
     };
-    const bool inner = p.ch - 2 * p.col + kRecCols <= E;
     int t0 = p.begin;
+    fetch(t0);
     if (inner)
         for (; t0 + tile <= p.end; t0 += tile) walk(std::true_type(), t0);
     for (; t0 < p.end; t0 += tile) walk(std::false_type(), t0);
@@ -217,16 +234,16 @@ template <typename T, bool GATED> hipError_t step(const RecArgs &a, float *state
 
 }  // namespace
 
-// Wavefronts of a workgroup and segments of the token axis.
-RecPlan rec_plan(int batch, int seqlen, int channels, int most_waves) {
+// Wavefronts of a workgroup and segments of the token axis, for strands of `strand` tokens.
+static RecPlan rec_plan(int batch, int seqlen, int channels, int strand, int most_waves) {
     RecPlan p;
     p.blocks = (channels + kRecCols - 1) / kRecCols;
     const long long units = (long long)batch * p.blocks;
-    const int wanted = (seqlen + kRecWaveTokens - 1) / kRecWaveTokens;  // wavefronts that have tokens
+    const int wanted = (seqlen + 4 * strand - 1) / (4 * strand);  // wavefronts that have tokens
     p.waves = units >= 512 ? 4 : units >= 128 ? 8 : 16;
     if (p.waves > most_waves) p.waves = most_waves;
     while (p.waves > 1 && p.waves / 2 >= wanted) p.waves /= 2;
-    const int tile = p.waves * kRecWaveTokens;
+    const int tile = p.waves * 4 * strand;
     const long long tiles = (seqlen + tile - 1LL) / tile;
     long long segs = 2048 / (units * p.waves);
     if (segs > tiles / 2) segs = tiles / 2;
@@ -237,6 +254,12 @@ RecPlan rec_plan(int batch, int seqlen, int channels, int most_waves) {
     p.segs = static_cast<int>((tiles + each - 1) / each);
     p.keeps = (seqlen + kRecKeep - 1) / kRecKeep;
     return p;
+}
+RecPlan rec_fwd_plan(int batch, int seqlen, int channels, bool bf16) {
+    return rec_plan(batch, seqlen, channels, bf16 ? rec_fwd_strand<bf16_t>() : rec_fwd_strand<float>(), 16);
+}
+RecPlan rec_bwd_plan(int batch, int seqlen, int channels) {
+    return rec_plan(batch, seqlen, channels, kRecBwdStrand, kRecBwdWaves);
 }
 
 unsigned rec_grid(const RecArgs &a, int segs) {

@@ -7,8 +7,8 @@
 // (log a / b goes to 0 with log a, so w does too, where the gradient of log a itself grows
 // without bound.)
 //
-// The walk goes back over the tiles. A wavefront's 32 tokens find the state entering
-// them in memory, where the forward kept one every kRecKeep tokens (1/8 of a byte a
+// The walk goes back over the tiles. A wavefront's 16 tokens find the state entering
+// them in memory, where the forward kept one every kRecKeep = 16 tokens (1/4 of a byte a
 // channel and token), and make their states from it again in registers; the adjoint is
 // put together like the forward's state, against the tokens' order.
 #include "recurrence.h"
@@ -17,12 +17,11 @@ namespace ssd {
 
 namespace {
 
-constexpr int kRecBwdWaves = 8;  // of a workgroup at most: its lanes hold a token's every operand
-
 // OUT: the gradients, from the adjoint that the later segments give. Else what
 // segments 1 .. segs - 1 do to the adjoint that comes to their end: seg_a, seg_h.
 template <typename T, bool GATED, bool PACKED, bool OUT>
-__global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b) {
+__global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b) {
+    constexpr int S = kRecBwdStrand;
     __shared__ float buf[2][kRecBwdWaves][16][4];
     const RecArgs &a = b.f;
     RecPlace p = rec_place(a, OUT ? a.segs : a.segs - 1);
@@ -32,7 +31,7 @@ __global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b
         p.begin = p.seg * a.seg_len;
         p.end = min(p.begin + a.seg_len, a.seqlen);
     }
-    const int tile = a.waves * kRecWaveTokens, E = a.channels;
+    const int tile = a.waves * 4 * S, E = a.channels;
     const size_t row0 = (size_t)p.batch * E + p.ch;
     // q: what comes to the last token walked so far from the tokens after it
     float rate[2] = {0.0f, 0.0f}, q[2] = {0.0f, 0.0f}, A[2] = {1.0f, 1.0f}, sum[2] = {0.0f, 0.0f};
@@ -52,9 +51,9 @@ __global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b
     int turn = 0;
     auto walk = [&](auto whole, int t0) {
         constexpr bool WHOLE = decltype(whole)::value;
-        const int tw = t0 + p.wave * kRecWaveTokens, ts = tw + p.sub * kStrand;
-        const int nt = min(max(p.end - ts, 0), kStrand);
-        RecPair<T> x[kStrand], r[kStrand], in[kStrand], z[kStrand], dy[kStrand];
+        const int tw = t0 + p.wave * 4 * S, ts = tw + p.sub * S;
+        const int nt = min(max(p.end - ts, 0), S);
+        RecPair<T> x[S], r[S], in[S], z[S], dy[S];
         rec_load<T, WHOLE>(r, a.r, rb + tw * a.r_token, a.r_token, p, nt);
         rec_load<T, WHOLE>(dy, b.dy, yb + (size_t)tw * E, E, p, nt);
         if (a.z) rec_load<T, WHOLE>(z, a.z, zb + tw * a.z_token, a.z_token, p, nt);
@@ -68,23 +67,27 @@ __global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b
             if (p.nch > 0) hw[0] = s[0];
             if (p.nch > 1) hw[1] = s[1];
         }
-        int code[kStrand];
+        int code[S];
         if (PACKED)
 #pragma unroll
-            for (int j = 0; j < kStrand; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
-        float av[kStrand][2], hv[kStrand][2], gv[kStrand][2];
+            for (int j = 0; j < S; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
+        float av[S][2], hv[S][2], gv[S][2];
+        float rv[S][2], iv[S][2], bv[S][2];  // the gates, and sqrt(1 - a^2)
         RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mg[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
 #pragma unroll
-        for (int j = 0; j < kStrand; ++j)
+        for (int j = 0; j < S; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float d, u = 0.0f;
                 if (GATED) {
-                    const float la = rate[e] * sigmoid_f32(r[j].get(e));
+                    rv[j][e] = sigmoid_f32(r[j].get(e));
+                    const float la = rate[e] * rv[j][e];
                     d = __builtin_amdgcn_exp2f(la);
-                    if (OUT)
-                        u = __builtin_amdgcn_sqrtf(one_minus_square(2.0f * kLn2 * la, d)) *
-                            sigmoid_f32(in[j].get(e)) * x[j].get(e);
+                    if (OUT) {
+                        bv[j][e] = __builtin_amdgcn_sqrtf(one_minus_square(2.0f * kLn2 * la, d));
+                        iv[j][e] = sigmoid_f32(in[j].get(e));
+                        u = bv[j][e] * iv[j][e] * x[j].get(e);
+                    }
                 } else {
                     d = __builtin_amdgcn_exp2f(kLog2e * r[j].get(e));
                     if (OUT) u = x[j].get(e);
@@ -113,7 +116,7 @@ __global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b
                 rec_wave<PACKED, false>(m[e], p.sub, before, all);
                 float h = rec_apply<PACKED>(before, hw[e]);
 #pragma unroll
-                for (int j = 0; j < kStrand; ++j) {  // the state before each token, in its input's place
+                for (int j = 0; j < S; ++j) {  // the state before each token, in its input's place
                     const float next = rec_apply<PACKED>({av[j][e], hv[j][e]}, h);
                     hv[j][e] = h;
                     h = next;
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b
             }
         // a token passes a (g + what comes to it) on to the one before, nothing from a first one
 #pragma unroll
-        for (int j = kStrand - 1; j >= 0; --j)
+        for (int j = S - 1; j >= 0; --j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const bool first = PACKED && av[j][e] < 0.0f;
@@ -149,19 +152,13 @@ __global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b
         }
         turn ^= 1;
         if (!OUT) return;
-        // the gates are made again: to keep those of all tokens takes more registers than there are
-#pragma unroll
-        for (int j = 0; j < kStrand; ++j) {
-            r[j].fresh();
-            if (GATED) in[j].fresh();
-        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) qs[e] = rec_apply<PACKED>(after[e], qs[e]);
         const size_t at = (yb + (size_t)tw * E) * sizeof(T);
         const uint32_t step = rec_bytes<T>(E);
-        uint32_t off = rec_offset<T>(step, p) + (kStrand - 1) * step;
+        uint32_t off = rec_offset<T, S>(step, p) + (S - 1) * step;
 #pragma unroll
-        for (int j = kStrand - 1; j >= 0; --j, off -= step) {
+        for (int j = S - 1; j >= 0; --j, off -= step) {
             float ox[2], orr[2], oi[2], oz[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -170,11 +167,9 @@ __global__ __launch_bounds__(kRecBwdWaves * 64) void rec_bwd_kernel(RecBwdArgs b
                 const float g = gv[j][e] + qs[e];
                 float d = av[j][e], u = xv;
                 if (GATED) {
-                    const float sr = sigmoid_f32(r[j].get(e)), la = rate[e] * sr * kLn2;
+                    const float sr = rv[j][e], la = rate[e] * sr * kLn2, si = iv[j][e], beta = bv[j][e];
                     if (PACKED) d = __builtin_amdgcn_exp2f(rate[e] * sr);
-                    const float s2 = one_minus_square(2.0f * la, d);
-                    const float inv = s2 > 0.0f ? __builtin_amdgcn_rsqf(s2) : 0.0f;
-                    const float si = sigmoid_f32(in[j].get(e)), beta = s2 * inv, gs = g * si;
+                    const float inv = beta > 0.0f ? __builtin_amdgcn_rcpf(beta) : 0.0f, gs = g * si;
                     u = beta * si * xv;
                     ox[e] = gs * beta;
                     oi[e] = ox[e] * xv * (1.0f - si);
@@ -267,10 +262,6 @@ template <typename T, bool GATED, bool PACKED> hipError_t bwd(const RecBwdArgs &
 }
 
 }  // namespace
-
-RecPlan rec_bwd_plan(int batch, int seqlen, int channels) {
-    return rec_plan(batch, seqlen, channels, kRecBwdWaves);
-}
 
 hipError_t launch_rec_bwd(const RecBwdArgs &b, bool bf16, hipStream_t stream) {
     const bool gated = b.f.decay != nullptr, packed = b.f.token != nullptr;

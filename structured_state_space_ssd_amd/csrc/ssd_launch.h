@@ -350,7 +350,11 @@ hipError_t launch_block_bwd(const BlockBwdArgs &a, bool bf16, bool stream_bf16, 
 
 // ---- gated recurrence (recurrence.hip, recurrence_bwd.hip)
 // x, r, i, z [Bt][L][E] with strides in elements between sequences and tokens; channels dense.
-constexpr int kRecKeep = 32;      // tokens between the states that the backward starts from
+constexpr int kRecKeep = 16;      // tokens between the states that the backward starts from
+// The backward's tokens to a strand (a wavefront holds kRecKeep) and wavefronts to a
+// workgroup at most: its lanes hold a token's every operand.
+constexpr int kRecBwdStrand = 4, kRecBwdWaves = 8;
+static_assert(4 * kRecBwdStrand == kRecKeep, "a wavefront starts from a state that is kept");
 struct RecArgs {
     const void *x, *r, *i, *z;    // z nullable; i NULL without decay
     size_t x_batch, x_token, r_batch, r_token, i_batch, i_token, z_batch, z_token;
@@ -359,7 +363,7 @@ struct RecArgs {
     const float *init;            // [Bt][E], nullable
     const int *token;             // packed sequences: launch_rec_tokens' codes, else NULL
     int batch, seqlen, channels;
-    int blocks, waves, segs, seg_len, keeps;  // rec_plan
+    int blocks, waves, segs, seg_len, keeps;  // the plan
     float *seg_a, *seg_h;         // [Bt][segs - 1][E]: scratch
     void *y;                      // [Bt][L][E] dense (NULL: states only)
     float *final_state;           // [Bt or nseq][E], nullable
@@ -368,7 +372,7 @@ struct RecArgs {
 struct RecPlan {
     int blocks, waves, segs, seg_len, keeps;
 };
-RecPlan rec_plan(int batch, int seqlen, int channels, int most_waves);
+RecPlan rec_fwd_plan(int batch, int seqlen, int channels, bool bf16);
 RecPlan rec_bwd_plan(int batch, int seqlen, int channels);
 unsigned rec_grid(const RecArgs &a, int segs);
 // The codes of a packed axis' tokens; zeroes `final` ([nseq][E], nullable).

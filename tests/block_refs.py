@@ -11,6 +11,7 @@ import torch
 import layer_refs as R
 
 JOINS = 60  # sums and products that join strands, wavefronts (16) and segments (32)
+KEEP = 16   # tokens between the states that the forward keeps
 
 
 def _d(t):
@@ -59,11 +60,11 @@ def recurrence(x, r, i=None, decay=None, z=None, init=None, c=8.0, cu=None, grad
     H, Er = h.abs(), zero
     # states, their magnitudes and errors before and behind every token
     before, after = torch.zeros(2, 3, Bt, L, E, dtype=torch.float64)
-    states, states_err = torch.zeros(2, Bt, -(-L // 32), E, dtype=torch.float64)
+    states, states_err = torch.zeros(2, Bt, -(-L // KEEP), E, dtype=torch.float64)
     final, final_err = torch.zeros(2, len(spans), E, dtype=torch.float64)
     for t in range(L):
-        if t % 32 == 0:
-            states[:, t // 32], states_err[:, t // 32] = h, Er + JOINS * H
+        if t % KEEP == 0:
+            states[:, t // KEEP], states_err[:, t // KEEP] = h, Er + JOINS * H
         if t in first:
             h, H, Er = zero, zero, zero
         before[0][:, t], before[1][:, t], before[2][:, t] = h, H, Er

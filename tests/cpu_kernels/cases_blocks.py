@@ -49,7 +49,7 @@ def recurrence(size, dtype, gated, gate, pad, ends, cu=None, keep=True):
     nseq = 0 if cu is None else len(cu) - 1
     dy, dfinal = r(Bt, L, E), r(nseq or Bt, E, dt=F32) if ends else None
     want = B.recurrence(*a.values(), init, 8.0, cu, (dy, dfinal))
-    keeps = -(-L // 32)
+    keeps = -(-L // B.KEEP)
 
     def inputs(m):
         p = {k: m.put(v) for k, v in a.items()}
@@ -111,7 +111,7 @@ def bad_offsets(cu):
 
     def run(m):
         px, pr, pd, pc = m.put(x), m.put(-x.abs()), m.put(x), m.put(torch.tensor(cu, dtype=torch.int32))
-        o = dict(y=m.new((1, L, E)), final=m.new((nseq, E)), states=m.new((1, 4, E)), dx=m.new((1, L, E)),
+        o = dict(y=m.new((1, L, E)), final=m.new((nseq, E)), states=m.new((1, 7, E)), dx=m.new((1, L, E)),
                  dr=m.new((1, L, E)))
         ws = scratch(m, lib.ssd_recurrence_forward_workspace_size(1, L, E, 1, 0))
         ok(lib.ssd_recurrence_forward(ptr(px), ptr(pr), None, None, 8.0, None, 1, L, E, 0, None, ptr(pc), nseq,

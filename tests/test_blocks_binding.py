@@ -115,8 +115,8 @@ def test_recurrence_c_abi_backward_and_step(lib):
     size = lib.ssd_recurrence_backward_workspace_size
     n = size(2, 6, 8, 0, 0, 1)
     assert n > 0 and size(2, 6, 8, 0, 0, 3) == 0 and size(2, 0, 8, 0, 0, 1) == 0
-    # the states that the caller has not kept: one for every 32 tokens
-    assert size(8, 64, 512, 0, 0, 1) - size(8, 64, 512, 0, 1, 1) == 8 * 2 * 512 * 4
+    # the states that the caller has not kept: one for every 16 tokens
+    assert size(8, 64, 512, 0, 0, 1) - size(8, 64, 512, 0, 1, 1) == 8 * 4 * 512 * 4
     assert lib.ssd_recurrence_forward_workspace_size(1, 100, 8, 1, 1) - lib.ssd_recurrence_forward_workspace_size(
         1, 100, 8, 0, 1) == 512  # a code for each token
 
