@@ -46,9 +46,10 @@ int check_recurrence(int batch, int seqlen, int channels, int dtype) {
     return SSD_OK;
 }
 
-bool plan_fits(int batch, const ssd::RecPlan &p) {  // fewer than 2^32 lanes, and units in an int
-    const long long units = (long long)batch * p.blocks * p.segs;
-    return units < (1LL << 30) && (units + 8) * p.waves * 64 < (1LL << 32);
+// Fewer than 2^32 lanes, and tokens of a last tile in an int.
+bool plan_fits(int batch, const ssd::RecPlan &p) {
+    const long long units = (long long)batch * p.blocks;
+    return units < (1LL << 28) && (units + 8) * p.tiles < (1LL << 32) / 64 / p.waves;
 }
 
 // Inputs, strides (NULL: dense) and checks that go beyond sizes.
@@ -83,31 +84,49 @@ int check_packed(const int *cu_seqlens, int nseq, int batch, const float *init) 
     return init ? SSD_ERR_UNSUPPORTED : SSD_OK;
 }
 
-void use_plan(ssd::RecArgs &a, const ssd::RecPlan &p) {
-    a.blocks = p.blocks; a.waves = p.waves; a.segs = p.segs; a.seg_len = p.seg_len; a.keeps = p.keeps;
-}
+// What a pass needs beside its tensors: the words that its tiles exchange, all one after the
+// other, and the codes of a packed axis.
+struct RecScratch {
+    size_t maps, enter, ticket, end, token;
+    void take(Taker &k, const ssd::RecPlan &p, int packed_tokens) {
+        maps = k.take(2 * p.map_words);
+        enter = k.take(2 * p.enter_words);
+        ticket = k.take(p.tickets);
+        end = k.o;
+        token = k.take(packed_tokens);
+    }
+    void use(ssd::RecArgs &a, const ssd::RecPlan &p, char *base) const {
+        a.blocks = p.blocks; a.waves = p.waves; a.tiles = p.tiles; a.keeps = p.keeps;
+        a.maps = reinterpret_cast<unsigned long long *>(base + maps);
+        a.enter = reinterpret_cast<unsigned long long *>(base + enter);
+        a.ticket = reinterpret_cast<unsigned *>(base + ticket);
+    }
+    hipError_t prepare(ssd::RecArgs &a, const int *cu, int nseq, float *final, char *base, hipStream_t s) const {
+        int *t = reinterpret_cast<int *>(base + token);
+        a.token = cu ? t : nullptr;
+        return ssd::launch_rec_prepare(a, base + maps, end - maps, cu, nseq, t, final, s);
+    }
+};
 
 struct RecLayout {
     ssd::RecPlan plan;
-    size_t token, seg_a, seg_h, total;
+    RecScratch scratch;
+    size_t total;
 };
 RecLayout recurrence_layout(int batch, int seqlen, int channels, bool packed, int dtype) {
     RecLayout w{};
     w.plan = ssd::rec_fwd_plan(batch, seqlen, channels, dtype == SSD_BF16);
     Taker k;
-    const size_t segs = (size_t)batch * (w.plan.segs - 1) * channels;
-    w.token = k.take(packed ? seqlen : 0);
-    w.seg_a = k.take(segs);
-    w.seg_h = k.take(segs);
+    w.scratch.take(k, w.plan, packed ? seqlen : 0);
     w.total = k.o;
     return w;
 }
 
-// Backward: the walk back's plan and scratch, and those of the walk that makes the states
-// where the caller has none.
+// Backward: its own pass and, where the caller has no states, the one that makes them.
 struct RecBwdLayout {
     ssd::RecPlan plan, keep;
-    size_t token, seg_a, seg_h, part, states, total;
+    RecScratch scratch, keep_scratch;
+    size_t part, spare, states, total;
 };
 RecBwdLayout recurrence_bwd_layout(int batch, int seqlen, int channels, bool packed, bool have_states,
                                    int dtype) {
@@ -115,14 +134,14 @@ RecBwdLayout recurrence_bwd_layout(int batch, int seqlen, int channels, bool pac
     w.plan = ssd::rec_bwd_plan(batch, seqlen, channels);
     w.keep = ssd::rec_fwd_plan(batch, seqlen, channels, dtype == SSD_BF16);
     const size_t be = (size_t)batch * channels;
-    size_t segs = be * (w.plan.segs - 1);
-    if (!have_states && be * (w.keep.segs - 1) > segs) segs = be * (w.keep.segs - 1);
     Taker k;
-    w.token = k.take(packed ? seqlen : 0);
-    w.seg_a = k.take(segs);  // the two walks' in turn
-    w.seg_h = k.take(segs);
-    w.part = k.take(be * w.plan.segs);
-    w.states = k.take(have_states ? 0 : be * w.plan.keeps);
+    w.scratch.take(k, w.plan, packed ? seqlen : 0);
+    w.part = k.take(be * w.plan.tiles);
+    w.spare = k.take((long long)batch * w.plan.tiles > ssd::kColsumRows ? (size_t)ssd::kColsumChunks * channels : 0);
+    if (!have_states) {
+        w.keep_scratch.take(k, w.keep, packed ? seqlen : 0);
+        w.states = k.take(be * w.plan.keeps);
+    }
     w.total = k.o;
     return w;
 }
@@ -193,20 +212,14 @@ int ssd_recurrence_forward(const void *x, const void *r, const void *i, const fl
     rc = check_workspace(workspace, workspace_bytes, w.total);
     if (rc != SSD_OK) return rc;
     char *base = static_cast<char *>(workspace);
-    use_plan(a, w.plan);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    w.scratch.use(a, w.plan, base);
     a.init = init_state;
-    a.seg_a = reinterpret_cast<float *>(base + w.seg_a);
-    a.seg_h = reinterpret_cast<float *>(base + w.seg_h);
     a.y = y;
     a.final_state = final_state;
     a.states = states;
-    const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (cu_seqlens) {
-        int *token = reinterpret_cast<int *>(base + w.token);
-        a.token = token;
-        const hipError_t e = ssd::launch_rec_tokens(a, cu_seqlens, nseq, token, final_state, s);
-        if (e != hipSuccess) return status_of(e);
-    }
+    const hipError_t e = w.scratch.prepare(a, cu_seqlens, nseq, final_state, base, s);
+    if (e != hipSuccess) return status_of(e);
     return status_of(ssd::launch_rec_fwd(a, dtype == SSD_BF16, s));
 }
 
@@ -249,37 +262,34 @@ int ssd_recurrence_backward(const void *x, const void *r, const void *i, const f
     const RecBwdLayout w = recurrence_bwd_layout(batch, seqlen, channels, cu_seqlens != nullptr,
                                                  states != nullptr, dtype);
     if (!plan_fits(batch, w.plan) || !plan_fits(batch, w.keep) ||
-        !ssd::colsum_grid_ok(batch * w.plan.segs, channels, false))
+        (long long)batch * w.plan.tiles > kMaxExtent ||
+        !ssd::colsum_grid_ok(batch * w.plan.tiles, channels, true))
         return SSD_ERR_UNSUPPORTED;
     rc = check_workspace(workspace, workspace_bytes, w.total);
     if (rc != SSD_OK) return rc;
     char *base = static_cast<char *>(workspace);
     auto at = [&](size_t off) { return reinterpret_cast<float *>(base + off); };
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    a.seg_a = at(w.seg_a);
-    a.seg_h = at(w.seg_h);
-    hipError_t e;
-    if (cu_seqlens) {
-        int *token = reinterpret_cast<int *>(base + w.token);
-        a.token = token;
-        e = ssd::launch_rec_tokens(a, cu_seqlens, nseq, token, nullptr, s);
-        if (e != hipSuccess) return status_of(e);
-    }
     a.states = const_cast<float *>(states);
+    hipError_t e;
     if (!states) {
-        use_plan(a, w.keep);
+        w.keep_scratch.use(a, w.keep, base);
         a.init = init_state;
         a.states = at(w.states);
-        e = ssd::launch_rec_fwd(a, dtype == SSD_BF16, s);
+        e = w.keep_scratch.prepare(a, cu_seqlens, nseq, nullptr, base, s);
+        if (e == hipSuccess) e = ssd::launch_rec_fwd(a, dtype == SSD_BF16, s);
         if (e != hipSuccess) return status_of(e);
     }
-    use_plan(a, w.plan);
+    w.scratch.use(a, w.plan, base);
+    e = w.scratch.prepare(a, cu_seqlens, nseq, nullptr, base, s);
+    if (e != hipSuccess) return status_of(e);
     b.dy = dy;
     b.dfinal = dfinal_state;
     b.dx = dx; b.dr = dr; b.di = di; b.dz = dz;
     b.ddecay = ddecay;
     b.dinit = dinit_state;
     b.part = at(w.part);
+    b.spare = (long long)batch * w.plan.tiles > ssd::kColsumRows ? at(w.spare) : nullptr;
     return status_of(ssd::launch_rec_bwd(b, dtype == SSD_BF16, s));
 }
 

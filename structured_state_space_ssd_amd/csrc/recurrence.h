@@ -1,12 +1,14 @@
-// Device code shared by the gated recurrence's walks, forward (recurrence.hip) and
-// back (recurrence_bwd.hip). The layout of a workgroup:
-//   it holds 32 channels of one sequence; a strand of 16 lanes with two channels
-//   each holds S (4 or 8) consecutive tokens, a wavefront four strands one after the
-//   other, the workgroup `waves` wavefronts one after the other: a tile of
-//   4 S waves tokens, which it walks along the token axis.
+// Device code shared by the gated recurrence's passes, forward (recurrence.hip) and back
+// (recurrence_bwd.hip). The layout of a workgroup:
+//   it holds one tile: 32 channels of one sequence (a unit) for 4 S waves consecutive
+//   tokens. A strand of 16 lanes with two channels each holds S (4 or 8) consecutive
+//   tokens, a wavefront four strands one after the other, the workgroup `waves`
+//   wavefronts one after the other.
 // A strand's tokens are a map h -> A h + H of the state entering it; maps are put
-// together across the strands of a wavefront by swaps of registers and across the
-// wavefronts through LDS, so one barrier a tile is all that the walk waits for.
+// together across the strands of a wavefront by swaps of registers, across the
+// wavefronts through LDS and across the tiles of a unit through memory (rec_enter), so
+// that every operand is read once, whatever the number of channels, and tokens and
+// channels alike fill the GPU.
 //
 // A map that starts a sequence anew inside (packed sequences) is marked by a
 // negative A (a product of decays is not): the state before it does not
@@ -60,40 +62,29 @@ template <> struct RecPair<float> {
     static __device__ __forceinline__ void store_one(char *p, float a) { *reinterpret_cast<float *>(p) = a; }
 };
 
-// Where a lane is: its strand, channels and the workgroup's unit.
+// Where a lane is: its strand and channels, and the workgroup's unit.
 struct RecPlace {
-    int batch, seg, ch, nch;      // nch: channels of the lane inside the tensor, 0 to 2
+    int unit, batch, ch, nch;     // nch: channels of the lane inside the tensor, 0 to 2
     int wave, sub, col;           // strand `sub` of wavefront `wave`, lane `col` of the strand
-    int begin, end;               // the segment's tokens
     bool live;                    // a unit of the grid that there is
 };
-// Units one after the other along the channels go to the same XCD (workgroups
-// are dealt to the eight XCDs in turn): they share cache lines.
-__device__ __forceinline__ RecPlace rec_place(const RecArgs &a, int segs) {
+// Every unit has as many workgroups as tiles. Units one after the other along the channels
+// go to the same XCD (workgroups are dealt to the eight XCDs in turn): they share
+// cache lines.
+__device__ __forceinline__ RecPlace rec_place(const RecArgs &a) {
     RecPlace p;
-    const int units = a.batch * a.blocks * segs, each = (units + 7) >> 3;
-    const int id = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
-    p.live = (int)(blockIdx.x >> 3) < each && id < units;
-    const int rest = id / a.blocks, block = id - rest * a.blocks;
-    p.batch = rest / segs;
-    p.seg = rest - p.batch * segs;
+    const int units = a.batch * a.blocks, each = (units + 7) >> 3;
+    p.unit = (blockIdx.x & 7) * each + (blockIdx.x >> 3) % each;
+    p.live = p.unit < units;
+    p.batch = p.unit / a.blocks;
     p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     p.sub = (threadIdx.x >> 4) & 3;
     p.col = threadIdx.x & 15;
-    p.ch = block * kRecCols + 2 * p.col;
+    p.ch = (p.unit - p.batch * a.blocks) * kRecCols + 2 * p.col;
     p.nch = min(max(a.channels - p.ch, 0), 2);
-    p.begin = p.seg * a.seg_len;
-    p.end = min(p.begin + a.seg_len, a.seqlen);
     return p;
 }
 
-// Bytes between tokens, as a value that the compiler takes anew in every tile: offsets
-// made of it ahead of the walk would fill the registers.
-template <typename T> __device__ __forceinline__ uint32_t rec_bytes(size_t token) {
-    uint32_t step = static_cast<uint32_t>(token * sizeof(T));
-    asm volatile("" : "+s"(step));
-    return step;
-}
 // Byte offset of a lane's first token and channel (strides are below 2^24 elements).
 template <typename T, int S> __device__ __forceinline__ uint32_t rec_offset(uint32_t step, const RecPlace &p) {
     return static_cast<uint32_t>(p.sub * S) * step + p.ch * static_cast<uint32_t>(sizeof(T));
@@ -104,7 +95,7 @@ template <typename T, bool WHOLE, int S>
 __device__ __forceinline__ void rec_load(RecPair<T> (&r)[S], const void *t, size_t at, size_t token,
                                          const RecPlace &p, int nt) {
     const char *base = static_cast<const char *>(t) + at * sizeof(T);
-    const uint32_t step = rec_bytes<T>(token);
+    const uint32_t step = static_cast<uint32_t>(token * sizeof(T));
     uint32_t off = rec_offset<T, S>(step, p);
 #pragma unroll
     for (int j = 0; j < S; ++j, off += step) {
@@ -190,6 +181,124 @@ __device__ __forceinline__ void rec_wave(RecMap m, int sub, RecMap &before, RecM
     const RecMap in = second ? mate : none;
     const RecMap joined = rec_then<PACKED>(pairs, in);
     before = later ? (second ? joined : pairs) : in;
+}
+
+
+// ---- across the tiles of a unit -------------------------------------------------------
+//
+// A unit's tiles are taken in the order in which its workgroups start: the first one
+// to start takes the first tile (the last one, back). So the tiles that come before a
+// workgroup's own are held by workgroups that have started, which wait for tiles before
+// theirs only: every wait ends, in whatever order and however few at a time the GPU
+// runs the workgroups.
+//
+// A tile first makes the map of all its tokens known, then waits for those of the tiles
+// before it in its group of kRecGroup and for the state that enters the group, which the last tile
+// of the group before makes known: its state comes from the same maps in the same
+// order every time, and the way of a state through a long sequence is one wait for
+// kRecGroup tiles. Each value travels in a 64-bit word of its own with what says that it is
+// there, so nothing has to be ordered; before the pass all words are set to ~0.
+
+constexpr int kRecGroup = 16;  // the strands of four wavefronts, each of which waits for one tile
+constexpr uint32_t kRecUnset = 0xffffffffu;
+
+struct RecShared {
+    int tile;
+    float wave[16][16][4];                // the wavefronts' maps
+    float before[kRecGroup + 1][16][4];   // the maps of the group's tiles before, and its state
+};
+
+// The workgroup's tile, in the order of starting.
+__device__ __forceinline__ int rec_ticket(const RecArgs &a, const RecPlace &p, RecShared &sh) {
+    if (a.tiles == 1) return 0;
+    if (threadIdx.x == 0)
+        sh.tile = static_cast<int>(__hip_atomic_fetch_add(a.ticket + p.unit, 1u, __ATOMIC_RELAXED,
+                                                          __HIP_MEMORY_SCOPE_AGENT) + 1u);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(sh.tile);
+}
+__device__ __forceinline__ void rec_tell(unsigned long long *at, float value, uint32_t mark) {
+    __hip_atomic_store(at, static_cast<unsigned long long>(__float_as_uint(value)) << 32 | mark, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void rec_wait(const unsigned long long *at, float &value, uint32_t &mark) {
+    unsigned long long v;
+    while (static_cast<uint32_t>(v = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) == kRecUnset)
+        __builtin_amdgcn_s_sleep(1);
+    value = __uint_as_float(static_cast<uint32_t>(v >> 32));
+    mark = static_cast<uint32_t>(v);
+}
+
+// All lanes of the workgroup, with the maps of their wavefronts (the same in every strand)
+// and what enters the unit's first tile: what enters the lane's wavefront. `left`: what
+// leaves the tile. order: the tile's place in the order of the walk; REVERSE: the
+// last wavefront comes first.
+template <bool PACKED, bool REVERSE>
+__device__ __forceinline__ void rec_enter(const RecArgs &a, const RecPlace &p, int order, const RecMap (&whole)[2],
+                                          const float (&first)[2], float (&enters)[2], float (&left)[2], RecShared &sh) {
+    if (p.sub == 0)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            sh.wave[p.wave][p.col][2 * e] = whole[e].a;
+            sh.wave[p.wave][p.col][2 * e + 1] = whole[e].h;
+        }
+    __syncthreads();
+    RecMap pre[2], all[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
+    for (int k = 0; k < a.waves; ++k) {
+        const int w = REVERSE ? a.waves - 1 - k : k;
+        const float *v = sh.wave[w][p.col];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (w == p.wave) pre[e] = all[e];
+            all[e] = rec_then<PACKED>(all[e], {v[2 * e], v[2 * e + 1]});
+        }
+    }
+    float in[2] = {first[0], first[1]};
+    if (a.tiles > 1) {
+        const int place = order % kRecGroup, group = order / kRecGroup, strand = p.wave * 4 + p.sub;
+        const size_t unit = (size_t)p.unit * kRecCols + 2 * p.col;
+        const size_t tiles = (size_t)a.batch * a.blocks * kRecCols;  // words of one tile of every unit
+        if (strand == 0 && place < kRecGroup - 1)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // (any number but the mark of none; a decay that is not a number is one of its own)
+                uint32_t mark = __float_as_uint(all[e].a);
+                if (all[e].a != all[e].a) mark = 0x7fc00000u;
+                rec_tell(a.maps + order * tiles + unit + e, all[e].h, mark);
+            }
+        if (strand < place || (strand == kRecGroup - 1 && group > 0)) {
+            const bool state = strand == kRecGroup - 1;
+            const unsigned long long *at = state ? a.enter + group * tiles + unit
+                                                 : a.maps + ((size_t)group * kRecGroup + strand) * tiles + unit;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float value;
+                uint32_t mark;
+                rec_wait(at + e, value, mark);
+                sh.before[strand][p.col][2 * e] = __uint_as_float(mark);
+                sh.before[strand][p.col][2 * e + 1] = value;
+            }
+        }
+        __syncthreads();
+        if (group > 0)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) in[e] = sh.before[kRecGroup - 1][p.col][2 * e + 1];
+        for (int k = 0; k < place; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                in[e] = rec_apply<PACKED>({sh.before[k][p.col][2 * e], sh.before[k][p.col][2 * e + 1]}, in[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        left[e] = rec_apply<PACKED>(all[e], in[e]);
+        enters[e] = rec_apply<PACKED>(pre[e], in[e]);
+    }
+    if (a.tiles > 1 && p.wave == 0 && p.sub == 0 && order % kRecGroup == kRecGroup - 1 && order + 1 < a.tiles) {
+        const size_t tiles = (size_t)a.batch * a.blocks * kRecCols;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            rec_tell(a.enter + (order / kRecGroup + 1) * tiles + (size_t)p.unit * kRecCols + 2 * p.col + e, left[e], 0);
+    }
 }
 
 }  // namespace ssd

@@ -7,62 +7,38 @@
 // (log a / b goes to 0 with log a, so w does too, where the gradient of log a itself grows
 // without bound.)
 //
-// The walk goes back over the tiles. A wavefront's 16 tokens find the state entering
-// them in memory, where the forward kept one every kRecKeep = 16 tokens (1/4 of a byte a
-// channel and token), and make their states from it again in registers; the adjoint is
-// put together like the forward's state, against the tokens' order.
+// A wavefront's 16 tokens find the state entering them in memory, where the forward
+// kept one every kRecKeep = 16 tokens (1/4 of a byte a channel and token), and make their
+// states from it again in registers; the adjoint is put together like the forward's
+// state, against the tokens' order.
 #include "recurrence.h"
 
 namespace ssd {
 
 namespace {
 
-// OUT: the gradients, from the adjoint that the later segments give. Else what
-// segments 1 .. segs - 1 do to the adjoint that comes to their end: seg_a, seg_h.
-template <typename T, bool GATED, bool PACKED, bool OUT>
+template <typename T, bool GATED, bool PACKED>
 __global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b) {
     constexpr int S = kRecBwdStrand;
-    __shared__ float buf[2][kRecBwdWaves][16][4];
+    __shared__ RecShared sh;
     const RecArgs &a = b.f;
-    RecPlace p = rec_place(a, OUT ? a.segs : a.segs - 1);
+    const RecPlace p = rec_place(a);
     if (!p.live) return;
-    if (!OUT) {
-        ++p.seg;
-        p.begin = p.seg * a.seg_len;
-        p.end = min(p.begin + a.seg_len, a.seqlen);
-    }
-    const int tile = a.waves * 4 * S, E = a.channels;
+    const int order = rec_ticket(a, p, sh), tile = a.tiles - 1 - order;
+    const int E = a.channels, tw = (tile * a.waves + p.wave) * 4 * S, ts = tw + p.sub * S;
+    const int nt = min(max(a.seqlen - ts, 0), S);
     const size_t row0 = (size_t)p.batch * E + p.ch;
-    // q: what comes to the last token walked so far from the tokens after it
-    float rate[2] = {0.0f, 0.0f}, q[2] = {0.0f, 0.0f}, A[2] = {1.0f, 1.0f}, sum[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-        if (e < p.nch) {
-            if (GATED) rate[e] = rec_rate(a.decay[p.ch + e], a.c);
-            if (OUT && !PACKED && b.dfinal) q[e] = b.dfinal[row0 + e];
-            if (OUT)
-                for (int s = a.segs - 1; s > p.seg; --s) {
-                    const size_t k = ((size_t)p.batch * (a.segs - 1) + s - 1) * E + p.ch + e;
-                    q[e] = rec_apply<PACKED>({a.seg_a[k], a.seg_h[k]}, q[e]);
-                }
-        }
-    const size_t xb = p.batch * a.x_batch, rb = p.batch * a.r_batch, ib = p.batch * a.i_batch, zb = p.batch * a.z_batch;
-    const size_t yb = (size_t)p.batch * a.seqlen * E;
-    int turn = 0;
-    auto walk = [&](auto whole, int t0) {
-        constexpr bool WHOLE = decltype(whole)::value;
-        const int tw = t0 + p.wave * 4 * S, ts = tw + p.sub * S;
-        const int nt = min(max(p.end - ts, 0), S);
+    auto run = [&](auto whole_tile) {
+        constexpr bool WHOLE = decltype(whole_tile)::value;
         RecPair<T> x[S], r[S], in[S], z[S], dy[S];
-        rec_load<T, WHOLE>(r, a.r, rb + tw * a.r_token, a.r_token, p, nt);
-        rec_load<T, WHOLE>(dy, b.dy, yb + (size_t)tw * E, E, p, nt);
-        if (a.z) rec_load<T, WHOLE>(z, a.z, zb + tw * a.z_token, a.z_token, p, nt);
-        if (OUT) {
-            rec_load<T, WHOLE>(x, a.x, xb + tw * a.x_token, a.x_token, p, nt);
-            if (GATED) rec_load<T, WHOLE>(in, a.i, ib + tw * a.i_token, a.i_token, p, nt);
-        }
+        const size_t at = ((size_t)p.batch * a.seqlen + tw) * E;
+        rec_load<T, WHOLE>(r, a.r, p.batch * a.r_batch + tw * a.r_token, a.r_token, p, nt);
+        rec_load<T, WHOLE>(dy, b.dy, at, E, p, nt);
+        if (a.z) rec_load<T, WHOLE>(z, a.z, p.batch * a.z_batch + tw * a.z_token, a.z_token, p, nt);
+        if (GATED) rec_load<T, WHOLE>(in, a.i, p.batch * a.i_batch + tw * a.i_token, a.i_token, p, nt);
+        rec_load<T, WHOLE>(x, a.x, p.batch * a.x_batch + tw * a.x_token, a.x_token, p, nt);
         float hw[2] = {0.0f, 0.0f};  // the state entering the wavefront's tokens
-        if (OUT && (WHOLE || tw < p.end)) {
+        if (WHOLE || tw < a.seqlen) {
             const float *s = a.states + ((size_t)p.batch * a.keeps + tw / kRecKeep) * E + p.ch;
             if (p.nch > 0) hw[0] = s[0];
             if (p.nch > 1) hw[1] = s[1];
@@ -71,6 +47,14 @@ __global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArg
         if (PACKED)
 #pragma unroll
             for (int j = 0; j < S; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
+        // q: what comes to the last token from behind
+        float rate[2] = {0.0f, 0.0f}, q[2] = {0.0f, 0.0f}, sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (e < p.nch) {
+                if (GATED) rate[e] = rec_rate(a.decay[p.ch + e], a.c);
+                if (!PACKED && b.dfinal) q[e] = b.dfinal[row0 + e];
+            }
         float av[S][2], hv[S][2], gv[S][2];
         float rv[S][2], iv[S][2], bv[S][2];  // the gates, and sqrt(1 - a^2)
         RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mg[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
@@ -78,19 +62,17 @@ __global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArg
         for (int j = 0; j < S; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float d, u = 0.0f;
+                float d, u;
                 if (GATED) {
                     rv[j][e] = sigmoid_f32(r[j].get(e));
                     const float la = rate[e] * rv[j][e];
                     d = __builtin_amdgcn_exp2f(la);
-                    if (OUT) {
-                        bv[j][e] = __builtin_amdgcn_sqrtf(one_minus_square(2.0f * kLn2 * la, d));
-                        iv[j][e] = sigmoid_f32(in[j].get(e));
-                        u = bv[j][e] * iv[j][e] * x[j].get(e);
-                    }
+                    bv[j][e] = __builtin_amdgcn_sqrtf(one_minus_square(2.0f * kLn2 * la, d));
+                    iv[j][e] = sigmoid_f32(in[j].get(e));
+                    u = bv[j][e] * iv[j][e] * x[j].get(e);
                 } else {
                     d = __builtin_amdgcn_exp2f(kLog2e * r[j].get(e));
-                    if (OUT) u = x[j].get(e);
+                    u = x[j].get(e);
                 }
                 float g = dy[j].get(e);
                 if (a.z) g *= silu_f32(z[j].get(e));
@@ -107,21 +89,20 @@ __global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArg
                 av[j][e] = d;
                 hv[j][e] = u;
                 gv[j][e] = g;
-                if (OUT) m[e] = rec_then<PACKED>(m[e], {d, u});
+                m[e] = rec_then<PACKED>(m[e], {d, u});
             }
-        if (OUT)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                RecMap before, all;
-                rec_wave<PACKED, false>(m[e], p.sub, before, all);
-                float h = rec_apply<PACKED>(before, hw[e]);
+        for (int e = 0; e < 2; ++e) {
+            RecMap before, whole;
+            rec_wave<PACKED, false>(m[e], p.sub, before, whole);
+            float h = rec_apply<PACKED>(before, hw[e]);
 #pragma unroll
-                for (int j = 0; j < S; ++j) {  // the state before each token, in its input's place
-                    const float next = rec_apply<PACKED>({av[j][e], hv[j][e]}, h);
-                    hv[j][e] = h;
-                    h = next;
-                }
+            for (int j = 0; j < S; ++j) {  // the state before each token, in its input's place
+                const float next = rec_apply<PACKED>({av[j][e], hv[j][e]}, h);
+                hv[j][e] = h;
+                h = next;
             }
+        }
         // a token passes a (g + what comes to it) on to the one before, nothing from a first one
 #pragma unroll
         for (int j = S - 1; j >= 0; --j)
@@ -131,31 +112,18 @@ __global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArg
                 mg[e] = {first || (PACKED && mg[e].a < 0.0f) ? -1.0f : av[j][e] * mg[e].a,
                          first ? 0.0f : av[j][e] * (gv[j][e] + mg[e].h)};
             }
-        RecMap after[2], all[2];
+        RecMap after[2], whole[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) rec_wave<PACKED, true>(mg[e], p.sub, after[e], all[e]);
-        if (p.sub == 0) {
-            float *w = buf[turn][p.wave][p.col];
-            w[0] = all[0].a; w[1] = all[0].h; w[2] = all[1].a; w[3] = all[1].h;
-        }
-        __syncthreads();
-        float qs[2] = {q[0], q[1]};
-        for (int w = a.waves - 1; w >= 0; --w) {
-            const float *v = buf[turn][w][p.col];
-            const RecMap mw[2] = {{v[0], v[1]}, {v[2], v[3]}};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (w == p.wave) qs[e] = q[e];
-                q[e] = rec_apply<PACKED>(mw[e], q[e]);
-                if (!OUT) A[e] = PACKED && (A[e] < 0.0f || mw[e].a < 0.0f) ? -1.0f : A[e] * mw[e].a;
-            }
-        }
-        turn ^= 1;
-        if (!OUT) return;
+        for (int e = 0; e < 2; ++e) rec_wave<PACKED, true>(mg[e], p.sub, after[e], whole[e]);
+        float qs[2], left[2];
+        rec_enter<PACKED, true>(a, p, order, whole, q, qs, left, sh);
 #pragma unroll
         for (int e = 0; e < 2; ++e) qs[e] = rec_apply<PACKED>(after[e], qs[e]);
-        const size_t at = (yb + (size_t)tw * E) * sizeof(T);
-        const uint32_t step = rec_bytes<T>(E);
+        if (!PACKED && b.dinit && tile == 0 && p.wave == 0 && p.sub == 0) {
+            if (p.nch > 0) b.dinit[row0] = left[0];
+            if (p.nch > 1) b.dinit[row0 + 1] = left[1];
+        }
+        const uint32_t step = static_cast<uint32_t>(E * sizeof(T));
         uint32_t off = rec_offset<T, S>(step, p) + (S - 1) * step;
 #pragma unroll
         for (int j = S - 1; j >= 0; --j, off -= step) {
@@ -191,74 +159,49 @@ __global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArg
             if (!WHOLE && j >= nt) continue;
             if (PACKED && code[j] < 0) ox[0] = ox[1] = orr[0] = orr[1] = oi[0] = oi[1] = oz[0] = oz[1] = 0.0f;
             const auto out = [&](void *t, float (&v)[2]) {
-                rec_store<T, WHOLE>(static_cast<char *>(t) + at, off, p.nch, v[0], v[1]);
+                rec_store<T, WHOLE>(static_cast<char *>(t) + at * sizeof(T), off, p.nch, v[0], v[1]);
             };
             out(b.dx, ox);
             out(b.dr, orr);
             if (GATED) out(b.di, oi);
             if (a.z) out(b.dz, oz);
         }
-    };
-    const bool inner = p.ch - 2 * p.col + kRecCols <= E;
-    int t0 = p.begin + (p.end - p.begin - 1) / tile * tile;
-    for (; t0 >= p.begin; t0 -= tile) {
-        if (inner && t0 + tile <= p.end) walk(std::true_type(), t0);
-        else walk(std::false_type(), t0);
-    }
-    if (OUT && GATED) {  // the strands' sums of w, then the wavefronts'
-        float v[2] = {sum[0], sum[1]};
+        if (!GATED) return;
+        // the strands' sums of w, then the wavefronts'
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[e]), __float_as_uint(v[e]), false, false);
-            v[e] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-            const auto k = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[e]), __float_as_uint(v[e]), false, false);
-            v[e] = __uint_as_float(k[0]) + __uint_as_float(k[1]);
-        }
-        // (the buffer that the last tile did not read)
-        if (p.sub == 0) {
-            buf[turn][p.wave][p.col][0] = v[0];
-            buf[turn][p.wave][p.col][1] = v[1];
+            const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(sum[e]), __float_as_uint(sum[e]), false, false);
+            sum[e] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+            const auto k = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum[e]), __float_as_uint(sum[e]), false, false);
+            sum[e] = __uint_as_float(k[0]) + __uint_as_float(k[1]);
         }
         __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            sum[e] = 0.0f;
-            for (int w = 0; w < a.waves; ++w) sum[e] += buf[turn][w][p.col][e];
+        if (p.sub == 0) {
+            sh.wave[p.wave][p.col][0] = sum[0];
+            sh.wave[p.wave][p.col][1] = sum[1];
         }
-    }
-    if (p.wave || p.sub) return;
+        __syncthreads();
+        if (p.wave || p.sub) return;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-        if (e < p.nch) {
-            if (!OUT) {
-                const size_t k = ((size_t)p.batch * (a.segs - 1) + p.seg - 1) * E + p.ch + e;
-                a.seg_a[k] = A[e];
-                a.seg_h[k] = q[e];
-                continue;
-            }
-            if (GATED) {
+        for (int e = 0; e < 2; ++e)
+            if (e < p.nch) {
+                float s = 0.0f;
+                for (int w = 0; w < a.waves; ++w) s += sh.wave[w][p.col][e];
                 // sigmoid / softplus goes to 1 as both go to e^decay, and beyond what 32 bits hold of that
-                const float v = a.decay[p.ch + e];
-                const float k = v < -20.0f ? 1.0f : sigmoid_f32(v) / softplus_f32(v);
-                b.part[((size_t)p.batch * a.segs + p.seg) * E + p.ch + e] = k * sum[e];
+                const float v = a.decay[p.ch + e], k = v < -20.0f ? 1.0f : sigmoid_f32(v) / softplus_f32(v);
+                b.part[((size_t)p.batch * a.tiles + tile) * E + p.ch + e] = k * s;
             }
-            if (!PACKED && b.dinit && p.seg == 0) b.dinit[row0 + e] = q[e];
-        }
+    };
+    if (p.ch - 2 * p.col + kRecCols <= E && (tile + 1) * a.waves * 4 * S <= a.seqlen) run(std::true_type());
+    else run(std::false_type());
 }
 
 template <typename T, bool GATED, bool PACKED> hipError_t bwd(const RecBwdArgs &b, hipStream_t stream) {
     const RecArgs &a = b.f;
-    const int threads = a.waves * 64;
-    hipError_t e;
-    if (a.segs > 1) {
-        rec_bwd_kernel<T, GATED, PACKED, false><<<rec_grid(a, a.segs - 1), threads, 0, stream>>>(b);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    rec_bwd_kernel<T, GATED, PACKED, true><<<rec_grid(a, a.segs), threads, 0, stream>>>(b);
-    e = hipGetLastError();
+    rec_bwd_kernel<T, GATED, PACKED><<<rec_grid(a), a.waves * 64, 0, stream>>>(b);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !GATED) return e;
-    return launch_colsum(b.part, a.batch * a.segs, a.channels, a.channels, b.ddecay, nullptr, stream);
+    return launch_colsum(b.part, a.batch * a.tiles, a.channels, a.channels, b.ddecay, nullptr, stream, b.spare);
 }
 
 }  // namespace

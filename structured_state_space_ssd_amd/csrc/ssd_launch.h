@@ -351,9 +351,9 @@ hipError_t launch_block_bwd(const BlockBwdArgs &a, bool bf16, bool stream_bf16, 
 // ---- gated recurrence (recurrence.hip, recurrence_bwd.hip)
 // x, r, i, z [Bt][L][E] with strides in elements between sequences and tokens; channels dense.
 constexpr int kRecKeep = 16;      // tokens between the states that the backward starts from
-// The backward's tokens to a strand (a wavefront holds kRecKeep) and wavefronts to a
-// workgroup at most: its lanes hold a token's every operand.
-constexpr int kRecBwdStrand = 4, kRecBwdWaves = 8;
+// The backward's tokens to a strand (a wavefront holds kRecKeep: its lanes hold a token's
+// every operand) and wavefronts to a workgroup at most.
+constexpr int kRecBwdStrand = 4, kRecBwdWaves = 4;
 static_assert(4 * kRecBwdStrand == kRecKeep, "a wavefront starts from a state that is kept");
 struct RecArgs {
     const void *x, *r, *i, *z;    // z nullable; i NULL without decay
@@ -361,22 +361,28 @@ struct RecArgs {
     const float *decay;           // [E]; NULL: r is the log-decay, x the input term
     float c;
     const float *init;            // [Bt][E], nullable
-    const int *token;             // packed sequences: launch_rec_tokens' codes, else NULL
+    const int *token;             // packed sequences: launch_rec_prepare's codes, else NULL
     int batch, seqlen, channels;
-    int blocks, waves, segs, seg_len, keeps;  // the plan
-    float *seg_a, *seg_h;         // [Bt][segs - 1][E]: scratch
+    int blocks, waves, tiles, keeps;  // the plan
+    // Scratch, with several tiles, set to ~0 by launch_rec_prepare: the tiles' maps, the
+    // states entering groups of them, and how many of a unit's tiles are taken.
+    unsigned long long *maps, *enter;
+    unsigned *ticket;
     void *y;                      // [Bt][L][E] dense (NULL: states only)
     float *final_state;           // [Bt or nseq][E], nullable
     float *states;                // [Bt][keeps][E]: the state before every so many tokens, nullable
 };
 struct RecPlan {
-    int blocks, waves, segs, seg_len, keeps;
+    int blocks, waves, tiles, keeps;
+    size_t map_words, enter_words, tickets;
 };
 RecPlan rec_fwd_plan(int batch, int seqlen, int channels, bool bf16);
 RecPlan rec_bwd_plan(int batch, int seqlen, int channels);
-unsigned rec_grid(const RecArgs &a, int segs);
-// The codes of a packed axis' tokens; zeroes `final` ([nseq][E], nullable).
-hipError_t launch_rec_tokens(const RecArgs &a, const int *cu, int nseq, int *token, float *final, hipStream_t stream);
+unsigned rec_grid(const RecArgs &a);
+// Sets `bytes` at `unset` (multiples of 16) to ~0, makes the codes of a packed axis' tokens
+// (cu not NULL) and zeroes `final` ([nseq][E], nullable).
+hipError_t launch_rec_prepare(const RecArgs &a, void *unset, size_t bytes, const int *cu, int nseq, int *token,
+                              float *final, hipStream_t stream);
 hipError_t launch_rec_fwd(const RecArgs &a, bool bf16, hipStream_t stream);
 // One token: the token strides and init are not read.
 hipError_t launch_rec_step(const RecArgs &a, float *state, bool bf16, hipStream_t stream);
@@ -386,7 +392,8 @@ struct RecBwdArgs {
     const float *dfinal;          // [Bt or nseq][E], nullable
     void *dx, *dr, *di, *dz;      // dense
     float *ddecay, *dinit;        // dinit nullable
-    float *part;                  // [Bt][segs][E]: scratch
+    float *part;                  // [Bt][tiles][E]: scratch
+    float *spare;                 // kColsumChunks rows of E, where there are more than kColsumRows
 };
 hipError_t launch_rec_bwd(const RecBwdArgs &b, bool bf16, hipStream_t stream);
 

@@ -21,7 +21,10 @@ def library(tmp_path_factory):
         pytest.skip("no ROCm clang here")
     build.SOURCES += ("recurrence.hip", "recurrence_bwd.hip", "dropout.hip", "block_norm.hip", "blocks_api.hip")
     build.HEADERS += ("recurrence.h", "dropout.h")
-    flags = ("-D__builtin_amdgcn_sqrtf=sqrtf", "-D__builtin_amdgcn_rsqf(x)=(1.0f/sqrtf(x))")
+    # (workgroups run one after the other, so a word that one waits for is there, or never comes)
+    flags = ("-D__builtin_amdgcn_sqrtf=sqrtf", "-D__builtin_amdgcn_s_sleep(x)=cpu::fail(\"waits for what does not come\")",
+             "-D__hip_atomic_load(p,o,s)=(*(p))", "-D__hip_atomic_store(p,v,o,s)=(*(p)=(v))",
+             "-D__hip_atomic_fetch_add(p,v,o,s)=((*(p)+=(v))-(v))", "-include", os.path.join(HERE, "vectors.h"))
     return build.build(str(tmp_path_factory.mktemp("cpu_blocks")), flags)
 
 
