@@ -87,24 +87,32 @@ int check_packed(const int *cu_seqlens, int nseq, int batch, const float *init) 
 // What a pass needs beside its tensors: the words that its tiles exchange, all one after the
 // other, and the codes of a packed axis.
 struct RecScratch {
-    size_t maps, enter, ticket, end, token;
-    void take(Taker &k, const ssd::RecPlan &p, int packed_tokens) {
+    size_t maps, enter, ticket, end, rate, token;
+    void take(Taker &k, const ssd::RecPlan &p, int channels, int packed_tokens) {
         maps = k.take(2 * p.map_words);
         enter = k.take(2 * p.enter_words);
         ticket = k.take(p.tickets);
         end = k.o;
+        rate = k.take(p.tiles > 1 || packed_tokens ? channels : 0);
         token = k.take(packed_tokens);
     }
     void use(ssd::RecArgs &a, const ssd::RecPlan &p, char *base) const {
         a.blocks = p.blocks; a.waves = p.waves; a.tiles = p.tiles; a.keeps = p.keeps;
+        a.by_blocks = p.by_blocks; a.by_each = p.by_each;
         a.maps = reinterpret_cast<unsigned long long *>(base + maps);
         a.enter = reinterpret_cast<unsigned long long *>(base + enter);
         a.ticket = reinterpret_cast<unsigned *>(base + ticket);
+        a.rate = nullptr;
+        a.token = nullptr;
     }
+    // What a pass over one tile of each unit does without is left out.
     hipError_t prepare(ssd::RecArgs &a, const int *cu, int nseq, float *final, char *base, hipStream_t s) const {
+        if (a.tiles == 1 && !cu) return hipSuccess;
         int *t = reinterpret_cast<int *>(base + token);
+        float *r = reinterpret_cast<float *>(base + rate);
         a.token = cu ? t : nullptr;
-        return ssd::launch_rec_prepare(a, base + maps, end - maps, cu, nseq, t, final, s);
+        a.rate = a.decay ? r : nullptr;
+        return ssd::launch_rec_prepare(a, base + maps, end - maps, r, cu, nseq, t, final, s);
     }
 };
 
@@ -117,7 +125,7 @@ RecLayout recurrence_layout(int batch, int seqlen, int channels, bool packed, in
     RecLayout w{};
     w.plan = ssd::rec_fwd_plan(batch, seqlen, channels, dtype == SSD_BF16);
     Taker k;
-    w.scratch.take(k, w.plan, packed ? seqlen : 0);
+    w.scratch.take(k, w.plan, channels, packed ? seqlen : 0);
     w.total = k.o;
     return w;
 }
@@ -135,11 +143,11 @@ RecBwdLayout recurrence_bwd_layout(int batch, int seqlen, int channels, bool pac
     w.keep = ssd::rec_fwd_plan(batch, seqlen, channels, dtype == SSD_BF16);
     const size_t be = (size_t)batch * channels;
     Taker k;
-    w.scratch.take(k, w.plan, packed ? seqlen : 0);
+    w.scratch.take(k, w.plan, channels, packed ? seqlen : 0);
     w.part = k.take(be * w.plan.tiles);
     w.spare = k.take((long long)batch * w.plan.tiles > ssd::kColsumRows ? (size_t)ssd::kColsumChunks * channels : 0);
     if (!have_states) {
-        w.keep_scratch.take(k, w.keep, packed ? seqlen : 0);
+        w.keep_scratch.take(k, w.keep, channels, packed ? seqlen : 0);
         w.states = k.take(be * w.plan.keeps);
     }
     w.total = k.o;

@@ -24,7 +24,7 @@ namespace ssd {
 // The code of a token that no sequence of a packed axis holds: padding, which starts from a
 // zero state like a first token and gives zeros, whatever it holds.
 constexpr int kRecNone = -0x7fffffff;
-constexpr int kRecCols = 32;
+constexpr int kRecCols = 32, kRecWaves = 8;  // a workgroup's channels, and wavefronts at most
 
 // Two channels' values of one token.
 template <typename T> struct RecPair;
@@ -68,15 +68,18 @@ struct RecPlace {
     int wave, sub, col;           // strand `sub` of wavefront `wave`, lane `col` of the strand
     bool live;                    // a unit of the grid that there is
 };
+__device__ __forceinline__ int rec_quotient(int n, const RecDivisor &d) {
+    return static_cast<int>(static_cast<unsigned long long>(n) * d.mul >> d.shift);
+}
 // Every unit has as many workgroups as tiles. Units one after the other along the channels
 // go to the same XCD (workgroups are dealt to the eight XCDs in turn): they share
 // cache lines.
 __device__ __forceinline__ RecPlace rec_place(const RecArgs &a) {
     RecPlace p;
-    const int units = a.batch * a.blocks, each = (units + 7) >> 3;
-    p.unit = (blockIdx.x & 7) * each + (blockIdx.x >> 3) % each;
+    const int units = a.batch * a.blocks, each = (units + 7) >> 3, slot = blockIdx.x >> 3;
+    p.unit = (blockIdx.x & 7) * each + (slot - rec_quotient(slot, a.by_each) * each);
     p.live = p.unit < units;
-    p.batch = p.unit / a.blocks;
+    p.batch = rec_quotient(p.unit, a.by_blocks);
     p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     p.sub = (threadIdx.x >> 4) & 3;
     p.col = threadIdx.x & 15;
@@ -120,6 +123,12 @@ __device__ __forceinline__ void rec_store(char *base, uint32_t off, int nch, flo
 
 // -c softplus(decay) log2(e): what a channel's open gate decays by, in log2.
 __device__ __forceinline__ float rec_rate(float decay, float c) { return -c * softplus_f32(decay) * kLog2e; }
+// The lane's channels' (0 past the last one).
+__device__ __forceinline__ void rec_rates(float (&rate)[2], const RecArgs &a, const RecPlace &p) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        rate[e] = e < p.nch ? a.rate ? a.rate[p.ch + e] : rec_rate(a.decay[p.ch + e], a.c) : 0.0f;
+}
 
 // 1 - e^t for t <= 0, to a few roundings of itself: the series up to t^6 where 1 and
 // e^t cancel (the next term is below 2^-24 of the sum), else 1 - a^2 with the given
@@ -199,13 +208,13 @@ __device__ __forceinline__ void rec_wave(RecMap m, int sub, RecMap &before, RecM
 // kRecGroup tiles. Each value travels in a 64-bit word of its own with what says that it is
 // there, so nothing has to be ordered; before the pass all words are set to ~0.
 
-constexpr int kRecGroup = 16;  // the strands of four wavefronts, each of which waits for one tile
+constexpr int kRecGroup = 16;  // four tiles for each strand of a wavefront to wait for
 constexpr uint32_t kRecUnset = 0xffffffffu;
 
 struct RecShared {
     int tile;
-    float wave[16][16][4];                // the wavefronts' maps
-    float before[kRecGroup + 1][16][4];   // the maps of the group's tiles before, and its state
+    float map[kRecWaves][16][4];    // the wavefronts' maps
+    float state[kRecWaves][16][2];  // what enters them
 };
 
 // The workgroup's tile, in the order of starting.
@@ -221,84 +230,86 @@ __device__ __forceinline__ void rec_tell(unsigned long long *at, float value, ui
     __hip_atomic_store(at, static_cast<unsigned long long>(__float_as_uint(value)) << 32 | mark, __ATOMIC_RELAXED,
                        __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void rec_wait(const unsigned long long *at, float &value, uint32_t &mark) {
-    unsigned long long v;
-    while (static_cast<uint32_t>(v = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) == kRecUnset)
+__device__ __forceinline__ unsigned long long rec_look(const unsigned long long *at) {
+    return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// `v`: what rec_look has seen there.
+__device__ __forceinline__ RecMap rec_wait(const unsigned long long *at, unsigned long long v) {
+    while (static_cast<uint32_t>(v) == kRecUnset) {
         __builtin_amdgcn_s_sleep(1);
-    value = __uint_as_float(static_cast<uint32_t>(v >> 32));
-    mark = static_cast<uint32_t>(v);
+        v = rec_look(at);
+    }
+    return {__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32))};
 }
 
 // All lanes of the workgroup, with the maps of their wavefronts (the same in every strand)
-// and what enters the unit's first tile: what enters the lane's wavefront. `left`: what
-// leaves the tile. order: the tile's place in the order of the walk; REVERSE: the
-// last wavefront comes first.
+// and what enters the unit's first tile. Returns what enters the lane's wavefront, and
+// in wavefront 0 what leaves the tile. order: the tile's place in the order of the
+// walk; REVERSE: the last wavefront comes first. Wavefront 0 does it for all.
 template <bool PACKED, bool REVERSE>
 __device__ __forceinline__ void rec_enter(const RecArgs &a, const RecPlace &p, int order, const RecMap (&whole)[2],
                                           const float (&first)[2], float (&enters)[2], float (&left)[2], RecShared &sh) {
     if (p.sub == 0)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            sh.wave[p.wave][p.col][2 * e] = whole[e].a;
-            sh.wave[p.wave][p.col][2 * e + 1] = whole[e].h;
+            sh.map[p.wave][p.col][2 * e] = whole[e].a;
+            sh.map[p.wave][p.col][2 * e + 1] = whole[e].h;
         }
     __syncthreads();
-    RecMap pre[2], all[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
-    for (int k = 0; k < a.waves; ++k) {
-        const int w = REVERSE ? a.waves - 1 - k : k;
-        const float *v = sh.wave[w][p.col];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (w == p.wave) pre[e] = all[e];
-            all[e] = rec_then<PACKED>(all[e], {v[2 * e], v[2 * e + 1]});
-        }
-    }
-    float in[2] = {first[0], first[1]};
-    if (a.tiles > 1) {
-        const int place = order % kRecGroup, group = order / kRecGroup, strand = p.wave * 4 + p.sub;
+    if (p.wave == 0) {
+        left[0] = first[0];
+        left[1] = first[1];
+        const size_t words = (size_t)a.batch * a.blocks * kRecCols;  // of one tile of every unit
         const size_t unit = (size_t)p.unit * kRecCols + 2 * p.col;
-        const size_t tiles = (size_t)a.batch * a.blocks * kRecCols;  // words of one tile of every unit
-        if (strand == 0 && place < kRecGroup - 1)
+        const int place = order % kRecGroup, group = order / kRecGroup;
+        auto wave_map = [&](int k, int e) {
+            const float *v = sh.map[REVERSE ? a.waves - 1 - k : k][p.col];
+            return RecMap{v[2 * e], v[2 * e + 1]};
+        };
+        if (a.tiles > 1) {
+            if (p.sub == 0 && place < kRecGroup - 1 && order + 1 < a.tiles)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    RecMap all = wave_map(0, e);
+                    for (int k = 1; k < a.waves; ++k) all = rec_then<PACKED>(all, wave_map(k, e));
+                    // (any number but the mark of none; a decay that is not a number is one of its own)
+                    rec_tell(a.maps + order * words + unit + e, all.h, all.a != all.a ? 0x7fc00000u : __float_as_uint(all.a));
+                }
+            constexpr int N = kRecGroup / 4;
+            const unsigned long long *maps = a.maps + ((size_t)group * kRecGroup + p.sub * N) * words + unit;
+            const unsigned long long *enter = a.enter + group * words + unit;
+            unsigned long long seen[N][2], state[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                // (any number but the mark of none; a decay that is not a number is one of its own)
-                uint32_t mark = __float_as_uint(all[e].a);
-                if (all[e].a != all[e].a) mark = 0x7fc00000u;
-                rec_tell(a.maps + order * tiles + unit + e, all[e].h, mark);
+                if (group > 0) state[e] = rec_look(enter + e);
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (p.sub * N + k < place) seen[k][e] = rec_look(maps + k * words + e);
             }
-        if (strand < place || (strand == kRecGroup - 1 && group > 0)) {
-            const bool state = strand == kRecGroup - 1;
-            const unsigned long long *at = state ? a.enter + group * tiles + unit
-                                                 : a.maps + ((size_t)group * kRecGroup + strand) * tiles + unit;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float value;
-                uint32_t mark;
-                rec_wait(at + e, value, mark);
-                sh.before[strand][p.col][2 * e] = __uint_as_float(mark);
-                sh.before[strand][p.col][2 * e + 1] = value;
+                RecMap mine = {1.0f, 0.0f}, before, tiles;
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (p.sub * N + k < place) mine = rec_then<PACKED>(mine, rec_wait(maps + k * words + e, seen[k][e]));
+                if (place > 0) rec_wave<PACKED, false>(mine, p.sub, before, tiles);
+                if (group > 0) left[e] = rec_wait(enter + e, state[e]).h;
+                if (place > 0) left[e] = rec_apply<PACKED>(tiles, left[e]);
             }
         }
-        __syncthreads();
-        if (group > 0)
+        for (int k = 0; k < a.waves; ++k)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) in[e] = sh.before[kRecGroup - 1][p.col][2 * e + 1];
-        for (int k = 0; k < place; ++k)
+            for (int e = 0; e < 2; ++e) {
+                if (p.sub == 0) sh.state[REVERSE ? a.waves - 1 - k : k][p.col][e] = left[e];
+                left[e] = rec_apply<PACKED>(wave_map(k, e), left[e]);
+            }
+        if (p.sub == 0 && place == kRecGroup - 1 && order + 1 < a.tiles)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                in[e] = rec_apply<PACKED>({sh.before[k][p.col][2 * e], sh.before[k][p.col][2 * e + 1]}, in[e]);
+            for (int e = 0; e < 2; ++e) rec_tell(a.enter + (group + 1) * words + unit + e, left[e], 0);
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        left[e] = rec_apply<PACKED>(all[e], in[e]);
-        enters[e] = rec_apply<PACKED>(pre[e], in[e]);
-    }
-    if (a.tiles > 1 && p.wave == 0 && p.sub == 0 && order % kRecGroup == kRecGroup - 1 && order + 1 < a.tiles) {
-        const size_t tiles = (size_t)a.batch * a.blocks * kRecCols;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            rec_tell(a.enter + (order / kRecGroup + 1) * tiles + (size_t)p.unit * kRecCols + 2 * p.col + e, left[e], 0);
-    }
+    __syncthreads();
+    enters[0] = sh.state[p.wave][p.col][0];
+    enters[1] = sh.state[p.wave][p.col][1];
 }
 
 }  // namespace ssd

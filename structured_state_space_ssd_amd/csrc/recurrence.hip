@@ -15,16 +15,19 @@ namespace ssd {
 namespace {
 
 // Before a pass: the words that its tiles wait for are set to ~0 (`words` vectors of 16
-// bytes), and, for a packed axis, the tokens' codes are made: bit 0, the first of its
+// bytes), the channels' rates are made, and, for a packed axis, the tokens' codes: bit 0, the first of its
 // sequence; above, 1 + the number of the sequence whose last token it is; kRecNone: in no
 // sequence. `final`: set to the state of an empty sequence. Any contents of `cu` are read
 // within its nseq + 1 entries.
 __global__ __launch_bounds__(256) void rec_prepare_kernel(uint4 *__restrict__ unset, long long words,
                                                           const int *__restrict__ cu, int nseq, int L,
                                                           int *__restrict__ token, float *__restrict__ final,
-                                                          long long finals) {
+                                                          long long finals, const float *__restrict__ decay,
+                                                          float c, int E, float *__restrict__ rate) {
     const long long id = (long long)blockIdx.x * 256 + threadIdx.x, all = (long long)gridDim.x * 256;
     for (long long k = id; k < words; k += all) unset[k] = make_uint4(kRecUnset, kRecUnset, kRecUnset, kRecUnset);
+    if (decay)
+        for (long long k = id; k < E; k += all) rate[k] = rec_rate(decay[k], c);
     if (!cu) return;
     if (final)
         for (long long k = id; k < finals; k += all) final[k] = 0.0f;
@@ -42,10 +45,9 @@ __global__ __launch_bounds__(256) void rec_prepare_kernel(uint4 *__restrict__ un
 
 // Tokens of a strand: float32 operands of 8 do not fit the registers.
 template <typename T> constexpr int rec_fwd_strand() { return sizeof(T) == 2 ? 8 : 4; }
-constexpr int kRecFwdWaves = 4;
 
 template <typename T, bool GATED, bool PACKED>
-__global__ __launch_bounds__(kRecFwdWaves * 64) void rec_fwd_kernel(RecArgs a) {
+__global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
     constexpr int S = rec_fwd_strand<T>();
     __shared__ RecShared sh;
     const RecPlace p = rec_place(a);
@@ -65,13 +67,11 @@ __global__ __launch_bounds__(kRecFwdWaves * 64) void rec_fwd_kernel(RecArgs a) {
         if (PACKED)
 #pragma unroll
             for (int j = 0; j < S; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
-        float rate[2] = {0.0f, 0.0f}, h0[2] = {0.0f, 0.0f};
+        float rate[2], h0[2] = {0.0f, 0.0f};
+        if (GATED) rec_rates(rate, a, p);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            if (e < p.nch) {
-                if (GATED) rate[e] = rec_rate(a.decay[p.ch + e], a.c);
-                if (a.init) h0[e] = a.init[row0 + e];
-            }
+            if (a.init && e < p.nch) h0[e] = a.init[row0 + e];
         float av[S][2], uv[S][2];
         RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
 #pragma unroll
@@ -184,8 +184,13 @@ template <typename T, bool GATED> hipError_t step(const RecArgs &a, float *state
 
 }  // namespace
 
-// Wavefronts of a workgroup, and tiles, for strands of `strand` tokens. Several tiles take
-// four wavefronts at least: as many strands as a tile has others to wait for.
+static RecDivisor rec_divisor(int d) {  // of numbers below 2^28
+    int bits = 0;
+    while (1LL << bits < d) ++bits;
+    return {static_cast<uint32_t>(((1ULL << (28 + bits)) + d - 1) / d), 28 + bits};
+}
+
+// Wavefronts of a workgroup, and tiles, for strands of `strand` tokens.
 static RecPlan rec_plan(int batch, int seqlen, int channels, int strand) {
     RecPlan p;
     p.blocks = (channels + kRecCols - 1) / kRecCols;
@@ -198,6 +203,8 @@ static RecPlan rec_plan(int batch, int seqlen, int channels, int strand) {
     p.map_words = p.tiles > 1 ? words * p.tiles : 0;
     p.enter_words = p.tiles > 1 ? words * ((p.tiles + kRecGroup - 1) / kRecGroup) : 0;
     p.tickets = p.tiles > 1 ? units : 0;
+    p.by_blocks = rec_divisor(p.blocks);
+    p.by_each = rec_divisor(static_cast<int>((units + 7) / 8 < (1u << 28) ? (units + 7) / 8 : 1));
     return p;
 }
 RecPlan rec_fwd_plan(int batch, int seqlen, int channels, bool bf16) {
@@ -211,15 +218,13 @@ unsigned rec_grid(const RecArgs &a) {
     return static_cast<unsigned>(((long long)a.batch * a.blocks + 7) / 8 * 8 * a.tiles);
 }
 
-hipError_t launch_rec_prepare(const RecArgs &a, void *unset, size_t bytes, const int *cu, int nseq, int *token,
-                              float *final, hipStream_t stream) {
+hipError_t launch_rec_prepare(const RecArgs &a, void *unset, size_t bytes, float *rate, const int *cu, int nseq,
+                              int *token, float *final, hipStream_t stream) {
     const long long words = bytes / 16, finals = (long long)nseq * a.channels;
-    long long most = words > a.seqlen ? words : a.seqlen;
-    if (!cu) most = words;
-    if (most == 0) return hipSuccess;
+    const long long most = cu && a.seqlen > words ? a.seqlen : words;
     const unsigned want = static_cast<unsigned>(most / 256 + 1), grid = want < 2048 ? want : 2048;
     rec_prepare_kernel<<<grid, 256, 0, stream>>>(static_cast<uint4 *>(unset), words, cu, nseq, a.seqlen, token, final,
-                                                 finals);
+                                                 finals, a.decay, a.c, a.channels, rate);
     return hipGetLastError();
 }
 

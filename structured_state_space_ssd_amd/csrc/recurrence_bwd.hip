@@ -18,7 +18,7 @@ namespace ssd {
 namespace {
 
 template <typename T, bool GATED, bool PACKED>
-__global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b) {
+__global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b) {
     constexpr int S = kRecBwdStrand;
     __shared__ RecShared sh;
     const RecArgs &a = b.f;
@@ -48,13 +48,11 @@ __global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArg
 #pragma unroll
             for (int j = 0; j < S; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
         // q: what comes to the last token from behind
-        float rate[2] = {0.0f, 0.0f}, q[2] = {0.0f, 0.0f}, sum[2] = {0.0f, 0.0f};
+        float rate[2], q[2] = {0.0f, 0.0f}, sum[2] = {0.0f, 0.0f};
+        if (GATED) rec_rates(rate, a, p);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            if (e < p.nch) {
-                if (GATED) rate[e] = rec_rate(a.decay[p.ch + e], a.c);
-                if (!PACKED && b.dfinal) q[e] = b.dfinal[row0 + e];
-            }
+            if (!PACKED && b.dfinal && e < p.nch) q[e] = b.dfinal[row0 + e];
         float av[S][2], hv[S][2], gv[S][2];
         float rv[S][2], iv[S][2], bv[S][2];  // the gates, and sqrt(1 - a^2)
         RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mg[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
@@ -177,8 +175,8 @@ __global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArg
         }
         __syncthreads();
         if (p.sub == 0) {
-            sh.wave[p.wave][p.col][0] = sum[0];
-            sh.wave[p.wave][p.col][1] = sum[1];
+            sh.state[p.wave][p.col][0] = sum[0];
+            sh.state[p.wave][p.col][1] = sum[1];
         }
         __syncthreads();
         if (p.wave || p.sub) return;
@@ -186,7 +184,7 @@ __global__ __launch_bounds__(kRecBwdWaves * 64, 3) void rec_bwd_kernel(RecBwdArg
         for (int e = 0; e < 2; ++e)
             if (e < p.nch) {
                 float s = 0.0f;
-                for (int w = 0; w < a.waves; ++w) s += sh.wave[w][p.col][e];
+                for (int w = 0; w < a.waves; ++w) s += sh.state[w][p.col][e];
                 // sigmoid / softplus goes to 1 as both go to e^decay, and beyond what 32 bits hold of that
                 const float v = a.decay[p.ch + e], k = v < -20.0f ? 1.0f : sigmoid_f32(v) / softplus_f32(v);
                 b.part[((size_t)p.batch * a.tiles + tile) * E + p.ch + e] = k * s;

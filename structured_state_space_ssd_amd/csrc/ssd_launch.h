@@ -352,9 +352,13 @@ hipError_t launch_block_bwd(const BlockBwdArgs &a, bool bf16, bool stream_bf16, 
 // x, r, i, z [Bt][L][E] with strides in elements between sequences and tokens; channels dense.
 constexpr int kRecKeep = 16;      // tokens between the states that the backward starts from
 // The backward's tokens to a strand (a wavefront holds kRecKeep: its lanes hold a token's
-// every operand) and wavefronts to a workgroup at most.
-constexpr int kRecBwdStrand = 4, kRecBwdWaves = 4;
+// every operand).
+constexpr int kRecBwdStrand = 4;
 static_assert(4 * kRecBwdStrand == kRecKeep, "a wavefront starts from a state that is kept");
+struct RecDivisor {               // n / d = n mul >> shift for n below 2^28
+    uint32_t mul;
+    int shift;
+};
 struct RecArgs {
     const void *x, *r, *i, *z;    // z nullable; i NULL without decay
     size_t x_batch, x_token, r_batch, r_token, i_batch, i_token, z_batch, z_token;
@@ -364,6 +368,8 @@ struct RecArgs {
     const int *token;             // packed sequences: launch_rec_prepare's codes, else NULL
     int batch, seqlen, channels;
     int blocks, waves, tiles, keeps;  // the plan
+    RecDivisor by_blocks, by_each;    // each: units (batch x blocks) to an XCD
+    const float *rate;            // [E]: launch_rec_prepare's, or NULL: made where they are needed
     // Scratch, with several tiles, set to ~0 by launch_rec_prepare: the tiles' maps, the
     // states entering groups of them, and how many of a unit's tiles are taken.
     unsigned long long *maps, *enter;
@@ -375,14 +381,16 @@ struct RecArgs {
 struct RecPlan {
     int blocks, waves, tiles, keeps;
     size_t map_words, enter_words, tickets;
+    RecDivisor by_blocks, by_each;
 };
 RecPlan rec_fwd_plan(int batch, int seqlen, int channels, bool bf16);
 RecPlan rec_bwd_plan(int batch, int seqlen, int channels);
 unsigned rec_grid(const RecArgs &a);
-// Sets `bytes` at `unset` (multiples of 16) to ~0, makes the codes of a packed axis' tokens
-// (cu not NULL) and zeroes `final` ([nseq][E], nullable).
-hipError_t launch_rec_prepare(const RecArgs &a, void *unset, size_t bytes, const int *cu, int nseq, int *token,
-                              float *final, hipStream_t stream);
+// Sets `bytes` at `unset` (a multiple of 16) to ~0, makes the channels' rates (decay not
+// NULL) and the codes of a packed axis' tokens (cu not NULL) and zeroes `final` ([nseq][E],
+// nullable).
+hipError_t launch_rec_prepare(const RecArgs &a, void *unset, size_t bytes, float *rate, const int *cu, int nseq,
+                              int *token, float *final, hipStream_t stream);
 hipError_t launch_rec_fwd(const RecArgs &a, bool bf16, hipStream_t stream);
 // One token: the token strides and init are not read.
 hipError_t launch_rec_step(const RecArgs &a, float *state, bool bf16, hipStream_t stream);

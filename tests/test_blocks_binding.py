@@ -118,7 +118,7 @@ def test_recurrence_c_abi_backward_and_step(lib):
     # the states that the caller has not kept: one for every 16 tokens
     assert size(8, 64, 512, 0, 0, 1) - size(8, 64, 512, 0, 1, 1) == 8 * 4 * 512 * 4
     assert lib.ssd_recurrence_forward_workspace_size(1, 100, 8, 1, 1) - lib.ssd_recurrence_forward_workspace_size(
-        1, 100, 8, 0, 1) == 512  # a code for each token
+        1, 100, 8, 0, 1) == 512 + 256  # a code for each token, the rates
 
     def back(**kw):
         a = dict(x=FAKE, r=FAKE, i=FAKE, decay=FAKE, c=8.0, z=None, init=None, cu=None, nseq=0, states=None, dy=FAKE,
