@@ -24,7 +24,7 @@ namespace ssd {
 // The code of a token that no sequence of a packed axis holds: padding, which starts from a
 // zero state like a first token and gives zeros, whatever it holds.
 constexpr int kRecNone = -0x7fffffff;
-constexpr int kRecCols = 32, kRecWaves = 8;  // a workgroup's channels, and wavefronts at most
+constexpr int kRecCols = 32, kRecWaves = 4;  // a workgroup's channels, and wavefronts at most
 
 // Two channels' values of one token.
 template <typename T> struct RecPair;
@@ -89,19 +89,18 @@ __device__ __forceinline__ RecPlace rec_place(const RecArgs &a) {
 }
 
 // Byte offset of a lane's first token and channel (strides are below 2^24 elements).
-template <typename T, int S> __device__ __forceinline__ uint32_t rec_offset(uint32_t step, const RecPlace &p) {
-    return static_cast<uint32_t>(p.sub * S) * step + p.ch * static_cast<uint32_t>(sizeof(T));
+template <typename T, int S> __device__ __forceinline__ uint32_t rec_offset(size_t token, const RecPlace &p) {
+    return (static_cast<uint32_t>(p.sub * S) * static_cast<uint32_t>(token) + p.ch) * static_cast<uint32_t>(sizeof(T));
 }
-// A lane's tokens of one tensor, whose wavefront's first is element `at` (uniform).
-// WHOLE: every token and channel is there.
+// A lane's tokens of one tensor, whose wavefront's first is element `at`: uniform bases, one
+// offset. WHOLE: every token and channel is there.
 template <typename T, bool WHOLE, int S>
 __device__ __forceinline__ void rec_load(RecPair<T> (&r)[S], const void *t, size_t at, size_t token,
                                          const RecPlace &p, int nt) {
-    const char *base = static_cast<const char *>(t) + at * sizeof(T);
-    const uint32_t step = static_cast<uint32_t>(token * sizeof(T));
-    uint32_t off = rec_offset<T, S>(step, p);
+    const uint32_t off = rec_offset<T, S>(token, p);
 #pragma unroll
-    for (int j = 0; j < S; ++j, off += step) {
+    for (int j = 0; j < S; ++j) {
+        const char *base = static_cast<const char *>(t) + (at + j * token) * sizeof(T);
         if (WHOLE) r[j].load(base + off);
         else {
             r[j].zero();
@@ -112,7 +111,7 @@ __device__ __forceinline__ void rec_load(RecPair<T> (&r)[S], const void *t, size
         }
     }
 }
-// A token of a dense tensor, `base` as above and `off` its byte offset.
+// A token of a dense tensor: `base` uniform, `off` the lane's byte offset.
 template <typename T, bool WHOLE>
 __device__ __forceinline__ void rec_store(char *base, uint32_t off, int nch, float a, float b) {
     if (WHOLE || nch == 2) RecPair<T>::store(base + off, a, b);
@@ -130,16 +129,14 @@ __device__ __forceinline__ void rec_rates(float (&rate)[2], const RecArgs &a, co
         rate[e] = e < p.nch ? a.rate ? a.rate[p.ch + e] : rec_rate(a.decay[p.ch + e], a.c) : 0.0f;
 }
 
-// 1 - e^t for t <= 0, to a few roundings of itself: the series up to t^6 where 1 and
-// e^t cancel (the next term is below 2^-24 of the sum), else 1 - a^2 with the given
-// a = e^(t/2).
-__device__ __forceinline__ float one_minus_square(float t, float a) {
-    float s = fmaf(t, 1.0f / 720.0f, 1.0f / 120.0f);
-    s = fmaf(t, s, 1.0f / 24.0f);
-    s = fmaf(t, s, 1.0f / 6.0f);
-    s = fmaf(t, s, 0.5f);
-    s = fmaf(t, s, 1.0f);
-    return t > -0.25f ? -t * s : fmaf(-a, a, 1.0f);
+// 1 - a^2 for a = 2^l with l <= 0, to a few roundings of itself. Where 1 and a^2 cancel (a
+// above e^-0.25) it is -2 a sinh(log a): a l (c1 + c3 l^2 + c5 l^4) with c_n = -2 ln(2)^n / n!
+// (the next term is below 2^-24 of the sum).
+__device__ __forceinline__ float one_minus_square(float l, float a) {
+    const float l2 = l * l;
+    float s = fmaf(l2, -0.0026672267f, -0.11100822f);
+    s = fmaf(l2, s, -1.3862944f);
+    return l > -0.36067376f ? a * (l * s) : fmaf(-a, a, 1.0f);
 }
 
 constexpr float kLn2 = 0.6931471805599453f;

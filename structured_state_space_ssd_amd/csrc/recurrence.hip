@@ -82,7 +82,7 @@ __global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
                 if (GATED) {
                     const float la = rate[e] * sigmoid_f32(r[j].get(e));
                     d = __builtin_amdgcn_exp2f(la);
-                    u = __builtin_amdgcn_sqrtf(one_minus_square(2.0f * kLn2 * la, d)) *
+                    u = __builtin_amdgcn_sqrtf(one_minus_square(la, d)) *
                         sigmoid_f32(in[j].get(e)) * x[j].get(e);
                 } else {
                     d = __builtin_amdgcn_exp2f(kLog2e * r[j].get(e));
@@ -115,10 +115,9 @@ __global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
             if (p.nch > 1) s[1] = h[1];
         }
         char *y = static_cast<char *>(a.y) + ((size_t)p.batch * a.seqlen + tw) * E * sizeof(T);
-        const uint32_t step = static_cast<uint32_t>(E * sizeof(T));
-        uint32_t off = rec_offset<T, S>(step, p);
+        const uint32_t off = rec_offset<T, S>(E, p);
 #pragma unroll
-        for (int j = 0; j < S; ++j, off += step) {
+        for (int j = 0; j < S; ++j) {
             float o[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -127,7 +126,7 @@ __global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
                 if (a.z) o[e] *= silu_f32(z[j].get(e));
                 if (PACKED && code[j] < 0) o[e] = 0.0f;
             }
-            if (a.y && (WHOLE || j < nt)) rec_store<T, WHOLE>(y, off, p.nch, o[0], o[1]);
+            if (a.y && (WHOLE || j < nt)) rec_store<T, WHOLE>(y + (size_t)j * E * sizeof(T), off, p.nch, o[0], o[1]);
             if (PACKED && a.final_state && (WHOLE || j < nt) && code[j] > 1) {
                 float *f = a.final_state + (size_t)((code[j] >> 1) - 1) * E + p.ch;
                 if (p.nch > 0) f[0] = h[0];
@@ -161,7 +160,7 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs a, float *__restr
     for (int e = 0; e < V; ++e) {
         if (GATED) {
             const float la = rec_rate(d.get(e), a.c) * sigmoid_f32(r.get(e)), k = __builtin_amdgcn_exp2f(la);
-            h[e] = fmaf(k, s.get(e), __builtin_amdgcn_sqrtf(one_minus_square(2.0f * kLn2 * la, k)) *
+            h[e] = fmaf(k, s.get(e), __builtin_amdgcn_sqrtf(one_minus_square(la, k)) *
                                          sigmoid_f32(in.get(e)) * x.get(e));
         } else h[e] = fmaf(__builtin_amdgcn_exp2f(kLog2e * r.get(e)), s.get(e), x.get(e));
         o[e] = a.z ? h[e] * silu_f32(z.get(e)) : h[e];
@@ -190,12 +189,12 @@ static RecDivisor rec_divisor(int d) {  // of numbers below 2^28
     return {static_cast<uint32_t>(((1ULL << (28 + bits)) + d - 1) / d), 28 + bits};
 }
 
-// Wavefronts of a workgroup, and tiles, for strands of `strand` tokens.
-static RecPlan rec_plan(int batch, int seqlen, int channels, int strand) {
+// Wavefronts of a workgroup (at most `most`), and tiles, for strands of `strand` tokens.
+static RecPlan rec_plan(int batch, int seqlen, int channels, int strand, int most) {
     RecPlan p;
     p.blocks = (channels + kRecCols - 1) / kRecCols;
     const int wanted = (seqlen + 4 * strand - 1) / (4 * strand);  // wavefronts that have tokens
-    p.waves = 4;
+    p.waves = most;
     while (p.waves > 1 && p.waves / 2 >= wanted) p.waves /= 2;
     p.tiles = (wanted + p.waves - 1) / p.waves;
     p.keeps = (seqlen + kRecKeep - 1) / kRecKeep;
@@ -208,10 +207,14 @@ static RecPlan rec_plan(int batch, int seqlen, int channels, int strand) {
     return p;
 }
 RecPlan rec_fwd_plan(int batch, int seqlen, int channels, bool bf16) {
-    return rec_plan(batch, seqlen, channels, bf16 ? rec_fwd_strand<bf16_t>() : rec_fwd_strand<float>());
+    return rec_plan(batch, seqlen, channels, bf16 ? rec_fwd_strand<bf16_t>() : rec_fwd_strand<float>(), kRecWaves);
 }
+// Back, two wavefronts where there are many units (8 x 2048 tokens x 2560 channels, 640
+// units: 253 us with two, 265 with four), four where a tile has more others to wait for
+// (1 x 16384 tokens, 80 units, both ways: 394 and 374).
 RecPlan rec_bwd_plan(int batch, int seqlen, int channels) {
-    return rec_plan(batch, seqlen, channels, kRecBwdStrand);
+    const long long units = (long long)batch * ((channels + kRecCols - 1) / kRecCols);
+    return rec_plan(batch, seqlen, channels, kRecBwdStrand, units >= 256 ? 2 : kRecWaves);
 }
 
 unsigned rec_grid(const RecArgs &a) {

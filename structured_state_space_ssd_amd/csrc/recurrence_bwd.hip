@@ -1,11 +1,11 @@
 // Gradients of the gated recurrence (recurrence.hip). With g_t the gradient of h_t,
 //   g_t = dy_t silu(z_t) + a_{t+1} g_{t+1},  dinit = a_0 g_0,  dz = dy h silu'(z);
 // gated, with b = sqrt(1 - a^2), p = sigmoid(i) and w the gradient of log a times log a,
-//   dx = g b p,  di = g b p x (1 - p),  w = g log a (a h_{t-1} - p x a^2 / b),
+//   dx = g b p,  di = g u (1 - p),  w = g log a (a h_{t-1} - u a^2 / b^2),  u = b p x,
 //   dr = w (1 - sigmoid(r)),  ddecay = sum of w, times sigmoid(decay) / softplus(decay);
 // direct, dx = g and dr = g a h_{t-1}.
-// (log a / b goes to 0 with log a, so w does too, where the gradient of log a itself grows
-// without bound.)
+// (u log a / b^2 goes to 0 with log a, so w does too, where the gradient of log a itself
+// grows without bound.)
 //
 // A wavefront's 16 tokens find the state entering them in memory, where the forward
 // kept one every kRecKeep = 16 tokens (1/4 of a byte a channel and token), and make their
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
         for (int e = 0; e < 2; ++e)
             if (!PACKED && b.dfinal && e < p.nch) q[e] = b.dfinal[row0 + e];
         float av[S][2], hv[S][2], gv[S][2];
-        float rv[S][2], iv[S][2], bv[S][2];  // the gates, and sqrt(1 - a^2)
+        float rv[S][2], iv[S][2], bv[S][2], zv[S][2];  // the gates, and sqrt(1 - a^2)
         RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mg[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
 #pragma unroll
         for (int j = 0; j < S; ++j)
@@ -65,7 +65,7 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
                     rv[j][e] = sigmoid_f32(r[j].get(e));
                     const float la = rate[e] * rv[j][e];
                     d = __builtin_amdgcn_exp2f(la);
-                    bv[j][e] = __builtin_amdgcn_sqrtf(one_minus_square(2.0f * kLn2 * la, d));
+                    bv[j][e] = __builtin_amdgcn_sqrtf(one_minus_square(la, d));
                     iv[j][e] = sigmoid_f32(in[j].get(e));
                     u = bv[j][e] * iv[j][e] * x[j].get(e);
                 } else {
@@ -73,7 +73,10 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
                     u = x[j].get(e);
                 }
                 float g = dy[j].get(e);
-                if (a.z) g *= silu_f32(z[j].get(e));
+                if (a.z) {
+                    zv[j][e] = sigmoid_f32(z[j].get(e));
+                    g *= z[j].get(e) * zv[j][e];
+                }
                 if (!WHOLE && j >= nt) {
                     d = 1.0f;
                     u = g = 0.0f;
@@ -95,10 +98,10 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
             rec_wave<PACKED, false>(m[e], p.sub, before, whole);
             float h = rec_apply<PACKED>(before, hw[e]);
 #pragma unroll
-            for (int j = 0; j < S; ++j) {  // the state before each token, in its input's place
-                const float next = rec_apply<PACKED>({av[j][e], hv[j][e]}, h);
-                hv[j][e] = h;
-                h = next;
+            for (int j = 0; j < S; ++j) {  // what each token takes of the state before, in its input's place
+                const float carried = PACKED && av[j][e] < 0.0f ? 0.0f : av[j][e] * h;
+                h = carried + hv[j][e];
+                hv[j][e] = carried;
             }
         }
         // a token passes a (g + what comes to it) on to the one before, nothing from a first one
@@ -121,43 +124,41 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
             if (p.nch > 0) b.dinit[row0] = left[0];
             if (p.nch > 1) b.dinit[row0 + 1] = left[1];
         }
-        const uint32_t step = static_cast<uint32_t>(E * sizeof(T));
-        uint32_t off = rec_offset<T, S>(step, p) + (S - 1) * step;
+        const uint32_t off = rec_offset<T, S>(E, p);
 #pragma unroll
-        for (int j = S - 1; j >= 0; --j, off -= step) {
+        for (int j = S - 1; j >= 0; --j) {
             float ox[2], orr[2], oi[2], oz[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const bool first = PACKED && av[j][e] < 0.0f;
-                const float xv = x[j].get(e);
-                const float g = gv[j][e] + qs[e];
-                float d = av[j][e], u = xv;
+                const float xv = x[j].get(e), d = av[j][e], g = gv[j][e] + qs[e];
+                const float carried = hv[j][e];  // a h_{t-1}
+                float u = xv;
                 if (GATED) {
-                    const float sr = rv[j][e], la = rate[e] * sr * kLn2, si = iv[j][e], beta = bv[j][e];
-                    if (PACKED) d = __builtin_amdgcn_exp2f(rate[e] * sr);
-                    const float inv = beta > 0.0f ? __builtin_amdgcn_rcpf(beta) : 0.0f, gs = g * si;
+                    const float sr = rv[j][e], si = iv[j][e], beta = bv[j][e], la = rate[e] * sr * kLn2;
                     u = beta * si * xv;
-                    ox[e] = gs * beta;
-                    oi[e] = ox[e] * xv * (1.0f - si);
-                    // a^2 log a / b, the product that stays finite
-                    float w = -gs * xv * (d * d) * (la * inv);
-                    if (!first) w = fmaf(g * d * hv[j][e], la, w);
+                    ox[e] = g * (beta * si);
+                    oi[e] = g * u * (1.0f - si);
+                    // d sqrt(1 - a^2) / d log a = -a^2 / b, so p x times that is -u a^2 / b^2
+                    const float a2 = PACKED && first ? __builtin_amdgcn_exp2f(2.0f * rate[e] * sr) : d * d;
+                    const float q2 = beta > 0.0f ? a2 * __builtin_amdgcn_rcpf(beta * beta) : 0.0f;
+                    const float w = g * la * fmaf(-u, q2, carried);
                     orr[e] = w * (1.0f - sr);
                     if ((WHOLE || j < nt) && !(PACKED && code[j] < 0)) sum[e] += w;
                 } else {
                     ox[e] = g;
-                    orr[e] = first ? 0.0f : g * d * hv[j][e];
+                    orr[e] = g * carried;
                 }
-                if (a.z) {
-                    const float h = first ? u : fmaf(d, hv[j][e], u);
-                    oz[e] = dy[j].get(e) * h * silu_grad_f32(z[j].get(e));
+                if (a.z) {  // silu'(z) = p + z p (1 - p)
+                    const float pz = zv[j][e];
+                    oz[e] = dy[j].get(e) * (carried + u) * (pz * fmaf(z[j].get(e), 1.0f - pz, 1.0f));
                 }
                 qs[e] = first ? 0.0f : d * g;
             }
             if (!WHOLE && j >= nt) continue;
             if (PACKED && code[j] < 0) ox[0] = ox[1] = orr[0] = orr[1] = oi[0] = oi[1] = oz[0] = oz[1] = 0.0f;
             const auto out = [&](void *t, float (&v)[2]) {
-                rec_store<T, WHOLE>(static_cast<char *>(t) + at * sizeof(T), off, p.nch, v[0], v[1]);
+                rec_store<T, WHOLE>(static_cast<char *>(t) + (at + (size_t)j * E) * sizeof(T), off, p.nch, v[0], v[1]);
             };
             out(b.dx, ox);
             out(b.dr, orr);
