@@ -29,6 +29,11 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _like(x):
+    """A new dense tensor like x (the shorter way where x is dense: 0.4 us of a token's call)."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 # ---- gated linear recurrence ------------------------------------------------------
 
 def _recurrence_args(x, r, i, decay, z, ndim):
@@ -40,12 +45,21 @@ def _recurrence_args(x, r, i, decay, z, ndim):
     _int_sizes(*xs)
     if (i is None) != (decay is None):
         raise ValueError("i and decay go together: both, or neither where r is the log-decay")
-    pointers = (_slice(x, "x", xs, x), _slice(r, "r", xs, x), _slice(i, "i", xs, x),
-                _param(decay, "decay", xs[-1:], x), _slice(z, "z", xs, x))
-    strides = []  # (batch, token)
-    for t in (x, r, i, z):
-        s = (0, 0) if t is None else t.stride()
+    dtype, device = x.dtype, x.get_device()
+    pointers, strides = [], []  # strides: (batch, token)
+    for t, name in ((x, "x"), (r, "r"), (i, "i"), (z, "z")):
+        if t is None:
+            pointers.append(None)
+            strides += (0, 0)
+            continue
+        s = t.stride()
+        # one test where all is well: a token's call makes four of these
+        if t.shape == xs and t.dtype is dtype and s[-1] == 1 and t.get_device() == device:
+            pointers.append(t.data_ptr())
+        else:
+            pointers.append(_slice(t, name, xs, x))
         strides += (s[0], s[1] if ndim == 3 else 0)
+    pointers.insert(3, _param(decay, "decay", xs[-1:], x))
     return pointers, ctypes.byref(_native.SsdRecurrenceStrides(*strides))
 
 
@@ -81,7 +95,7 @@ def recurrence_forward(x, r, i=None, decay=None, z=None, init_state=None, c=8.0,
     cp, nseq = _recurrence_packed(cu_seqlens, x, init_state)
     _on_gpu(x)
     code = dtype_code(x.dtype)
-    y = x.new_empty((Bt, L, E))
+    y = _like(x)
     final = x.new_empty((nseq or Bt, E), dtype=_f32) if return_final_state else None
     states = x.new_empty((Bt, -(-L // KEEP), E), dtype=_f32) if return_states else None
     need = _native.lib.ssd_recurrence_forward_workspace_size(Bt, L, E, int(nseq > 0), code)
@@ -135,7 +149,7 @@ def recurrence_step(state, x, r, i=None, decay=None, z=None, c=8.0):
     Bt, E = x.shape
     sp = _param(state, "state", (Bt, E), x)
     _on_gpu(x)
-    y = x.new_empty((Bt, E))
+    y = _like(x)
     _call(_native.lib.ssd_recurrence_step, "ssd_recurrence_step", x.device, sp, *p[:4], c, p[4], Bt, E,
           dtype_code(x.dtype), y.data_ptr(), st)
     return y
@@ -175,7 +189,7 @@ def dropout(x, p, rng):
     rp = _random(p, (0, 0) if rng is None and not p else rng, x)
     _on_gpu(x)
     code = dtype_code(x.dtype)
-    y = x.new_empty(x.shape)
+    y = _like(x)
     _call(_native.lib.ssd_dropout, "ssd_dropout", x.device, x.data_ptr(), step, rows, x.shape[-1], rp, code,
           y.data_ptr())
     return y
@@ -229,8 +243,8 @@ def block_norm_forward(x, residual, weight=None, bias=None, post_weight=None, po
     random = _random(p, rng, x)
     _on_gpu(x)
     code = dtype_code(x.dtype)
-    total = x.new_empty(x.shape, dtype=residual.dtype)
-    y = None if weight is None else x.new_empty(x.shape)
+    total = torch.empty_like(residual)
+    y = None if weight is None else _like(x)
     stats = (None,) * 4
     if return_stats:
         new = lambda on: x.new_empty(x.shape[:-1], dtype=_f32) if on else None  # noqa: E731
@@ -276,9 +290,9 @@ def block_norm_backward(dy, dsum, x, total, stats, weight=None, bias=None, post_
     _on_gpu(x)
     code = dtype_code(x.dtype)
     like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
-    out = {"dx": x.new_empty(x.shape), "dresidual": x.new_empty(x.shape, dtype=total.dtype),
-           "dz": None if z is None else x.new_empty(x.shape), "dweight": like(weight), "dbias": like(bias),
-           "dpost_weight": like(post_weight), "dpost_bias": like(post_bias), "dscale": like(scale)}
+    out = {"dx": _like(x), "dresidual": torch.empty_like(total), "dz": None if z is None else _like(x),
+           "dweight": like(weight), "dbias": like(bias), "dpost_weight": like(post_weight),
+           "dpost_bias": like(post_bias), "dscale": like(scale)}
     need = _native.lib.ssd_block_norm_backward_workspace_size(rows, x.shape[-1], code)
     keep, ws, ws_bytes = _workspace(workspace, need, x)
     _call(_native.lib.ssd_block_norm_backward, "ssd_block_norm_backward", x.device, dyp, dsp, x.data_ptr(), step,

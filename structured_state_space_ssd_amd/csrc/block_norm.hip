@@ -26,9 +26,9 @@ namespace ssd {
 
 namespace {
 
-// Lanes of a workgroup at most, forward and backward: the backward's four sums per
-// column want registers.
-constexpr int kBlockFwdMost = 1024, kBlockBwdMost = 512;
+// Every kernel is there twice: for all options, and (FULL false) without biases and gate,
+// as models with root-mean-square norms have it, which leaves registers for more
+// wavefronts.
 
 // A column parameter's values at c .. c + V - 1; none given: `none`.
 template <int V>
@@ -52,8 +52,8 @@ __device__ __forceinline__ DropBits drop_bits(const DropState &rng, int c, long 
 }
 
 // T: type of x, z, y. R: type of the stream.
-template <typename T, typename R, int NV>
-__global__ __launch_bounds__(kBlockFwdMost, 4) void block_fwd_kernel(BlockArgs a, int lpr) {
+template <typename T, typename R, int NV, bool FULL>
+__global__ __launch_bounds__(1024, NV == 1 ? 6 : 5) void block_fwd_kernel(BlockArgs a, int lpr) {
     constexpr int V = vec_of<T>();
     __shared__ float buf[2][16];
     int turn = 0;  // sums take the two buffers in turn (row_sum)
@@ -62,13 +62,13 @@ __global__ __launch_bounds__(kBlockFwdMost, 4) void block_fwd_kernel(BlockArgs a
     const int D = a.width, step = (lpr ? lpr : (int)blockDim.x) * V;
     const float inv = 1.0f / static_cast<float>(D);
     const long long stride = (long long)gridDim.x * g.groups;
-    const T *x = static_cast<const T *>(a.x), *z = static_cast<const T *>(a.z);
+    const T *x = static_cast<const T *>(a.x), *z = FULL ? static_cast<const T *>(a.z) : nullptr;
     const R *res = static_cast<const R *>(a.residual);
     T *y = static_cast<T *>(a.y);
     R *sum = static_cast<R *>(a.sum);
     DropState rng{};
     if (a.drop.threshold) rng = drop_state(a.drop);
-    RowRaw<T, V> xr[NV], zr[NV];
+    RowRaw<T, V> xr[NV];
     RowRaw<R, V> rr[NV];
     auto fetch = [&](long long row) {
 #pragma unroll
@@ -77,8 +77,7 @@ __global__ __launch_bounds__(kBlockFwdMost, 4) void block_fwd_kernel(BlockArgs a
             xr[i].zero();
             if (row < a.rows && n > 0) {
                 xr[i].load(x + row * a.x_stride + c, n);
-                rr[i].load(res + row * D + c, n);
-                if (z) zr[i].load(z + row * a.z_stride + c, n);
+                if (!FULL) rr[i].load(res + row * D + c, n);
             }
         }
     };
@@ -111,20 +110,23 @@ __global__ __launch_bounds__(kBlockFwdMost, 4) void block_fwd_kernel(BlockArgs a
         return 1.0f / sqrtf(q[0] * inv + a.eps);
     };
     long long row = (long long)blockIdx.x * g.groups + g.group;
-    constexpr bool AHEAD = NV == 1;
+    constexpr bool AHEAD = NV == 1 && !(FULL && sizeof(R) > sizeof(T));
     if (AHEAD) fetch(row);
     for (; row < a.rows; row += stride) {
         if (!AHEAD) fetch(row);
         float u[NV][V], s[NV][V];
         RowRaw<T, V> zk[NV];
+        RowRaw<R, V> rk[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                u[i][e] = xr[i].get(e);
-                s[i][e] = rr[i].get(e);
+            for (int e = 0; e < V; ++e) u[i][e] = xr[i].get(e);
+            if (!FULL) rk[i] = rr[i];
+            const int c = g.lane * V + i * step, n = D - c;
+            if (FULL && n > 0) {  // all options leave no registers to fetch these a row ahead
+                rk[i].load(res + row * D + c, n);
+                if (z) zk[i].load(z + row * a.z_stride + c, n);
             }
-            zk[i] = zr[i];
         }
         if (AHEAD) fetch(row + stride);
         if (a.post_weight) {
@@ -140,7 +142,7 @@ __global__ __launch_bounds__(kBlockFwdMost, 4) void block_fwd_kernel(BlockArgs a
                 if (n <= 0) continue;
                 float w[V], b[V];
                 col_load(w, a.post_weight, c, n, 0.0f);
-                col_load(b, a.post_bias, c, n, 0.0f);
+                col_load(b, FULL ? a.post_bias : nullptr, c, n, 0.0f);
 #pragma unroll
                 for (int e = 0; e < V; ++e) u[i][e] = u[i][e] * r * w[e] + b[e];
             }
@@ -170,7 +172,7 @@ __global__ __launch_bounds__(kBlockFwdMost, 4) void block_fwd_kernel(BlockArgs a
             }
 #pragma unroll
             for (int e = 0; e < V; ++e)  // the next norm reads the stream as it is kept
-                s[i][e] = to_f32(from_f32<R>(fmaf(a.beta, u[i][e], a.alpha * s[i][e])));
+                s[i][e] = to_f32(from_f32<R>(fmaf(a.beta, u[i][e], a.alpha * rk[i].get(e))));
             row_store(sum + row * D + c, s[i], n);
 #pragma unroll
             for (int e = 0; e < V; ++e)
@@ -189,7 +191,7 @@ __global__ __launch_bounds__(kBlockFwdMost, 4) void block_fwd_kernel(BlockArgs a
             if (n <= 0) continue;
             float w[V], b[V];
             col_load(w, a.weight, c, n, 0.0f);
-            col_load(b, a.bias, c, n, 0.0f);
+            col_load(b, FULL ? a.bias : nullptr, c, n, 0.0f);
 #pragma unroll
             for (int e = 0; e < V; ++e) w[e] = s[i][e] * r * w[e] + b[e];
             row_store(y + row * D + c, w, n);
@@ -197,24 +199,47 @@ __global__ __launch_bounds__(kBlockFwdMost, 4) void block_fwd_kernel(BlockArgs a
     }
 }
 
-// Each workgroup (or, for short rows, each group of lanes) keeps its columns' four
-// sums in registers over its rows and writes them once at its end, those that are
-// wanted: part[workgroup][dw2, db2, P, Q][D]. block_sum_kernel adds them up in a fixed
-// order.
-template <typename T, typename R, int NV>
-__global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kernel(BlockBwdArgs a, int lpr) {
+// A row's lanes in the backward: `lpr` <= 64 of one wavefront (a power of two), or `waves`
+// whole wavefronts, of which a workgroup has several sets where that packs better.
+// The sums of K values over a row's lanes, in every one of them; buf as in row_sum.
+template <int K>
+__device__ __forceinline__ void set_sum(float (&v)[K], const BlockSets &s, int set, float (*buf)[K]) {
+    lane_sum(v, s.lpr ? s.lpr : 64);
+    if (s.lpr || blockDim.x == 64) return;
+    if (lane_id() == 0)
+#pragma unroll
+        for (int k = 0; k < K; ++k) buf[wave_id()][k] = v[k];
+    __syncthreads();
+    const int w = lane_id() & 15;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = w < s.waves ? buf[set * s.waves + w][k] : 0.0f;
+    lane_sum(v, 16);
+}
+
+// Lanes of a workgroup at most: with 12 wavefronts to a CU (all options) or 16.
+template <typename T, int NV, bool FULL> constexpr int block_bwd_lanes() {
+    return FULL && sizeof(T) == 2 ? (NV == 1 ? 768 : 512) : NV == 4 ? 512 : FULL && NV == 2 ? 768 : 1024;
+}
+
+// Each set of lanes (for short rows, each workgroup) keeps its columns' four sums in
+// registers over its rows and writes them once at its end, those that are wanted:
+// part[set][dw2, db2, P, Q][D]. block_sum_kernel adds them up in a fixed order.
+template <typename T, typename R, int NV, bool FULL>
+__global__ __launch_bounds__((block_bwd_lanes<T, NV, FULL>()), (block_bwd_lanes<T, NV, FULL>() / 256))
+void block_bwd_kernel(BlockBwdArgs a, BlockSets sets) {
     constexpr int V = vec_of<T>();
     constexpr bool AHEAD = NV == 1;  // wider rows leave no registers for the next one
-    __shared__ float buf[2][32];
+    __shared__ float buf[2][16][2];
     __shared__ float acc[NV == 1 ? kShortWaves * V * 64 : 1];
-    if (NV > 1) lpr = 0;  // only whole workgroups hold more than a vector per lane
-    const RowGroup g = row_group(lpr);
+    if (NV > 1) sets.lpr = 0;  // only whole wavefronts hold more than a vector per lane
+    const int lpr = sets.lpr, width = lpr ? lpr : 64 * sets.waves;
+    const int set = threadIdx.x / width, lane = threadIdx.x - set * width;
     const int D = a.width;
-    int step = (lpr ? lpr : (int)blockDim.x) * V;
+    int step = width * V;
     const float inv = 1.0f / static_cast<float>(D);
-    const long long stride = (long long)gridDim.x * g.groups;
+    const long long stride = (long long)gridDim.x * sets.sets;
     const T *dy = static_cast<const T *>(a.dy), *x = static_cast<const T *>(a.x);
-    const T *z = static_cast<const T *>(a.z);
+    const T *z = FULL ? static_cast<const T *>(a.z) : nullptr;
     const R *dsum = static_cast<const R *>(a.dsum), *sum = static_cast<const R *>(a.sum);
     DropState rng{};
     if (a.drop.threshold) rng = drop_state(a.drop);
@@ -245,7 +270,7 @@ __global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kern
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = g.lane * V + i * step, n = D - c;
+            const int c = lane * V + i * step, n = D - c;
             if (n <= 0) continue;
             if (a.weight) {
                 yn[i].load(dy + row * D + c, n);
@@ -255,10 +280,13 @@ __global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kern
             if (z) zn[i].load(z + row * a.z_stride + c, n);
         }
     };
-    long long row = (long long)blockIdx.x * g.groups + g.group;
     int turn = 0;  // sums take the two buffers in turn (row_sum)
-    if (AHEAD) fetch(row);
-    for (; row < a.rows; row += stride) {
+    // (the sets of a workgroup go round together: the last rows may be there for some)
+    long long row0 = (long long)blockIdx.x * sets.sets;
+    if (AHEAD) fetch(row0 + set);
+    for (; row0 < a.rows; row0 += stride) {
+        const long long row = row0 + set;
+        const bool live = row < a.rows;
         if (!AHEAD) {
             asm volatile("" : "+s"(step));  // the offsets anew each row: kept, they spill
             fetch(row);
@@ -272,11 +300,12 @@ __global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kern
             xr[i] = xn[i];
             zr[i] = zn[i];
             sr[i] = sn[i];
-            const int c = g.lane * V + i * step, n = D - c;
+            const int c = lane * V + i * step, n = D - c;
             dr[i].zero();
-            if (dsum && n > 0) dr[i].load(dsum + row * D + c, n);
+            if (dsum && n > 0 && live) dr[i].load(dsum + row * D + c, n);
         }
         if (AHEAD) fetch(row + stride);
+        if (lpr && !live) continue;
         float ds[NV][V];
         if (!a.weight) {
 #pragma unroll
@@ -289,25 +318,25 @@ __global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kern
             auto normal = [&](int i, int e, int n) { return e < n ? (sr[i].get(e) - m2) * r2 : 0.0f; };
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = g.lane * V + i * step, n = D - c;
+                const int c = lane * V + i * step, n = D - c;
                 if (n <= 0) continue;
                 float w[V];
                 col_load(w, a.weight, c, n, 0.0f);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float d = yr[i].get(e), nn = normal(i, e, n), t = d * w[e];
-                    dw[i][e] += d * nn;
-                    db[i][e] += d;
+                    if (live) dw[i][e] += d * nn;
+                    if (FULL && live) db[i][e] += d;
                     s[0] += t;
                     s[1] += t * nn;
                 }
             }
-            row_sum(s, lpr, buf[turn]);
+            set_sum(s, sets, set, buf[turn]);
             turn ^= 1;
             const float c0 = a.mean ? s[0] * inv : 0.0f, c1 = s[1] * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = g.lane * V + i * step, n = D - c;
+                const int c = lane * V + i * step, n = D - c;
                 if (n <= 0) continue;
                 float w[V];
                 col_load(w, a.weight, c, n, 0.0f);
@@ -321,7 +350,7 @@ __global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kern
         auto inner = [&](int i, int e, int n) { return e < n ? (xr[i].get(e) - m1) * r1 : 0.0f; };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = g.lane * V + i * step, n = D - c;
+            const int c = lane * V + i * step, n = D - c;
             if (n <= 0) continue;
             float o[V];
 #pragma unroll
@@ -329,7 +358,7 @@ __global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kern
                 o[e] = a.alpha * ds[i][e];
                 ds[i][e] *= a.beta;
             }
-            row_store(static_cast<R *>(a.dresidual) + row * D + c, o, n);
+            if (live) row_store(static_cast<R *>(a.dresidual) + row * D + c, o, n);
             if (a.drop.threshold) {
                 const DropBits bits = drop_bits<V>(rng, c, row);
 #pragma unroll
@@ -341,20 +370,20 @@ __global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kern
             col_load(w, a.post_weight, c, n, 1.0f);
             if (z) {
                 float b[V];
-                col_load(b, a.post_bias, c, n, 0.0f);
+                col_load(b, FULL ? a.post_bias : nullptr, c, n, 0.0f);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float zv = zr[i].get(e);
                     o[e] = ds[i][e] * (inner(i, e, n) * w[e] + b[e]) * k[e] * silu_grad_f32(zv);
                     ds[i][e] *= silu_f32(zv);
                 }
-                row_store(static_cast<T *>(a.dz) + row * D + c, o, n);
+                if (live) row_store(static_cast<T *>(a.dz) + row * D + c, o, n);
             }
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float nn = inner(i, e, n);
-                sp[i][e] += ds[i][e] * nn;
-                sq[i][e] += ds[i][e];
+                if (live) sp[i][e] += ds[i][e] * nn;
+                if (FULL && live) sq[i][e] += ds[i][e];
                 ds[i][e] *= k[e] * w[e];
                 if (e < n) s[0] += ds[i][e];
                 s[1] += ds[i][e] * nn;
@@ -362,24 +391,23 @@ __global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kern
         }
         float c0 = 0.0f, c1 = 0.0f;
         if (a.post_weight) {
-            row_sum(s, lpr, buf[turn]);
+            set_sum(s, sets, set, buf[turn]);
             turn ^= 1;
             c0 = a.post_mean ? s[0] * inv : 0.0f;
             c1 = s[1] * inv;
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = g.lane * V + i * step, n = D - c;
+            const int c = lane * V + i * step, n = D - c;
             if (n <= 0) continue;
             float o[V];
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 o[e] = a.post_weight ? r1 * (ds[i][e] - c0 - inner(i, e, n) * c1) : ds[i][e];
-            row_store(static_cast<T *>(a.dx) + row * D + c, o, n);
+            if (live) row_store(static_cast<T *>(a.dx) + row * D + c, o, n);
         }
     }
-    // [workgroup][the wanted of dw2, db2, P, Q][D]
-    float *p = a.part + (size_t)blockIdx.x * a.sums * D;
+    float *p = a.part + ((size_t)blockIdx.x * (lpr ? 1 : sets.sets) + (lpr ? 0 : set)) * a.sums * D;
     auto put = [&](float (&v)[NV][V]) {
         if (NV == 1 && lpr) {  // short rows: the groups of a wavefront meet, then the wavefronts
             const int w = wave_id(), l = lane_id();
@@ -398,114 +426,179 @@ __global__ __launch_bounds__(kBlockBwdMost, NV == 1 ? 3 : 2) void block_bwd_kern
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = g.lane * V + i * step, n = D - c;
+            const int c = lane * V + i * step, n = D - c;
             if (n > 0 && (!lpr || threadIdx.x < (unsigned)lpr)) row_store(p + c, v[i], n);
         }
         p += D;
     };
     if (a.dweight) put(dw);
-    if (a.dbias) put(db);
+    if (FULL && a.dbias) put(db);
     if (a.want_p) put(sp);
-    if (a.want_q) put(sq);
+    if (FULL && a.want_q) put(sq);
 }
 
-// Adds up the partial rows, 32 strands of them to a column, and makes the parameters'
-// gradients of the sums: blockIdx.y 0 the norm before's, 1 what lies after the block.
-__global__ __launch_bounds__(1024) void block_sum_kernel(BlockBwdArgs a, int rows) {
-    __shared__ float buf[32][32];
-    const int col = threadIdx.x & 31, strand = threadIdx.x >> 5, D = a.width;
-    const int c = blockIdx.x * 32 + col;
-    const bool first = blockIdx.y == 0;
-    auto total = [&](int which) {  // of partial row `which` of every workgroup
-        float s = 0.0f;
-        if (c < D)
-#pragma unroll 4
-            for (int k = strand; k < rows; k += 32) s += a.part[((size_t)k * a.sums + which) * D + c];
-        __syncthreads();
-        buf[strand][col] = s;
-        __syncthreads();
-        s = 0.0f;
-        if (strand == 0)
+// Adds up the partial rows, 1024 / COLS strands of them to a column, and makes the
+// parameters' gradients of the sums: blockIdx.y 0 the norm before's, 1 what lies after the
+// block. 16 columns to a workgroup where there are many rows (768 of 2 x 2560 columns: 7.9
+// us, with 32 columns 11.4), else 32 (256 of 4 x 5120: 10.3 and 8.3).
+template <int COLS> __global__ __launch_bounds__(1024) void block_sum_kernel(BlockBwdArgs a, int rows) {
+    constexpr int STRANDS = 1024 / COLS;
+    __shared__ float buf[2][16][COLS];
+    const int col = threadIdx.x % COLS, strand = threadIdx.x / COLS, D = a.width;
+    const int c = blockIdx.x * COLS + col;
+    const bool before = blockIdx.y == 0;
+    const int pre = (a.dweight != nullptr) + (a.dbias != nullptr);
+    const bool one = before ? a.dweight != nullptr : a.want_p, two = before ? a.dbias != nullptr : a.want_q;
+    const float *part = a.part + (size_t)(before ? 0 : pre) * D + c;
+    float s[2] = {0.0f, 0.0f};
+    if (c < D)
+#pragma unroll 8
+        for (int k = strand; k < rows; k += STRANDS) {
+            const float *p = part + (size_t)k * a.sums * D;
+            if (one) s[0] += p[0];
+            if (two) s[1] += p[one ? D : 0];
+        }
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s += buf[k][col];
-        return s;
-    };
-    const bool out = strand == 0 && c < D;
-    const int before = (a.dweight != nullptr) + (a.dbias != nullptr);
-    if (first) {
-        int k = 0;
-        if (a.dweight) {
-            const float s = total(k++);
-            if (out) a.dweight[c] = s;
+    for (int k = 0; k < 2; ++k) {  // the strands of a wavefront, then the wavefronts
+        if (COLS == 16) {
+            const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(s[k]), __float_as_uint(s[k]), false, false);
+            s[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
         }
-        if (a.dbias) {
-            const float s = total(k++);
-            if (out) a.dbias[c] = s;
-        }
+        const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(s[k]), __float_as_uint(s[k]), false, false);
+        s[k] = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+    }
+    if (lane_id() < COLS) {
+        buf[0][wave_id()][col] = s[0];
+        buf[1][wave_id()][col] = s[1];
+    }
+    __syncthreads();
+    if (strand || c >= D) return;
+    s[0] = s[1] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        s[0] += buf[0][k][col];
+        s[1] += buf[1][k][col];
+    }
+    if (before) {
+        if (one) a.dweight[c] = s[0];
+        if (two) a.dbias[c] = s[1];
         return;
     }
-    const float p = a.want_p ? total(before) : 0.0f, q = a.want_q ? total(before + a.want_p) : 0.0f;
-    if (!out) return;
     const float g = a.scale ? a.scale[c] : 1.0f;
-    if (a.dpost_weight) a.dpost_weight[c] = g * p;
-    if (a.dpost_bias) a.dpost_bias[c] = g * q;
+    if (a.dpost_weight) a.dpost_weight[c] = g * s[0];
+    if (a.dpost_bias) a.dpost_bias[c] = g * s[1];
     if (a.dscale)
-        a.dscale[c] = a.post_weight ? a.post_weight[c] * p + (a.post_bias ? a.post_bias[c] * q : 0.0f) : p;
+        a.dscale[c] = a.post_weight ? a.post_weight[c] * s[0] + (a.post_bias ? a.post_bias[c] * s[1] : 0.0f) : s[0];
 }
 
-constexpr int kBlockFwdLanes = 1024, kBlockBwdLanes = 768;
-
-// Workgroups: as many as run at once, but no more than there are rows for.
-int block_blocks(long long rows, const NormShape &s, int lanes) {
-    const long long want = (rows + s.groups - 1) / s.groups;
-    const int resident = 256 * (lanes / s.threads > 1 ? lanes / s.threads : 1);
+// Workgroups: as many as run at once, but no more than there are rows for. A SIMD holds
+// `waves` wavefronts, and a workgroup's start on the first one.
+int block_blocks(long long rows, int sets, int threads, int waves) {
+    const long long want = (rows + sets - 1) / sets;
+    const int first = (threads / 64 + 3) / 4, resident = 256 * (waves / first > 1 ? waves / first : 1);
     return static_cast<int>(want < resident ? want : resident);
 }
 
-template <typename T, typename R> hipError_t block_fwd(const BlockArgs &a, hipStream_t stream) {
-    const NormShape s = norm_shape(a.width, vec_of<T>(), kBlockFwdMost);
-    const int grid = block_blocks(a.rows, s, kBlockFwdLanes);
+template <typename T, typename R, bool FULL> hipError_t block_fwd(const BlockArgs &a, hipStream_t stream) {
+    const NormShape s = norm_shape(a.width, vec_of<T>(), 1024);
+    const int grid = block_blocks(a.rows, s.groups, s.threads, s.nv == 1 ? 6 : 5);
     if (s.nv == 1) {
-        block_fwd_kernel<T, R, 1><<<grid, s.threads, 0, stream>>>(a, s.lpr);
+        block_fwd_kernel<T, R, 1, FULL><<<grid, s.threads, 0, stream>>>(a, s.lpr);
         return hipGetLastError();
     }
     if constexpr (sizeof(T) == 4)  // 8192 float32 values are two vectors of 4 for 1024 lanes
         if (s.nv == 2) {
-            block_fwd_kernel<T, R, 2><<<grid, s.threads, 0, stream>>>(a, s.lpr);
+            block_fwd_kernel<T, R, 2, FULL><<<grid, s.threads, 0, stream>>>(a, s.lpr);
             return hipGetLastError();
         }
     return hipErrorInvalidValue;
 }
 
-template <typename T, typename R> hipError_t block_bwd(const BlockBwdArgs &a, hipStream_t stream) {
-    const NormShape s = norm_shape(a.width, vec_of<T>(), kBlockBwdMost);
-    const int grid = block_blocks(a.rows, s, kBlockBwdLanes);
-    constexpr int WIDEST = kMaxBlockWidth / kBlockBwdMost / vec_of<T>();  // 2, float32 4
-    if (s.nv == 1) block_bwd_kernel<T, R, 1><<<grid, s.threads, 0, stream>>>(a, s.lpr);
-    else if (s.nv == 2) block_bwd_kernel<T, R, 2><<<grid, s.threads, 0, stream>>>(a, s.lpr);
-    else if (s.nv == WIDEST) block_bwd_kernel<T, R, WIDEST><<<grid, s.threads, 0, stream>>>(a, s.lpr);
-    else return hipErrorInvalidValue;
+// The backward's lanes for rows of D: vectors to a lane, sets of lanes to a workgroup.
+struct BlockBwdShape {
+    int nv, threads, lanes;  // lanes: of a CU
+    BlockSets sets;
+};
+template <typename T, bool FULL> BlockBwdShape block_bwd_shape(int D) {
+    const int nvec = (D + vec_of<T>() - 1) / vec_of<T>();
+    BlockBwdShape s;
+    s.sets.lpr = 0;
+    s.nv = 1;
+    s.lanes = FULL && sizeof(T) == 2 ? 768 : 1024;
+    if (nvec <= 64) {
+        s.sets.lpr = 1;
+        while (s.sets.lpr < nvec) s.sets.lpr <<= 1;
+        s.threads = 64 * kShortWaves;
+        s.sets.waves = 1;
+        s.sets.sets = s.threads / s.sets.lpr;
+        return s;
+    }
+    if (nvec > block_bwd_lanes<T, 1, FULL>()) {
+        s.nv = 2;
+        s.lanes = block_bwd_lanes<T, 2, FULL>();
+    }
+    if (sizeof(T) == 4 && nvec > 2 * s.lanes) {
+        s.nv = 4;
+        s.lanes = block_bwd_lanes<T, 4, FULL>();
+    }
+    const int w = ((nvec + s.nv - 1) / s.nv + 63) / 64;
+    s.sets.waves = w;
+    // Wavefronts of a workgroup start on the first SIMD: unless they fill all four alike, the
+    // first one is full before the others. So sets that do not are put together, as many as
+    // the CU holds (16384 rows of 2560, five wavefronts each: 284 us one by one).
+    s.sets.sets = w % 4 == 0 || w < 3 || s.lanes / (64 * w) < 1 ? 1 : s.lanes / (64 * w);
+    s.threads = 64 * w * s.sets.sets;
+    return s;
+}
+int block_bwd_rows(const BlockBwdShape &s, int grid) { return s.sets.lpr ? grid : grid * s.sets.sets; }
+
+template <typename T, typename R, bool FULL> hipError_t block_bwd(const BlockBwdArgs &a, hipStream_t stream) {
+    const BlockBwdShape s = block_bwd_shape<T, FULL>(a.width);
+    const int grid = block_blocks(a.rows, s.sets.sets, s.threads, s.lanes / 256);
+    if (s.nv == 1) block_bwd_kernel<T, R, 1, FULL><<<grid, s.threads, 0, stream>>>(a, s.sets);
+    else if (s.nv == 2) {
+        if constexpr (sizeof(T) == 4 || FULL) block_bwd_kernel<T, R, 2, FULL><<<grid, s.threads, 0, stream>>>(a, s.sets);
+        else return hipErrorInvalidValue;  // 8192 values are one vector of 8 for 1024 lanes
+    } else {
+        if constexpr (sizeof(T) == 4 && FULL) block_bwd_kernel<T, R, 4, FULL><<<grid, s.threads, 0, stream>>>(a, s.sets);
+        else return hipErrorInvalidValue;
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.sums == 0) return e;
-    block_sum_kernel<<<dim3((a.width + 31) / 32, a.want_p || a.want_q ? 2 : 1), 1024, 0, stream>>>(a, grid);
+    const int rows = block_bwd_rows(s, grid), per = rows > 512 ? 16 : 32;
+    const dim3 sums((a.width + per - 1) / per, a.want_p || a.want_q ? 2 : 1);
+    if (per == 16) block_sum_kernel<16><<<sums, 1024, 0, stream>>>(a, rows);
+    else block_sum_kernel<32><<<sums, 1024, 0, stream>>>(a, rows);
     return hipGetLastError();
+}
+
+template <typename T, bool FULL> size_t block_part_rows(long long rows, int width) {
+    const BlockBwdShape s = block_bwd_shape<T, FULL>(width);
+    return block_bwd_rows(s, block_blocks(rows, s.sets.sets, s.threads, s.lanes / 256));
 }
 
 }  // namespace
 
-size_t block_bwd_part_bytes(long long rows, int width, bool bf16, int sums) {
-    const NormShape s = norm_shape(width, bf16 ? 8 : 4, kBlockBwdMost);
-    return (size_t)block_blocks(rows, s, kBlockBwdLanes) * sums * width * sizeof(float);
+size_t block_bwd_part_bytes(long long rows, int width, bool bf16, bool full, int sums) {
+    const size_t n = bf16 ? full ? block_part_rows<bf16_t, true>(rows, width) : block_part_rows<bf16_t, false>(rows, width)
+                          : full ? block_part_rows<float, true>(rows, width) : block_part_rows<float, false>(rows, width);
+    return n * sums * width * sizeof(float);
 }
 
 hipError_t launch_block_fwd(const BlockArgs &a, bool bf16, bool stream_bf16, hipStream_t stream) {
-    if (!bf16) return block_fwd<float, float>(a, stream);
-    return stream_bf16 ? block_fwd<bf16_t, bf16_t>(a, stream) : block_fwd<bf16_t, float>(a, stream);
+    const bool full = a.z || a.bias || a.post_bias;
+    if (!bf16) return full ? block_fwd<float, float, true>(a, stream) : block_fwd<float, float, false>(a, stream);
+    if (stream_bf16)
+        return full ? block_fwd<bf16_t, bf16_t, true>(a, stream) : block_fwd<bf16_t, bf16_t, false>(a, stream);
+    return full ? block_fwd<bf16_t, float, true>(a, stream) : block_fwd<bf16_t, float, false>(a, stream);
 }
 
 hipError_t launch_block_bwd(const BlockBwdArgs &a, bool bf16, bool stream_bf16, hipStream_t stream) {
-    if (!bf16) return block_bwd<float, float>(a, stream);
-    return stream_bf16 ? block_bwd<bf16_t, bf16_t>(a, stream) : block_bwd<bf16_t, float>(a, stream);
+    const bool full = block_bwd_full(a);
+    if (!bf16) return full ? block_bwd<float, float, true>(a, stream) : block_bwd<float, float, false>(a, stream);
+    if (stream_bf16)
+        return full ? block_bwd<bf16_t, bf16_t, true>(a, stream) : block_bwd<bf16_t, bf16_t, false>(a, stream);
+    return full ? block_bwd<bf16_t, float, true>(a, stream) : block_bwd<bf16_t, float, false>(a, stream);
 }
 
 }  // namespace ssd

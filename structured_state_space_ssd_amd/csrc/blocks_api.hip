@@ -347,7 +347,9 @@ int ssd_block_norm_forward(const void *x, long long x_row_stride, const void *re
 
 size_t ssd_block_norm_backward_workspace_size(long long rows, int width, int dtype) {
     if (rows < 1 || rows > kMaxRows || width < 1 || width > ssd::kMaxBlockWidth || !valid_dtype(dtype)) return 0;
-    return ssd::block_bwd_part_bytes(rows, width, dtype == SSD_BF16, 4);
+    const size_t full = ssd::block_bwd_part_bytes(rows, width, dtype == SSD_BF16, true, 4);
+    const size_t lean = ssd::block_bwd_part_bytes(rows, width, dtype == SSD_BF16, false, 2);
+    return full > lean ? full : lean;
 }
 
 int ssd_block_norm_backward(const void *dy, const void *dsum, const void *x, long long x_row_stride,
@@ -371,9 +373,6 @@ int ssd_block_norm_backward(const void *dy, const void *dsum, const void *x, lon
     rc = drop_args(a.drop, random);
     if (rc != SSD_OK) return rc;
     a.sums = block_sums(dweight, dbias, dpost_weight, dpost_bias, dscale, block->post_bias, &a.want_p, &a.want_q);
-    rc = check_workspace(workspace, workspace_bytes,
-                         ssd::block_bwd_part_bytes(rows, width, dtype == SSD_BF16, a.sums));
-    if (rc != SSD_OK) return rc;
     a.dy = dy; a.dsum = dsum; a.x = x; a.sum = sum; a.z = z;
     a.x_stride = static_cast<size_t>(x_row_stride);
     a.z_stride = static_cast<size_t>(z_row_stride);
@@ -389,6 +388,9 @@ int ssd_block_norm_backward(const void *dy, const void *dsum, const void *x, lon
     a.dweight = dweight; a.dbias = dbias;
     a.dpost_weight = dpost_weight; a.dpost_bias = dpost_bias; a.dscale = dscale;
     a.part = static_cast<float *>(workspace);
+    rc = check_workspace(workspace, workspace_bytes,
+                         ssd::block_bwd_part_bytes(rows, width, dtype == SSD_BF16, ssd::block_bwd_full(a), a.sums));
+    if (rc != SSD_OK) return rc;
     return status_of(ssd::launch_block_bwd(a, dtype == SSD_BF16, stream_dtype == SSD_BF16,
                                            static_cast<hipStream_t>(stream)));
 }

@@ -345,7 +345,14 @@ struct BlockBwdArgs {
     int want_p, want_q, sums;  // the sums behind the last three; how many sums there are in all
     float *part;               // block_bwd_part_bytes of scratch
 };
-size_t block_bwd_part_bytes(long long rows, int width, bool bf16, int sums);
+// Whether the backward's kernels for all options are needed, or those without biases and gate.
+inline bool block_bwd_full(const BlockBwdArgs &a) {
+    return a.z || a.post_bias || a.dbias || a.dpost_bias;
+}
+struct BlockSets {
+    int lpr, waves, sets;  // lanes of a row within a wavefront, or its wavefronts; rows at once
+};
+size_t block_bwd_part_bytes(long long rows, int width, bool bf16, bool full, int sums);
 hipError_t launch_block_bwd(const BlockBwdArgs &a, bool bf16, bool stream_bf16, hipStream_t stream);
 
 // ---- gated recurrence (recurrence.hip, recurrence_bwd.hip)

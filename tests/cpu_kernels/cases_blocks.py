@@ -173,9 +173,9 @@ def run_dropout():
 # ---- block norm -----------------------------------------------------------------------------
 
 # every lane count of short rows, one, two and four vectors to a lane of long ones, rows past
-# the groups of a workgroup
-BLOCK = [(1, 1), (3, 7), (300, 8), (70, 16), (65, 40), (9, 250), (5, 511), (3, 513), (2, 2000), (2, 4097), (1, 8191),
-         (1, 8192)]
+# the groups of a workgroup, and some of the last round of several rows to a workgroup
+BLOCK = [(1, 1), (3, 7), (300, 8), (70, 16), (65, 40), (9, 250), (5, 511), (3, 513), (7, 1300), (2, 2000), (4, 2563),
+         (2, 4097), (1, 5200), (1, 6200), (1, 8191), (1, 8192)]
 
 
 def block(rows, D, dtype, stream, rms, post, pre, bias, scale, gate, p, pad, skip):

@@ -31,8 +31,8 @@ def make(rows, D, dtype, stream, post, pre, bias, scale, gate, pad, seed=0):
 
 # widths below, at and past a vector, a wavefront's vectors, the lanes of a workgroup with one, two and
 # four vectors, odd ones, the largest; rows around those of a workgroup and past the grid's
-SIZES = [(1, 1), (3, 2), (5, 7), (300, 8), (17, 9), (70, 16), (9, 100), (33, 255), (4, 257), (6, 511), (3, 513), (7, 1000),
-         (2, 2049), (2, 4095), (3, 4097), (5, 5119), (2, 8191), (2, 8192), (2000, 24), (1500, 1000)]
+SIZES = [(1, 1), (3, 2), (5, 7), (300, 8), (17, 9), (70, 16), (9, 100), (33, 255), (4, 257), (6, 511), (3, 513), (7, 1000), (5, 1300),
+         (2, 2049), (4, 2560), (3, 3001), (2, 4095), (3, 4097), (5, 5119), (2, 8191), (2, 6145), (2, 8192), (2000, 24), (1500, 1000), (1601, 2560)]
 # T, stream, rms, post, pre, bias, scale, gate, p, dsum
 KINDS = [(BF, F32, True, 1, 1, 0, 1, 0, 0.1, 1), (BF, BF, False, 1, 1, 1, 0, 1, 0.0, 1), (F32, F32, False, 1, 1, 1, 1, 1, 0.5, 0),
          (BF, F32, False, 0, 1, 0, 1, 1, 0.0, 1), (F32, F32, True, 1, 0, 1, 0, 0, 0.25, 1), (BF, BF, True, 0, 1, 1, 0, 0, 0.9, 0)]
