@@ -37,6 +37,8 @@ template <> struct RecPair<bf16_t> {
     __device__ __forceinline__ float get(int e) const {
         return __uint_as_float(e ? (w & 0xffff0000u) : (w << 16));
     }
+    // as a value that the compiler has not seen
+    __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(w)); }
     static __device__ __forceinline__ void store(char *p, float a, float b) {
         *reinterpret_cast<u32_any *>(p) = pack_bf16(a, b);
     }
@@ -56,6 +58,12 @@ template <> struct RecPair<float> {
         w[1] = 0.0f;
     }
     __device__ __forceinline__ float get(int e) const { return w[e]; }
+    __device__ __forceinline__ void fresh() {
+        float u = w[0], v = w[1];
+        asm volatile("" : "+v"(u));
+        asm volatile("" : "+v"(v));
+        w[0] = u; w[1] = v;
+    }
     static __device__ __forceinline__ void store(char *p, float a, float b) {
         *reinterpret_cast<f32x2_any *>(p) = f32x2_any{a, b};
     }
@@ -205,20 +213,21 @@ __device__ __forceinline__ void rec_wave(RecMap m, int sub, RecMap &before, RecM
 // kRecGroup tiles. Each value travels in a 64-bit word of its own with what says that it is
 // there, so nothing has to be ordered; before the pass all words are set to ~0.
 
-constexpr int kRecGroup = 16;  // four tiles for each strand of a wavefront to wait for
+constexpr int kRecGroup = 16, kRecAtOnce = 2;  // tiles that a lane looks at together
 constexpr uint32_t kRecUnset = 0xffffffffu;
 
 struct RecShared {
     int tile;
-    float map[kRecWaves][16][4];    // the wavefronts' maps
-    float state[kRecWaves][16][2];  // what enters them
+    float map[kRecWaves][kRecCols][2];                     // the wavefronts' maps, by channel
+    float before[kRecGroup / kRecAtOnce][kRecCols][2];     // those of the tiles before
+    float state[kRecCols];                                 // what enters the group
 };
 
 // The workgroup's tile, in the order of starting.
 __device__ __forceinline__ int rec_ticket(const RecArgs &a, const RecPlace &p, RecShared &sh) {
     if (a.tiles == 1) return 0;
     if (threadIdx.x == 0)
-        sh.tile = static_cast<int>(__hip_atomic_fetch_add(a.ticket + p.unit, 1u, __ATOMIC_RELAXED,
+        sh.tile = static_cast<int>(__hip_atomic_fetch_add(a.ticket + (size_t)p.unit * kRecTicketStep, 1u, __ATOMIC_RELAXED,
                                                           __HIP_MEMORY_SCOPE_AGENT) + 1u);
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(sh.tile);
@@ -240,73 +249,68 @@ __device__ __forceinline__ RecMap rec_wait(const unsigned long long *at, unsigne
 }
 
 // All lanes of the workgroup, with the maps of their wavefronts (the same in every strand)
-// and what enters the unit's first tile. Returns what enters the lane's wavefront, and
-// in wavefront 0 what leaves the tile. order: the tile's place in the order of the
-// walk; REVERSE: the last wavefront comes first. Wavefront 0 does it for all.
+// and what enters the unit's first tile: what enters the lane's wavefront. `left`: what
+// leaves the tile. REVERSE: the last wavefront comes first. order: the tile's place in the
+// order of the walk. For the wait a lane is a channel, and half a wavefront looks at
+// kRecAtOnce tiles.
 template <bool PACKED, bool REVERSE>
 __device__ __forceinline__ void rec_enter(const RecArgs &a, const RecPlace &p, int order, const RecMap (&whole)[2],
                                           const float (&first)[2], float (&enters)[2], float (&left)[2], RecShared &sh) {
     if (p.sub == 0)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            sh.map[p.wave][p.col][2 * e] = whole[e].a;
-            sh.map[p.wave][p.col][2 * e + 1] = whole[e].h;
+            sh.map[p.wave][2 * p.col + e][0] = whole[e].a;
+            sh.map[p.wave][2 * p.col + e][1] = whole[e].h;
         }
     __syncthreads();
-    if (p.wave == 0) {
-        left[0] = first[0];
-        left[1] = first[1];
-        const size_t words = (size_t)a.batch * a.blocks * kRecCols;  // of one tile of every unit
-        const size_t unit = (size_t)p.unit * kRecCols + 2 * p.col;
-        const int place = order % kRecGroup, group = order / kRecGroup;
-        auto wave_map = [&](int k, int e) {
-            const float *v = sh.map[REVERSE ? a.waves - 1 - k : k][p.col];
-            return RecMap{v[2 * e], v[2 * e + 1]};
-        };
-        if (a.tiles > 1) {
-            if (p.sub == 0 && place < kRecGroup - 1 && order + 1 < a.tiles)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    RecMap all = wave_map(0, e);
-                    for (int k = 1; k < a.waves; ++k) all = rec_then<PACKED>(all, wave_map(k, e));
-                    // (any number but the mark of none; a decay that is not a number is one of its own)
-                    rec_tell(a.maps + order * words + unit + e, all.h, all.a != all.a ? 0x7fc00000u : __float_as_uint(all.a));
-                }
-            constexpr int N = kRecGroup / 4;
-            const unsigned long long *maps = a.maps + ((size_t)group * kRecGroup + p.sub * N) * words + unit;
-            const unsigned long long *enter = a.enter + group * words + unit;
-            unsigned long long seen[N][2], state[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (group > 0) state[e] = rec_look(enter + e);
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (p.sub * N + k < place) seen[k][e] = rec_look(maps + k * words + e);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                RecMap mine = {1.0f, 0.0f}, before, tiles;
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (p.sub * N + k < place) mine = rec_then<PACKED>(mine, rec_wait(maps + k * words + e, seen[k][e]));
-                if (place > 0) rec_wave<PACKED, false>(mine, p.sub, before, tiles);
-                if (group > 0) left[e] = rec_wait(enter + e, state[e]).h;
-                if (place > 0) left[e] = rec_apply<PACKED>(tiles, left[e]);
-            }
+    auto wave_map = [&](int k, int c) {
+        const float *v = sh.map[REVERSE ? a.waves - 1 - k : k][c];
+        return RecMap{v[0], v[1]};
+    };
+    const int place = order % kRecGroup, group = order / kRecGroup;
+    const size_t words = (size_t)a.batch * a.blocks * kRecCols;  // of one tile of every unit
+    if (a.tiles > 1) {
+        const int c = threadIdx.x & (kRecCols - 1), part = threadIdx.x / kRecCols, parts = 2 * a.waves;
+        const size_t at = (size_t)p.unit * kRecCols + c;
+        if (part == 0 && place < kRecGroup - 1 && order + 1 < a.tiles) {
+            RecMap all = wave_map(0, c);
+            for (int k = 1; k < a.waves; ++k) all = rec_then<PACKED>(all, wave_map(k, c));
+            // (any number but the mark of none; a decay that is not a number is one of its own)
+            rec_tell(a.maps + order * words + at, all.h, all.a != all.a ? 0x7fc00000u : __float_as_uint(all.a));
         }
-        for (int k = 0; k < a.waves; ++k)
+        for (int q = part; q * kRecAtOnce < place; q += parts) {
+            const int n = place - q * kRecAtOnce;
+            const unsigned long long *maps = a.maps + ((size_t)group * kRecGroup + q * kRecAtOnce) * words + at;
+            unsigned long long seen[kRecAtOnce];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (p.sub == 0) sh.state[REVERSE ? a.waves - 1 - k : k][p.col][e] = left[e];
-                left[e] = rec_apply<PACKED>(wave_map(k, e), left[e]);
-            }
-        if (p.sub == 0 && place == kRecGroup - 1 && order + 1 < a.tiles)
+            for (int k = 0; k < kRecAtOnce; ++k)
+                if (k < n) seen[k] = rec_look(maps + k * words);
+            RecMap tiles = {1.0f, 0.0f};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) rec_tell(a.enter + (group + 1) * words + unit + e, left[e], 0);
+            for (int k = 0; k < kRecAtOnce; ++k)
+                if (k < n) tiles = rec_then<PACKED>(tiles, rec_wait(maps + k * words, seen[k]));
+            sh.before[q][c][0] = tiles.a;
+            sh.before[q][c][1] = tiles.h;
+        }
+        if (group > 0 && part == parts - 1) {
+            const unsigned long long *enter = a.enter + group * words + at;
+            sh.state[c] = rec_wait(enter, rec_look(enter)).h;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    enters[0] = sh.state[p.wave][p.col][0];
-    enters[1] = sh.state[p.wave][p.col][1];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int c = 2 * p.col + e;
+        float in = group > 0 ? sh.state[c] : first[e];
+        for (int q = 0; q * kRecAtOnce < place; ++q) in = rec_apply<PACKED>({sh.before[q][c][0], sh.before[q][c][1]}, in);
+        for (int k = 0; k < a.waves; ++k) {
+            if ((REVERSE ? a.waves - 1 - k : k) == p.wave) enters[e] = in;
+            in = rec_apply<PACKED>(wave_map(k, c), in);
+        }
+        left[e] = in;
+        if (p.wave == 0 && p.sub == 0 && place == kRecGroup - 1 && order + 1 < a.tiles)
+            rec_tell(a.enter + (group + 1) * words + (size_t)p.unit * kRecCols + c, in, 0);
+    }
 }
 
 }  // namespace ssd

@@ -189,32 +189,28 @@ static RecDivisor rec_divisor(int d) {  // of numbers below 2^28
     return {static_cast<uint32_t>(((1ULL << (28 + bits)) + d - 1) / d), 28 + bits};
 }
 
-// Wavefronts of a workgroup (at most `most`), and tiles, for strands of `strand` tokens.
-static RecPlan rec_plan(int batch, int seqlen, int channels, int strand, int most) {
+// Wavefronts of a workgroup, and tiles, for strands of `strand` tokens.
+static RecPlan rec_plan(int batch, int seqlen, int channels, int strand) {
     RecPlan p;
     p.blocks = (channels + kRecCols - 1) / kRecCols;
     const int wanted = (seqlen + 4 * strand - 1) / (4 * strand);  // wavefronts that have tokens
-    p.waves = most;
+    p.waves = kRecWaves;
     while (p.waves > 1 && p.waves / 2 >= wanted) p.waves /= 2;
     p.tiles = (wanted + p.waves - 1) / p.waves;
     p.keeps = (seqlen + kRecKeep - 1) / kRecKeep;
     const size_t units = (size_t)batch * p.blocks, words = units * kRecCols;
     p.map_words = p.tiles > 1 ? words * p.tiles : 0;
     p.enter_words = p.tiles > 1 ? words * ((p.tiles + kRecGroup - 1) / kRecGroup) : 0;
-    p.tickets = p.tiles > 1 ? units : 0;
+    p.tickets = p.tiles > 1 ? units * kRecTicketStep : 0;
     p.by_blocks = rec_divisor(p.blocks);
     p.by_each = rec_divisor(static_cast<int>((units + 7) / 8 < (1u << 28) ? (units + 7) / 8 : 1));
     return p;
 }
 RecPlan rec_fwd_plan(int batch, int seqlen, int channels, bool bf16) {
-    return rec_plan(batch, seqlen, channels, bf16 ? rec_fwd_strand<bf16_t>() : rec_fwd_strand<float>(), kRecWaves);
+    return rec_plan(batch, seqlen, channels, bf16 ? rec_fwd_strand<bf16_t>() : rec_fwd_strand<float>());
 }
-// Back, two wavefronts where there are many units (8 x 2048 tokens x 2560 channels, 640
-// units: 253 us with two, 265 with four), four where a tile has more others to wait for
-// (1 x 16384 tokens, 80 units, both ways: 394 and 374).
 RecPlan rec_bwd_plan(int batch, int seqlen, int channels) {
-    const long long units = (long long)batch * ((channels + kRecCols - 1) / kRecCols);
-    return rec_plan(batch, seqlen, channels, kRecBwdStrand, units >= 256 ? 2 : kRecWaves);
+    return rec_plan(batch, seqlen, channels, kRecBwdStrand);
 }
 
 unsigned rec_grid(const RecArgs &a) {

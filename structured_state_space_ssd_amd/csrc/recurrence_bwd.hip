@@ -18,7 +18,7 @@ namespace ssd {
 namespace {
 
 template <typename T, bool GATED, bool PACKED>
-__global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b) {
+__global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bwd_kernel(RecBwdArgs b) {
     constexpr int S = kRecBwdStrand;
     __shared__ RecShared sh;
     const RecArgs &a = b.f;
@@ -53,8 +53,8 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
 #pragma unroll
         for (int e = 0; e < 2; ++e)
             if (!PACKED && b.dfinal && e < p.nch) q[e] = b.dfinal[row0 + e];
-        float av[S][2], hv[S][2], gv[S][2];
-        float rv[S][2], iv[S][2], bv[S][2], zv[S][2];  // the gates, and sqrt(1 - a^2)
+        float av[S][2], hv[S][2];
+        float rv[S][2], iv[S][2], bv[S][2];  // the gates, and sqrt(1 - a^2)
         RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mg[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
 #pragma unroll
         for (int j = 0; j < S; ++j)
@@ -72,24 +72,16 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
                     d = __builtin_amdgcn_exp2f(kLog2e * r[j].get(e));
                     u = x[j].get(e);
                 }
-                float g = dy[j].get(e);
-                if (a.z) {
-                    zv[j][e] = sigmoid_f32(z[j].get(e));
-                    g *= z[j].get(e) * zv[j][e];
-                }
                 if (!WHOLE && j >= nt) {
                     d = 1.0f;
-                    u = g = 0.0f;
+                    u = 0.0f;
                 }
                 if (PACKED) {
                     if (code[j] & 1) d = -1.0f;
-                    if (code[j] < 0) u = g = 0.0f;
-                    if (b.dfinal && code[j] > 1 && e < p.nch)
-                        g += b.dfinal[(size_t)((code[j] >> 1) - 1) * E + p.ch + e];
+                    if (code[j] < 0) u = 0.0f;
                 }
                 av[j][e] = d;
                 hv[j][e] = u;
-                gv[j][e] = g;
                 m[e] = rec_then<PACKED>(m[e], {d, u});
             }
 #pragma unroll
@@ -104,6 +96,15 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
                 hv[j][e] = carried;
             }
         }
+        // what reaches a token's state by its output (made twice: kept, it takes registers)
+        auto own = [&](int j, int e) {
+            float g = dy[j].get(e);
+            if (a.z) g *= silu_f32(z[j].get(e));
+            if ((!WHOLE && j >= nt) || (PACKED && code[j] < 0)) g = 0.0f;
+            if (PACKED && b.dfinal && code[j] > 1 && e < p.nch)
+                g += b.dfinal[(size_t)((code[j] >> 1) - 1) * E + p.ch + e];
+            return g;
+        };
         // a token passes a (g + what comes to it) on to the one before, nothing from a first one
 #pragma unroll
         for (int j = S - 1; j >= 0; --j)
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
             for (int e = 0; e < 2; ++e) {
                 const bool first = PACKED && av[j][e] < 0.0f;
                 mg[e] = {first || (PACKED && mg[e].a < 0.0f) ? -1.0f : av[j][e] * mg[e].a,
-                         first ? 0.0f : av[j][e] * (gv[j][e] + mg[e].h)};
+                         first ? 0.0f : av[j][e] * (own(j, e) + mg[e].h)};
             }
         RecMap after[2], whole[2];
 #pragma unroll
@@ -124,6 +125,12 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
             if (p.nch > 0) b.dinit[row0] = left[0];
             if (p.nch > 1) b.dinit[row0 + 1] = left[1];
         }
+        // (the values anew: what the compiler keeps of them from above fills the registers)
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+            dy[j].fresh();
+            z[j].fresh();
+        }
         const uint32_t off = rec_offset<T, S>(E, p);
 #pragma unroll
         for (int j = S - 1; j >= 0; --j) {
@@ -131,7 +138,7 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const bool first = PACKED && av[j][e] < 0.0f;
-                const float xv = x[j].get(e), d = av[j][e], g = gv[j][e] + qs[e];
+                const float xv = x[j].get(e), d = av[j][e], g = own(j, e) + qs[e];
                 const float carried = hv[j][e];  // a h_{t-1}
                 float u = xv;
                 if (GATED) {
@@ -149,10 +156,7 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
                     ox[e] = g;
                     orr[e] = g * carried;
                 }
-                if (a.z) {  // silu'(z) = p + z p (1 - p)
-                    const float pz = zv[j][e];
-                    oz[e] = dy[j].get(e) * (carried + u) * (pz * fmaf(z[j].get(e), 1.0f - pz, 1.0f));
-                }
+                if (a.z) oz[e] = dy[j].get(e) * (carried + u) * silu_grad_f32(z[j].get(e));
                 qs[e] = first ? 0.0f : d * g;
             }
             if (!WHOLE && j >= nt) continue;
@@ -176,8 +180,8 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
         }
         __syncthreads();
         if (p.sub == 0) {
-            sh.state[p.wave][p.col][0] = sum[0];
-            sh.state[p.wave][p.col][1] = sum[1];
+            sh.map[p.wave][2 * p.col][0] = sum[0];
+            sh.map[p.wave][2 * p.col + 1][0] = sum[1];
         }
         __syncthreads();
         if (p.wave || p.sub) return;
@@ -185,7 +189,7 @@ __global__ __launch_bounds__(kRecWaves * 64, 3) void rec_bwd_kernel(RecBwdArgs b
         for (int e = 0; e < 2; ++e)
             if (e < p.nch) {
                 float s = 0.0f;
-                for (int w = 0; w < a.waves; ++w) s += sh.state[w][p.col][e];
+                for (int w = 0; w < a.waves; ++w) s += sh.map[w][2 * p.col + e][0];
                 // sigmoid / softplus goes to 1 as both go to e^decay, and beyond what 32 bits hold of that
                 const float v = a.decay[p.ch + e], k = v < -20.0f ? 1.0f : sigmoid_f32(v) / softplus_f32(v);
                 b.part[((size_t)p.batch * a.tiles + tile) * E + p.ch + e] = k * s;

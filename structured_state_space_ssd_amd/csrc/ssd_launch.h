@@ -362,6 +362,7 @@ constexpr int kRecKeep = 16;      // tokens between the states that the backward
 // every operand).
 constexpr int kRecBwdStrand = 4;
 static_assert(4 * kRecBwdStrand == kRecKeep, "a wavefront starts from a state that is kept");
+constexpr int kRecTicketStep = 32;
 struct RecDivisor {               // n / d = n mul >> shift for n below 2^28
     uint32_t mul;
     int shift;
@@ -378,7 +379,8 @@ struct RecArgs {
     RecDivisor by_blocks, by_each;    // each: units (batch x blocks) to an XCD
     const float *rate;            // [E]: launch_rec_prepare's, or NULL: made where they are needed
     // Scratch, with several tiles, set to ~0 by launch_rec_prepare: the tiles' maps, the
-    // states entering groups of them, and how many of a unit's tiles are taken.
+    // states entering groups of them, and how many of a unit's tiles are taken (each count
+    // in a cache line of its own).
     unsigned long long *maps, *enter;
     unsigned *ticket;
     void *y;                      // [Bt][L][E] dense (NULL: states only)
