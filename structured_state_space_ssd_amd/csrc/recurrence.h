@@ -96,6 +96,16 @@ __device__ __forceinline__ RecPlace rec_place(const RecArgs &a) {
     return p;
 }
 
+// Whether any of n tokens of a packed axis is a first or last one of a sequence, or in none:
+// of most tiles none is, and they go without the selections (1 x 16384 tokens x 2560
+// channels in 55 sequences, with them everywhere: 112 us forward and 245 back).
+__device__ __forceinline__ bool rec_cuts(const int *token, int n) {
+    float v[1] = {0.0f};
+    for (int k = lane_id(); k < n; k += 64) v[0] += token[k] != 0 ? 1.0f : 0.0f;
+    lane_sum(v, 64);
+    return __builtin_amdgcn_readfirstlane(__float_as_int(v[0])) != 0;
+}
+
 // Byte offset of a lane's first token and channel (strides are below 2^24 elements).
 template <typename T, int S> __device__ __forceinline__ uint32_t rec_offset(size_t token, const RecPlace &p) {
     return (static_cast<uint32_t>(p.sub * S) * static_cast<uint32_t>(token) + p.ch) * static_cast<uint32_t>(sizeof(T));
@@ -192,9 +202,8 @@ __device__ __forceinline__ void rec_wave(RecMap m, int sub, RecMap &before, RecM
     const bool second = REVERSE ? !(sub & 1) : (sub & 1), later = REVERSE ? !(sub & 2) : (sub & 2) != 0;
     const RecMap mate = REVERSE ? odd : even, pairs = REVERSE ? high : low;
     const RecMap none = {1.0f, 0.0f};
-    const RecMap in = second ? mate : none;
-    const RecMap joined = rec_then<PACKED>(pairs, in);
-    before = later ? (second ? joined : pairs) : in;
+    const RecMap in = second ? mate : none, joined = rec_then<PACKED>(pairs, in);
+    before = later ? joined : in;
 }
 
 
@@ -221,6 +230,7 @@ struct RecShared {
     float map[kRecWaves][kRecCols][2];                     // the wavefronts' maps, by channel
     float before[kRecGroup / kRecAtOnce][kRecCols][2];     // those of the tiles before
     float state[kRecCols];                                 // what enters the group
+    float enters[kRecWaves][kRecCols];                     // what enters the wavefronts
 };
 
 // The workgroup's tile, in the order of starting.
@@ -248,14 +258,14 @@ __device__ __forceinline__ RecMap rec_wait(const unsigned long long *at, unsigne
     return {__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32))};
 }
 
-// All lanes of the workgroup, with the maps of their wavefronts (the same in every strand)
-// and what enters the unit's first tile: what enters the lane's wavefront. `left`: what
-// leaves the tile. REVERSE: the last wavefront comes first. order: the tile's place in the
-// order of the walk. For the wait a lane is a channel, and half a wavefront looks at
-// kRecAtOnce tiles.
+// All lanes of the workgroup, with the maps of their wavefronts (the same in every strand):
+// what enters the lane's wavefront. first: what enters the unit's first tile, [Bt][E] or
+// NULL (zeros); last: what leaves its last one, the same. REVERSE: the last wavefront comes
+// first. order: the tile's place in the order of the walk. For the wait and what follows
+// a lane is a channel, and half a wavefront looks at kRecAtOnce tiles.
 template <bool PACKED, bool REVERSE>
 __device__ __forceinline__ void rec_enter(const RecArgs &a, const RecPlace &p, int order, const RecMap (&whole)[2],
-                                          const float (&first)[2], float (&enters)[2], float (&left)[2], RecShared &sh) {
+                                          const float *first, float *last, float (&enters)[2], RecShared &sh) {
     if (p.sub == 0)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -269,9 +279,9 @@ __device__ __forceinline__ void rec_enter(const RecArgs &a, const RecPlace &p, i
     };
     const int place = order % kRecGroup, group = order / kRecGroup;
     const size_t words = (size_t)a.batch * a.blocks * kRecCols;  // of one tile of every unit
+    const int c = threadIdx.x & (kRecCols - 1), part = threadIdx.x / kRecCols, parts = 2 * a.waves;
+    const size_t at = (size_t)p.unit * kRecCols + c;
     if (a.tiles > 1) {
-        const int c = threadIdx.x & (kRecCols - 1), part = threadIdx.x / kRecCols, parts = 2 * a.waves;
-        const size_t at = (size_t)p.unit * kRecCols + c;
         if (part == 0 && place < kRecGroup - 1 && order + 1 < a.tiles) {
             RecMap all = wave_map(0, c);
             for (int k = 1; k < a.waves; ++k) all = rec_then<PACKED>(all, wave_map(k, c));
@@ -298,19 +308,20 @@ __device__ __forceinline__ void rec_enter(const RecArgs &a, const RecPlace &p, i
         }
         __syncthreads();
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int c = 2 * p.col + e;
-        float in = group > 0 ? sh.state[c] : first[e];
+    if (part == 0) {
+        const int ch = (p.unit - p.batch * a.blocks) * kRecCols + c;
+        float in = group > 0 ? sh.state[c] : first && ch < a.channels ? first[(size_t)p.batch * a.channels + ch] : 0.0f;
         for (int q = 0; q * kRecAtOnce < place; ++q) in = rec_apply<PACKED>({sh.before[q][c][0], sh.before[q][c][1]}, in);
         for (int k = 0; k < a.waves; ++k) {
-            if ((REVERSE ? a.waves - 1 - k : k) == p.wave) enters[e] = in;
+            sh.enters[REVERSE ? a.waves - 1 - k : k][c] = in;
             in = rec_apply<PACKED>(wave_map(k, c), in);
         }
-        left[e] = in;
-        if (p.wave == 0 && p.sub == 0 && place == kRecGroup - 1 && order + 1 < a.tiles)
-            rec_tell(a.enter + (group + 1) * words + (size_t)p.unit * kRecCols + c, in, 0);
+        if (place == kRecGroup - 1 && order + 1 < a.tiles) rec_tell(a.enter + (group + 1) * words + at, in, 0);
+        if (last && order == a.tiles - 1 && ch < a.channels) last[(size_t)p.batch * a.channels + ch] = in;
     }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) enters[e] = sh.enters[p.wave][2 * p.col + e];
 }
 
 }  // namespace ssd

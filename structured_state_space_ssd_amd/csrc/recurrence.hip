@@ -55,23 +55,19 @@ __global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
     const int order = rec_ticket(a, p, sh);
     const int E = a.channels, tw = (order * a.waves + p.wave) * 4 * S, ts = tw + p.sub * S;
     const int nt = min(max(a.seqlen - ts, 0), S);
-    const size_t row0 = (size_t)p.batch * E + p.ch;
-    auto run = [&](auto whole_tile) {
-        constexpr bool WHOLE = decltype(whole_tile)::value;
+    auto run = [&](auto whole_tile, auto cuts) {
+        constexpr bool WHOLE = decltype(whole_tile)::value, CUTS = decltype(cuts)::value;
         RecPair<T> x[S], r[S], in[S], z[S];
         rec_load<T, WHOLE>(r, a.r, p.batch * a.r_batch + tw * a.r_token, a.r_token, p, nt);
         if (GATED) rec_load<T, WHOLE>(in, a.i, p.batch * a.i_batch + tw * a.i_token, a.i_token, p, nt);
         rec_load<T, WHOLE>(x, a.x, p.batch * a.x_batch + tw * a.x_token, a.x_token, p, nt);
         if (a.z) rec_load<T, WHOLE>(z, a.z, p.batch * a.z_batch + tw * a.z_token, a.z_token, p, nt);
         int code[S];
-        if (PACKED)
+        if (CUTS)
 #pragma unroll
             for (int j = 0; j < S; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
-        float rate[2], h0[2] = {0.0f, 0.0f};
+        float rate[2];
         if (GATED) rec_rates(rate, a, p);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (a.init && e < p.nch) h0[e] = a.init[row0 + e];
         float av[S][2], uv[S][2];
         RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
 #pragma unroll
@@ -92,23 +88,19 @@ __global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
                     d = 1.0f;
                     u = 0.0f;
                 }
-                if (PACKED && (code[j] & 1)) d = -1.0f;
-                if (PACKED && code[j] < 0) u = 0.0f;
+                if (CUTS && (code[j] & 1)) d = -1.0f;
+                if (CUTS && code[j] < 0) u = 0.0f;
                 av[j][e] = d;
                 uv[j][e] = u;
-                m[e] = rec_then<PACKED>(m[e], {d, u});
+                m[e] = rec_then<CUTS>(m[e], {d, u});
             }
         RecMap before[2], whole[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) rec_wave<PACKED, false>(m[e], p.sub, before[e], whole[e]);
-        float h[2], left[2];
-        rec_enter<PACKED, false>(a, p, order, whole, h0, h, left, sh);
+        for (int e = 0; e < 2; ++e) rec_wave<CUTS, false>(m[e], p.sub, before[e], whole[e]);
+        float h[2];
+        rec_enter<PACKED, false>(a, p, order, whole, a.init, PACKED ? nullptr : a.final_state, h, sh);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) h[e] = rec_apply<PACKED>(before[e], h[e]);
-        if (!PACKED && a.final_state && order == a.tiles - 1 && p.wave == 0 && p.sub == 0) {
-            if (p.nch > 0) a.final_state[row0] = left[0];
-            if (p.nch > 1) a.final_state[row0 + 1] = left[1];
-        }
+        for (int e = 0; e < 2; ++e) h[e] = rec_apply<CUTS>(before[e], h[e]);
         if (a.states && ts % kRecKeep == 0 && (WHOLE || nt > 0)) {
             float *s = a.states + ((size_t)p.batch * a.keeps + ts / kRecKeep) * E + p.ch;
             if (p.nch > 0) s[0] = h[0];
@@ -121,21 +113,30 @@ __global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
             float o[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                h[e] = rec_apply<PACKED>({av[j][e], uv[j][e]}, h[e]);
+                h[e] = rec_apply<CUTS>({av[j][e], uv[j][e]}, h[e]);
                 o[e] = h[e];
                 if (a.z) o[e] *= silu_f32(z[j].get(e));
-                if (PACKED && code[j] < 0) o[e] = 0.0f;
+                if (CUTS && code[j] < 0) o[e] = 0.0f;
             }
             if (a.y && (WHOLE || j < nt)) rec_store<T, WHOLE>(y + (size_t)j * E * sizeof(T), off, p.nch, o[0], o[1]);
-            if (PACKED && a.final_state && (WHOLE || j < nt) && code[j] > 1) {
+            if (CUTS && a.final_state && (WHOLE || j < nt) && code[j] > 1) {
                 float *f = a.final_state + (size_t)((code[j] >> 1) - 1) * E + p.ch;
                 if (p.nch > 0) f[0] = h[0];
                 if (p.nch > 1) f[1] = h[1];
             }
         }
     };
-    if (p.ch - 2 * p.col + kRecCols <= E && (order + 1) * a.waves * 4 * S <= a.seqlen) run(std::true_type());
-    else run(std::false_type());
+    const bool whole = p.ch - 2 * p.col + kRecCols <= E && (order + 1) * a.waves * 4 * S <= a.seqlen;
+    if constexpr (PACKED) {
+        const int t0 = order * a.waves * 4 * S;
+        if (rec_cuts(a.token + t0, min(a.waves * 4 * S, a.seqlen - t0))) {
+            if (whole) run(std::true_type(), std::true_type());
+            else run(std::false_type(), std::true_type());
+            return;
+        }
+    }
+    if (whole) run(std::true_type(), std::false_type());
+    else run(std::false_type(), std::false_type());
 }
 
 // One token: a lane takes four channels of one sequence.

@@ -27,9 +27,8 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
     const int order = rec_ticket(a, p, sh), tile = a.tiles - 1 - order;
     const int E = a.channels, tw = (tile * a.waves + p.wave) * 4 * S, ts = tw + p.sub * S;
     const int nt = min(max(a.seqlen - ts, 0), S);
-    const size_t row0 = (size_t)p.batch * E + p.ch;
-    auto run = [&](auto whole_tile) {
-        constexpr bool WHOLE = decltype(whole_tile)::value;
+    auto run = [&](auto whole_tile, auto cuts) {
+        constexpr bool WHOLE = decltype(whole_tile)::value, CUTS = decltype(cuts)::value;
         RecPair<T> x[S], r[S], in[S], z[S], dy[S];
         const size_t at = ((size_t)p.batch * a.seqlen + tw) * E;
         rec_load<T, WHOLE>(r, a.r, p.batch * a.r_batch + tw * a.r_token, a.r_token, p, nt);
@@ -44,15 +43,11 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
             if (p.nch > 1) hw[1] = s[1];
         }
         int code[S];
-        if (PACKED)
+        if (CUTS)
 #pragma unroll
             for (int j = 0; j < S; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
-        // q: what comes to the last token from behind
-        float rate[2], q[2] = {0.0f, 0.0f}, sum[2] = {0.0f, 0.0f};
+        float rate[2], sum[2] = {0.0f, 0.0f};
         if (GATED) rec_rates(rate, a, p);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (!PACKED && b.dfinal && e < p.nch) q[e] = b.dfinal[row0 + e];
         float av[S][2], hv[S][2];
         float rv[S][2], iv[S][2], bv[S][2];  // the gates, and sqrt(1 - a^2)
         RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mg[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
@@ -76,22 +71,22 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
                     d = 1.0f;
                     u = 0.0f;
                 }
-                if (PACKED) {
+                if (CUTS) {
                     if (code[j] & 1) d = -1.0f;
                     if (code[j] < 0) u = 0.0f;
                 }
                 av[j][e] = d;
                 hv[j][e] = u;
-                m[e] = rec_then<PACKED>(m[e], {d, u});
+                m[e] = rec_then<CUTS>(m[e], {d, u});
             }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             RecMap before, whole;
-            rec_wave<PACKED, false>(m[e], p.sub, before, whole);
-            float h = rec_apply<PACKED>(before, hw[e]);
+            rec_wave<CUTS, false>(m[e], p.sub, before, whole);
+            float h = rec_apply<CUTS>(before, hw[e]);
 #pragma unroll
             for (int j = 0; j < S; ++j) {  // what each token takes of the state before, in its input's place
-                const float carried = PACKED && av[j][e] < 0.0f ? 0.0f : av[j][e] * h;
+                const float carried = CUTS && av[j][e] < 0.0f ? 0.0f : av[j][e] * h;
                 h = carried + hv[j][e];
                 hv[j][e] = carried;
             }
@@ -100,8 +95,8 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
         auto own = [&](int j, int e) {
             float g = dy[j].get(e);
             if (a.z) g *= silu_f32(z[j].get(e));
-            if ((!WHOLE && j >= nt) || (PACKED && code[j] < 0)) g = 0.0f;
-            if (PACKED && b.dfinal && code[j] > 1 && e < p.nch)
+            if ((!WHOLE && j >= nt) || (CUTS && code[j] < 0)) g = 0.0f;
+            if (CUTS && b.dfinal && code[j] > 1 && e < p.nch)
                 g += b.dfinal[(size_t)((code[j] >> 1) - 1) * E + p.ch + e];
             return g;
         };
@@ -110,21 +105,18 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
         for (int j = S - 1; j >= 0; --j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const bool first = PACKED && av[j][e] < 0.0f;
-                mg[e] = {first || (PACKED && mg[e].a < 0.0f) ? -1.0f : av[j][e] * mg[e].a,
+                const bool first = CUTS && av[j][e] < 0.0f;
+                mg[e] = {first || (CUTS && mg[e].a < 0.0f) ? -1.0f : av[j][e] * mg[e].a,
                          first ? 0.0f : av[j][e] * (own(j, e) + mg[e].h)};
             }
         RecMap after[2], whole[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) rec_wave<PACKED, true>(mg[e], p.sub, after[e], whole[e]);
-        float qs[2], left[2];
-        rec_enter<PACKED, true>(a, p, order, whole, q, qs, left, sh);
+        for (int e = 0; e < 2; ++e) rec_wave<CUTS, true>(mg[e], p.sub, after[e], whole[e]);
+        // what comes to the wavefront's last token from behind
+        float qs[2];
+        rec_enter<PACKED, true>(a, p, order, whole, PACKED ? nullptr : b.dfinal, PACKED ? nullptr : b.dinit, qs, sh);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) qs[e] = rec_apply<PACKED>(after[e], qs[e]);
-        if (!PACKED && b.dinit && tile == 0 && p.wave == 0 && p.sub == 0) {
-            if (p.nch > 0) b.dinit[row0] = left[0];
-            if (p.nch > 1) b.dinit[row0 + 1] = left[1];
-        }
+        for (int e = 0; e < 2; ++e) qs[e] = rec_apply<CUTS>(after[e], qs[e]);
         // (the values anew: what the compiler keeps of them from above fills the registers)
 #pragma unroll
         for (int j = 0; j < S; ++j) {
@@ -137,7 +129,7 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
             float ox[2], orr[2], oi[2], oz[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const bool first = PACKED && av[j][e] < 0.0f;
+                const bool first = CUTS && av[j][e] < 0.0f;
                 const float xv = x[j].get(e), d = av[j][e], g = own(j, e) + qs[e];
                 const float carried = hv[j][e];  // a h_{t-1}
                 float u = xv;
@@ -147,11 +139,11 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
                     ox[e] = g * (beta * si);
                     oi[e] = g * u * (1.0f - si);
                     // d sqrt(1 - a^2) / d log a = -a^2 / b, so p x times that is -u a^2 / b^2
-                    const float a2 = PACKED && first ? __builtin_amdgcn_exp2f(2.0f * rate[e] * sr) : d * d;
+                    const float a2 = CUTS && first ? __builtin_amdgcn_exp2f(2.0f * rate[e] * sr) : d * d;
                     const float q2 = beta > 0.0f ? a2 * __builtin_amdgcn_rcpf(beta * beta) : 0.0f;
                     const float w = g * la * fmaf(-u, q2, carried);
                     orr[e] = w * (1.0f - sr);
-                    if ((WHOLE || j < nt) && !(PACKED && code[j] < 0)) sum[e] += w;
+                    if ((WHOLE || j < nt) && !(CUTS && code[j] < 0)) sum[e] += w;
                 } else {
                     ox[e] = g;
                     orr[e] = g * carried;
@@ -160,7 +152,7 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
                 qs[e] = first ? 0.0f : d * g;
             }
             if (!WHOLE && j >= nt) continue;
-            if (PACKED && code[j] < 0) ox[0] = ox[1] = orr[0] = orr[1] = oi[0] = oi[1] = oz[0] = oz[1] = 0.0f;
+            if (CUTS && code[j] < 0) ox[0] = ox[1] = orr[0] = orr[1] = oi[0] = oi[1] = oz[0] = oz[1] = 0.0f;
             const auto out = [&](void *t, float (&v)[2]) {
                 rec_store<T, WHOLE>(static_cast<char *>(t) + (at + (size_t)j * E) * sizeof(T), off, p.nch, v[0], v[1]);
             };
@@ -195,8 +187,17 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
                 b.part[((size_t)p.batch * a.tiles + tile) * E + p.ch + e] = k * s;
             }
     };
-    if (p.ch - 2 * p.col + kRecCols <= E && (tile + 1) * a.waves * 4 * S <= a.seqlen) run(std::true_type());
-    else run(std::false_type());
+    const bool whole = p.ch - 2 * p.col + kRecCols <= E && (tile + 1) * a.waves * 4 * S <= a.seqlen;
+    if constexpr (PACKED) {
+        const int t0 = tile * a.waves * 4 * S;
+        if (rec_cuts(a.token + t0, min(a.waves * 4 * S, a.seqlen - t0))) {
+            if (whole) run(std::true_type(), std::true_type());
+            else run(std::false_type(), std::true_type());
+            return;
+        }
+    }
+    if (whole) run(std::true_type(), std::false_type());
+    else run(std::false_type(), std::false_type());
 }
 
 template <typename T, bool GATED, bool PACKED> hipError_t bwd(const RecBwdArgs &b, hipStream_t stream) {
