@@ -10,7 +10,7 @@ import torch
 
 import layer_refs as R
 
-JOINS = 60  # sums and products that join strands, wavefronts (16) and segments (32)
+JOINS = 60  # sums and products that join strands (4), wavefronts (4) and a group's tiles (16), each way
 KEEP = 16   # tokens between the states that the forward keeps
 
 

@@ -35,7 +35,8 @@ SIZES = [(1, 1), (3, 2), (5, 7), (300, 8), (17, 9), (70, 16), (9, 100), (33, 255
          (2, 2049), (4, 2560), (3, 3001), (2, 4095), (3, 4097), (5, 5119), (2, 8191), (2, 6145), (2, 8192), (2000, 24), (1500, 1000), (1601, 2560)]
 # T, stream, rms, post, pre, bias, scale, gate, p, dsum
 KINDS = [(BF, F32, True, 1, 1, 0, 1, 0, 0.1, 1), (BF, BF, False, 1, 1, 1, 0, 1, 0.0, 1), (F32, F32, False, 1, 1, 1, 1, 1, 0.5, 0),
-         (BF, F32, False, 0, 1, 0, 1, 1, 0.0, 1), (F32, F32, True, 1, 0, 1, 0, 0, 0.25, 1), (BF, BF, True, 0, 1, 1, 0, 0, 0.9, 0)]
+         (BF, F32, False, 0, 1, 0, 1, 1, 0.0, 1), (F32, F32, True, 1, 0, 1, 0, 0, 0.25, 1), (BF, BF, True, 0, 1, 1, 0, 0, 0.9, 0),
+         (BF, F32, False, 1, 0, 0, 1, 0, 0.0, 1), (F32, F32, False, 0, 1, 0, 0, 0, 0.1, 1), (F32, F32, True, 1, 1, 0, 1, 0, 0.0, 1)]
 
 
 @pytest.mark.parametrize("size", SIZES, ids=str)

@@ -37,10 +37,10 @@ def check_all(name, got, want, keys):
 
 
 # (batch, tokens, channels): one token, parts of strands (8 tokens), wavefronts (32), tiles
-# of 1 to 16 wavefronts, ragged ones, odd channels around a workgroup's 32, more channels
-# than an XCD has workgroups for, plans with and without segments
+# of 1 to 4 wavefronts, ragged ones, odd channels around a workgroup's 32, one tile to a unit
+# and many, in one group of tiles and several, more workgroups than run at once
 SIZES = [(1, 1, 1), (3, 1, 70), (2, 7, 33), (1, 8, 32), (2, 31, 31), (1, 33, 66), (5, 64, 129), (1, 130, 700),
-         (2, 517, 40), (1, 2050, 34), (17, 100, 1000), (1, 4100, 3), (600, 40, 33)]
+         (2, 517, 40), (1, 2050, 34), (17, 100, 1000), (1, 4100, 3), (600, 40, 33), (8, 700, 1000)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
@@ -64,6 +64,20 @@ def test_recurrence(ssd, size, dtype):
         check_all((size, gated), got, want, keys)
         again = ssd.recurrence_backward(**a, dy=dy, init_state=init, dfinal_state=dfinal)
         assert all(torch.equal(got[k], again[k]) for k in keys)  # with states of its own, and every time
+
+
+@pytest.mark.parametrize("gated", [True, False])
+def test_recurrence_long(ssd, gated):
+    """Hundreds of tiles one after the other, the state entering each through many groups."""
+    a, r = make(1, 30001, 40, BF, gated, False)
+    if not gated:
+        a["r"] = (a["r"].float() * 1e-3).bfloat16()  # a state that keeps thousands of tokens
+    dy, init, dfinal = r(1, 30001, 40, dt=BF), r(1, 40), r(1, 40)
+    want = B.recurrence(*a.values(), init, 8.0, None, (dy, dfinal))
+    y, final, states = ssd.recurrence_forward(**a, init_state=init, return_final_state=True, return_states=True)
+    check_all(gated, dict(y=y, final=final, states=states), want, ("y", "final", "states"))
+    got = ssd.recurrence_backward(**a, dy=dy, init_state=init, dfinal_state=dfinal, states=states)
+    check_all(gated, got, want, [k for k in got if got[k] is not None])
 
 
 CUS = [[0, 40], [0, 0, 1, 2, 2, 15, 31, 40, 40], [0, 3, 300, 300, 301, 511, 700], [0, 64, 1000, 1100],
