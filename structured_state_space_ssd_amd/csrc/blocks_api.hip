@@ -78,9 +78,10 @@ int recurrence_args(ssd::RecArgs &a, const void *x, const void *r, const void *i
     return SSD_OK;
 }
 
+// (a token's code holds twice the number of a sequence)
 int check_packed(const int *cu_seqlens, int nseq, int batch, const float *init) {
     if (!cu_seqlens) return SSD_OK;
-    if (batch != 1 || nseq < 1 || nseq > kMaxExtent) return SSD_ERR_SHAPE;
+    if (batch != 1 || nseq < 1 || nseq >= kMaxExtent) return SSD_ERR_SHAPE;
     return init ? SSD_ERR_UNSUPPORTED : SSD_OK;
 }
 

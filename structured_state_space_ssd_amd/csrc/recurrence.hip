@@ -221,7 +221,11 @@ unsigned rec_grid(const RecArgs &a) {
 hipError_t launch_rec_prepare(const RecArgs &a, void *unset, size_t bytes, float *rate, const int *cu, int nseq,
                               int *token, float *final, hipStream_t stream) {
     const long long words = bytes / 16, finals = (long long)nseq * a.channels;
-    const long long most = cu && a.seqlen > words ? a.seqlen : words;
+    // its loops' extents: 32 packed tokens of 5120 channels in 32 sequences with final states take
+    // 31 us where the tokens alone set the grid, 8 so
+    long long most = words;
+    for (long long n : {cu ? a.seqlen : 0LL, cu && final ? finals : 0LL, a.decay ? a.channels : 0LL})
+        if (n > most) most = n;
     const unsigned want = static_cast<unsigned>(most / 256 + 1), grid = want < 2048 ? want : 2048;
     rec_prepare_kernel<<<grid, 256, 0, stream>>>(static_cast<uint4 *>(unset), words, cu, nseq, a.seqlen, token, final,
                                                  finals, a.decay, a.c, a.channels, rate);

@@ -100,6 +100,7 @@ BAD_C = [
     (dict(strides=(48, 8, 48, 8, 48, -1, 48, 8)), -2), (dict(strides=(48, 8, -48, 8, 48, 8, 48, 8)), -2),
     (dict(strides=(48, 1 << 24, 48, 8, 48, 8, 48, 8)), -3),
     (dict(cu=FAKE, nseq=2), -2), (dict(cu=FAKE, nseq=0, batch=1), -2), (dict(cu=FAKE, nseq=(1 << 30) + 1, batch=1), -2),
+    (dict(cu=FAKE, nseq=1 << 30, batch=1), -2),
     (dict(cu=FAKE, nseq=2, batch=1, init=FAKE), -3),
     (dict(batch=1 << 30, channels=1 << 20), -3),
     (dict(cu=FAKE, nseq=2, batch=1), -4), (dict(cu=FAKE, nseq=2, batch=1, ws=ctypes.c_void_p(0x100010), bytes=1 << 20), -4),
