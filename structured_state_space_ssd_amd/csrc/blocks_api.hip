@@ -298,6 +298,15 @@ int ssd_recurrence_backward(const void *x, const void *r, const void *i, const f
     b.ddecay = ddecay;
     b.dinit = dinit_state;
     b.part = at(w.part);
+    b.words = true;
+    if (dtype == SSD_BF16) {
+        for (const void *t : {x, r, i, z, dy, static_cast<const void *>(dx), static_cast<const void *>(dr),
+                              static_cast<const void *>(di), static_cast<const void *>(dz)})
+            if (reinterpret_cast<uintptr_t>(t) & 3u) b.words = false;
+        for (size_t v : {a.x_batch, a.x_token, a.r_batch, a.r_token, a.i_batch, a.i_token, a.z_batch, a.z_token,
+                         static_cast<size_t>(channels)})
+            if (v & 1u) b.words = false;
+    }
     b.spare = (long long)batch * w.plan.tiles > ssd::kColsumRows ? at(w.spare) : nullptr;
     return status_of(ssd::launch_rec_bwd(b, dtype == SSD_BF16, s));
 }

@@ -17,6 +17,47 @@ namespace ssd {
 
 namespace {
 
+// Whole tiles go through buffer loads and stores: a wavefront's base and a token's distance
+// from it in scalar registers, one offset per lane. By addresses, which the compiler adds
+// up per lane in 64 bits, a tile takes 7 % more vector instructions (8 x 2048 x 2560 bf16
+// with gate: 243 us, so 232; forward, with fewer tensors, no gain). A pair of channels has
+// to lie on 32-bit words, else the tile goes the way of ragged ones.
+typedef __amdgpu_buffer_rsrc_t rec_buffer;
+__device__ __forceinline__ rec_buffer rec_buffer_at(const void *t, size_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(t) + bytes;
+    const uint64_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)) & 0xffffffffu,
+                   hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(hi << 32 | lo), 0, -1, 0x00020000);
+}
+__device__ __forceinline__ void rec_get(RecPair<bf16_t> &r, rec_buffer t, uint32_t off, uint32_t row) {
+    r.w = __builtin_amdgcn_raw_buffer_load_b32(t, off, row, 0);
+}
+__device__ __forceinline__ void rec_get(RecPair<float> &r, rec_buffer t, uint32_t off, uint32_t row) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b64(t, off, row, 0);
+    r.w[0] = __uint_as_float(v[0]);
+    r.w[1] = __uint_as_float(v[1]);
+}
+template <typename T, bool WHOLE, int S>
+__device__ __forceinline__ void rec_get(RecPair<T> (&r)[S], const void *t, size_t at, size_t token,
+                                        const RecPlace &p, int nt) {
+    if (!WHOLE) return rec_load<T, false>(r, t, at, token, p, nt);
+    const rec_buffer from = rec_buffer_at(t, at * sizeof(T));
+    const uint32_t off = rec_offset<T, S>(token, p), row = static_cast<uint32_t>(token) * static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+    for (int j = 0; j < S; ++j) rec_get(r[j], from, off, j * row);
+}
+typedef unsigned rec_word2 __attribute__((ext_vector_type(2)));
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void rec_put(void *t, size_t at, uint32_t row, uint32_t off, int nch, const float (&v)[2]) {
+    if (!WHOLE) rec_store<T, false>(static_cast<char *>(t) + at + row, off, nch, v[0], v[1]);
+    else if constexpr (sizeof(T) == 2)
+        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(v[0], v[1]), rec_buffer_at(t, at), off, row, 0);
+    else {
+        const rec_word2 w = {__float_as_uint(v[0]), __float_as_uint(v[1])};
+        __builtin_amdgcn_raw_buffer_store_b64(w, rec_buffer_at(t, at), off, row, 0);
+    }
+}
+
 template <typename T, bool GATED, bool PACKED>
 __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bwd_kernel(RecBwdArgs b) {
     constexpr int S = kRecBwdStrand;
@@ -31,11 +72,11 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
         constexpr bool WHOLE = decltype(whole_tile)::value, CUTS = decltype(cuts)::value;
         RecPair<T> x[S], r[S], in[S], z[S], dy[S];
         const size_t at = ((size_t)p.batch * a.seqlen + tw) * E;
-        rec_load<T, WHOLE>(r, a.r, p.batch * a.r_batch + tw * a.r_token, a.r_token, p, nt);
-        rec_load<T, WHOLE>(dy, b.dy, at, E, p, nt);
-        if (a.z) rec_load<T, WHOLE>(z, a.z, p.batch * a.z_batch + tw * a.z_token, a.z_token, p, nt);
-        if (GATED) rec_load<T, WHOLE>(in, a.i, p.batch * a.i_batch + tw * a.i_token, a.i_token, p, nt);
-        rec_load<T, WHOLE>(x, a.x, p.batch * a.x_batch + tw * a.x_token, a.x_token, p, nt);
+        rec_get<T, WHOLE>(r, a.r, p.batch * a.r_batch + tw * a.r_token, a.r_token, p, nt);
+        rec_get<T, WHOLE>(dy, b.dy, at, E, p, nt);
+        if (a.z) rec_get<T, WHOLE>(z, a.z, p.batch * a.z_batch + tw * a.z_token, a.z_token, p, nt);
+        if (GATED) rec_get<T, WHOLE>(in, a.i, p.batch * a.i_batch + tw * a.i_token, a.i_token, p, nt);
+        rec_get<T, WHOLE>(x, a.x, p.batch * a.x_batch + tw * a.x_token, a.x_token, p, nt);
         float hw[2] = {0.0f, 0.0f};  // the state entering the wavefront's tokens
         if (WHOLE || tw < a.seqlen) {
             const float *s = a.states + ((size_t)p.batch * a.keeps + tw / kRecKeep) * E + p.ch;
@@ -48,6 +89,7 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
             for (int j = 0; j < S; ++j) code[j] = WHOLE || j < nt ? a.token[ts + j] : 0;
         float rate[2], sum[2] = {0.0f, 0.0f};
         if (GATED) rec_rates(rate, a, p);
+        const float rate_e[2] = {rate[0] * kLn2, rate[1] * kLn2};
         float av[S][2], hv[S][2];
         float rv[S][2], iv[S][2], bv[S][2];  // the gates, and sqrt(1 - a^2)
         RecMap m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mg[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
@@ -134,13 +176,14 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
                 const float carried = hv[j][e];  // a h_{t-1}
                 float u = xv;
                 if (GATED) {
-                    const float sr = rv[j][e], si = iv[j][e], beta = bv[j][e], la = rate[e] * sr * kLn2;
+                    const float sr = rv[j][e], si = iv[j][e], beta = bv[j][e], la = rate_e[e] * sr;
                     u = beta * si * xv;
                     ox[e] = g * (beta * si);
                     oi[e] = g * u * (1.0f - si);
                     // d sqrt(1 - a^2) / d log a = -a^2 / b, so p x times that is -u a^2 / b^2
                     const float a2 = CUTS && first ? __builtin_amdgcn_exp2f(2.0f * rate[e] * sr) : d * d;
-                    const float q2 = beta > 0.0f ? a2 * __builtin_amdgcn_rcpf(beta * beta) : 0.0f;
+                    // (where b is 0, so is u)
+                    const float q2 = a2 * __builtin_amdgcn_rcpf(fmaxf(beta * beta, 1.17549435e-38f));
                     const float w = g * la * fmaf(-u, q2, carried);
                     orr[e] = w * (1.0f - sr);
                     if ((WHOLE || j < nt) && !(CUTS && code[j] < 0)) sum[e] += w;
@@ -154,7 +197,7 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
             if (!WHOLE && j >= nt) continue;
             if (CUTS && code[j] < 0) ox[0] = ox[1] = orr[0] = orr[1] = oi[0] = oi[1] = oz[0] = oz[1] = 0.0f;
             const auto out = [&](void *t, float (&v)[2]) {
-                rec_store<T, WHOLE>(static_cast<char *>(t) + (at + (size_t)j * E) * sizeof(T), off, p.nch, v[0], v[1]);
+                rec_put<T, WHOLE>(t, at * sizeof(T), static_cast<uint32_t>(j * E) * static_cast<uint32_t>(sizeof(T)), off, p.nch, v);
             };
             out(b.dx, ox);
             out(b.dr, orr);
@@ -187,7 +230,7 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
                 b.part[((size_t)p.batch * a.tiles + tile) * E + p.ch + e] = k * s;
             }
     };
-    const bool whole = p.ch - 2 * p.col + kRecCols <= E && (tile + 1) * a.waves * 4 * S <= a.seqlen;
+    const bool whole = b.words && p.ch - 2 * p.col + kRecCols <= E && (tile + 1) * a.waves * 4 * S <= a.seqlen;
     if constexpr (PACKED) {
         const int t0 = tile * a.waves * 4 * S;
         if (rec_cuts(a.token + t0, min(a.waves * 4 * S, a.seqlen - t0))) {

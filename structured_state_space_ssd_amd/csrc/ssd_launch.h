@@ -410,6 +410,7 @@ struct RecBwdArgs {
     void *dx, *dr, *di, *dz;      // dense
     float *ddecay, *dinit;        // dinit nullable
     float *part;                  // [Bt][tiles][E]: scratch
+    bool words;                   // every pair of channels of every tensor starts on 32 bits
     float *spare;                 // kColsumChunks rows of E, where there are more than kColsumRows
 };
 hipError_t launch_rec_bwd(const RecBwdArgs &b, bool bf16, hipStream_t stream);
