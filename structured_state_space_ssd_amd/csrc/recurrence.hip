@@ -46,7 +46,8 @@ __global__ __launch_bounds__(256) void rec_prepare_kernel(uint4 *__restrict__ un
 // Tokens of a strand: float32 operands of 8 do not fit the registers.
 template <typename T> constexpr int rec_fwd_strand() { return sizeof(T) == 2 ? 8 : 4; }
 
-template <typename T, bool GATED, bool PACKED>
+// GATE: whether there is a z (known to the compiler: see the backward's).
+template <typename T, bool GATED, bool PACKED, bool GATE>
 __global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
     constexpr int S = rec_fwd_strand<T>();
     __shared__ RecShared sh;
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
         rec_load<T, WHOLE>(r, a.r, p.batch * a.r_batch + tw * a.r_token, a.r_token, p, nt);
         if (GATED) rec_load<T, WHOLE>(in, a.i, p.batch * a.i_batch + tw * a.i_token, a.i_token, p, nt);
         rec_load<T, WHOLE>(x, a.x, p.batch * a.x_batch + tw * a.x_token, a.x_token, p, nt);
-        if (a.z) rec_load<T, WHOLE>(z, a.z, p.batch * a.z_batch + tw * a.z_token, a.z_token, p, nt);
+        if (GATE) rec_load<T, WHOLE>(z, a.z, p.batch * a.z_batch + tw * a.z_token, a.z_token, p, nt);
         int code[S];
         if (CUTS)
 #pragma unroll
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
             for (int e = 0; e < 2; ++e) {
                 h[e] = rec_apply<CUTS>({av[j][e], uv[j][e]}, h[e]);
                 o[e] = h[e];
-                if (a.z) o[e] *= silu_f32(z[j].get(e));
+                if (GATE) o[e] *= silu_f32(z[j].get(e));
                 if (CUTS && code[j] < 0) o[e] = 0.0f;
             }
             if (a.y && (WHOLE || j < nt)) rec_store<T, WHOLE>(y + (size_t)j * E * sizeof(T), off, p.nch, o[0], o[1]);
@@ -171,7 +172,8 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs a, float *__restr
 }
 
 template <typename T, bool GATED, bool PACKED> hipError_t fwd(const RecArgs &a, hipStream_t stream) {
-    rec_fwd_kernel<T, GATED, PACKED><<<rec_grid(a), a.waves * 64, 0, stream>>>(a);
+    if (a.z) rec_fwd_kernel<T, GATED, PACKED, true><<<rec_grid(a), a.waves * 64, 0, stream>>>(a);
+    else rec_fwd_kernel<T, GATED, PACKED, false><<<rec_grid(a), a.waves * 64, 0, stream>>>(a);
     return hipGetLastError();
 }
 
