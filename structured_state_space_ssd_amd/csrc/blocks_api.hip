@@ -95,7 +95,7 @@ struct RecScratch {
         ticket = k.take(p.tickets);
         end = k.o;
         rate = k.take(p.tiles > 1 || packed_tokens ? channels : 0);
-        token = k.take(packed_tokens);
+        token = k.take(packed_tokens ? (size_t)packed_tokens + (packed_tokens + 63) / 64 : 0);  // and cuts behind
     }
     void use(ssd::RecArgs &a, const ssd::RecPlan &p, char *base) const {
         a.blocks = p.blocks; a.waves = p.waves; a.tiles = p.tiles; a.keeps = p.keeps;
@@ -104,16 +104,17 @@ struct RecScratch {
         a.enter = reinterpret_cast<unsigned long long *>(base + enter);
         a.ticket = reinterpret_cast<unsigned *>(base + ticket);
         a.rate = nullptr;
-        a.token = nullptr;
+        a.token = a.cuts = nullptr;
     }
     // What a pass over one tile of each unit does without is left out.
     hipError_t prepare(ssd::RecArgs &a, const int *cu, int nseq, float *final, char *base, hipStream_t s) const {
         if (a.tiles == 1 && !cu) return hipSuccess;
-        int *t = reinterpret_cast<int *>(base + token);
+        int *t = reinterpret_cast<int *>(base + token), *u = t + a.seqlen;
         float *r = reinterpret_cast<float *>(base + rate);
         a.token = cu ? t : nullptr;
+        a.cuts = cu ? u : nullptr;
         a.rate = a.decay ? r : nullptr;
-        return ssd::launch_rec_prepare(a, base + maps, end - maps, r, cu, nseq, t, final, s);
+        return ssd::launch_rec_prepare(a, base + maps, end - maps, r, cu, nseq, t, u, final, s);
     }
 };
 

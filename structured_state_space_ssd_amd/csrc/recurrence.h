@@ -96,14 +96,13 @@ __device__ __forceinline__ RecPlace rec_place(const RecArgs &a) {
     return p;
 }
 
-// Whether any of n tokens of a packed axis is a first or last one of a sequence, or in none:
-// of most tiles none is, and they go without the selections (1 x 16384 tokens x 2560
-// channels in 55 sequences, with them everywhere: 112 us forward and 245 back).
-__device__ __forceinline__ bool rec_cuts(const int *token, int n) {
-    float v[1] = {0.0f};
-    for (int k = lane_id(); k < n; k += 64) v[0] += token[k] != 0 ? 1.0f : 0.0f;
-    lane_sum(v, 64);
-    return __builtin_amdgcn_readfirstlane(__float_as_int(v[0])) != 0;
+// Whether any of a tile's n tokens of a packed axis is a first or last one of a sequence, or
+// in none: of most tiles none is, and they go without the selections (1 x 16384 tokens x 2560
+// channels in 55 sequences, with them everywhere: 112 us forward and 245 back). cuts: per 64
+// tokens, whether any is; a tile begins at the first of 64 and has 128 at most.
+__device__ __forceinline__ bool rec_cuts(const int *cuts, int from, int n) {
+    const int *at = cuts + from / 64;
+    return (at[0] | at[n > 64]) != 0;
 }
 
 // Byte offset of a lane's first token and channel (strides are below 2^24 elements).

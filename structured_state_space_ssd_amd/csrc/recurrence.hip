@@ -17,11 +17,12 @@ namespace {
 // Before a pass: the words that its tiles wait for are set to ~0 (`words` vectors of 16
 // bytes), the channels' rates are made, and, for a packed axis, the tokens' codes: bit 0, the first of its
 // sequence; above, 1 + the number of the sequence whose last token it is; kRecNone: in no
-// sequence. `final`: set to the state of an empty sequence. Any contents of `cu` are read
+// sequence; and per 64 tokens whether any code is not 0 (rec_cuts). `final`: set to the state of an empty sequence. Any contents of `cu` are read
 // within its nseq + 1 entries.
 __global__ __launch_bounds__(256) void rec_prepare_kernel(uint4 *__restrict__ unset, long long words,
                                                           const int *__restrict__ cu, int nseq, int L,
-                                                          int *__restrict__ token, float *__restrict__ final,
+                                                          int *__restrict__ token, int *__restrict__ cuts,
+                                                          float *__restrict__ final,
                                                           long long finals, const float *__restrict__ decay,
                                                           float c, int E, float *__restrict__ rate) {
     const long long id = (long long)blockIdx.x * 256 + threadIdx.x, all = (long long)gridDim.x * 256;
@@ -31,7 +32,7 @@ __global__ __launch_bounds__(256) void rec_prepare_kernel(uint4 *__restrict__ un
     if (!cu) return;
     if (final)
         for (long long k = id; k < finals; k += all) final[k] = 0.0f;
-    for (long long t = id; t < L; t += all) {
+    for (long long t = id; t - lane_id() < L; t += all) {
         int lo = 0, hi = nseq;  // the last sequence that begins at or before t
         while (hi - lo > 1) {
             const int mid = lo + (hi - lo) / 2;
@@ -39,7 +40,11 @@ __global__ __launch_bounds__(256) void rec_prepare_kernel(uint4 *__restrict__ un
             else hi = mid;
         }
         const int from = cu[lo], to = cu[lo + 1];
-        token[t] = t < from || t >= to ? kRecNone : (from == t ? 1 : 0) | (to - 1 == t ? 2 * (lo + 1) : 0);
+        const int code = t < from || t >= to ? kRecNone : (from == t ? 1 : 0) | (to - 1 == t ? 2 * (lo + 1) : 0);
+        if (t < L) token[t] = code;
+        float any[1] = {t < L && code != 0 ? 1.0f : 0.0f};
+        lane_sum(any, 64);
+        if (lane_id() == 0) cuts[t / 64] = any[0] != 0.0f;
     }
 }
 
@@ -48,7 +53,7 @@ template <typename T> constexpr int rec_fwd_strand() { return sizeof(T) == 2 ? 8
 
 // GATE: whether there is a z (known to the compiler: see the backward's).
 template <typename T, bool GATED, bool PACKED, bool GATE>
-__global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
+__global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? GATE ? 5 : 6 : 7) void rec_fwd_kernel(RecArgs a) {
     constexpr int S = rec_fwd_strand<T>();
     __shared__ RecShared sh;
     const RecPlace p = rec_place(a);
@@ -130,7 +135,7 @@ __global__ __launch_bounds__(kRecWaves * 64) void rec_fwd_kernel(RecArgs a) {
     const bool whole = p.ch - 2 * p.col + kRecCols <= E && (order + 1) * a.waves * 4 * S <= a.seqlen;
     if constexpr (PACKED) {
         const int t0 = order * a.waves * 4 * S;
-        if (rec_cuts(a.token + t0, min(a.waves * 4 * S, a.seqlen - t0))) {
+        if (rec_cuts(a.cuts, t0, min(a.waves * 4 * S, a.seqlen - t0))) {
             if (whole) run(std::true_type(), std::true_type());
             else run(std::false_type(), std::true_type());
             return;
@@ -221,7 +226,7 @@ unsigned rec_grid(const RecArgs &a) {
 }
 
 hipError_t launch_rec_prepare(const RecArgs &a, void *unset, size_t bytes, float *rate, const int *cu, int nseq,
-                              int *token, float *final, hipStream_t stream) {
+                              int *token, int *cuts, float *final, hipStream_t stream) {
     const long long words = bytes / 16, finals = (long long)nseq * a.channels;
     // its loops' extents: 32 packed tokens of 5120 channels in 32 sequences with final states take
     // 31 us where the tokens alone set the grid, 8 so
@@ -229,7 +234,7 @@ hipError_t launch_rec_prepare(const RecArgs &a, void *unset, size_t bytes, float
     for (long long n : {cu ? a.seqlen : 0LL, cu && final ? finals : 0LL, a.decay ? a.channels : 0LL})
         if (n > most) most = n;
     const unsigned want = static_cast<unsigned>(most / 256 + 1), grid = want < 2048 ? want : 2048;
-    rec_prepare_kernel<<<grid, 256, 0, stream>>>(static_cast<uint4 *>(unset), words, cu, nseq, a.seqlen, token, final,
+    rec_prepare_kernel<<<grid, 256, 0, stream>>>(static_cast<uint4 *>(unset), words, cu, nseq, a.seqlen, token, cuts, final,
                                                  finals, a.decay, a.c, a.channels, rate);
     return hipGetLastError();
 }

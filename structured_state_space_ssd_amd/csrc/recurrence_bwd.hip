@@ -247,7 +247,7 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
     const bool whole = b.words && p.ch - 2 * p.col + kRecCols <= E && (tile + 1) * a.waves * 4 * S <= a.seqlen;
     if constexpr (PACKED) {
         const int t0 = tile * a.waves * 4 * S;
-        if (rec_cuts(a.token + t0, min(a.waves * 4 * S, a.seqlen - t0))) {
+        if (rec_cuts(a.cuts, t0, min(a.waves * 4 * S, a.seqlen - t0))) {
             if (whole) run(std::true_type(), std::true_type());
             else run(std::false_type(), std::true_type());
             return;

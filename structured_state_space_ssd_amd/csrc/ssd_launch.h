@@ -373,7 +373,7 @@ struct RecArgs {
     const float *decay;           // [E]; NULL: r is the log-decay, x the input term
     float c;
     const float *init;            // [Bt][E], nullable
-    const int *token;             // packed sequences: launch_rec_prepare's codes, else NULL
+    const int *token, *cuts;      // packed sequences: launch_rec_prepare's codes, else NULL
     int batch, seqlen, channels;
     int blocks, waves, tiles, keeps;  // the plan
     RecDivisor by_blocks, by_each;    // each: units (batch x blocks) to an XCD
@@ -399,7 +399,7 @@ unsigned rec_grid(const RecArgs &a);
 // NULL) and the codes of a packed axis' tokens (cu not NULL) and zeroes `final` ([nseq][E],
 // nullable).
 hipError_t launch_rec_prepare(const RecArgs &a, void *unset, size_t bytes, float *rate, const int *cu, int nseq,
-                              int *token, float *final, hipStream_t stream);
+                              int *token, int *cuts, float *final, hipStream_t stream);
 hipError_t launch_rec_fwd(const RecArgs &a, bool bf16, hipStream_t stream);
 // One token: the token strides and init are not read.
 hipError_t launch_rec_step(const RecArgs &a, float *state, bool bf16, hipStream_t stream);

@@ -80,6 +80,23 @@ def test_recurrence_long(ssd, gated):
     check_all(gated, got, want, [k for k in got if got[k] is not None])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("pad", [0, 2, 1], ids=["dense", "words", "off words"])
+@pytest.mark.parametrize("packed", [False, True], ids=["batch", "packed"])
+def test_recurrence_pairs_of_channels(ssd, packed, pad, dtype):
+    """Whole tiles whose pairs of channels lie on 32-bit words, and beside them."""
+    Bt, L, E, cu = (1, 520, 96, [0, 200, 520]) if packed else (3, 260, 96, None)
+    a, r = make(Bt, L, E, dtype, True, True, pad)
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda") if packed else None
+    init, dy = None if packed else r(Bt, E), r(Bt, L, E, dt=dtype)
+    want = B.recurrence(*a.values(), init, 8.0, cu, (dy, None))
+    y, final, states = ssd.recurrence_forward(**a, init_state=init, cu_seqlens=c, return_final_state=True,
+                                              return_states=True)
+    check_all((packed, pad), dict(y=y, final=final), want, ("y", "final"))
+    got = ssd.recurrence_backward(**a, dy=dy, init_state=init, cu_seqlens=c, states=states)
+    check_all((packed, pad), got, want, [k for k in got if got[k] is not None])
+
+
 CUS = [[0, 40], [0, 0, 1, 2, 2, 15, 31, 40, 40], [0, 3, 300, 300, 301, 511, 700], [0, 64, 1000, 1100],
        list(range(0, 1031, 103)), [7, 9, 64, 200, 300], [0, 2049]]
 
