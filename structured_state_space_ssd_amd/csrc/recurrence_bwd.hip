@@ -11,6 +11,11 @@
 // kept one every kRecKeep = 16 tokens (1/4 of a byte a channel and token), and make their
 // states from it again in registers; the adjoint is put together like the forward's
 // state, against the tokens' order.
+//
+// 8 x 2048 x 2560 bf16 with z: 210 us for 765 MB, 3.6 TB/s. The same loads and stores
+// alone take 185 us, the 94 vector instructions of an element 113; a SIMD holds four
+// wavefronts (about 120 registers), which hide most of the one behind the other. Two
+// wavefronts to a tile in place of four, and stores that pass the caches by, gained nothing.
 #include "recurrence.h"
 
 namespace ssd {
