@@ -108,6 +108,10 @@ SIGNATURES = {
     "ssd_norm_backward_workspace_size": (_sz, [_ll, _i, _i, _i]),
     "ssd_norm_backward": (_i, [_vp, _vp, _ll, _i, _vp, _ll, _vp, _vp, _vp, _vp, _ll, _i, _i]
                           + [_vp] * 6 + [_sz, _vp]),
+}
+
+# the same of the operators of a recurrent block
+BLOCK_SIGNATURES = {
     "ssd_recurrence_forward_workspace_size": (_sz, [_i] * 5),
     "ssd_recurrence_forward": (_i, [_vp] * 4 + [_f, _vp] + [_i] * 4 + [_vp, _vp, _i] + [_vp] * 4 + [_sz, _rsp, _vp]),
     "ssd_recurrence_step": (_i, [_vp] * 5 + [_f, _vp] + [_i] * 3 + [_vp, _rsp, _vp]),
@@ -128,7 +132,7 @@ def _load():
             f"{LIB_PATH} is not built; run `python structured_state_space_ssd_amd/build.py` "
             "(there is no fallback implementation)")
     lib = ctypes.CDLL(LIB_PATH)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in {**SIGNATURES, **BLOCK_SIGNATURES}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -16,9 +16,8 @@ from structured_state_space_ssd_amd import _native  # noqa: E402
 
 BF, F32, ptr, code, ok, every_way = K.BF, K.F32, K.ptr, K.code, K.ok, K.every_way
 lib = K.lib
-for _name, (_res, _args) in _native.SIGNATURES.items():
-    if any(k in _name for k in ("recurrence", "dropout", "block")):
-        getattr(lib, _name).restype, getattr(lib, _name).argtypes = _res, _args
+for _name, (_res, _args) in _native.BLOCK_SIGNATURES.items():
+    getattr(lib, _name).restype, getattr(lib, _name).argtypes = _res, _args
 
 
 def scratch(m, size):
