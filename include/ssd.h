@@ -688,6 +688,9 @@ int ssd_norm_backward(const void *dy, const void *x, long long x_row_stride, int
  *   states     nullable, float32 [Bt][ceil(L / 16)][E]: the state before every 16th
  *              token, for ssd_recurrence_backward.
  *   workspace  ssd_recurrence_forward_workspace_size bytes, 256-byte aligned.
+ * Tiles of a sequence wait for those before them through the workspace: while a call runs,
+ * nothing else may write there (as for every workspace; here the tiles would wait, for a second
+ * or so each, for what does not come, and give what is not a number).
  * All in float32 with one rounding at the end. 1 - a^2 is formed without
  * cancellation, so channels that hardly decay keep their input. The result does not
  * depend on timing.

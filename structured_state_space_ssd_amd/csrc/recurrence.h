@@ -232,7 +232,8 @@ struct RecShared {
     float enters[kRecWaves][kRecCols];                     // what enters the wavefronts
 };
 
-// The workgroup's tile, in the order of starting.
+// The workgroup's tile, in the order of starting (one that there is not, where another call has
+// written over the workspace).
 __device__ __forceinline__ int rec_ticket(const RecArgs &a, const RecPlace &p, RecShared &sh) {
     if (a.tiles == 1) return 0;
     if (threadIdx.x == 0)
@@ -248,9 +249,11 @@ __device__ __forceinline__ void rec_tell(unsigned long long *at, float value, ui
 __device__ __forceinline__ unsigned long long rec_look(const unsigned long long *at) {
     return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// `v`: what rec_look has seen there.
+// `v`: what rec_look has seen there. A wait of about a second (a tile takes microseconds) means
+// that another call has written over the workspace; it ends with what is not a number.
+constexpr int kRecLooks = 1 << 20;
 __device__ __forceinline__ RecMap rec_wait(const unsigned long long *at, unsigned long long v) {
-    while (static_cast<uint32_t>(v) == kRecUnset) {
+    for (int k = 0; static_cast<uint32_t>(v) == kRecUnset && k < kRecLooks; ++k) {
         __builtin_amdgcn_s_sleep(1);
         v = rec_look(at);
     }

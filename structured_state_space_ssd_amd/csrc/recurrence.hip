@@ -66,6 +66,7 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? GATE ? 5 : 6 : 7) 
     const RecPlace p = rec_place(a);
     if (!p.live) return;
     const int order = rec_ticket(a, p, sh);
+    if (static_cast<unsigned>(order) >= static_cast<unsigned>(a.tiles)) return;
     const int E = a.channels, tw = (order * a.waves + p.wave) * 4 * S, ts = tw + p.sub * S;
     const int nt = min(max(a.seqlen - ts, 0), S);
     auto run = [&](auto whole_tile, auto cuts) {

@@ -73,6 +73,7 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
     const RecPlace p = rec_place(a);
     if (!p.live) return;
     const int order = rec_ticket(a, p, sh), tile = a.tiles - 1 - order;
+    if (static_cast<unsigned>(order) >= static_cast<unsigned>(a.tiles)) return;
     const int E = a.channels, tw = (tile * a.waves + p.wave) * 4 * S, ts = tw + p.sub * S;
     const int nt = min(max(a.seqlen - ts, 0), S);
     auto run = [&](auto whole_tile, auto cuts) {
