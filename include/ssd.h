@@ -694,6 +694,11 @@ int ssd_norm_backward(const void *dy, const void *x, long long x_row_stride, int
  * All in float32 with one rounding at the end. 1 - a^2 is formed without
  * cancellation, so channels that hardly decay keep their input. The result does not
  * depend on timing.
+ * Ends of the range: the direct form is made for r <= 0. Above 0 a state grows, and the
+ * decays of up to 256 tokens are multiplied before they meet it: where such a product passes
+ * float32 a state of zero stays zero, another one becomes infinite or NaN, at times before the
+ * formula's does (exp(r) of one token has to be finite in float32). An infinite state stays
+ * not finite, but becomes NaN where the decays of so many tokens go to 0.
  */
 typedef struct {
     long long x_batch, x_token, r_batch, r_token, i_batch, i_token, z_batch, z_token;

@@ -81,7 +81,9 @@ def recurrence_forward(x, r, i=None, decay=None, z=None, init_state=None, c=8.0,
 
     With i and decay the gates are formed here, log a_t = -c softplus(decay)
     sigmoid(r_t) and u_t = sqrt(1 - a_t^2) sigmoid(i_t) x_t; without them r is the
-    log-decay itself, a_t = exp(r_t), and u_t = x_t.
+    log-decay itself, a_t = exp(r_t), and u_t = x_t. It is made for r at most 0: where r
+    above 0 makes the decays of up to 256 tokens together pass float32, a state that is
+    not zero becomes infinite or NaN there.
     x, r, i, z [Bt, L, E] float32 or bfloat16 (slices of wider projections are
     fine), decay [E] float32, init_state [Bt, E] float32 or None (zeros).
     cu_seqlens: packed sequences as for ``forward_varlen`` (Bt 1, no init_state);

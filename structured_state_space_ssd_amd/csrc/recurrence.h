@@ -163,22 +163,27 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct RecMap {
     float a, h;
 };
+// a h + v. GROWS (the direct form, where decays may pass 1): the product of many may be
+// infinite, and a state of zero stays out of it.
+template <bool GROWS> __device__ __forceinline__ float rec_carry(float a, float h, float v) {
+    return GROWS && h == 0.0f ? v : fmaf(a, h, v);
+}
 // first, then second
-template <bool PACKED> __device__ __forceinline__ RecMap rec_then(RecMap first, RecMap second) {
+template <bool PACKED, bool GROWS> __device__ __forceinline__ RecMap rec_then(RecMap first, RecMap second) {
     if (PACKED) {
         const bool cut = second.a < 0.0f;
         return {cut || first.a < 0.0f ? -1.0f : first.a * second.a,
-                cut ? second.h : fmaf(second.a, first.h, second.h)};
+                cut ? second.h : rec_carry<GROWS>(second.a, first.h, second.h)};
     }
-    return {first.a * second.a, fmaf(second.a, first.h, second.h)};
+    return {first.a * second.a, rec_carry<GROWS>(second.a, first.h, second.h)};
 }
-template <bool PACKED> __device__ __forceinline__ float rec_apply(RecMap m, float h) {
-    return PACKED && m.a < 0.0f ? m.h : fmaf(m.a, h, m.h);
+template <bool PACKED, bool GROWS> __device__ __forceinline__ float rec_apply(RecMap m, float h) {
+    return PACKED && m.a < 0.0f ? m.h : rec_carry<GROWS>(m.a, h, m.h);
 }
 
 // The wavefront's four strands put together in the order of their tokens, or against
 // it (REVERSE): `whole` all of them, `before` those that come before the lane's own.
-template <bool PACKED, bool REVERSE>
+template <bool PACKED, bool GROWS, bool REVERSE>
 __device__ __forceinline__ void rec_wave(RecMap m, int sub, RecMap &before, RecMap &whole) {
     auto swap16 = [](float v, float &even, float &odd) {
         const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -193,15 +198,15 @@ __device__ __forceinline__ void rec_wave(RecMap m, int sub, RecMap &before, RecM
     RecMap even, odd, low, high;
     swap16(m.a, even.a, odd.a);
     swap16(m.h, even.h, odd.h);
-    const RecMap pair = REVERSE ? rec_then<PACKED>(odd, even) : rec_then<PACKED>(even, odd);
+    const RecMap pair = REVERSE ? rec_then<PACKED, GROWS>(odd, even) : rec_then<PACKED, GROWS>(even, odd);
     swap32(pair.a, low.a, high.a);
     swap32(pair.h, low.h, high.h);
-    whole = REVERSE ? rec_then<PACKED>(high, low) : rec_then<PACKED>(low, high);
+    whole = REVERSE ? rec_then<PACKED, GROWS>(high, low) : rec_then<PACKED, GROWS>(low, high);
     // within the pair, the second of the two comes after the first; the same for the pairs
     const bool second = REVERSE ? !(sub & 1) : (sub & 1), later = REVERSE ? !(sub & 2) : (sub & 2) != 0;
     const RecMap mate = REVERSE ? odd : even, pairs = REVERSE ? high : low;
     const RecMap none = {1.0f, 0.0f};
-    const RecMap in = second ? mate : none, joined = rec_then<PACKED>(pairs, in);
+    const RecMap in = second ? mate : none, joined = rec_then<PACKED, GROWS>(pairs, in);
     before = later ? joined : in;
 }
 
@@ -265,7 +270,7 @@ __device__ __forceinline__ RecMap rec_wait(const unsigned long long *at, unsigne
 // NULL (zeros); last: what leaves its last one, the same. REVERSE: the last wavefront comes
 // first. order: the tile's place in the order of the walk. For the wait and what follows
 // a lane is a channel, and half a wavefront looks at kRecAtOnce tiles.
-template <bool PACKED, bool REVERSE>
+template <bool PACKED, bool GROWS, bool REVERSE>
 __device__ __forceinline__ void rec_enter(const RecArgs &a, const RecPlace &p, int order, const RecMap (&whole)[2],
                                           const float *first, float *last, float (&enters)[2], RecShared &sh) {
     if (p.sub == 0)
@@ -286,7 +291,7 @@ __device__ __forceinline__ void rec_enter(const RecArgs &a, const RecPlace &p, i
     if (a.tiles > 1) {
         if (part == 0 && place < kRecGroup - 1 && order + 1 < a.tiles) {
             RecMap all = wave_map(0, c);
-            for (int k = 1; k < a.waves; ++k) all = rec_then<PACKED>(all, wave_map(k, c));
+            for (int k = 1; k < a.waves; ++k) all = rec_then<PACKED, GROWS>(all, wave_map(k, c));
             // (any number but the mark of none; a decay that is not a number is one of its own)
             rec_tell(a.maps + order * words + at, all.h, all.a != all.a ? 0x7fc00000u : __float_as_uint(all.a));
         }
@@ -300,7 +305,7 @@ __device__ __forceinline__ void rec_enter(const RecArgs &a, const RecPlace &p, i
             RecMap tiles = {1.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < kRecAtOnce; ++k)
-                if (k < n) tiles = rec_then<PACKED>(tiles, rec_wait(maps + k * words, seen[k]));
+                if (k < n) tiles = rec_then<PACKED, GROWS>(tiles, rec_wait(maps + k * words, seen[k]));
             sh.before[q][c][0] = tiles.a;
             sh.before[q][c][1] = tiles.h;
         }
@@ -313,10 +318,10 @@ __device__ __forceinline__ void rec_enter(const RecArgs &a, const RecPlace &p, i
     if (part == 0) {
         const int ch = (p.unit - p.batch * a.blocks) * kRecCols + c;
         float in = group > 0 ? sh.state[c] : first && ch < a.channels ? first[(size_t)p.batch * a.channels + ch] : 0.0f;
-        for (int q = 0; q * kRecAtOnce < place; ++q) in = rec_apply<PACKED>({sh.before[q][c][0], sh.before[q][c][1]}, in);
+        for (int q = 0; q * kRecAtOnce < place; ++q) in = rec_apply<PACKED, GROWS>({sh.before[q][c][0], sh.before[q][c][1]}, in);
         for (int k = 0; k < a.waves; ++k) {
             sh.enters[REVERSE ? a.waves - 1 - k : k][c] = in;
-            in = rec_apply<PACKED>(wave_map(k, c), in);
+            in = rec_apply<PACKED, GROWS>(wave_map(k, c), in);
         }
         if (place == kRecGroup - 1 && order + 1 < a.tiles) rec_tell(a.enter + (group + 1) * words + at, in, 0);
         if (last && order == a.tiles - 1 && ch < a.channels) last[(size_t)p.batch * a.channels + ch] = in;

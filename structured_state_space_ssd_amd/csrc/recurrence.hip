@@ -106,15 +106,15 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? GATE ? 5 : 6 : 7) 
                 if (CUTS && code[j] < 0) u = 0.0f;
                 av[j][e] = d;
                 uv[j][e] = u;
-                m[e] = rec_then<CUTS>(m[e], {d, u});
+                m[e] = rec_then<CUTS, false>(m[e], {d, u});
             }
         RecMap before[2], whole[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) rec_wave<CUTS, false>(m[e], p.sub, before[e], whole[e]);
+        for (int e = 0; e < 2; ++e) rec_wave<CUTS, !GATED, false>(m[e], p.sub, before[e], whole[e]);
         float h[2];
-        rec_enter<PACKED, false>(a, p, order, whole, a.init, PACKED ? nullptr : a.final_state, h, sh);
+        rec_enter<PACKED, !GATED, false>(a, p, order, whole, a.init, PACKED ? nullptr : a.final_state, h, sh);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) h[e] = rec_apply<CUTS>(before[e], h[e]);
+        for (int e = 0; e < 2; ++e) h[e] = rec_apply<CUTS, !GATED>(before[e], h[e]);
         if (a.states && ts % kRecKeep == 0 && (WHOLE || nt > 0)) {
             float *s = a.states + ((size_t)p.batch * a.keeps + ts / kRecKeep) * E + p.ch;
             if (p.nch > 0) s[0] = h[0];
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? GATE ? 5 : 6 : 7) 
             float o[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                h[e] = rec_apply<CUTS>({av[j][e], uv[j][e]}, h[e]);
+                h[e] = rec_apply<CUTS, false>({av[j][e], uv[j][e]}, h[e]);
                 o[e] = h[e];
                 if (GATE) o[e] *= silu_f32(z[j].get(e));
                 if (CUTS && code[j] < 0) o[e] = 0.0f;

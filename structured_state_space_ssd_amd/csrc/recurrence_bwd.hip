@@ -127,13 +127,13 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
                 }
                 av[j][e] = d;
                 hv[j][e] = u;
-                m[e] = rec_then<CUTS>(m[e], {d, u});
+                m[e] = rec_then<CUTS, false>(m[e], {d, u});
             }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             RecMap before, whole;
-            rec_wave<CUTS, false>(m[e], p.sub, before, whole);
-            float h = rec_apply<CUTS>(before, hw[e]);
+            rec_wave<CUTS, !GATED, false>(m[e], p.sub, before, whole);
+            float h = rec_apply<CUTS, !GATED>(before, hw[e]);
 #pragma unroll
             for (int j = 0; j < S; ++j) {  // what each token takes of the state before, in its input's place
                 const float carried = CUTS && av[j][e] < 0.0f ? 0.0f : av[j][e] * h;
@@ -170,12 +170,12 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
             }
         RecMap after[2], whole[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) rec_wave<CUTS, true>(mg[e], p.sub, after[e], whole[e]);
+        for (int e = 0; e < 2; ++e) rec_wave<CUTS, !GATED, true>(mg[e], p.sub, after[e], whole[e]);
         // what comes to the wavefront's last token from behind
         float qs[2];
-        rec_enter<PACKED, true>(a, p, order, whole, PACKED ? nullptr : b.dfinal, PACKED ? nullptr : b.dinit, qs, sh);
+        rec_enter<PACKED, !GATED, true>(a, p, order, whole, PACKED ? nullptr : b.dfinal, PACKED ? nullptr : b.dinit, qs, sh);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) qs[e] = rec_apply<CUTS>(after[e], qs[e]);
+        for (int e = 0; e < 2; ++e) qs[e] = rec_apply<CUTS, !GATED>(after[e], qs[e]);
         // (the values anew: what the compiler keeps of them from above fills the registers)
 #pragma unroll
         for (int j = 0; j < S; ++j) {

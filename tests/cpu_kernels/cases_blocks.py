@@ -126,6 +126,42 @@ def bad_offsets(cu):
     every_way(cu, run)
 
 
+def growth(L, rate, dtype, cu=None):
+    """Log-decays above 0 over tiles of zero inputs, whose products pass float32: a state of zero
+    stays zero. Inputs are at the last tokens only, gradients of y at the first."""
+    E, few = 5, 6
+    g = torch.Generator().manual_seed(L)
+    x, r, dy = (torch.zeros(1, L, E, dtype=dtype) for _ in range(3))
+    r.fill_(rate)
+    x[:, -few:], dy[:, :few] = torch.randn(1, few, E, generator=g).to(dtype), torch.randn(1, few, E, generator=g).to(dtype)
+    nseq = 0 if cu is None else len(cu) - 1
+    want = B.recurrence(x, r, cu=cu, grads=(dy, None))
+
+    def run(m):
+        px, pr, pd, pc = m.put(x), m.put(r), m.put(dy), None if cu is None else m.put(torch.tensor(cu, dtype=torch.int32))
+        o = dict(y=m.new((1, L, E), dtype), final=m.new((nseq or 1, E)), dx=m.new((1, L, E), dtype), dr=m.new((1, L, E), dtype))
+        c = code(dtype)
+        ws = scratch(m, lib.ssd_recurrence_forward_workspace_size(1, L, E, int(nseq > 0), c))
+        ok(lib.ssd_recurrence_forward(ptr(px), ptr(pr), None, None, 8.0, None, 1, L, E, c, None, ptr(pc), nseq, ptr(o["y"]),
+                                      ptr(o["final"]), None, *ws, None, None), "forward")
+        ws = scratch(m, lib.ssd_recurrence_backward_workspace_size(1, L, E, int(nseq > 0), 0, c))
+        ok(lib.ssd_recurrence_backward(ptr(px), ptr(pr), None, None, 8.0, None, None, ptr(pc), nseq, None, ptr(pd), None,
+                                       1, L, E, c, ptr(o["dx"]), ptr(o["dr"]), None, None, None, None, *ws, None, None),
+           "backward")
+        return o
+
+    for k, v in every_way((L, rate, cu), run).items():
+        R.check((L, rate, str(dtype), cu, k), v, want[k], want[k + "_err"], 1.0)
+
+
+def run_growth():
+    for L, rate in ((100, 1.0), (520, 1.0), (1100, 0.5), (2500, 0.5), (300, 8.0)):
+        for dtype in (BF, F32):
+            for cu in (None, [0, 3, L]):
+                print("growth", L, rate, dtype, cu, flush=True)
+                growth(L, rate, dtype, cu)
+
+
 def run_recurrence():
     for size in SIZES:
         for args in ((BF, True, True, 3, True), (F32, True, False, 0, False), (BF, False, False, 0, True),

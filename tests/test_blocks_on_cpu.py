@@ -40,6 +40,13 @@ def test_blocks_on_cpu(library, which):
     assert r.returncode == 0 and "all cases done" in r.stdout, (r.returncode, r.stdout[-300:], r.stderr[-2000:])
 
 
+def test_growing_states_on_cpu(library):
+    """The direct form's log-decays above 0, whose products over tiles are infinite."""
+    r = subprocess.run([sys.executable, os.path.join(HERE, "cases_blocks.py"), library, "growth"],
+                       capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and "all cases done" in r.stdout, (r.returncode, r.stdout[-300:], r.stderr[-2000:])
+
+
 LOST = """
 import ctypes, sys
 import numpy as np

@@ -235,3 +235,28 @@ def test_recurrence_prompt_then_tokens(ssd):
         R.check("pieces", torch.cat(ys, 1), want["y"], want["y_err"], 1.0)
         R.check("final", s, want["final"], want["final_err"], 1.0)
         R.check("whole", final, want["final"], want["final_err"], 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("cu", [None, [0, 3, 1300]], ids=["batch", "packed"])
+def test_recurrence_growing_states(ssd, cu, dtype):
+    """Log-decays above 0, whose products over tiles pass float32 where the state is still (or, going
+    back, the gradient) zero: inputs at the last tokens only, gradients of y at the first."""
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    for L, E, rate in ((1300, 40, 0.5), (1300, 33, 1.0), (1300, 200, 8.0)):
+        r, few = normal(int(8 * rate)), 6
+        x, g, dy = (torch.zeros(1, L, E, dtype=dtype, device="cuda") for _ in range(3))
+        g.fill_(rate)
+        x[:, -few:], dy[:, :few] = r(1, few, E, dt=dtype), r(1, few, E, dt=dtype)
+        want = B.recurrence(x, g, cu=cu, grads=(dy, None))
+        y, final, states = ssd.recurrence_forward(x, g, cu_seqlens=c, return_final_state=True, return_states=True)
+        check_all((L, rate), dict(y=y, final=final), want, ("y", "final"))
+        for s in (states, None):
+            got = ssd.recurrence_backward(x, g, None, None, dy, cu_seqlens=c, states=s)
+            check_all((L, rate), got, want, ("dx", "dr"))
+        # from a state of zero that is given, and a gradient of zero
+        if cu is None:
+            zero = torch.zeros(1, E, device="cuda")
+            assert torch.equal(ssd.recurrence_forward(x, g, init_state=zero), y)
+            got = ssd.recurrence_backward(x, g, None, None, dy, init_state=zero, dfinal_state=zero)
+            check_all((L, rate), got, want, ("dx", "dr", "dinit"))
