@@ -779,7 +779,8 @@ int ssd_dropout(const void *x, long long x_row_stride, long long rows, int width
  *   random     NULL: no dropout.
  *   y          dense, dtype. mean, rstd, post_mean, post_rstd: nullable, float32
  *              [rows], the norms' statistics (means not written with rms).
- * Outputs must not overlap inputs.
+ * What z and, without post_weight, x hold where an element is dropped (infinities, NaN)
+ * reaches no output, nor any gradient. Outputs must not overlap inputs.
  */
 typedef struct {
     const float *weight, *bias, *post_weight, *post_bias, *scale;

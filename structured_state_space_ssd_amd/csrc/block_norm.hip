@@ -365,8 +365,13 @@ void block_bwd_kernel(BlockBwdArgs a, BlockSets sets) {
             if (a.drop.threshold) {
                 const DropBits bits = drop_bits<V>(rng, c, row);
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    ds[i][e] = bits.keep(e, a.drop.threshold) ? ds[i][e] * a.drop.scale : 0.0f;
+                for (int e = 0; e < V; ++e) {
+                    const bool keep = bits.keep(e, a.drop.threshold);
+                    ds[i][e] = keep ? ds[i][e] * a.drop.scale : 0.0f;
+                    // (what a dropped element holds is not multiplied by that zero: it may be infinite)
+                    if (z) zr[i].clear(e, keep);
+                    if (!a.post_weight) xr[i].clear(e, keep);
+                }
             }
             float k[V], w[V];
             col_load(k, a.scale, c, n, 1.0f);

@@ -47,6 +47,10 @@ template <> struct RowRaw<bf16_t, 8> {
         const uint32_t v = w[e >> 1];
         return __uint_as_float((e & 1) ? (v & 0xffff0000u) : (v << 16));
     }
+    // 0 in its place unless `keep`
+    __device__ __forceinline__ void clear(int e, bool keep) {
+        w[e >> 1] = keep ? w[e >> 1] : w[e >> 1] & ((e & 1) ? 0x0000ffffu : 0xffff0000u);
+    }
 };
 template <> struct RowRaw<bf16_t, 4> {
     uint32_t w[2];
@@ -91,6 +95,7 @@ template <int V> struct RowRaw<float, V> {
             if (e < n) w[e] = p[e];
     }
     __device__ __forceinline__ float get(int e) const { return w[e]; }
+    __device__ __forceinline__ void clear(int e, bool keep) { w[e] = keep ? w[e] : 0.0f; }
 };
 
 // Two values rounded to bf16 (nearest even, one instruction), the first one low.

@@ -281,6 +281,57 @@ def run_block():
             block(rows, D, *args)
 
 
+def dropped(rows, D, dtype, stream, rms, post, bias, gate, p, bad):
+    """What x (without a norm in front) and the gate hold where an element is dropped reaches no
+    result and no gradient: the same bits as with zeros there."""
+    g = torch.Generator().manual_seed(rows + D)
+    r = lambda *s, dt=F32, off=0.0: (torch.randn(*s, generator=g) + off).to(dt)  # noqa: E731
+    rng, kept = (5, 6), B.kept(rows, D, p, 5, 6)
+    x, res, dy, dsum = r(rows, D, dt=dtype), r(rows, D, dt=stream), r(rows, D, dt=dtype), r(rows, D, dt=stream)
+    par = [r(D, off=1.0), r(D) if bias else None, r(D, off=1.0) if post else None, r(D) if post and bias else None, r(D)]
+    z = r(rows, D, dt=dtype) if gate else None
+
+    def run(fill):
+        tx = x if post else x.masked_fill(~kept, fill)
+        tz = z.masked_fill(~kept, fill) if gate else None
+
+        def both(m):
+            put = [m.put(t) for t in par]
+            opt = ctypes.byref(_native.SsdBlock(*map(ptr, put), 1.25, -0.75, int(rms), 1e-5))
+            rnd = ctypes.byref(_native.SsdRandom(p, *rng, None))
+            px, pr, pz, pd, ps = m.put(tx), m.put(res), m.put(tz), m.put(dy), m.put(dsum)
+            o = dict(y=m.new((rows, D), dtype), sum=m.new((rows, D), stream), mean=None if rms else m.new((rows,)),
+                     rstd=m.new((rows,)), post_mean=m.new((rows,)) if post and not rms else None,
+                     post_rstd=m.new((rows,)) if post else None)
+            stats = [ptr(o[k]) for k in ("mean", "rstd", "post_mean", "post_rstd")]
+            ok(lib.ssd_block_norm_forward(ptr(px), D, ptr(pr), code(stream), ptr(pz), D, opt, rnd, rows, D, code(dtype),
+                                          ptr(o["y"]), ptr(o["sum"]), *stats, None), "forward")
+            q = dict(dx=m.new((rows, D), dtype), dresidual=m.new((rows, D), stream), dz=m.new((rows, D), dtype) if gate else None)
+            for k, t in zip(("dweight", "dbias", "dpost_weight", "dpost_bias", "dscale"), par):
+                q[k] = None if t is None else m.new((D,))
+            ws = scratch(m, lib.ssd_block_norm_backward_workspace_size(rows, D, code(dtype)))
+            ok(lib.ssd_block_norm_backward(ptr(pd), ptr(ps), ptr(px), D, ptr(o["sum"]), code(stream), ptr(pz), D, opt, rnd,
+                                           *stats, rows, D, code(dtype), *map(ptr, q.values()), *ws, None), "backward")
+            return {**o, **q}
+
+        return every_way((rows, D, fill), both)
+
+    want, got = run(0.0), run(bad)
+    for k, t in got.items():
+        assert t is None or torch.equal(t, want[k]), (k, "what is dropped matters")
+        assert t is None or bool(t.isfinite().all()), k
+
+
+def run_dropped():
+    for rows, D in ((5, 9), (3, 513), (2, 2563), (1, 8192)):
+        for args in ((BF, F32, True, False, False, False, 0.5), (BF, F32, False, True, True, True, 0.3),
+                     (F32, F32, False, False, True, True, 0.5), (BF, BF, True, False, False, True, 0.9),
+                     (F32, F32, True, False, False, False, 1.0), (F32, F32, True, True, False, True, 0.1)):
+            for bad in (float("inf"), float("nan")):
+                print("dropped", rows, D, *args, bad, flush=True)
+                dropped(rows, D, *args, bad)
+
+
 if __name__ == "__main__":
     torch.set_num_threads(1)
     for which in sys.argv[2:] or ("recurrence", "dropout", "block"):

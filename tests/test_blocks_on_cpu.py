@@ -47,6 +47,13 @@ def test_growing_states_on_cpu(library):
     assert r.returncode == 0 and "all cases done" in r.stdout, (r.returncode, r.stdout[-300:], r.stderr[-2000:])
 
 
+def test_dropped_values_on_cpu(library):
+    """Infinities and NaN where the block norm's dropout drops, forward and back."""
+    r = subprocess.run([sys.executable, os.path.join(HERE, "cases_blocks.py"), library, "dropped"],
+                       capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and "all cases done" in r.stdout, (r.returncode, r.stdout[-300:], r.stderr[-2000:])
+
+
 LOST = """
 import ctypes, sys
 import numpy as np

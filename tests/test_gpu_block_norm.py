@@ -140,3 +140,25 @@ def test_block_norm_far_rows(ssd):
     a = ssd.block_norm_backward(dy, res, x, total, stats, **par, z=x)
     b = ssd.block_norm_backward(dy, res, far, total, stats, **par, z=far)
     assert all(torch.equal(a[k], b[k]) for k in a if a[k] is not None)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")], ids=["inf", "nan"])
+@pytest.mark.parametrize("kind", [(BF, F32, True, 0, 0), (BF, F32, False, 1, 1), (F32, F32, False, 0, 1), (BF, BF, True, 0, 1)],
+                         ids=str)
+def test_block_norm_dropped_values(ssd, kind, bad):
+    """What x (without a norm in front) and the gate hold where an element is dropped reaches no
+    result and no gradient: the same bits as with zeros there."""
+    dtype, stream, rms, post, gate = kind
+    for rows, D, p in ((300, 8, 0.5), (7, 1000, 0.1), (5, 2560, 0.9), (3, 8192, 1.0)):
+        x, res, par, r = make(rows, D, dtype, stream, post, 1, not rms, 1, gate, 0)
+        kw = dict(p=p, rng=(5, 6))
+        lost = ~B.kept(rows, D, p, 5, 6).cuda()
+        dy, dsum = r(rows, D), r(rows, D, dt=stream)
+        out = []
+        for fill in (0.0, bad):
+            tx = x if post else x.masked_fill(lost, fill)
+            q = dict(par, z=par["z"].masked_fill(lost, fill)) if gate else par
+            y, total, stats = ssd.block_norm_forward(tx, res, **q, **kw, rms=rms, return_stats=True)
+            out.append({**ssd.block_norm_backward(dy, dsum, tx, total, stats, **q, **kw), "y": y, "sum": total})
+        for k, t in out[0].items():
+            assert t is None or torch.equal(out[1][k], t) and bool(t.isfinite().all()), (rows, D, k)
