@@ -114,7 +114,7 @@ def recurrence_backward(x, r, i, decay, dy, z=None, init_state=None, dfinal_stat
     ``recurrence_forward`` with the same inputs (ssd_recurrence_backward).
 
     states: what recurrence_forward returned of that name for the same inputs;
-    None: they are made again, at the cost of reading x, r and i once more.
+    None: they are made again, at the cost of reading x, r, i and z once more.
     dfinal_state: like final_state ([nseq, E] with cu_seqlens).
     Returns a dict: dx, dr, di, dz (dense, in x's type), ddecay [E] and dinit
     [Bt, E] float32; di and ddecay are None without decay, dz without z, dinit
@@ -224,7 +224,8 @@ def block_norm_forward(x, residual, weight=None, bias=None, post_weight=None, po
     """A block's output joined with the residual stream, and the next block's input
     (ssd_block_norm_forward):
     sum = residual_scale * residual + branch_scale * dropout(norm(x) * scale * silu(z)),
-    y = norm(sum).
+    y = norm(sum). Where that is only residual + x and its norm, ``norm_forward`` with a
+    residual does the same, and its backward reads less.
 
     post_weight, post_bias: of the norm after the block (of x; None: x itself);
     weight, bias: of the norm before the next (None: no y). Layer norms, with rms their

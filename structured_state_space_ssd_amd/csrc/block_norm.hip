@@ -19,8 +19,12 @@
 // the two norms are two rounds of sums over it. Nothing between x and y goes
 // through memory but the stream and, for training, four numbers a row. Measured, bf16 with a
 // float32 stream: 16384 x 2560, both norms in the root-mean-square form, scale and dropout, forward
-// 109 us (4.6 TB/s), backward 185 (4.1 TB/s) and 8 for the sums of the partial rows; 4099 x
-// 5120, layer norms with gate, 72, 129 and 8 (4.1 and 3.6 TB/s).
+// 108 us (4.7 TB/s), backward 189 (4.0 TB/s) and 8 for the sums of the partial rows; 4099 x
+// 5120, layer norms with gate, 71, 130 and 8 (4.1 and 3.6 TB/s). float32 throughout, the same
+// number of elements as the latter: 8192 x 2560 all options 114, 184 and 8, without biases and gate 69, 136
+// and 6 (4.9 and 3.7 TB/s); 2560 x 8192 118, 182 and 9, and 82, 116 and 6. Rows of little more
+// than 64 vectors leave most of their second wavefront without work: 80659 x 520 bf16 202, 350
+// and 8, where 40960 x 1024 takes 118, 205 and 8.
 #include "dropout.h"
 #include "ssd_launch.h"
 #include "ssd_rows.h"
@@ -447,8 +451,11 @@ void block_bwd_kernel(BlockBwdArgs a, BlockSets sets) {
 
 // Adds up the partial rows, 1024 / COLS strands of them to a column, and makes the
 // parameters' gradients of the sums: blockIdx.y 0 the norm before's, 1 what lies after the
-// block. 16 columns to a workgroup where there are many rows (768 of 2 x 2560 columns: 7.9
-// us, with 32 columns 11.4), else 32 (256 of 4 x 5120: 10.3 and 8.3).
+// block. 16 columns to a workgroup where there are many rows, else 32. Measured, 16 and 32 columns:
+// 768 rows of 2 x 2560 columns 7.6 and 10.9 us, 768 of 4 x 520 10.6 and 17.8; 256 rows of 4 x 5120
+// 11.0 and 8.6, of 4 x 8192 13.0 and 9.2, of 2 x 8192 8.7 and 6.1. Between them the columns
+// count for more than the rows, which this rule leaves: 512 rows of 4 x 2560 9.2 and 12.8, 501 of
+// 2 x 2560 7.3 and 9.4, 256 of 4 x 520 5.1 and 7.5, 64 of 2 x 2560 3.4 both.
 template <int COLS> __global__ __launch_bounds__(1024) void block_sum_kernel(BlockBwdArgs a, int rows) {
     constexpr int STRANDS = 1024 / COLS;
     __shared__ float buf[2][16][COLS];
@@ -553,7 +560,10 @@ template <typename T, bool FULL> BlockBwdShape block_bwd_shape(int D) {
     s.sets.waves = w;
     // Wavefronts of a workgroup start on the first SIMD: unless they fill all four alike, the
     // first one is full before the others. So sets that do not are put together, as many as
-    // the CU holds (16384 rows of 2560, five wavefronts each: 284 us one by one).
+    // the CU holds (16384 rows of 2560, five wavefronts each: 284 us one by one, 185 so). Rows of
+    // two wavefronts go one by one, which is not the faster way: back, with the sums of the partial
+    // rows, 40960 x 1024 bf16 212 us, together 187, 54613 x 768 261 and 210, 80659 x 520 357 and 273;
+    // with gate 20480 x 1024 167 and 138; float32 40960 x 512 160 and 120, with gate 221 and 178.
     s.sets.sets = w % 4 == 0 || w < 3 || s.lanes / (64 * w) < 1 ? 1 : s.lanes / (64 * w);
     s.threads = 64 * w * s.sets.sets;
     return s;

@@ -7,8 +7,8 @@
 // A strand's tokens are a map h -> A h + H of the state entering it; maps are put
 // together across the strands of a wavefront by swaps of registers, across the
 // wavefronts through LDS and across the tiles of a unit through memory (rec_enter), so
-// that every operand is read once, whatever the number of channels, and tokens and
-// channels alike fill the GPU.
+// that every operand is read once, whatever the number of channels, and tokens fill the
+// GPU as channels do. Few units are the exception (rec_place).
 //
 // A map that starts a sequence anew inside (packed sequences) is marked by a
 // negative A (a product of decays is not): the state before it does not
@@ -81,7 +81,11 @@ __device__ __forceinline__ int rec_quotient(int n, const RecDivisor &d) {
 }
 // Every unit has as many workgroups as tiles. Units one after the other along the channels
 // go to the same XCD (workgroups are dealt to the eight XCDs in turn): they share
-// cache lines.
+// cache lines. So every XCD takes ceil(units / 8) of them from the first one on, and few units
+// leave XCDs without: 1 of 8 works on one unit, 5 on 9 or 10. 1 x 16384 tokens bf16 without z:
+// 17 us forward and 27 back with 32 channels, 21 and 32 with 256 (8 units), 22 and 40 with 288
+// (9), 22 and 40 with 512 (16): with so few a state's way through the 128 tiles (256 back)
+// takes the time, and where the units lie shows back from 9 on.
 __device__ __forceinline__ RecPlace rec_place(const RecArgs &a) {
     RecPlace p;
     const int units = a.batch * a.blocks, each = (units + 7) >> 3, slot = blockIdx.x >> 3;
@@ -98,7 +102,8 @@ __device__ __forceinline__ RecPlace rec_place(const RecArgs &a) {
 
 // Whether any of a tile's n tokens of a packed axis is a first or last one of a sequence, or
 // in none: of most tiles none is, and they go without the selections (1 x 16384 tokens x 2560
-// channels in 55 sequences, with them everywhere: 112 us forward and 245 back). cuts: per 64
+// channels in 55 sequences, bf16 without z: back 217 us with them everywhere, 207 so; forward
+// 97 to 103 both ways, float32 157 and 153). cuts: per 64
 // tokens, whether any is; a tile begins at the first of 64 and has 128 at most.
 __device__ __forceinline__ bool rec_cuts(const int *cuts, int from, int n) {
     const int *at = cuts + from / 64;

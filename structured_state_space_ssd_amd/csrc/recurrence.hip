@@ -13,7 +13,11 @@
 // bytes a token take 35 and 92 us. Ways that took longer: two passes, the first of which
 // makes the segments' maps (94 us where the exchange between tiles took 61), workgroups that
 // stay for several tiles (70 to 81, where 57), 64 channels to a unit (prompt 74, where 57,
-// training 129, where 111), strands of 4 tokens in bf16 (124, where 113).
+// training 129, where 111), strands of 4 tokens in bf16 (124, where 113); each against the
+// step that it was tried on. float32 at 8 x 2048 x 2560: gated 140 us, with z 175 (4.9 TB/s).
+// Packed, the kernel holds its body four times (whole or ragged, with ends or without): 16384 x
+// 2560 bf16 without z 99 us, with 27 % more vector instructions than without sequences and 72
+// scalar registers spilled to lanes of vector registers, where there are none otherwise.
 #include "recurrence.h"
 
 namespace ssd {
@@ -58,7 +62,9 @@ __global__ __launch_bounds__(256) void rec_prepare_kernel(uint4 *__restrict__ un
 template <typename T> constexpr int rec_fwd_strand() { return sizeof(T) == 2 ? 8 : 4; }
 
 // GATE: whether there is a z (known to the compiler: see the backward's). The wavefronts of a
-// SIMD are what fits without spilling; packed without z left to itself, five: 108 us, so 104.
+// SIMD are what fits without spilling vector registers. Left to the compiler: packed bf16 without
+// z 104 us (so 97 to 103), packed float32 156 and 183 with z (so 153 and 179), bf16 with z 102
+// (so 104).
 template <typename T, bool GATED, bool PACKED, bool GATE>
 __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? GATE ? 5 : 6 : 7) void rec_fwd_kernel(RecArgs a) {
     constexpr int S = rec_fwd_strand<T>();

@@ -12,10 +12,14 @@
 // states from it again in registers; the adjoint is put together like the forward's
 // state, against the tokens' order.
 //
-// 8 x 2048 x 2560 bf16 with z: 210 us for 765 MB, 3.6 TB/s. The same loads and stores
-// alone take 185 us, the 94 vector instructions of an element 113; a SIMD holds four
+// 8 x 2048 x 2560 bf16 with z: 209 us for 765 MB, 3.7 TB/s. The same loads and stores
+// alone take 185 us, the 94 vector instructions of an element 114; a SIMD holds four
 // wavefronts (about 120 registers), which hide most of the one behind the other. Two
 // wavefronts to a tile in place of four, and stores that pass the caches by, gained nothing.
+// float32, gated: 266 us, with z 331 (4.6 TB/s). Packed, bf16 without z, 16384 x 2560: 201 us; its
+// four bodies spill 67 scalar registers, 105 with z, where the kernel without sequences spills 9 and 17.
+// Without kept states the forward kernel runs first, with its z if there is one, though only the
+// states are kept of it: 8 x 2048 x 2560 bf16 with z 93 us more, without 74.
 #include "recurrence.h"
 
 namespace ssd {
@@ -25,8 +29,8 @@ namespace {
 // Whole tiles go through buffer loads and stores: a wavefront's base and a token's distance
 // from it in scalar registers, one offset per lane. By addresses, which the compiler adds
 // up per lane in 64 bits, a tile takes 7 % more vector instructions (8 x 2048 x 2560 bf16
-// with gate: 243 us, so 232; forward, with fewer tensors, no gain). A pair of channels has
-// to lie on 32-bit words, else the tile goes the way of ragged ones.
+// with z: 234 us, so 216; float32 340 and 331; forward, with fewer tensors, no gain). A pair of
+// channels has to lie on 32-bit words, else the tile goes the way of ragged ones (254 us).
 typedef __amdgpu_buffer_rsrc_t rec_buffer;
 __device__ __forceinline__ rec_buffer rec_buffer_at(const void *t, size_t bytes) {
     const uint64_t at = reinterpret_cast<uint64_t>(t) + bytes;
@@ -142,8 +146,8 @@ __global__ __launch_bounds__(kRecWaves * 64, sizeof(T) == 2 ? 4 : 3) void rec_bw
             }
         }
         // What reaches a token's state by its output, formed twice. The gate's sigmoid stays where
-        // the registers that it takes leave the wavefronts of a SIMD as many (231 us without, 222
-        // so); with float32 operands they do not.
+        // the registers that it takes leave the wavefronts of a SIMD as many (8 x 2048 x 2560 222 us
+        // without, 216 so); with float32 operands they do not.
         constexpr bool KEEP = sizeof(T) == 2;
         float zv[S][2];
         if (GATE && KEEP)

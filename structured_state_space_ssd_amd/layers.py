@@ -381,7 +381,8 @@ def norm_forward(x, weight, bias=None, residual=None, z=None, eps=1e-5, rms=Fals
     like x, in x's type or float32; z like x (not together with residual).
     Returns y like x, dense; with residual (y, the sum in residual's type); with
     return_stats also the rows' mean (None if rms) and reciprocal standard
-    deviation, float32, as norm_backward takes them.
+    deviation, float32, as norm_backward takes them. With a norm of the
+    block's output, layer scale, a gate beside the residual or dropout: ``block_norm_forward``.
     """
     _required(x=x, weight=weight)
     rows, step = _rows(x, "x")
